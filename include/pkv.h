@@ -59,6 +59,18 @@ typedef enum pkv_status {
 
 typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1 } pkv_dtype;
 
+/* Which elements of a head form pair i of its first r = rotary_dim ones:
+ * (i, i + r/2), or (2i, 2i + 1). */
+typedef enum pkv_rotary_layout { PKV_ROTARY_HALF = 0, PKV_ROTARY_INTERLEAVED = 1 } pkv_rotary_layout;
+
+/* How rotary_table stretches the angles for contexts beyond those a model was
+ * trained on (see there). */
+typedef enum pkv_rotary_scaling {
+    PKV_ROTARY_UNSCALED = 0,
+    PKV_ROTARY_LINEAR = 1,
+    PKV_ROTARY_BY_PARTS = 2
+} pkv_rotary_scaling;
+
 /* ---------------------------------------------------------------------------
  * kv_reshape_and_cache -- the fused reshape + block write ("vLLM &
  * PagedAttention" §X, first kernel; §V steps 2-3).
@@ -80,6 +92,171 @@ pkv_status kv_reshape_and_cache(const void *key_dev, const void *value_dev,
                                 const int64_t *slot_mapping_dev, int num_tokens,
                                 int num_kv_heads, int head_dim, int block_size,
                                 int num_blocks, pkv_dtype dtype, struct CUstream_st *stream);
+
+/* ---------------------------------------------------------------------------
+ * rotary_table -- cosines and sines of the rotary angles.  The pages have no
+ * counterpart for the rotary calls: they take keys as given; models that mark
+ * positions by rotation need it on the way into the cache.
+ *
+ *   table[p][i] = magnitude * (cos(p * theta_i), sin(p * theta_i)),
+ *   p < num_positions, i < r/2, r = rotary_dim, with w_i = base^(-2i/r) and
+ *   UNSCALED   theta_i = w_i
+ *   LINEAR     theta_i = w_i / factor
+ *   BY_PARTS   theta_i = w_i * (y + (1 - y) / factor),
+ *              y = clamp((n_i - low_turns) / (high_turns - low_turns), 0, 1),
+ *              n_i = original_positions * w_i / 2 pi, the turns pair i makes
+ *              over the original positions: pairs that turn often keep their
+ *              angle, slow ones are stretched.
+ * magnitude (usually 1) scales queries and keys alike.
+ *   cos_sin_dev   fp32 [num_positions][rotary_dim / 2][2], written whole
+ * rotary_dim a multiple of 16 up to 256; base > 1; factor >= 1 (ignored when
+ * UNSCALED); BY_PARTS: original_positions > 0, low_turns < high_turns.
+ * ------------------------------------------------------------------------- */
+pkv_status rotary_table(float *cos_sin_dev, int num_positions, int rotary_dim, double base,
+                        pkv_rotary_scaling scaling, double factor, int original_positions,
+                        double low_turns, double high_turns, double magnitude,
+                        struct CUstream_st *stream);
+
+/* ---------------------------------------------------------------------------
+ * kv_rotary_and_cache -- kv_reshape_and_cache with the rotary rotation on the
+ * way, and the queries' rotation, in one launch.
+ *
+ * Token t at position p = positions[t]: pair (a, b) of the first rotary_dim
+ * elements of each query and key head (layout says which) becomes
+ *   (a cos - b sin, a sin + b cos),  (cos, sin) = table[p][i],
+ * computed in fp32 and rounded once; the other elements pass through.  The
+ * queries go to query_out, the keys to their slots in key_cache, the values,
+ * copied bit for bit, to theirs in value_cache.
+ *   query_dev        [num_tokens][num_heads][head_dim]; NULL with num_heads 0
+ *   query_out_dev    [num_tokens][num_heads][head_dim] contiguous; may be
+ *                    query_dev itself when query_stride is num_heads * head_dim
+ *   key_dev, value_dev  [num_tokens][num_kv_heads][head_dim]
+ *   *_stride         elements from one token to the next (a multiple of 8, at
+ *                    least heads * head_dim): the three may be slices of one
+ *                    projection's rows
+ *   cos_sin_dev      the table of rotary_table, num_positions rows
+ *   positions_dev    [num_tokens] int32.  A position outside the table latches
+ *                    PKV_EINDEX and its token is skipped.
+ *   slot_mapping_dev [num_tokens] int64, as for kv_reshape_and_cache: a
+ *                    negative slot is a padding token, whose keys and values
+ *                    are skipped (its query is rotated if its position is in
+ *                    the table, without error otherwise).  Slots must be
+ *                    distinct.
+ * head_dim in {64, 128}; rotary_dim a multiple of 16 up to head_dim;
+ * block_size a power of two.  num_tokens may be 0 (nothing launched).
+ * ------------------------------------------------------------------------- */
+pkv_status kv_rotary_and_cache(void *query_out_dev, const void *query_dev, const void *key_dev,
+                               const void *value_dev, void *key_cache_dev, void *value_cache_dev,
+                               const float *cos_sin_dev, const int32_t *positions_dev,
+                               const int64_t *slot_mapping_dev, int num_tokens, int num_heads,
+                               int num_kv_heads, int head_dim, int rotary_dim, int num_positions,
+                               pkv_rotary_layout layout, int64_t query_stride, int64_t key_stride,
+                               int64_t value_stride, int block_size, int num_blocks,
+                               pkv_dtype dtype, struct CUstream_st *stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit cache.  key_cache and value_cache hold e4m3 codes in the layout
+ * above; scales_dev holds, for every block and kv head, the key scale and the
+ * value scale: value = code * scale.
+ *   scales  fp32 [num_blocks][Hs][2], Hs = num_kv_heads rounded up to even:
+ *           [b][g][0] for the keys, [b][g][1] for the values of kv head g
+ * A block's codes (num_kv_heads * block_size * head_dim bytes) and its scales
+ * (8 * Hs bytes) are multiples of 16 bytes: copy_blocks and swap_blocks move
+ * them (keys, values and scales, one call each).
+ *
+ * kv_rotary_and_cache_fp8 -- as kv_rotary_and_cache, into the 8-bit cache.
+ * For each block, kv head and for keys and values on their own:
+ *   need = the smallest 2^e, e >= -60, with |x| <= 448 * 2^e for every
+ *          element x of the tokens that this call writes there (after the
+ *          rotation, in fp32; infinities count as the largest finite number,
+ *          NaN does not count)
+ *   A call that writes offset 0 starts the block anew: its scale becomes
+ *   need, whatever it held.  Otherwise the scale becomes max(old, need), and
+ *   when that is larger than the old one the block's other rows are rounded
+ *   again under it (exact but for codes that become subnormal).
+ *   code = x / scale rounded to nearest even; magnitudes above 448 (infinite
+ *   ones) become 448, NaN stays NaN.
+ * The tokens of one block must stand next to one another in slot_mapping
+ * (sequence by sequence, as the allocator returns them); a block that appears
+ * in two places races.  rotary_dim = 0 with num_heads = 0 and NULL table and
+ * positions appends without rotation.  block_size a power of two in [4, 128].
+ * A token whose position is outside the table latches PKV_EINDEX; what its
+ * block then holds is unspecified.
+ * ------------------------------------------------------------------------- */
+pkv_status kv_rotary_and_cache_fp8(void *query_out_dev, const void *query_dev, const void *key_dev,
+                                   const void *value_dev, void *key_cache_dev,
+                                   void *value_cache_dev, float *scales_dev,
+                                   const float *cos_sin_dev, const int32_t *positions_dev,
+                                   const int64_t *slot_mapping_dev, int num_tokens, int num_heads,
+                                   int num_kv_heads, int head_dim, int rotary_dim,
+                                   int num_positions, pkv_rotary_layout layout,
+                                   int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                                   int block_size, int num_blocks, pkv_dtype dtype,
+                                   struct CUstream_st *stream);
+
+/* ---------------------------------------------------------------------------
+ * paged_attention_decode_fp8 -- paged_attention_decode over the 8-bit cache:
+ * the same attention with K_t = key code * scales[b][g][0] and
+ * V_t = value code * scales[b][g][1].  dtype is that of query and out.  The
+ * codes enter the products exactly; fp16 queries too, bf16 ones too unless
+ * they lie 2^31 below their row's largest; probabilities carry 22 bits.
+ * Arguments as for paged_attention_decode, but:
+ *   partition_size  0 (the library chooses) or a multiple of 64.
+ *   workspace_dev   at least paged_attention_decode_fp8_workspace_size(...)
+ *                   bytes, prepared once by paged_attention_fp8_workspace_init
+ *                   (a workspace of the 16-bit calls latches PKV_EINVAL).
+ *                   Calls of any sizes, decode and prompt phase, captured in
+ *                   graphs or not, may follow one another on it; calls that
+ *                   may overlap on the GPU need one each.  After a call that
+ *                   reported PKV_ETIMEOUT, prepare it again.
+ * num_seqs <= 65535 (2048 to a launch); any number of query heads per kv head;
+ * scale finite.
+ * ------------------------------------------------------------------------- */
+pkv_status paged_attention_decode_fp8(void *out_dev, const void *query_dev,
+                                      const void *key_cache_dev, const void *value_cache_dev,
+                                      const float *scales_dev, const int32_t *block_tables_dev,
+                                      const int32_t *context_lens_dev, int num_seqs,
+                                      int max_blocks_per_seq, int max_context_len, int block_size,
+                                      int num_blocks, int num_heads, int num_kv_heads,
+                                      int head_dim, float scale, int partition_size,
+                                      void *workspace_dev, size_t workspace_bytes, pkv_dtype dtype,
+                                      struct CUstream_st *stream);
+
+size_t paged_attention_decode_fp8_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                                 int head_dim, int max_context_len,
+                                                 int partition_size);
+
+/* Prepare a workspace of the 8-bit cache's attention calls (asynchronous on
+ * `stream`; one small kernel).  At least the bytes either size call returns. */
+pkv_status paged_attention_fp8_workspace_init(void *workspace_dev, size_t workspace_bytes,
+                                              struct CUstream_st *stream);
+
+/* ---------------------------------------------------------------------------
+ * paged_attention_prefill_fp8 -- paged_attention_prefill over the 8-bit cache.
+ * The contexts' blocks are first widened to `dtype` in the workspace (exact
+ * for bf16, and for fp16 where code * scale is within its range), then the
+ * prompt-phase kernel runs on them: two launches.  Arguments as for
+ * paged_attention_prefill, but:
+ *   max_context_len  host-side upper bound on every context_lens[s] (0 =
+ *                    max_blocks_per_seq * block_size); a context beyond its
+ *                    ceil(max_context_len / block_size) blocks latches
+ *                    PKV_EINDEX.  It sizes the workspace.
+ *   workspace_dev    as for paged_attention_decode_fp8, at least
+ *                    paged_attention_prefill_fp8_workspace_size(...) bytes.
+ * ------------------------------------------------------------------------- */
+pkv_status paged_attention_prefill_fp8(void *out_dev, const void *query_dev,
+                                       const void *key_cache_dev, const void *value_cache_dev,
+                                       const float *scales_dev, const int32_t *block_tables_dev,
+                                       const int32_t *context_lens_dev,
+                                       const int32_t *query_start_dev, int num_seqs, int num_tokens,
+                                       int max_query_len, int max_context_len,
+                                       int max_blocks_per_seq, int block_size, int num_blocks,
+                                       int num_heads, int num_kv_heads, int head_dim, float scale,
+                                       void *workspace_dev, size_t workspace_bytes, pkv_dtype dtype,
+                                       struct CUstream_st *stream);
+
+size_t paged_attention_prefill_fp8_workspace_size(int num_seqs, int num_kv_heads, int head_dim,
+                                                  int block_size, int max_context_len);
 
 /* ---------------------------------------------------------------------------
  * paged_attention_decode -- block-table gather + decode attention ("vLLM &

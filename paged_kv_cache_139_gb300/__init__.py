@@ -11,6 +11,9 @@ missing, the first call raises.
     paged_attention_decode   block-table gather + decode attention
     copy_blocks              copy-on-write block copy
     BlockAllocator           the native ref-counted block allocator
+    rotary_table             cosines and sines of the rotary positions
+    kv_rotary_and_cache      the K/V write with the rotary rotation on the way
+    *_fp8                    the K/V write and the attention of an 8-bit cache
 """
 from __future__ import annotations
 
@@ -27,6 +30,9 @@ __all__ = ["PkvError", "PkvOOM", "kv_reshape_and_cache", "paged_attention_decode
            "paged_attention_decode_noalloc", "paged_attention_decode_write", "paged_attention_prefill", "paged_attention_workspace_size",
            "make_workspace",
            "paged_attention_partition_size", "copy_blocks",
+           "rotary_table", "kv_rotary_and_cache", "kv_rotary_and_cache_fp8", "kv_scales",
+           "paged_attention_decode_fp8", "paged_attention_decode_fp8_workspace_size",
+           "paged_attention_prefill_fp8", "paged_attention_prefill_fp8_workspace_size", "make_fp8_workspace",
            "validate_copy_pairs", "swap_blocks", "check", "launch_count", "version", "BlockAllocator", "library_path"]
 
 PKV_F16, PKV_BF16 = 0, 1
@@ -288,6 +294,284 @@ def paged_attention_decode_noalloc(out: torch.Tensor, query: torch.Tensor, key_c
         S, block_tables.shape[1], max_context_len, B, NB, H, Hkv, d, float(scale), partition_size,
         _dtype_code(query), _stream(stream, query.device))
     _ck(rc, "paged_attention_decode_noalloc")
+    return out
+
+
+# -- rotary positions ---------------------------------------------------------------
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
+
+
+class _on:
+    """The library launches on the current device: makes that the tensors'
+    own (a no-op when it is)."""
+
+    __slots__ = ("index", "was")
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.was = torch.cuda.current_device()
+        if self.index is not None and self.index != self.was:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.index is not None and self.index != self.was:
+            torch.cuda.set_device(self.was)
+
+
+def _one_device(what: str, device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{what}: tensors on {t.device} and {device}")
+
+
+def _rows(t: torch.Tensor, name: str, T: int, h: int, d: int):
+    """Pointer and token stride of a [T][h][d] tensor whose tokens may lie
+    further apart than h * d elements (a slice of a wider projection)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.shape != (T, h, d):
+        raise ValueError(f"{name} must be [{T}][{h}][{d}], got shape {tuple(t.shape)}")
+    st, sh, sd = t.stride()
+    if T <= 1:
+        st = h * d
+    if T and ((h > 1 and sh != d) or sd != 1 or st < h * d or st % 8):
+        raise ValueError(f"{name}: a token's heads must be contiguous, tokens a multiple of 8 elements apart")
+    return t.data_ptr(), st
+
+
+def rotary_table(num_positions: int, rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                 factor: float = 1.0, original_positions: int = 0, low_turns: float = 1.0, high_turns: float = 32.0,
+                 magnitude: float = 1.0, device="cuda", out: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """fp32 [num_positions][rotary_dim / 2][2]: magnitude * (cos, sin) of
+    position times theta_i, theta_i = base^(-2i / rotary_dim), scaled for long
+    contexts: "none", "linear" (theta / factor), or "by_parts" (pairs that turn
+    at least high_turns times over original_positions keep their angle, those
+    below low_turns are divided by factor, a ramp between).  Written into out
+    when given."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"rotary_table: scaling {scaling!r} not one of {sorted(_SCALINGS)}")
+    if out is None:
+        out = torch.empty(num_positions, rotary_dim // 2, 2, dtype=torch.float32, device=device)
+    elif out.shape != (num_positions, rotary_dim // 2, 2):
+        raise ValueError("rotary_table: out must be [num_positions][rotary_dim / 2][2]")
+    with _on(out.device):
+        rc = load().rotary_table(_dev(out, "out", torch.float32), num_positions, rotary_dim, float(base),
+                                 _SCALINGS[scaling], float(factor), original_positions, float(low_turns),
+                                 float(high_turns), float(magnitude), _stream(stream, out.device))
+    _ck(rc, "rotary_table")
+    return out
+
+
+def kv_scales(num_blocks: int, num_kv_heads: int, device="cuda", pin_memory: bool = False) -> torch.Tensor:
+    """The block scales of an 8-bit cache, zero: fp32
+    [num_blocks][num_kv_heads rounded up to even][2] (key, value)."""
+    return torch.zeros(num_blocks, num_kv_heads + num_kv_heads % 2, 2, dtype=torch.float32,
+                       device="cpu" if pin_memory else device, pin_memory=pin_memory)
+
+
+def _append(what, fp8, query, key, value, cos_sin, positions, key_cache, value_cache, scales, slot_mapping, layout,
+            query_out, stream):
+    if layout not in _LAYOUTS:
+        raise ValueError(f"{what}: layout {layout!r} not one of {sorted(_LAYOUTS)}")
+    NB, Hkv, B, d = key_cache.shape
+    T = key.shape[0]
+    if value_cache.shape != key_cache.shape or slot_mapping.shape != (T,):
+        raise ValueError(f"{what}: caches of different shapes, or slot_mapping not [num_tokens]")
+    if value.dtype != key.dtype or (query is not None and query.dtype != key.dtype):
+        raise TypeError(f"{what}: query, key and value must have one dtype")
+    cache_dtype = torch.float8_e4m3fn if fp8 else key.dtype
+    if key_cache.dtype != cache_dtype or value_cache.dtype != cache_dtype:
+        raise TypeError(f"{what}: caches must be {cache_dtype}")
+    dev = key_cache.device
+    _one_device(what, dev, query, key, value, cos_sin, positions, value_cache, scales, slot_mapping, query_out)
+    rot = npos = H = 0
+    cs_ptr = pos_ptr = q_ptr = qo_ptr = sc_ptr = None
+    q_stride = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 3 or cos_sin.shape[2] != 2 or positions is None or positions.shape != (T,):
+            raise ValueError(f"{what}: cos_sin must be [positions][rotary_dim / 2][2], positions [num_tokens]")
+        npos, rot = cos_sin.shape[0], 2 * cos_sin.shape[1]
+        cs_ptr, pos_ptr = _dev(cos_sin, "cos_sin", torch.float32), _dev(positions, "positions", torch.int32)
+    if query is not None:
+        if cos_sin is None:
+            raise ValueError(f"{what}: a query needs a table to rotate it by")
+        H = query.shape[1]
+        q_ptr, q_stride = _rows(query, "query", T, H, d)
+        if query_out is None:
+            query_out = torch.empty(T, H, d, dtype=query.dtype, device=dev)
+        elif query_out.shape != query.shape or query_out.dtype != query.dtype:
+            raise ValueError(f"{what}: query_out must be shaped and typed like query")
+        qo_ptr = _dev(query_out, "query_out")
+    k_ptr, k_stride = _rows(key, "key", T, Hkv, d)
+    v_ptr, v_stride = _rows(value, "value", T, Hkv, d)
+    if fp8:
+        if scales.shape != (NB, Hkv + Hkv % 2, 2):
+            raise ValueError(f"{what}: scales must be [num_blocks][num_kv_heads rounded up to even][2]")
+        sc_ptr = _dev(scales, "scales", torch.float32)
+    caches = (_dev(key_cache, "key_cache"), _dev(value_cache, "value_cache"))
+    slots = _dev(slot_mapping, "slot_mapping", torch.int64)
+    sizes = (T, H, Hkv, d, rot, npos, _LAYOUTS[layout], q_stride, k_stride, v_stride, B, NB, _dtype_code(key))
+    with _on(dev):
+        st = _stream(stream, dev)
+        if fp8:
+            rc = load().kv_rotary_and_cache_fp8(qo_ptr, q_ptr, k_ptr, v_ptr, *caches, sc_ptr, cs_ptr, pos_ptr, slots,
+                                                *sizes, st)
+        else:
+            rc = load().kv_rotary_and_cache(qo_ptr, q_ptr, k_ptr, v_ptr, *caches, cs_ptr, pos_ptr, slots, *sizes, st)
+    _ck(rc, what)
+    return query_out
+
+
+def kv_rotary_and_cache(query: Optional[torch.Tensor], key: torch.Tensor, value: torch.Tensor, cos_sin: torch.Tensor,
+                        positions: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                        slot_mapping: torch.Tensor, layout: str = "half", query_out: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Rotate query [T][H][d] (None: keys only) and key [T][Hkv][d] by their
+    tokens' positions (int32 [T]) and write the keys and values at their slots,
+    in one launch.  cos_sin comes from rotary_table; layout "half" pairs (i,
+    i + rotary_dim / 2), "interleaved" (2i, 2i + 1).  query, key and value may
+    be slices of one projection's rows.  Returns the rotated queries
+    (query_out, which may be a contiguous query itself)."""
+    if cos_sin is None:
+        raise ValueError("kv_rotary_and_cache: needs a table (kv_reshape_and_cache writes without rotation)")
+    return _append("kv_rotary_and_cache", False, query, key, value, cos_sin, positions, key_cache, value_cache, None,
+                   slot_mapping, layout, query_out, stream)
+
+
+def kv_rotary_and_cache_fp8(query: Optional[torch.Tensor], key: torch.Tensor, value: torch.Tensor,
+                            cos_sin: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                            key_cache: torch.Tensor, value_cache: torch.Tensor, scales: torch.Tensor,
+                            slot_mapping: torch.Tensor, layout: str = "half",
+                            query_out: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """kv_rotary_and_cache into an 8-bit cache: float8_e4m3fn caches
+    [NB][Hkv][B][d] and their block scales (kv_scales), which the call keeps.
+    cos_sin, positions and query None: append without rotation.  The tokens of
+    one block must stand next to one another in slot_mapping."""
+    return _append("kv_rotary_and_cache_fp8", True, query, key, value, cos_sin, positions, key_cache, value_cache,
+                   scales, slot_mapping, layout, query_out, stream)
+
+
+# -- attention over an 8-bit cache ---------------------------------------------------
+
+def paged_attention_decode_fp8_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                              max_context_len: int, partition_size: int = 0) -> int:
+    return int(load().paged_attention_decode_fp8_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                                max_context_len, partition_size))
+
+
+def paged_attention_prefill_fp8_workspace_size(num_seqs: int, num_kv_heads: int, head_dim: int, block_size: int,
+                                               max_context_len: int) -> int:
+    return int(load().paged_attention_prefill_fp8_workspace_size(num_seqs, num_kv_heads, head_dim, block_size,
+                                                                 max_context_len))
+
+
+_FP8_WS_MIN = 256 + 65536 * 4              # ticket headers and merge counters
+
+
+def make_fp8_workspace(device, nbytes: int, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """A device buffer of at least nbytes, prepared for
+    paged_attention_decode_fp8 and paged_attention_prefill_fp8.  Returns once
+    the preparation has finished, so any stream may use the buffer."""
+    dev = torch.device(device)
+    buf = torch.empty(max(nbytes, _FP8_WS_MIN), dtype=torch.uint8, device=dev)
+    with _on(buf.device):
+        _ck(load().paged_attention_fp8_workspace_init(buf.data_ptr(), buf.numel(), _stream(stream, buf.device)),
+            "paged_attention_fp8_workspace_init")
+        (stream or torch.cuda.current_stream(buf.device)).synchronize()
+    return buf
+
+
+_ws8_cache: dict = {}
+
+
+def _workspace8(device, nbytes: int) -> torch.Tensor:
+    """The binding's own 8-bit workspace per device, as _workspace."""
+    buf = _ws8_cache.get(device)
+    if buf is None or buf.numel() < nbytes:
+        if buf is not None:
+            _ws_retired.append(buf)
+        buf = make_fp8_workspace(device, nbytes)
+        _ws8_cache[device] = buf
+    return buf
+
+
+def _check8(what, out, query, key_cache, value_cache, scales, block_tables, context_lens, S):
+    NB, Hkv, B, d = key_cache.shape
+    if query.shape[2] != d or out.shape != query.shape or value_cache.shape != key_cache.shape:
+        raise ValueError(f"{what}: shape mismatch")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError(f"{what}: block_tables must be [S][max_blocks], context_lens [S]")
+    if scales.shape != (NB, Hkv + Hkv % 2, 2):
+        raise ValueError(f"{what}: scales must be [num_blocks][num_kv_heads rounded up to even][2]")
+    if query.dtype != out.dtype or key_cache.dtype != torch.float8_e4m3fn or value_cache.dtype != key_cache.dtype:
+        raise TypeError(f"{what}: out must be typed like query, caches float8_e4m3fn")
+    _one_device(what, query.device, out, key_cache, value_cache, scales, block_tables, context_lens)
+    return (_dev(out, "out"), _dev(query, "query"), _dev(key_cache, "key_cache"), _dev(value_cache, "value_cache"),
+            _dev(scales, "scales", torch.float32), _dev(block_tables, "block_tables", torch.int32),
+            _dev(context_lens, "context_lens", torch.int32))
+
+
+def paged_attention_decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                               value_cache: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
+                               context_lens: torch.Tensor, scale: Optional[float] = None, max_context_len: int = 0,
+                               partition_size: int = 0, workspace: Optional[torch.Tensor] = None,
+                               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_attention_decode over an 8-bit cache (float8_e4m3fn caches and
+    their block scales).  workspace from make_fp8_workspace, one call at a
+    time; None takes the binding's own per-device buffer, which every 8-bit
+    call without a workspace shares.  Returns out."""
+    S, H, d = query.shape
+    ptrs = _check8("paged_attention_decode_fp8", out, query, key_cache, value_cache, scales, block_tables,
+                   context_lens, S)
+    NB, Hkv, B, _ = key_cache.shape
+    mb = block_tables.shape[1]
+    dev = query.device
+    with _on(dev):
+        if workspace is None:
+            workspace = _workspace8(dev, paged_attention_decode_fp8_workspace_size(
+                S, H, Hkv, d, max_context_len if max_context_len > 0 else mb * B, partition_size))
+        rc = load().paged_attention_decode_fp8(
+            *ptrs, S, mb, max_context_len, B, NB, H, Hkv, d, float(1.0 / math.sqrt(d) if scale is None else scale),
+            partition_size, _dev(workspace, "workspace", torch.uint8), workspace.numel(), _dtype_code(query),
+            _stream(stream, dev))
+    _ck(rc, "paged_attention_decode_fp8")
+    return out
+
+
+def paged_attention_prefill_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                value_cache: torch.Tensor, scales: torch.Tensor, block_tables: torch.Tensor,
+                                context_lens: torch.Tensor, query_start: torch.Tensor,
+                                scale: Optional[float] = None, max_query_len: int = 0, max_context_len: int = 0,
+                                workspace: Optional[torch.Tensor] = None,
+                                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_attention_prefill over an 8-bit cache.  max_context_len bounds the
+    contexts and sizes the workspace (0: the whole table).  workspace as for
+    paged_attention_decode_fp8.  Returns out."""
+    T, H, d = query.shape
+    S = context_lens.shape[0]
+    ptrs = _check8("paged_attention_prefill_fp8", out, query, key_cache, value_cache, scales, block_tables,
+                   context_lens, S)
+    if query_start.shape != (S + 1,):
+        raise ValueError("paged_attention_prefill_fp8: query_start must be [S+1]")
+    _one_device("paged_attention_prefill_fp8", query.device, query_start)
+    NB, Hkv, B, _ = key_cache.shape
+    mb = block_tables.shape[1]
+    dev = query.device
+    with _on(dev):
+        if workspace is None:
+            workspace = _workspace8(dev, paged_attention_prefill_fp8_workspace_size(
+                S, Hkv, d, B, max_context_len if max_context_len > 0 else mb * B))
+        rc = load().paged_attention_prefill_fp8(
+            *ptrs, _dev(query_start, "query_start", torch.int32), S, T, max_query_len, max_context_len, mb, B, NB, H,
+            Hkv, d, float(1.0 / math.sqrt(d) if scale is None else scale), _dev(workspace, "workspace", torch.uint8),
+            workspace.numel(), _dtype_code(query), _stream(stream, dev))
+    _ck(rc, "paged_attention_prefill_fp8")
     return out
 
 

@@ -11,6 +11,7 @@ _i = ctypes.c_int
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 _f = ctypes.c_float
+_d = ctypes.c_double
 _pi32 = ctypes.POINTER(ctypes.c_int32)
 _pi64 = ctypes.POINTER(ctypes.c_int64)
 _pint = ctypes.POINTER(ctypes.c_int)
@@ -29,6 +30,18 @@ SIGNATURES = {
     "paged_attention_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "paged_attention_workspace_init": (_i, [_p, _sz, _p]),
     "paged_attention_partition_size": (_i, [_i, _i, _i, _i, _i, _i]),
+    "rotary_table": (_i, [_p, _i, _i, _d, _i, _d, _i, _d, _d, _d, _p]),
+    "kv_rotary_and_cache": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i64, _i64, _i64,
+                                 _i, _i, _i, _p]),
+    "kv_rotary_and_cache_fp8": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i64, _i64,
+                                     _i64, _i, _i, _i, _p]),
+    "paged_attention_decode_fp8": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _p, _sz,
+                                        _i, _p]),
+    "paged_attention_decode_fp8_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "paged_attention_fp8_workspace_init": (_i, [_p, _sz, _p]),
+    "paged_attention_prefill_fp8": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
+                                         _p, _sz, _i, _p]),
+    "paged_attention_prefill_fp8_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "copy_blocks": (_i, [_p, _p, _i, _i64, _i, _p]),
     "swap_blocks": (_i, [_p, _p, _p, _i, _i64, _i, _i, _p]),
     "pkv_validate_copy_pairs": (_i, [_p, _i, _i]),

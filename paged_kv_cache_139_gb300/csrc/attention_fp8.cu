@@ -1,0 +1,931 @@
+// Paged decode attention over the 8-bit cache, and the prompt phase over it.
+//
+// What it computes: for sequence s, query head h and its kv head g,
+//     out = sum_t softmax_t(scale * q . k_t) v_t,
+//     k_t = e4m3 code * scales[b][g][0],  v_t = e4m3 code * scales[b][g][1],
+// token t in block b = block_tables[s][t / B] at offset t % B.
+//
+// Decode is bound by the bytes of the cache, half those of a 16-bit one, so
+// there are twice the tokens per byte to compute on: at 7 TB/s an SM has to
+// take in about 24 codes a clock.  So the products run on the tensor cores
+// for every group of query heads, one included, and what each code costs is
+// kept down to its share of a conversion:
+//   * The query heads of a kv head (up to 8) are rows 0-7 of the 16-row MMA
+//     tile.  A code converts exactly to fp16, two at a time, straight into the
+//     B operand: the products' inner index and columns may be numbered at
+//     will, so a lane takes sixteen consecutive codes of a row with one load
+//     and needs no transposition for K; for V two rows' bytes are interleaved
+//     (one byte permute per two columns).  fp16 queries enter as they are;
+//     bf16 ones scaled by a power of two per row into fp16's range, exactly.
+//   * Rows 8-15 would be idle: they carry what fp16 loses of the
+//     probabilities, so that P V has 22 bits of P at no extra product.
+//   * The key scale multiplies the finished score; the value scale enters P
+//     as an exponent, with a running maximum of its own (score + log2 of the
+//     scale), so that blocks of any scales combine without overflow.
+//   * K and V tiles come by tiled TMA, swizzled; tokens are numbered within
+//     groups of eight so that the wide loads of both are free of bank
+//     conflicts (see perm_token).
+// One producer and one consumer warp per CTA, several CTAs per SM, persistent
+// over (sequence, partition, head tile) items claimed by tickets.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <climits>
+#include <cstring>
+#include <type_traits>
+
+#include "pkv_attention.cuh"
+#include "pkv_fp8.cuh"
+#include "pkv_host.cuh"
+#include "pkv_tmap.h"
+
+namespace pkv {
+namespace {
+
+#ifndef PKV_FP8_SLOTS_D128
+#define PKV_FP8_SLOTS_D128 2
+#endif
+#ifndef PKV_FP8_SLOTS_D64
+#define PKV_FP8_SLOTS_D64 4
+#endif
+#ifndef PKV_FP8_CTAS_PER_SM
+#define PKV_FP8_CTAS_PER_SM 6
+#endif
+
+constexpr int kTokens = 64;                 // tokens per ring stage
+constexpr int kMinBlock = 4;
+constexpr int kStageBlocks = kTokens / kMinBlock;
+constexpr int kTileHeads = 8;               // query heads per item at most
+constexpr int kLaunchSeqs = 2048;           // sequences per launch (their lengths sit in shared memory)
+constexpr int kCounters = 65536;            // merge counters of a workspace
+constexpr float kPExp = 15.f;               // probabilities enter the product times 2^15 (fp16 reaches 2^16)
+
+// The workspace: two ticket headers (decode; the prompt phase at 128), the
+// merge counters, then what a call needs.  The counters' place depends on no
+// size, and every call leaves them at zero: calls of any sizes, captured or
+// not, may follow one another on a workspace.
+constexpr size_t kPrefillHeader = 128;
+constexpr size_t kCounterOff = kWsHeaderBytes;
+constexpr size_t kBodyOff = kCounterOff + kCounters * sizeof(unsigned int);
+
+struct F8Args {
+    AttnArgs a;
+    const float2 *scales;        // [NB][scale_heads]
+    int scale_heads;
+    int tile;                    // query heads per item (the last tile of a kv head may hold fewer)
+};
+
+template <int D> struct F8Layout {
+    static constexpr int R = D >= 128 ? PKV_FP8_SLOTS_D128 : PKV_FP8_SLOTS_D64;
+    static constexpr uint32_t tensor = kTokens * D;                                // bytes of a stage's K or V
+    static constexpr uint32_t ring = 0;
+    static constexpr uint32_t q = ring + R * 2 * tensor;                            // [R][8][D] 16-bit
+    static constexpr uint32_t sc = q + R * kTileHeads * D * 2;                      // [R][kStageBlocks] float2
+    static constexpr uint32_t bars = sc + R * kStageBlocks * 8;
+    static constexpr uint32_t meta = bars + 2 * R * 8;
+    static constexpr uint32_t misc = meta + R * 32;
+    static constexpr uint32_t seqs = misc + 64 * 4;
+    static size_t bytes(int S) { return seqs + (size_t)(2 * S + 1) * sizeof(int); }
+};
+
+enum : int { kFirst = 1, kLast = 2, kStop = 4 };
+
+struct F8Meta {
+    int s, h0, rows, part, nparts;   // the item: query heads h0 .. h0 + rows - 1
+    int nvalid;                      // tokens of the stage
+    int flags, qbuf;
+};
+
+// Column j of a group of eight tokens is token perm_token(j) of it.  The
+// numbers make the quarter-warps of the wide loads hit distinct banks: of K,
+// columns 2i and 2i + 1 (four chunks each); of V, the four even or the four
+// odd columns (two chunks each), under the swizzle of 128- or 64-byte rows.
+template <int D> __device__ __forceinline__ int perm_token(int j) {
+    if (D >= 128) return j ^ ((j & 1) << 2);                              // 0 5 2 7 4 1 6 3
+    const int even = ((j & 2) << 1) | (j >> 2);                           // 0 4 1 5 of columns 0 2 4 6
+    return (j & 1) ? even ^ 3 : even;                                     // 0 3 4 7 1 2 5 6
+}
+
+// Byte offset of 16-byte chunk `chunk` of token row `row` in a stage.
+template <int D> __device__ __forceinline__ int chunk_at(int row, int chunk) {
+    if (D >= 128) return row * 128 + ((chunk ^ (row & 7)) << 4);
+    return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+}
+
+template <int D> struct F8State {
+    float o[D / 8][4];     // columns d of row lane / 4: [0], [1] from P's fp16 part, [2], [3] from its rest
+    float m, l;            // running max (log2 domain) and this lane's share of the sum of exponentials
+    float m2;              // running max of score + log2(value scale): o is relative to it
+};
+
+template <int D> __device__ __forceinline__ void f8_reset(F8State<D> &st) {
+#pragma unroll
+    for (int j = 0; j < D / 8; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) st.o[j][e] = 0.f;
+    st.m = st.m2 = -INFINITY;
+    st.l = 0.f;
+}
+
+__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
+    return __byte_perm(a, b, sel);
+}
+
+// Query row lane / 4 as A fragments.  k-step ks of lane column c covers
+// d = (ks / 4) * 64 + 16 c + 4 (ks % 4) .. + 3.  Returns the factor that undoes
+// the row's power of two.
+template <int D, typename T>
+__device__ __forceinline__ float f8_load_q(uint32_t (&qa)[D / 16][2], const T *q, int rows, int lane) {
+    const int row = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ks++) {
+        uint2 v = make_uint2(0u, 0u);
+        if (row < rows) v = *reinterpret_cast<const uint2 *>(q + row * D + (ks >> 2) * 64 + c * 16 + (ks & 3) * 4);
+        qa[ks][0] = v.x;
+        qa[ks][1] = v.y;
+    }
+    if constexpr (std::is_same<T, __half>::value) {
+        return 1.f;
+    } else {
+        float amax = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qa[ks][e]));
+                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+        // the row's largest value goes to [2^14, 2^15): bf16's 8 bits then stay exact over 31 binades below it
+        int sh = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
+        sh = amax == 0.f || amax == INFINITY ? 0 : (sh > 100 ? 100 : sh);
+        const float up = __uint_as_float((unsigned)(sh + 127) << 23);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qa[ks][e]));
+                qa[ks][e] = Mma<__half>::pack(f.x * up, f.y * up);
+            }
+        return __uint_as_float((unsigned)(127 - sh) << 23);
+    }
+}
+
+// Thirty-two tokens from row `base` of a stage.  sc: the stage's block scales
+// (key scale * softmax scale * log2 e, log2 of the value scale), a block per
+// 2^log2_rows tokens.
+template <int D, bool FULL>
+__device__ __forceinline__ void f8_consume(const unsigned char *Ks, const unsigned char *Vs, const float2 *sc,
+                                           int log2_rows, int base, int nvalid, int lane,
+                                           const uint32_t (&qa)[D / 16][2], float qf, F8State<D> &st) {
+    const int n = lane >> 2, c = lane & 3;
+    const int pn = perm_token<D>(n), pe = perm_token<D>(2 * c), po = perm_token<D>(2 * c + 1);
+    // S = Q K^T: four groups of eight tokens
+    float s[4][4];
+#pragma unroll
+    for (int nt = 0; nt < 4; nt++) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) s[nt][e] = 0.f;
+        const int row = base + nt * 8 + pn;
+        uint32_t w[D / 16];
+#pragma unroll
+        for (int k = 0; k < D / 64; k++) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(Ks + chunk_at<D>(row, c + 4 * k));
+            w[4 * k] = v.x;
+            w[4 * k + 1] = v.y;
+            w[4 * k + 2] = v.z;
+            w[4 * k + 3] = v.w;
+        }
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks++) {
+            const uint32_t a[4] = {qa[ks][0], 0u, qa[ks][1], 0u};
+            Mma<__half>::run(s[nt], a, e4m3x2_lo(w[ks]), e4m3x2_hi(w[ks]));
+        }
+    }
+    // scores of row lane / 4, this lane's tokens 8 nt + pe and 8 nt + po
+    float x[8], x2[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const int tok = base + (j >> 1) * 8 + ((j & 1) ? po : pe);
+        const float2 f = sc[tok >> log2_rows];
+        x[j] = s[j >> 1][j & 1] * qf * f.x;
+        x2[j] = x[j] + f.y;
+        if (!FULL && tok >= nvalid) x[j] = x2[j] = -INFINITY;
+    }
+    float mx = x[0], mx2 = x2[0];
+#pragma unroll
+    for (int j = 1; j < 8; j++) {
+        mx = fmaxf(mx, x[j]);
+        mx2 = fmaxf(mx2, x2[j]);
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+    mx2 = fmaxf(mx2, __shfl_xor_sync(kFull, mx2, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+    mx2 = fmaxf(mx2, __shfl_xor_sync(kFull, mx2, 2));
+    const float mnew = fmaxf(st.m, mx);
+    const float m2new = fmaxf(fmaxf(st.m2, mx2), -1e30f);     // finite: value scales of zero leave -inf
+    const float alpha = exp2f(st.m - mnew), alpha2 = exp2f(st.m2 - m2new);
+    float psum = 0.f;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int nt = 0; nt < 4; nt++) {
+        psum += exp2f(x[2 * nt] - mnew) + exp2f(x[2 * nt + 1] - mnew);
+        const float p0 = exp2f(x2[2 * nt] - (m2new - kPExp)), p1 = exp2f(x2[2 * nt + 1] - (m2new - kPExp));
+        hi[nt] = Mma<__half>::pack(p0, p1);
+        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[nt]));
+        lo[nt] = Mma<__half>::pack(p0 - h.x, p1 - h.y);
+    }
+    st.l = st.l * alpha + psum;
+    st.m = mnew;
+    st.m2 = m2new;
+    if (__any_sync(kFull, alpha2 != 1.f)) {
+#pragma unroll
+        for (int j = 0; j < D / 8; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) st.o[j][e] *= alpha2;
+    }
+    // O += P V: sixteen tokens a step, output column (j, n) is d = (D / 8) n + j
+#pragma unroll
+    for (int kt = 0; kt < 2; kt++) {
+        const uint32_t pa[4] = {hi[2 * kt], lo[2 * kt], hi[2 * kt + 1], lo[2 * kt + 1]};
+        const int t = base + kt * 16;
+        const int rows[4] = {t + pe, t + po, t + 8 + pe, t + 8 + po};
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if constexpr (D >= 128) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(Vs + chunk_at<D>(rows[i], n));
+                v[i][0] = w.x;
+                v[i][1] = w.y;
+                v[i][2] = w.z;
+                v[i][3] = w.w;
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2 *>(Vs + chunk_at<D>(rows[i], n >> 1) + (n & 1) * 8);
+                v[i][0] = w.x;
+                v[i][1] = w.y;
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; w++) {
+            const uint32_t a01 = byte_perm(v[0][w], v[1][w], 0x5140u), a23 = byte_perm(v[2][w], v[3][w], 0x5140u);
+            const uint32_t b01 = byte_perm(v[0][w], v[1][w], 0x7362u), b23 = byte_perm(v[2][w], v[3][w], 0x7362u);
+            Mma<__half>::run(st.o[4 * w], pa, e4m3x2_lo(a01), e4m3x2_lo(a23));
+            Mma<__half>::run(st.o[4 * w + 1], pa, e4m3x2_hi(a01), e4m3x2_hi(a23));
+            Mma<__half>::run(st.o[4 * w + 2], pa, e4m3x2_lo(b01), e4m3x2_lo(b23));
+            Mma<__half>::run(st.o[4 * w + 3], pa, e4m3x2_hi(b01), e4m3x2_hi(b23));
+        }
+    }
+}
+
+// A work item as the producer sees it.  ent holds, on lane j, block-table
+// entry win + j of the sequence (-1 past its blocks), sc that block's scales.
+struct F8Item {
+    int s, part, nparts, g, h0, rows, tok0, ntok, nst, nblk, win, ent;
+    float2 sc;
+};
+
+__device__ __forceinline__ void f8_load_scales(const F8Args &f, int g, int ent, float2 &sc) {
+    sc = make_float2(0.f, -INFINITY);
+    if (ent >= 0 && ent < f.a.num_blocks) {
+        const float2 v = __ldg(f.scales + (size_t)ent * f.scale_heads + g);
+        sc.x = v.x * f.a.scale_log2;
+        sc.y = v.y > 0.f ? log2f(v.y) : -INFINITY;
+    }
+}
+
+__device__ __forceinline__ void f8_decode_item(const F8Args &f, const int *pref, const int *ctxs, int S, int tiles,
+                                               unsigned int t, int lane, F8Item &it) {
+    const AttnArgs &a = f.a;
+    const int pidx = (int)(t / (unsigned int)tiles);
+    const int tile = (int)(t % (unsigned int)tiles);
+    int lo = 0, hi = S;                                            // pref[lo] <= pidx < pref[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pref[mid] <= pidx) lo = mid; else hi = mid;
+    }
+    it.s = lo;
+    it.part = pidx - pref[lo];
+    it.nparts = pref[lo + 1] - pref[lo];
+    it.g = tile / a.head_tiles;
+    const int group = a.num_heads / a.num_kv_heads, first = (tile % a.head_tiles) * f.tile;
+    it.h0 = it.g * group + first;
+    it.rows = group - first < f.tile ? group - first : f.tile;
+    const int ctx = ctxs[lo];
+    it.tok0 = it.part * a.partition;
+    const int ntok = ctx - it.tok0 < a.partition ? ctx - it.tok0 : a.partition;
+    it.ntok = ntok < 0 ? 0 : ntok;
+    it.nst = (it.ntok + kTokens - 1) / kTokens;
+    it.nblk = (ctx + (1 << a.log2_block) - 1) >> a.log2_block;
+    it.win = it.tok0 >> a.log2_block;
+    const int j = it.win + lane;
+    it.ent = j < it.nblk ? __ldg(a.tables + (size_t)lo * a.max_blocks + j) : -1;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
+    paged_attention_fp8_kernel(const F8Args f, const __grid_constant__ CUtensorMap tmk,
+                               const __grid_constant__ CUtensorMap tmv) {
+    using L = F8Layout<D>;
+    constexpr int R = L::R;
+    const AttnArgs &a = f.a;
+    // the 128-byte swizzle repeats every 1024 bytes: the ring starts on such a boundary
+    extern __shared__ __align__(1024) unsigned char smem8[];
+    unsigned char *smem = smem8;
+    unsigned char *ring = smem + L::ring;                            // [R][2][kTokens][D]
+    T *qs = reinterpret_cast<T *>(smem + L::q);                      // [R][8][D]
+    float2 *scs = reinterpret_cast<float2 *>(smem + L::sc);          // [R][kStageBlocks]
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::bars);
+    uint64_t *empty = full + R;
+    F8Meta *meta = reinterpret_cast<F8Meta *>(smem + L::meta);
+    const int S = a.num_seqs;
+    int &cta_flags = *reinterpret_cast<int *>(smem + L::misc);
+    int *scan_tmp = reinterpret_cast<int *>(smem + L::misc) + 32;
+    int *pref = reinterpret_cast<int *>(smem + L::seqs);             // [S + 1] partitions before s
+    int *ctxs = pref + S + 1;                                        // [S]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tiles = a.num_kv_heads * a.head_tiles;
+    WsHeader *hdr = a.hdr;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < R; i++) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        fence_mbar_init();
+    }
+    pdl_trigger();
+    pdl_wait();
+    if (threadIdx.x == 0)
+        cta_flags = (timed_out(a.st) ? 1 : 0) | (hdr->magic != kWsMagic8 ? 2 : 0) | ((smem_u32(smem) & 1023u) ? 4 : 0);
+    for (int i = threadIdx.x; i < S; i += blockDim.x) {
+        int c = a.ctx_lens[i];
+        if (c < 0 || c > a.max_ctx) {
+            if (blockIdx.x == 0) latch(a.st, kFlagBadContext, c);
+            c = c < 0 ? 0 : a.max_ctx;
+        }
+        ctxs[i] = c;
+        pref[i + 1] = c > 0 ? (c + a.partition - 1) / a.partition : 1;
+    }
+    __syncthreads();
+    if (cta_flags) {                                   // uniform over the CTA
+        if ((cta_flags & 2) && blockIdx.x == 0 && threadIdx.x == 0) latch(a.st, kFlagBadWorkspace, hdr->magic);
+        if ((cta_flags & 4) && blockIdx.x == 0 && threadIdx.x == 0) latch(a.st, kFlagTimeout, -2);
+        return;
+    }
+    block_prefix_sum(pref, S, scan_tmp);
+    const unsigned int N = (unsigned int)pref[S] * (unsigned int)tiles;
+    const int B = 1 << a.log2_block;
+    const int log2_rows = a.log2_block < 6 ? a.log2_block : 6;       // tokens per copy: a block or 64 of it
+
+    if (warp == 1) {
+        // ---------------- producer: tickets -> items -> tiled copies ----------------
+        const T *qg = static_cast<const T *>(a.q);
+        const int rows_per_copy = 1 << log2_rows;
+        const int cps = kTokens >> log2_rows;                        // blocks per stage
+        const uint32_t copy_bytes = (uint32_t)rows_per_copy * D;
+        // another head tile of the same kv head reads the same tiles next
+        const uint64_t policy = a.head_tiles > 1 ? policy_evict_last() : policy_evict_first();
+        unsigned int cur_t = blockIdx.x;
+        F8Item cur, nx;
+        if (cur_t < N) {
+            f8_decode_item(f, pref, ctxs, S, tiles, cur_t, lane, cur);
+            f8_load_scales(f, cur.g, cur.ent, cur.sc);
+        }
+        int kk = 0, items = 0;
+        bool dead = false;
+        while (cur_t < N && !dead) {
+            // The next ticket is claimed three stages before the item's last, its table entries
+            // are requested a stage later and their blocks' scales another stage later: each
+            // has arrived when it is needed.
+            unsigned int nxt_raw = 0, nxt_t = 0xffffffffu;
+            int step = 0;                                            // claimed, decoded, scales requested
+            auto next_item = [&]() {
+                if (step == 0) {
+                    if (lane == 0) nxt_raw = gridDim.x + atomicAdd(&hdr->next, 1u);
+                } else if (step == 1) {
+                    nxt_t = __shfl_sync(kFull, nxt_raw, 0);
+                    if (nxt_t < N) f8_decode_item(f, pref, ctxs, S, tiles, nxt_t, lane, nx);
+                } else {
+                    if (nxt_t < N) f8_load_scales(f, nx.g, nx.ent, nx.sc);
+                }
+                step++;
+            };
+            const int npad = cur.nst > 0 ? cur.nst : 1;              // an empty context still has a stage
+            const int32_t *trow = a.tables + (size_t)cur.s * a.max_blocks;
+            const int qb = items % R;
+            int win = cur.win, ent = cur.ent;
+            float2 sc = cur.sc;
+            for (int i = 0; i < npad; i++, kk++) {
+                if (i >= npad - 3) next_item();
+                const int slot = kk % R;
+                const bool withq = i == 0 && cur.nst > 0;
+                int nv = 0, nb = 0, off0 = 0, pj = -1;
+                float2 sj = make_float2(0.f, 0.f);
+                if (i < cur.nst) {                                   // uniform over the warp
+                    const int t_first = cur.tok0 + i * kTokens;
+                    const int lb0 = t_first >> a.log2_block;
+                    off0 = t_first & (B - 1);
+                    nv = cur.ntok - i * kTokens < kTokens ? cur.ntok - i * kTokens : kTokens;
+                    nb = (nv + rows_per_copy - 1) >> log2_rows;
+                    if (lb0 < win || lb0 + cps > win + 32) {
+                        win = lb0;
+                        const int j = win + lane;
+                        ent = j < cur.nblk ? __ldg(trow + j) : -1;
+                        f8_load_scales(f, cur.g, ent, sc);
+                    }
+                    const int jl = lane >> 1;                        // this lane's block of the stage
+                    const int from = (lb0 + jl - win) & 31;
+                    pj = __shfl_sync(kFull, ent, from);
+                    sj.x = __shfl_sync(kFull, sc.x, from);
+                    sj.y = __shfl_sync(kFull, sc.y, from);
+                    const bool bad = jl < nb && (pj < 0 || pj >= a.num_blocks);
+                    const unsigned badm = __ballot_sync(kFull, bad);
+                    if (badm) {                                      // stop the stage at the first bad block
+                        if (lane == __ffs(badm) - 1) latch(a.st, kFlagBadBlock, pj);
+                        nb = (__ffs(badm) - 1) >> 1;
+                        nv = nb << log2_rows;
+                    }
+                }
+                if (kk >= R && !__all_sync(kFull, mbar_wait(&empty[slot], ((kk / R) - 1) & 1, kWaitLimitCycles))) {
+                    if (lane == 0) latch(a.st, kFlagTimeout, kk);
+                    dead = true;
+                    break;
+                }
+                if ((lane & 1) == 0 && (lane >> 1) < nb) scs[slot * kStageBlocks + (lane >> 1)] = sj;
+                const uint32_t q_bytes = (uint32_t)(cur.rows * D * 2);
+                if (lane == 0) {
+                    int4 *mv = reinterpret_cast<int4 *>(&meta[slot]);
+                    mv[0] = make_int4(cur.s, cur.h0, cur.rows, cur.part);
+                    mv[1] = make_int4(cur.nparts, nv, (i == 0 ? kFirst : 0) | (i == npad - 1 ? kLast : 0), qb);
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[slot], 2u * copy_bytes * (uint32_t)nb + (withq ? q_bytes : 0u));
+                __syncwarp();
+                // lane 2j + t moves block j's K (t = 0) or V (t = 1) tile
+                if (lane < 2 * nb) {
+                    const int t = lane & 1;
+                    unsigned char *dst = ring + (size_t)(slot * 2 + t) * L::tensor + (size_t)(lane >> 1) * copy_bytes;
+                    tma_load_4d(dst, t ? (const void *)&tmv : (const void *)&tmk, 0, off0, cur.g, pj, &full[slot],
+                                policy);
+                }
+                if (withq && lane == 0)
+                    bulk_g2s(qs + (size_t)qb * kTileHeads * D, qg + ((size_t)cur.s * a.num_heads + cur.h0) * D, q_bytes,
+                             &full[slot]);
+            }
+            if (dead) break;
+            while (step < 3) next_item();
+            items++;
+            cur_t = nxt_t;
+            cur = nx;
+        }
+        if (lane == 0) {
+            for (int once = 0; once < 1 && !dead; once++, kk++) {    // the stop mark
+                const int slot = kk % R;
+                if (kk >= R && !mbar_wait(&empty[slot], ((kk / R) - 1) & 1, kWaitLimitCycles)) {
+                    latch(a.st, kFlagTimeout, kk);
+                    break;
+                }
+                meta[slot].flags = kStop;
+                mbar_arrive_expect_tx(&full[slot], 0u);
+            }
+            // the last CTA to finish leaves the counters at zero for the next call
+            __threadfence();
+            if (atomicAdd(&hdr->done, 1u) == gridDim.x - 1) {
+                hdr->next = 0;
+                hdr->done = 0;
+                __threadfence();
+            }
+        }
+        return;
+    }
+
+    // ---------------- consumer ----------------
+    uint32_t qa[D / 16][2];
+    float qf = 1.f;
+    F8State<D> st;
+    f8_reset(st);
+    for (int k = 0;; k++) {
+        const int slot = k % R;
+        if (!__all_sync(kFull, mbar_wait(&full[slot], (k / R) & 1, kWaitLimitCycles))) {
+            if (lane == 0) latch(a.st, kFlagTimeout, k);
+            break;
+        }
+        const F8Meta md = meta[slot];
+        if (md.flags & kStop) break;
+        const unsigned char *Ks = ring + (size_t)(slot * 2) * L::tensor;
+        unsigned char *Vs = ring + (size_t)(slot * 2 + 1) * L::tensor;
+        const float2 *sc = scs + slot * kStageBlocks;
+        if ((md.flags & kFirst) && md.nvalid > 0)
+            qf = f8_load_q<D, T>(qa, qs + (size_t)md.qbuf * kTileHeads * D, md.rows, lane);
+        if (md.nvalid == kTokens) {
+            f8_consume<D, true>(Ks, Vs, sc, log2_rows, 0, kTokens, lane, qa, qf, st);
+            f8_consume<D, true>(Ks, Vs, sc, log2_rows, 32, kTokens, lane, qa, qf, st);
+        } else if (md.nvalid > 0) {
+            // rows past the context may hold anything: zero them in V (0 * NaN would poison the sum)
+            const int end = (md.nvalid + 31) & ~31;
+            for (int v = md.nvalid * (D / 16) + lane; v < end * (D / 16); v += 32)
+                reinterpret_cast<uint4 *>(Vs)[v] = make_uint4(0u, 0u, 0u, 0u);
+            __syncwarp();
+            for (int base = 0; base < md.nvalid; base += 32)
+                f8_consume<D, false>(Ks, Vs, sc, log2_rows, base, md.nvalid, lane, qa, qf, st);
+            fence_proxy_async_smem();            // the zeroed rows, before TMA refills the slot
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        if (!(md.flags & kLast)) continue;
+
+        // ---- the item's end: this warp holds its whole state ----
+        float l = st.l;
+        l += __shfl_xor_sync(kFull, l, 1);
+        l += __shfl_xor_sync(kFull, l, 2);
+        const int row = lane >> 2, c = lane & 3;
+        // o is relative to m2 - 15, the sum of exponentials to m
+        const float rel = l > 0.f || l != l ? exp2f(st.m2 - kPExp - st.m) : 0.f;
+        if (row < md.rows) {
+            const size_t sh = (size_t)md.s * a.num_heads + md.h0 + row;
+            constexpr int W = D / 8;             // d = W n + j; this lane's columns n = 2c and 2c + 1
+            float v[2 * W];
+#pragma unroll
+            for (int j = 0; j < W; j++) {
+                v[j] = (st.o[j][0] + st.o[j][2]) * rel;
+                v[W + j] = (st.o[j][1] + st.o[j][3]) * rel;
+            }
+            if (md.nparts <= 1) {
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + sh * D + c * 2 * W);
+#pragma unroll
+                for (int j = 0; j < 2 * W; j += 8)
+                    dst[j / 8] = make_uint4(Mma<T>::pack(v[j] * inv, v[j + 1] * inv),
+                                            Mma<T>::pack(v[j + 2] * inv, v[j + 3] * inv),
+                                            Mma<T>::pack(v[j + 4] * inv, v[j + 5] * inv),
+                                            Mma<T>::pack(v[j + 6] * inv, v[j + 7] * inv));
+            } else {
+                const size_t sp = sh * a.max_parts + md.part;
+                float4 *dst = reinterpret_cast<float4 *>(a.ws_o + sp * D + c * 2 * W);
+#pragma unroll
+                for (int j = 0; j < 2 * W; j += 4) dst[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                if (c == 0) {
+                    a.ws_m[sp] = st.m;
+                    a.ws_l[sp] = l;
+                }
+            }
+        }
+        if (a.fused_merge && md.nparts > 1) {
+            // count this partition in; the one that completes the set merges it
+            __threadfence();
+            __syncwarp();
+            unsigned int done = 0;
+            const int g = md.h0 / (a.num_heads / a.num_kv_heads);
+            const int tile = g * a.head_tiles + (md.h0 - g * (a.num_heads / a.num_kv_heads)) / f.tile;
+            unsigned int *cnt = a.cnt + (size_t)md.s * tiles + tile;
+            if (lane == 0) done = atomicAdd(cnt, 1u);
+            done = __shfl_sync(kFull, done, 0);
+            if (done == (unsigned int)md.nparts - 1) {
+                __threadfence();
+                merge_partitions_warp<D, T>(a, md.s, md.h0, md.rows, md.nparts, lane);
+                if (lane == 0) *cnt = 0u;
+            }
+        }
+        f8_reset(st);
+    }
+}
+
+__global__ void fp8_workspace_init_kernel(uint4 *ws, size_t n16) {
+    pdl_trigger();
+    pdl_wait();
+    const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n16) return;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (i == 0) v.z = kWsMagic8;                              // WsHeader: next, done, magic, pad
+    if (i == kPrefillHeader / 16) v.z = kWsMagic;
+    ws[i] = v;
+}
+
+// A work item's bytes: 64 to 1024 tokens.  Long items cost less to begin and
+// leave fewer partials; short ones fill the GPU and end together.
+int choose_partition8(int partition_size, int num_seqs, int items_per_partition, int max_ctx) {
+    if (partition_size > 0) return partition_size;
+    int P = 1024;
+    while (P > 128 && (long long)num_seqs * items_per_partition * parts_for(max_ctx, P) < 8192) P /= 2;
+    return P;
+}
+
+struct F8Sizes {
+    int tile, head_tiles, P, MP;
+    size_t m_off, l_off, o_off, bytes;
+};
+
+F8Sizes f8_sizes(int S, int H, int Hkv, int D, int max_ctx, int partition_size) {
+    F8Sizes z;
+    const int group = H / Hkv;
+    z.head_tiles = (group + kTileHeads - 1) / kTileHeads;
+    z.tile = (group + z.head_tiles - 1) / z.head_tiles;
+    z.P = choose_partition8(partition_size, S, Hkv * z.head_tiles, max_ctx);
+    z.MP = parts_for(max_ctx, z.P);
+    const size_t n = z.MP > 1 ? (size_t)S * H * z.MP : 0;
+    z.m_off = kBodyOff;
+    z.l_off = z.m_off + align256(n * sizeof(float));
+    z.o_off = z.l_off + align256(n * sizeof(float));
+    z.bytes = z.o_off + align256(n * D * sizeof(float));
+    return z;
+}
+
+// The cache [NB][Hkv][B][D] of bytes as a 4-D tensor (innermost first); a box
+// is a row by min(B, 64) tokens of one (block, kv head), swizzled over rows.
+bool encode_cache_map8(CUtensorMap *map, const void *base, int num_blocks, int Hkv, int B, int D) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)B, (cuuint64_t)Hkv, (cuuint64_t)(num_blocks > 0 ? num_blocks : 1)};
+    const cuuint64_t strides[3] = {(cuuint64_t)D, (cuuint64_t)B * D, (cuuint64_t)Hkv * B * D};
+    const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(B < kTokens ? B : kTokens), 1u, 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, typename T> cudaError_t launch_decode8(const F8Args &f, cudaStream_t stream) {
+    auto kern = paged_attention_fp8_kernel<D, T>;
+    const size_t smem = F8Layout<D>::bytes(f.a.num_seqs);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)F8Layout<D>::bytes(kLaunchSeqs));
+    if (e != cudaSuccess) return e;
+    CUtensorMap tmk, tmv;
+    const AttnArgs &a = f.a;
+    if (!encode_cache_map8(&tmk, a.k_cache, a.num_blocks, a.num_kv_heads, 1 << a.log2_block, D) ||
+        !encode_cache_map8(&tmv, a.v_cache, a.num_blocks, a.num_kv_heads, 1 << a.log2_block, D))
+        return cudaErrorInvalidValue;
+    const long long items = (long long)a.num_seqs * a.max_parts * a.num_kv_heads * a.head_tiles;
+    // resident CTAs: the sequence table's size may allow fewer than the registers do (228 KB per SM, 1 KB per CTA)
+    const long long fit = (long long)(228 * 1024 / (smem + 1024));
+    long long ctas = sm_count() * (fit < PKV_FP8_CTAS_PER_SM ? fit : (long long)PKV_FP8_CTAS_PER_SM);
+    if (ctas > items) ctas = items;
+    return launch(kern, dim3((unsigned)ctas), dim3(64), smem, stream, f, tmk, tmv);
+}
+
+// ---- the prompt phase ------------------------------------------------------------
+
+// Logical block j of sequence s, as 16-bit values, to block s * width + j of a
+// scratch pool of the same layout; new_tables names those blocks.  A code
+// times a power of two is exact in bf16, and in fp16 within its range.  Rows
+// past the context become zeros.  One CTA per block, sixteen codes of K and of
+// V to a thread: bound by the bytes read and twice as many written.
+constexpr int kWidenThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void widen16(const uint4 &w, float s, uint4 (&out)[2]) {
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t lo = e4m3x2_lo(in[i]), hi = e4m3x2_hi(in[i]);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        o[2 * i] = Mma<T>::pack(x.x * s, x.y * s);
+        o[2 * i + 1] = Mma<T>::pack(y.x * s, y.y * s);
+    }
+    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kWidenThreads) widen_blocks_kernel(
+    uint4 *__restrict__ k_out, uint4 *__restrict__ v_out, int32_t *__restrict__ new_tables, const WsHeader *hdr,
+    const uint4 *__restrict__ k_cache, const uint4 *__restrict__ v_cache, const float2 *__restrict__ scales,
+    const int32_t *__restrict__ tables, const int32_t *__restrict__ ctx_lens, int width, int max_blocks, int log2_block,
+    int num_blocks, int num_kv_heads, int row_chunks, DeviceStatus *st) {
+    pdl_trigger();
+    pdl_wait();
+    if (hdr->magic != kWsMagic8) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) latch(st, kFlagBadWorkspace, hdr->magic);
+        return;
+    }
+    const int s = (int)(blockIdx.x / (unsigned)width), j = (int)(blockIdx.x % (unsigned)width);
+    const int B = 1 << log2_block;
+    if (threadIdx.x == 0) new_tables[blockIdx.x] = (int)blockIdx.x;
+    const int rows = ctx_lens[s] - (j << log2_block);                // tokens of the context in this block and after
+    if (rows <= 0 || j >= max_blocks) return;
+    const int32_t b = tables[(size_t)s * max_blocks + j];
+    if (b < 0 || b >= num_blocks) {
+        if (threadIdx.x == 0) latch(st, kFlagBadBlock, b);
+        return;
+    }
+    const int per_head = row_chunks << log2_block;                    // sixteen-code chunks of a (block, head)
+    const int chunks = per_head * num_kv_heads;
+    const float2 *sc = scales + (size_t)b * scale_heads(num_kv_heads);
+    const uint4 *kin = k_cache + (size_t)b * chunks, *vin = v_cache + (size_t)b * chunks;
+    uint4 *ko = k_out + (size_t)blockIdx.x * chunks * 2, *vo = v_out + (size_t)blockIdx.x * chunks * 2;
+    for (int i = threadIdx.x; i < chunks; i += kWidenThreads) {
+        const uint4 kw = kin[i], vw = vin[i];
+        const float2 f = sc[i / per_head];
+        uint4 k2[2], v2[2];
+        widen16<T>(kw, f.x, k2);
+        widen16<T>(vw, f.y, v2);
+        if (rows < B && (i % per_head) / row_chunks >= rows)
+            k2[0] = k2[1] = v2[0] = v2[1] = make_uint4(0u, 0u, 0u, 0u);
+        ko[2 * i] = k2[0];
+        ko[2 * i + 1] = k2[1];
+        vo[2 * i] = v2[0];
+        vo[2 * i + 1] = v2[1];
+    }
+}
+
+struct WidenSizes {
+    int width;                   // blocks per sequence
+    size_t k_off, v_off, bytes;
+};
+
+WidenSizes widen_sizes(int S, int Hkv, int D, int B, int max_ctx) {
+    WidenSizes z;
+    z.width = (int)(((long long)max_ctx + B - 1) / B);
+    const size_t blocks = (size_t)S * z.width;
+    z.k_off = kBodyOff + align256(blocks * sizeof(int32_t));
+    z.v_off = z.k_off + align256(blocks * Hkv * B * D * 2);
+    z.bytes = z.v_off + align256(blocks * Hkv * B * D * 2);
+    return z;
+}
+
+// What both calls ask of the cache.
+pkv_status check_cache8(const char *what, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                        pkv_dtype dtype) {
+    if (dtype != PKV_F16 && dtype != PKV_BF16) return fail(PKV_EINVAL, "%s: bad dtype %d", what, (int)dtype);
+    if (head_dim != 64 && head_dim != 128)
+        return fail(PKV_EINVAL, "%s: head_dim %d not supported (64 or 128)", what, head_dim);
+    if (!is_pow2(block_size) || block_size < kMinBlock || block_size > 128)
+        return fail(PKV_EINVAL, "%s: block_size %d not a power of two in [4, 128]", what, block_size);
+    if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads)
+        return fail(PKV_EINVAL, "%s: %d query heads do not group over %d kv heads", what, num_heads, num_kv_heads);
+    return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+pkv_status paged_attention_fp8_workspace_init(void *workspace, size_t workspace_bytes, struct CUstream_st *stream) {
+    using namespace pkv;
+    if (!workspace || workspace_bytes < kBodyOff || !aligned16(workspace))
+        return fail(PKV_EINVAL, "paged_attention_fp8_workspace_init: need a 16-byte aligned workspace of at least %zu bytes",
+                    kBodyOff);
+    const size_t n16 = kBodyOff / 16;
+    cudaError_t e = launch(fp8_workspace_init_kernel, dim3((unsigned)((n16 + 255) / 256)), dim3(256), 0, stream,
+                           static_cast<uint4 *>(workspace), n16);
+    if (e != cudaSuccess) return fail(PKV_ECUDA, "paged_attention_fp8_workspace_init: launch: %s", cudaGetErrorString(e));
+    return PKV_OK;
+}
+
+size_t paged_attention_decode_fp8_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                 int max_context_len, int partition_size) {
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
+        max_context_len < 0 || partition_size < 0)
+        return 0;
+    return pkv::f8_sizes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len, partition_size).bytes;
+}
+
+pkv_status paged_attention_decode_fp8(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                      const float *scales, const int32_t *block_tables, const int32_t *context_lens,
+                                      int num_seqs, int max_blocks_per_seq, int max_context_len, int block_size,
+                                      int num_blocks, int num_heads, int num_kv_heads, int head_dim, float scale,
+                                      int partition_size, void *workspace, size_t workspace_bytes, pkv_dtype dtype,
+                                      struct CUstream_st *stream) {
+    using namespace pkv;
+    const char *what = "paged_attention_decode_fp8";
+    const pkv_status ok = check_cache8(what, num_heads, num_kv_heads, head_dim, block_size, dtype);
+    if (ok != PKV_OK) return ok;
+    if (num_seqs < 0 || num_seqs > 65535 || max_blocks_per_seq < 0 || num_blocks < 0)
+        return fail(PKV_EINVAL, "%s: bad sizes (seqs %d, table width %d, blocks %d)", what, num_seqs, max_blocks_per_seq,
+                    num_blocks);
+    if (partition_size < 0 || partition_size % kTokens)
+        return fail(PKV_EINVAL, "%s: partition_size %d not a multiple of %d", what, partition_size, kTokens);
+    if (!std::isfinite(scale)) return fail(PKV_EINVAL, "%s: scale must be finite", what);
+    const int64_t table_cap = (int64_t)max_blocks_per_seq * block_size;
+    if (max_context_len < 0 || max_context_len > table_cap)
+        return fail(PKV_EINVAL, "%s: max_context_len %d beyond the table (%lld tokens)", what, max_context_len,
+                    (long long)table_cap);
+    if (num_seqs == 0) return PKV_OK;
+    const int max_ctx = max_context_len > 0 ? max_context_len : (int)(table_cap > INT32_MAX / 2 ? INT32_MAX / 2 : table_cap);
+    if (!out || !query || !key_cache || !value_cache || !scales || !block_tables || !context_lens)
+        return fail(PKV_EINVAL, "%s: NULL pointer", what);
+    if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) || !aligned16(scales))
+        return fail(PKV_EINVAL, "%s: pointers must be 16-byte aligned", what);
+    const F8Sizes z = f8_sizes(num_seqs, num_heads, num_kv_heads, head_dim, max_ctx, partition_size);
+    if (z.MP > 65535 || (long long)num_seqs * z.MP * num_kv_heads * z.head_tiles > INT_MAX / 2)
+        return fail(PKV_EINVAL, "%s: %d partitions per sequence", what, z.MP);
+    if (!workspace || workspace_bytes < z.bytes || !aligned16(workspace))
+        return fail(PKV_EINVAL, "%s: workspace of %zu bytes needed, %zu given", what, z.bytes,
+                    workspace ? workspace_bytes : (size_t)0);
+    DeviceStatus *st = status_ptr();
+    if (!st) return fail(PKV_ECUDA, "%s: no device status word", what);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    F8Args f;
+    std::memset(&f, 0, sizeof f);
+    AttnArgs &a = f.a;
+    a.hdr = reinterpret_cast<WsHeader *>(ws);
+    a.cnt = reinterpret_cast<unsigned int *>(ws + kCounterOff);
+    a.k_cache = key_cache;
+    a.v_cache = value_cache;
+    a.st = st;
+    a.max_blocks = max_blocks_per_seq;
+    a.max_ctx = max_ctx;
+    a.log2_block = ilog2(block_size);
+    a.num_blocks = num_blocks;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_tiles = z.head_tiles;
+    a.partition = z.P;
+    a.max_parts = z.MP;
+    a.scale_log2 = scale * kLog2e;
+    f.scales = reinterpret_cast<const float2 *>(scales);
+    f.scale_heads = scale_heads(num_kv_heads);
+    f.tile = z.tile;
+    const size_t row = (size_t)num_heads * head_dim;
+    for (int s0 = 0; s0 < num_seqs; s0 += kLaunchSeqs) {
+        const int S = num_seqs - s0 < kLaunchSeqs ? num_seqs - s0 : kLaunchSeqs;
+        a.num_seqs = S;
+        a.out = static_cast<unsigned char *>(out) + s0 * row * 2;
+        a.q = static_cast<const unsigned char *>(query) + s0 * row * 2;
+        a.tables = block_tables + (size_t)s0 * max_blocks_per_seq;
+        a.ctx_lens = context_lens + s0;
+        const size_t part = (size_t)s0 * num_heads * z.MP;
+        a.ws_m = reinterpret_cast<float *>(ws + z.m_off) + part;
+        a.ws_l = reinterpret_cast<float *>(ws + z.l_off) + part;
+        a.ws_o = reinterpret_cast<float *>(ws + z.o_off) + part * head_dim;
+        a.fused_merge = z.MP > 1 && z.MP <= kFusedMaxParts &&
+                        (long long)S * num_kv_heads * z.head_tiles <= kCounters;
+        cudaError_t e;
+        if (head_dim == 128)
+            e = dtype == PKV_F16 ? launch_decode8<128, __half>(f, stream) : launch_decode8<128, __nv_bfloat16>(f, stream);
+        else
+            e = dtype == PKV_F16 ? launch_decode8<64, __half>(f, stream) : launch_decode8<64, __nv_bfloat16>(f, stream);
+        if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+        if (z.MP > 1 && !a.fused_merge) {
+            const dim3 rgrid((unsigned)num_heads, (unsigned)S);
+            e = dtype == PKV_F16 ? launch_reduce<__half>(head_dim, a, rgrid, stream)
+                                 : launch_reduce<__nv_bfloat16>(head_dim, a, rgrid, stream);
+            if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: reduce launch: %s", what, cudaGetErrorString(e));
+        }
+    }
+    return PKV_OK;
+}
+
+size_t paged_attention_prefill_fp8_workspace_size(int num_seqs, int num_kv_heads, int head_dim, int block_size,
+                                                  int max_context_len) {
+    if (num_seqs <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || max_context_len < 0) return 0;
+    return pkv::widen_sizes(num_seqs, num_kv_heads, head_dim, block_size, max_context_len).bytes;
+}
+
+pkv_status paged_attention_prefill_fp8(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                       const float *scales, const int32_t *block_tables, const int32_t *context_lens,
+                                       const int32_t *query_start, int num_seqs, int num_tokens, int max_query_len,
+                                       int max_context_len, int max_blocks_per_seq, int block_size, int num_blocks,
+                                       int num_heads, int num_kv_heads, int head_dim, float scale, void *workspace,
+                                       size_t workspace_bytes, pkv_dtype dtype, struct CUstream_st *stream) {
+    using namespace pkv;
+    const char *what = "paged_attention_prefill_fp8";
+    const pkv_status ok = check_cache8(what, num_heads, num_kv_heads, head_dim, block_size, dtype);
+    if (ok != PKV_OK) return ok;
+    if (num_seqs < 0 || num_seqs > 65535 || num_tokens < 0 || max_query_len < 0 || num_blocks < 0)
+        return fail(PKV_EINVAL, "%s: bad sizes (seqs %d, tokens %d, max query length %d, blocks %d)", what, num_seqs,
+                    num_tokens, max_query_len, num_blocks);
+    if (!(scale > 0.f) || scale == INFINITY) return fail(PKV_EINVAL, "%s: scale must be positive and finite", what);
+    const int64_t table_cap = (int64_t)max_blocks_per_seq * block_size;
+    if (max_blocks_per_seq < 0 || table_cap > INT_MAX || max_context_len < 0 || max_context_len > table_cap)
+        return fail(PKV_EINVAL, "%s: max_context_len %d beyond the table (%lld tokens)", what, max_context_len,
+                    (long long)table_cap);
+    if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+    const int max_ctx = max_context_len > 0 ? max_context_len : (int)table_cap;
+    if (max_ctx <= 0 || num_blocks <= 0)
+        return fail(PKV_EINVAL, "%s: num_blocks %d / table width %d not positive", what, num_blocks, max_blocks_per_seq);
+    if (!out || !query || !key_cache || !value_cache || !scales || !block_tables || !context_lens || !query_start)
+        return fail(PKV_EINVAL, "%s: NULL pointer", what);
+    if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) || !aligned16(scales))
+        return fail(PKV_EINVAL, "%s: pointers must be 16-byte aligned", what);
+    const WidenSizes z = widen_sizes(num_seqs, num_kv_heads, head_dim, block_size, max_ctx);
+    if ((long long)num_seqs * z.width > INT_MAX)
+        return fail(PKV_EINVAL, "%s: %lld blocks of context", what, (long long)num_seqs * z.width);
+    if (!workspace || workspace_bytes < z.bytes || !aligned16(workspace))
+        return fail(PKV_EINVAL, "%s: workspace of %zu bytes needed, %zu given", what, z.bytes,
+                    workspace ? workspace_bytes : (size_t)0);
+    DeviceStatus *st = status_ptr();
+    if (!st) return fail(PKV_ECUDA, "%s: no device status word", what);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    int32_t *new_tables = reinterpret_cast<int32_t *>(ws + kBodyOff);
+    const int blocks = num_seqs * z.width;
+    auto widen = dtype == PKV_F16 ? widen_blocks_kernel<__half> : widen_blocks_kernel<__nv_bfloat16>;
+    cudaError_t e = launch(widen, dim3((unsigned)blocks), dim3(kWidenThreads), 0, stream,
+                           reinterpret_cast<uint4 *>(ws + z.k_off), reinterpret_cast<uint4 *>(ws + z.v_off), new_tables,
+                           reinterpret_cast<const WsHeader *>(ws), static_cast<const uint4 *>(key_cache),
+                           static_cast<const uint4 *>(value_cache), reinterpret_cast<const float2 *>(scales), block_tables,
+                           context_lens, z.width, max_blocks_per_seq, ilog2(block_size), num_blocks, num_kv_heads,
+                           head_dim / 16, st);
+    if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+    return paged_attention_prefill(out, query, ws + z.k_off, ws + z.v_off, new_tables, context_lens, query_start, num_seqs,
+                                   num_tokens, max_query_len, z.width, block_size, blocks, num_heads, num_kv_heads,
+                                   head_dim, scale, ws + kPrefillHeader, kWsHeaderBytes, dtype, stream);
+}
+
+}  // extern "C"

@@ -29,6 +29,7 @@ enum : unsigned int {
     kFlagBadContext = 16u,     // context length negative or beyond the table
     kFlagBadWorkspace = 32u,   // attention workspace not initialised
     kFlagSlotNotLast = 64u,    // fused decode write: slot is not position context_len - 1 of its table
+    kFlagBadPosition = 128u,   // rotary position outside the table
 };
 
 __device__ __forceinline__ void latch(DeviceStatus *st, unsigned int flag, long long value) {
@@ -49,6 +50,7 @@ struct WsHeader {
     unsigned int pad;
 };
 constexpr unsigned int kWsMagic = 0x31766b70u;
+constexpr unsigned int kWsMagic8 = 0x38766b70u;    // a workspace of the 8-bit cache's attention
 constexpr size_t kWsHeaderBytes = 256;
 
 // Cycles a wait on an mbarrier may take before the kernel gives up (about

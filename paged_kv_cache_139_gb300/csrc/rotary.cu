@@ -1,0 +1,599 @@
+// Rotary positions on the way into the paged cache.
+//
+// Pair i of a head's first `rotary_dim` elements, (x[i], x[i + r/2]) in the
+// half layout or (x[2i], x[2i + 1]) in the interleaved one, is turned by the
+// angle p * theta_i of its token's position p:
+//     (a, b) -> (a cos - b sin, a sin + b cos),  theta_i = base^(-2i / r),
+// the other elements pass through.  The cosines and sines come from a table
+// [positions][r / 2][2] that rotary_table writes once per program.
+//
+// The append kernels rotate the queries into query_out and the keys into the
+// cache, and copy the values, in one launch: each element is read once and
+// written once, which is what bounds them.
+#include <cmath>
+#include <cstring>
+
+#include "pkv_fp8.cuh"
+#include "pkv_host.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kMaxRotaryDim = 256;
+constexpr int kRopeThreads = 256;
+
+// ---- the table ---------------------------------------------------------------
+
+// theta_i / 2 pi as a 64-bit fraction of a turn: position p's angle is
+// p * turn mod 2^64, exact whatever p, with no 64-bit floating point on the
+// device (the low bits of a far position's angle are all that 32-bit
+// arithmetic would keep).
+struct TurnTable {
+    unsigned long long turn[kMaxRotaryDim / 2];
+};
+
+__device__ __forceinline__ float2 cos_sin_of(unsigned long long turns, float magnitude) {
+    const int t = (int)(turns >> 32);                      // signed fraction of a turn, 2^-32 units
+    const int quarter = (int)(((unsigned)t + 0x20000000u) >> 30);   // nearest quarter turn
+    // the rest, at most an eighth of a turn, as a multiple of pi: 2^-31 units
+    const float x = (float)(int)((unsigned)t - ((unsigned)quarter << 30)) * 0x1p-31f;
+    float s, c;
+    sincospif(x, &s, &c);
+    const float cc = (quarter & 1) ? -s : c, ss = (quarter & 1) ? c : s;
+    const float sign = (quarter & 2) ? -magnitude : magnitude;
+    return make_float2(cc * sign, ss * sign);
+}
+
+// Thread t owns two neighbouring pairs (one 16-byte store) of every
+// (threads / columns)-th position of its CTA's stretch: its turns stay in
+// registers.  Bound by the writes and the two sincospif per store.
+__global__ void __launch_bounds__(kRopeThreads) rotary_table_kernel(float4 *__restrict__ out,
+                                                                    const __grid_constant__ TurnTable tab,
+                                                                    int num_positions, int columns, int rows,
+                                                                    int per_cta, float magnitude) {
+    pdl_trigger();
+    pdl_wait();
+    const int c = threadIdx.x % columns, r = threadIdx.x / columns;
+    if (r >= rows) return;
+    const unsigned long long t0 = tab.turn[2 * c], t1 = tab.turn[2 * c + 1];
+    const int begin = blockIdx.x * per_cta;
+    const int end = begin + per_cta < num_positions ? begin + per_cta : num_positions;
+    for (int p = begin + r; p < end; p += rows) {
+        const float2 a = cos_sin_of(t0 * (unsigned long long)p, magnitude);
+        const float2 b = cos_sin_of(t1 * (unsigned long long)p, magnitude);
+        out[(size_t)p * columns + c] = make_float4(a.x, a.y, b.x, b.y);
+    }
+}
+
+// ---- rotating sixteen elements --------------------------------------------------
+
+struct RopeArgs {
+    const void *q, *k, *v;         // [T][H or Hkv][D], tokens q_stride / k_stride / v_stride elements apart
+    void *q_out;                   // [T][H][D]
+    void *k_cache, *v_cache;       // [NB][Hkv][B][D]
+    float *scales;                 // 8-bit cache: [NB][scale_heads][2]
+    const float *cos_sin;          // [num_positions][rot / 2][2]
+    const int32_t *positions;      // [T]
+    const int64_t *slots;          // [T]
+    DeviceStatus *st;
+    int64_t q_stride, k_stride, v_stride;
+    int64_t num_slots;
+    int num_tokens, num_heads, num_kv_heads;
+    int rot, num_positions, log2_block;
+    int q_ctas;                    // 8-bit append: CTAs that rotate queries (after the others)
+    int tokens_per_cta, head_split;   // 8-bit append: tokens of a CTA, CTAs that share their heads
+};
+
+// A thread's unit of a head: sixteen elements as two 16-byte chunks that
+// begin at elements a and b.  Unit u below rot / 16 holds pairs 8u .. 8u + 7
+// whole, in either layout; the units after it hold what is not rotated.
+struct Unit {
+    int a, b;
+    bool rotated;
+};
+
+template <bool INTERLEAVED> __device__ __forceinline__ Unit unit_at(int u, int rot) {
+    Unit x;
+    x.rotated = u * 16 < rot;
+    const bool half = !INTERLEAVED && x.rotated;
+    x.a = half ? 8 * u : 16 * u;
+    x.b = half ? rot / 2 + 8 * u : 16 * u + 8;
+    return x;
+}
+
+// The eight (cos, sin) of unit u at position p.
+__device__ __forceinline__ void load_cos_sin(float4 (&cs)[4], const RopeArgs &a, int p, int u) {
+    const float4 *t = reinterpret_cast<const float4 *>(a.cos_sin + (size_t)p * a.rot + u * 16);
+#pragma unroll
+    for (int i = 0; i < 4; i++) cs[i] = __ldg(t + i);
+}
+
+// x[0..7] = chunk a, x[8..15] = chunk b, turned in place.  The products and
+// their sum are rounded one by one (no fused multiply-add), so that the
+// result is that of the formula in 32 bits, whoever evaluates it: a value on
+// the border between two 8-bit codes then falls the same way.
+template <bool INTERLEAVED> __device__ __forceinline__ void turn(float (&x)[16], const float4 (&cs)[4]) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float c = (i & 1) ? cs[i >> 1].z : cs[i >> 1].x;
+        const float s = (i & 1) ? cs[i >> 1].w : cs[i >> 1].y;
+        const int ia = INTERLEAVED ? 2 * i : i, ib = INTERLEAVED ? 2 * i + 1 : i + 8;
+        const float u = x[ia], v = x[ib];
+        x[ia] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
+        x[ib] = __fadd_rn(__fmul_rn(u, s), __fmul_rn(v, c));
+    }
+}
+
+template <typename T> __device__ __forceinline__ void widen(float (&x)[16], const uint4 &ra, const uint4 &rb) {
+    float f[8];
+    F16Traits<T>::to_f32(ra, f);
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = f[i];
+    F16Traits<T>::to_f32(rb, f);
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[8 + i] = f[i];
+}
+
+template <typename T> __device__ __forceinline__ uint4 narrow(const float *x) {
+    return make_uint4(Mma<T>::pack(x[0], x[1]), Mma<T>::pack(x[2], x[3]), Mma<T>::pack(x[4], x[5]),
+                      Mma<T>::pack(x[6], x[7]));
+}
+
+// A token's position, or -1 outside the table (latched by the thread that
+// tells, but for padding tokens).
+__device__ __forceinline__ int checked_position(const RopeArgs &a, int t, bool tell) {
+    const int p = a.positions[t];
+    if (p >= 0 && p < a.num_positions) return p;
+    if (tell && a.slots[t] >= 0) latch(a.st, kFlagBadPosition, p);
+    return -1;
+}
+
+// Rotates unit u of one row of a 16-bit tensor into another.
+template <typename T, bool INTERLEAVED>
+__device__ __forceinline__ void rotate_row(const RopeArgs &a, const T *src, T *dst, int u, int pos) {
+    const Unit x = unit_at<INTERLEAVED>(u, a.rot);
+    uint4 ra = *reinterpret_cast<const uint4 *>(src + x.a);
+    uint4 rb = *reinterpret_cast<const uint4 *>(src + x.b);
+    if (x.rotated) {
+        float4 cs[4];
+        load_cos_sin(cs, a, pos, u);
+        float f[16];
+        widen<T>(f, ra, rb);
+        turn<INTERLEAVED>(f, cs);
+        ra = narrow<T>(f);
+        rb = narrow<T>(f + 8);
+    }
+    *reinterpret_cast<uint4 *>(dst + x.a) = ra;
+    *reinterpret_cast<uint4 *>(dst + x.b) = rb;
+}
+
+// ---- append to the 16-bit cache ---------------------------------------------------
+
+// One thread per unit of a row; the rows of a token are its query heads, its
+// key heads and its value heads.
+template <int D, typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads) rotary_append_kernel(const RopeArgs a) {
+    constexpr int UPR = D / 16;
+    pdl_trigger();
+    pdl_wait();
+    const unsigned per_token = (unsigned)(a.num_heads + 2 * a.num_kv_heads) * UPR;
+    const unsigned long long i = (unsigned long long)blockIdx.x * kRopeThreads + threadIdx.x;
+    const unsigned long long t64 = i / per_token;
+    if (t64 >= (unsigned)a.num_tokens) return;
+    const int t = (int)t64;
+    const int r = (int)(i - t64 * per_token);
+    int row = r / UPR;
+    const int u = r % UPR;
+    if (row < a.num_heads) {
+        const int pos = checked_position(a, t, r == 0);
+        if (pos < 0) return;
+        rotate_row<T, INTERLEAVED>(a, static_cast<const T *>(a.q) + t * a.q_stride + row * D,
+                                   static_cast<T *>(a.q_out) + ((size_t)t * a.num_heads + row) * D, u, pos);
+        return;
+    }
+    row -= a.num_heads;
+    const bool isv = row >= a.num_kv_heads;
+    const int h = isv ? row - a.num_kv_heads : row;
+    const int64_t s = a.slots[t];
+    if (s < 0) return;                                     // padding token
+    const int pos = checked_position(a, t, row == 0 && u == 0 && a.num_heads == 0);
+    if (s >= a.num_slots) {
+        if (row == 0 && u == 0) latch(a.st, kFlagBadSlot, s);
+        return;
+    }
+    if (pos < 0) return;
+    const int64_t blk = s >> a.log2_block, off = s & ((1ll << a.log2_block) - 1);
+    const size_t dst = (size_t)(((blk * a.num_kv_heads + h) << a.log2_block) + off) * D;
+    if (isv) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) + t * a.v_stride + h * D) + 2 * u;
+        uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(a.v_cache) + dst) + 2 * u;
+        const uint4 x = src[0], y = src[1];
+        out[0] = x;
+        out[1] = y;
+    } else {
+        rotate_row<T, INTERLEAVED>(a, static_cast<const T *>(a.k) + t * a.k_stride + h * D,
+                                   static_cast<T *>(a.k_cache) + dst, u, pos);
+    }
+}
+
+// ---- append to the 8-bit cache ----------------------------------------------------
+
+// Neighbouring tokens of the call that go to one block, and their offsets there.
+struct Run {
+    int n;                     // tokens
+    unsigned written[4];       // bit o: offset o of the block (block sizes up to 128)
+};
+
+// The run that begins at token t (whose slot is in block blk), by the whole warp.
+__device__ __forceinline__ Run find_run(const RopeArgs &a, int t, int64_t blk, int lane) {
+    Run run;
+    run.n = 0;
+    run.written[0] = run.written[1] = run.written[2] = run.written[3] = 0u;
+    for (int base = t; base < a.num_tokens; base += 32) {
+        const int i = base + lane;
+        const int64_t s = i < a.num_tokens ? a.slots[i] : -1;
+        const bool in = s >= 0 && s < a.num_slots && (s >> a.log2_block) == blk;
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        const int cnt = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+        const int off = (int)(s & ((1ll << a.log2_block) - 1));
+#pragma unroll
+        for (int w = 0; w < 4; w++)
+            run.written[w] |= __reduce_or_sync(0xffffffffu, lane < cnt && (off >> 5) == w ? 1u << (off & 31) : 0u);
+        run.n += cnt;
+        if (cnt < 32) break;
+    }
+    return run;
+}
+
+__device__ __forceinline__ bool was_written(const Run &run, int off) {
+    const unsigned w = off < 64 ? (off < 32 ? run.written[0] : run.written[1])
+                                : (off < 96 ? run.written[2] : run.written[3]);
+    return (w >> (off & 31)) & 1u;
+}
+
+// The rows of run [t, t + run.n) of one kv head, keys or values, into block
+// blk, by one warp: D/16 lanes to a row.  A pass over the rows takes their
+// largest magnitude, the block gets its scale, and a second pass writes the
+// codes; a run of up to 16 rows stays in registers between the two.
+template <int D, typename T, bool INTERLEAVED>
+__device__ __forceinline__ void append8_rows(const RopeArgs &a, int t, const Run &run, int64_t blk, int h, bool isv,
+                                             int lane) {
+    constexpr int UPR = D / 16;            // lanes per row
+    constexpr int RP = 32 / UPR;           // rows side by side
+    constexpr int CH = 16 / RP;            // rows per lane and chunk of 16
+    const int r = lane / UPR, u = lane % UPR;
+    const int rot = isv ? 0 : a.rot;
+    const Unit x = unit_at<INTERLEAVED>(u, rot);
+    const T *src = (isv ? static_cast<const T *>(a.v) : static_cast<const T *>(a.k)) + h * D;
+    const int64_t stride = isv ? a.v_stride : a.k_stride;
+    const int B = 1 << a.log2_block;
+    float y[CH][16];
+
+    auto load = [&](int base) {
+        uint4 ra[CH], rb[CH];
+#pragma unroll
+        for (int i = 0; i < CH; i++) {
+            const int row = base + i * RP + r;
+            ra[i] = rb[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < run.n) {
+                const T *p = src + (t + row) * stride;
+                ra[i] = *reinterpret_cast<const uint4 *>(p + x.a);
+                rb[i] = *reinterpret_cast<const uint4 *>(p + x.b);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CH; i++) {
+            widen<T>(y[i], ra[i], rb[i]);
+            const int row = base + i * RP + r;
+            if (x.rotated && row < run.n) {
+                const int pos = a.positions[t + row];
+                if (pos >= 0 && pos < a.num_positions) {    // others are latched by the caller
+                    float4 cs[4];
+                    load_cos_sin(cs, a, pos, u);
+                    turn<INTERLEAVED>(y[i], cs);
+                }
+            }
+        }
+    };
+
+    // the largest finite magnitude; fmaxf passes NaN over
+    float amax = 0.f;
+    for (int base = 0; base < run.n; base += 16) {
+        load(base);
+#pragma unroll
+        for (int i = 0; i < CH; i++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) amax = fmaxf(amax, fabsf(y[i][e]));
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    amax = fminf(amax, 3.4028235e38f);
+
+    // a write at offset 0 starts the block anew; otherwise its scale can only grow
+    const bool fresh = run.written[0] & 1u;
+    float *sp = a.scales + ((size_t)blk * scale_heads(a.num_kv_heads) + h) * 2 + (isv ? 1 : 0);
+    const float need = pow2_scale(amax);
+    const float had = fresh ? 0.f : *sp;
+    const float scale = fmaxf(had, need);
+    unsigned char *rows = static_cast<unsigned char *>(isv ? a.v_cache : a.k_cache) +
+                          ((size_t)(blk * a.num_kv_heads + h) << a.log2_block) * D;
+    if (!fresh && scale != had) {
+        // the scale grew: the block's other rows are rounded again under it
+        const float ratio = __fdiv_rn(had, scale);
+        for (int o = r; o < B; o += RP) {
+            if (was_written(run, o)) continue;
+            uint4 *p = reinterpret_cast<uint4 *>(rows + (size_t)o * D) + u;
+            const uint4 w = *p;
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            uint32_t out[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t lo = e4m3x2_lo(in[j]), hi = e4m3x2_hi(in[j]);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+                const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                out[j] = to_e4m3x4(f.x * ratio, f.y * ratio, g.x * ratio, g.y * ratio);
+            }
+            *p = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+    }
+    __syncwarp();
+    if (lane == 0) *sp = scale;
+
+    // the reciprocal of a power of two is exact; a caller's own scale may be another number
+    const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0u;
+    const float inv = 1.f / scale;
+    for (int base = 0; base < run.n; base += 16) {
+        if (run.n > 16) load(base);
+#pragma unroll
+        for (int i = 0; i < CH; i++) {
+            const int row = base + i * RP + r;
+            if (row >= run.n) continue;
+            const int off = (int)(a.slots[t + row] & (B - 1));
+            float *f = y[i];
+            if (pow2) {
+#pragma unroll
+                for (int e = 0; e < 16; e++) f[e] *= inv;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; e++) f[e] = __fdiv_rn(f[e], scale);
+            }
+            unsigned char *p = rows + (size_t)off * D;
+            *reinterpret_cast<uint2 *>(p + x.a) =
+                make_uint2(to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
+            *reinterpret_cast<uint2 *>(p + x.b) =
+                make_uint2(to_e4m3x4(f[8], f[9], f[10], f[11]), to_e4m3x4(f[12], f[13], f[14], f[15]));
+        }
+    }
+}
+
+// The first CTAs append: each looks over tokens_per_cta tokens for those that
+// begin a run, and its warps take (run, kv head, keys or values) in turn.
+// The CTAs after them rotate queries, a thread to a unit.
+template <int D, typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads) rotary_append8_kernel(const RopeArgs a) {
+    constexpr int UPR = D / 16;
+    constexpr int W = kRopeThreads / 32;
+    pdl_trigger();
+    pdl_wait();
+    const int kv_ctas = (int)gridDim.x - a.q_ctas;
+    if ((int)blockIdx.x >= kv_ctas) {
+        const unsigned per_token = (unsigned)a.num_heads * UPR;
+        const unsigned long long i = (unsigned long long)(blockIdx.x - kv_ctas) * kRopeThreads + threadIdx.x;
+        const unsigned long long t64 = i / per_token;
+        if (t64 >= (unsigned)a.num_tokens) return;
+        const int t = (int)t64;
+        const int r = (int)(i - t64 * per_token);
+        const int row = r / UPR;
+        const int pos = a.rot ? checked_position(a, t, r == 0) : 0;
+        if (pos < 0) return;
+        rotate_row<T, INTERLEAVED>(a, static_cast<const T *>(a.q) + t * a.q_stride + row * D,
+                                   static_cast<T *>(a.q_out) + ((size_t)t * a.num_heads + row) * D, r % UPR, pos);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x % a.head_split;
+    const int first = (int)(blockIdx.x / a.head_split) * a.tokens_per_cta;
+    const int last = first + a.tokens_per_cta < a.num_tokens ? first + a.tokens_per_cta : a.num_tokens;
+    const bool tells = split == 0 && warp == 0 && lane == 0;
+    for (int t = first; t < last; t++) {
+        const int64_t s = a.slots[t];
+        if (s < 0) continue;                               // padding token
+        if (a.rot && tells) checked_position(a, t, a.num_heads == 0);
+        if (s >= a.num_slots) {
+            if (tells) latch(a.st, kFlagBadSlot, s);
+            continue;
+        }
+        const int64_t blk = s >> a.log2_block;
+        if (t > 0) {
+            const int64_t before = a.slots[t - 1];
+            if (before >= 0 && before < a.num_slots && (before >> a.log2_block) == blk) continue;
+        }
+        const Run run = find_run(a, t, blk, lane);
+        for (int j = split * W + warp; j < 2 * a.num_kv_heads; j += a.head_split * W)
+            append8_rows<D, T, INTERLEAVED>(a, t, run, blk, j >> 1, j & 1, lane);
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------
+
+template <int D, typename T>
+cudaError_t launch_append(const RopeArgs &a, bool interleaved, bool fp8, cudaStream_t stream) {
+    constexpr int UPR = D / 16;
+    RopeArgs b = a;
+    if (!fp8) {
+        const unsigned long long units = (unsigned long long)a.num_tokens * (a.num_heads + 2 * a.num_kv_heads) * UPR;
+        const unsigned grid = (unsigned)((units + kRopeThreads - 1) / kRopeThreads);
+        return launch(interleaved ? rotary_append_kernel<D, T, true> : rotary_append_kernel<D, T, false>, dim3(grid),
+                      dim3(kRopeThreads), 0, stream, b);
+    }
+    const unsigned long long qunits = (unsigned long long)a.num_tokens * a.num_heads * UPR;
+    b.q_ctas = (int)((qunits + kRopeThreads - 1) / kRopeThreads);
+    // long calls: 8 tokens to a CTA, so that most CTAs find a run; short ones: the heads of a token spread out
+    const int sms = sm_count() > 0 ? sm_count() : 1;
+    b.tokens_per_cta = a.num_tokens >= 64 * sms ? 8 : 1;
+    const int groups = (a.num_tokens + b.tokens_per_cta - 1) / b.tokens_per_cta;
+    const int most = (2 * a.num_kv_heads + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    b.head_split = 1;
+    while (b.head_split < most && groups * b.head_split < 4 * sms) b.head_split++;
+    const unsigned grid = (unsigned)(groups * b.head_split + b.q_ctas);
+    return launch(interleaved ? rotary_append8_kernel<D, T, true> : rotary_append8_kernel<D, T, false>, dim3(grid),
+                  dim3(kRopeThreads), 0, stream, b);
+}
+
+pkv_status append_impl(const char *what, bool fp8, void *query_out, const void *query, const void *key,
+                       const void *value, void *key_cache, void *value_cache, float *scales, const float *cos_sin,
+                       const int32_t *positions, const int64_t *slot_mapping, int num_tokens, int num_heads,
+                       int num_kv_heads, int head_dim, int rotary_dim, int num_positions, pkv_rotary_layout layout,
+                       int64_t query_stride, int64_t key_stride, int64_t value_stride, int block_size, int num_blocks,
+                       pkv_dtype dtype, cudaStream_t stream) {
+    if (dtype != PKV_F16 && dtype != PKV_BF16) return fail(PKV_EINVAL, "%s: bad dtype %d", what, (int)dtype);
+    if (layout != PKV_ROTARY_HALF && layout != PKV_ROTARY_INTERLEAVED)
+        return fail(PKV_EINVAL, "%s: bad layout %d", what, (int)layout);
+    if (head_dim != 64 && head_dim != 128)
+        return fail(PKV_EINVAL, "%s: head_dim %d not supported (64 or 128)", what, head_dim);
+    if (rotary_dim < 0 || rotary_dim % 16 || rotary_dim > head_dim || (!fp8 && rotary_dim == 0))
+        return fail(PKV_EINVAL, "%s: rotary_dim %d not a multiple of 16 within the head of %d", what, rotary_dim,
+                    head_dim);
+    if (num_tokens < 0 || num_heads < 0 || num_kv_heads <= 0 || num_blocks < 0 || num_positions < 0 ||
+        num_heads > 65536 || num_kv_heads > 65536)
+        return fail(PKV_EINVAL, "%s: bad sizes (tokens %d, heads %d, kv heads %d, blocks %d, positions %d)", what,
+                    num_tokens, num_heads, num_kv_heads, num_blocks, num_positions);
+    if (!is_pow2(block_size) || block_size > (fp8 ? 128 : 1 << 20) || (fp8 && block_size < 4))
+        return fail(PKV_EINVAL, "%s: block_size %d not a power of two%s", what, block_size, fp8 ? " in [4, 128]" : "");
+    if (rotary_dim == 0 && num_heads > 0)
+        return fail(PKV_EINVAL, "%s: queries given but nothing to rotate them by", what);
+    if (num_tokens == 0) return PKV_OK;
+    if (!key || !value || !key_cache || !value_cache || !slot_mapping || (fp8 && !scales) ||
+        (num_heads > 0 && (!query || !query_out)) || (rotary_dim > 0 && (!cos_sin || !positions)))
+        return fail(PKV_EINVAL, "%s: NULL pointer", what);
+    if (!aligned16(key) || !aligned16(value) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        !aligned16(query) || !aligned16(query_out) || !aligned16(scales) || !aligned16(cos_sin))
+        return fail(PKV_EINVAL, "%s: pointers must be 16-byte aligned", what);
+    if ((num_heads > 0 && (query_stride < (int64_t)num_heads * head_dim || query_stride % 8)) ||
+        key_stride < (int64_t)num_kv_heads * head_dim || key_stride % 8 ||
+        value_stride < (int64_t)num_kv_heads * head_dim || value_stride % 8)
+        return fail(PKV_EINVAL, "%s: token strides must be multiples of 8 elements that hold all heads "
+                                "(query %lld, key %lld, value %lld)",
+                    what, (long long)query_stride, (long long)key_stride, (long long)value_stride);
+    // one CTA or thread per token and unit: the launch's grid is a 31-bit number
+    const unsigned long long units =
+        (unsigned long long)num_tokens * (num_heads + 2ull * num_kv_heads) * (unsigned)(head_dim / 16);
+    if (units / 8 > 0x7fffffffull)
+        return fail(PKV_EINVAL, "%s: %d tokens of %d + 2 x %d heads in one call", what, num_tokens, num_heads,
+                    num_kv_heads);
+    DeviceStatus *st = status_ptr();
+    if (!st) return fail(PKV_ECUDA, "%s: no device status word", what);
+    RopeArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.q = query;
+    a.k = key;
+    a.v = value;
+    a.q_out = query_out;
+    a.k_cache = key_cache;
+    a.v_cache = value_cache;
+    a.scales = scales;
+    a.cos_sin = cos_sin;
+    a.positions = positions;
+    a.slots = slot_mapping;
+    a.st = st;
+    a.q_stride = query_stride;
+    a.k_stride = key_stride;
+    a.v_stride = value_stride;
+    a.num_slots = (int64_t)num_blocks * block_size;
+    a.num_tokens = num_tokens;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.rot = rotary_dim;
+    a.num_positions = num_positions;
+    a.log2_block = ilog2(block_size);
+    const bool il = layout == PKV_ROTARY_INTERLEAVED;
+    cudaError_t e;
+    if (head_dim == 128)
+        e = dtype == PKV_BF16 ? launch_append<128, __nv_bfloat16>(a, il, fp8, stream)
+                              : launch_append<128, __half>(a, il, fp8, stream);
+    else
+        e = dtype == PKV_BF16 ? launch_append<64, __nv_bfloat16>(a, il, fp8, stream)
+                              : launch_append<64, __half>(a, il, fp8, stream);
+    if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+    return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+pkv_status rotary_table(float *cos_sin, int num_positions, int rotary_dim, double base, pkv_rotary_scaling scaling,
+                        double factor, int original_positions, double low_turns, double high_turns, double magnitude,
+                        struct CUstream_st *stream) {
+    using namespace pkv;
+    if (num_positions < 0 || rotary_dim <= 0 || rotary_dim % 16 || rotary_dim > kMaxRotaryDim)
+        return fail(PKV_EINVAL, "rotary_table: bad sizes (%d positions, rotary_dim %d: a multiple of 16 up to %d)",
+                    num_positions, rotary_dim, kMaxRotaryDim);
+    if (!(base > 1.0) || !std::isfinite(base) || !std::isfinite(magnitude))
+        return fail(PKV_EINVAL, "rotary_table: base %g must be above 1, magnitude %g finite", base, magnitude);
+    if (scaling != PKV_ROTARY_UNSCALED && scaling != PKV_ROTARY_LINEAR && scaling != PKV_ROTARY_BY_PARTS)
+        return fail(PKV_EINVAL, "rotary_table: bad scaling %d", (int)scaling);
+    if (scaling != PKV_ROTARY_UNSCALED && (!(factor >= 1.0) || !std::isfinite(factor)))
+        return fail(PKV_EINVAL, "rotary_table: scaling factor %g below 1", factor);
+    if (scaling == PKV_ROTARY_BY_PARTS &&
+        (original_positions <= 0 || !(high_turns > low_turns) || !std::isfinite(high_turns) || !std::isfinite(low_turns)))
+        return fail(PKV_EINVAL, "rotary_table: scaling by parts needs the original positions (%d) and low turns (%g) "
+                                "below high turns (%g)",
+                    original_positions, low_turns, high_turns);
+    if (num_positions == 0) return PKV_OK;
+    if (!cos_sin || !aligned16(cos_sin))
+        return fail(PKV_EINVAL, "rotary_table: the table must be a 16-byte aligned device pointer");
+    TurnTable tab;
+    std::memset(&tab, 0, sizeof tab);
+    constexpr double kTwoPi = 6.283185307179586476925286766559;
+    for (int i = 0; i < rotary_dim / 2; i++) {
+        double theta = std::pow(base, -2.0 * i / rotary_dim);
+        if (scaling == PKV_ROTARY_LINEAR) {
+            theta /= factor;
+        } else if (scaling == PKV_ROTARY_BY_PARTS) {
+            // pairs that turn often over the original positions keep their angle, slow ones are stretched
+            const double turns = original_positions * theta / kTwoPi;
+            double keep = (turns - low_turns) / (high_turns - low_turns);
+            keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+            theta = theta * (keep + (1.0 - keep) / factor);
+        }
+        tab.turn[i] = (unsigned long long)std::nearbyint(theta / kTwoPi * 0x1p64);   // theta <= 1: below 2^62
+    }
+    const int columns = rotary_dim / 4, rows = kRopeThreads / columns;
+    // a few positions per thread, enough CTAs for every SM
+    int per_cta = rows * 4;
+    const long long ctas = ((long long)num_positions + per_cta - 1) / per_cta;
+    cudaError_t e = launch(rotary_table_kernel, dim3((unsigned)ctas), dim3(kRopeThreads), 0, stream,
+                           reinterpret_cast<float4 *>(cos_sin), tab, num_positions, columns, rows, per_cta,
+                           (float)magnitude);
+    if (e != cudaSuccess) return fail(PKV_ECUDA, "rotary_table: launch: %s", cudaGetErrorString(e));
+    return PKV_OK;
+}
+
+pkv_status kv_rotary_and_cache(void *query_out, const void *query, const void *key, const void *value,
+                               void *key_cache, void *value_cache, const float *cos_sin, const int32_t *positions,
+                               const int64_t *slot_mapping, int num_tokens, int num_heads, int num_kv_heads,
+                               int head_dim, int rotary_dim, int num_positions, pkv_rotary_layout layout,
+                               int64_t query_stride, int64_t key_stride, int64_t value_stride, int block_size,
+                               int num_blocks, pkv_dtype dtype, struct CUstream_st *stream) {
+    return pkv::append_impl("kv_rotary_and_cache", false, query_out, query, key, value, key_cache, value_cache, nullptr,
+                            cos_sin, positions, slot_mapping, num_tokens, num_heads, num_kv_heads, head_dim, rotary_dim,
+                            num_positions, layout, query_stride, key_stride, value_stride, block_size, num_blocks, dtype,
+                            stream);
+}
+
+pkv_status kv_rotary_and_cache_fp8(void *query_out, const void *query, const void *key, const void *value,
+                                   void *key_cache, void *value_cache, float *scales, const float *cos_sin,
+                                   const int32_t *positions, const int64_t *slot_mapping, int num_tokens,
+                                   int num_heads, int num_kv_heads, int head_dim, int rotary_dim, int num_positions,
+                                   pkv_rotary_layout layout, int64_t query_stride, int64_t key_stride,
+                                   int64_t value_stride, int block_size, int num_blocks, pkv_dtype dtype,
+                                   struct CUstream_st *stream) {
+    return pkv::append_impl("kv_rotary_and_cache_fp8", true, query_out, query, key, value, key_cache, value_cache,
+                            scales, cos_sin, positions, slot_mapping, num_tokens, num_heads, num_kv_heads, head_dim,
+                            rotary_dim, num_positions, layout, query_stride, key_stride, value_stride, block_size,
+                            num_blocks, dtype, stream);
+}
+
+}  // extern "C"

@@ -114,11 +114,13 @@ pkv_status pkv_check(struct CUstream_st *stream) {
     if (e != cudaSuccess) return pkv::fail(PKV_ECUDA, "pkv_check: clearing status: %s", cudaGetErrorString(e));
     if (h.flags & pkv::kFlagBadWorkspace)
         return pkv::fail(PKV_EINVAL, "device error flags 0x%x: attention workspace not initialised "
-                                     "(paged_attention_workspace_init)", h.flags);
+                                     "(paged_attention_workspace_init, or paged_attention_fp8_workspace_init "
+                                     "for the 8-bit cache)", h.flags);
     const char *what = (h.first_flag & pkv::kFlagBadSlot)      ? "slot outside the pool"
                        : (h.first_flag & pkv::kFlagBadBlock)   ? "block-table entry outside the pool"
                        : (h.first_flag & pkv::kFlagBadPair)    ? "copy pair outside the pool"
                        : (h.first_flag & pkv::kFlagBadContext) ? "context length outside the table"
+                       : (h.first_flag & pkv::kFlagBadPosition) ? "rotary position outside the table"
                        : (h.first_flag & pkv::kFlagSlotNotLast)
                            ? "decode slot is not position context_len - 1 of its sequence's block table"
                        : (h.first_flag & pkv::kFlagTimeout)    ? "device wait timed out"
