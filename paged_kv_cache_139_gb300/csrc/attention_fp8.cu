@@ -10,18 +10,23 @@
 // take in about 24 codes a clock.  So the products run on the tensor cores
 // for every group of query heads, one included, and what each code costs is
 // kept down to its share of a conversion:
-//   * The query heads of a kv head (up to 8) are rows 0-7 of the 16-row MMA
-//     tile.  A code converts exactly to fp16, two at a time, straight into the
-//     B operand: the products' inner index and columns may be numbered at
-//     will, so a lane takes sixteen consecutive codes of a row with one load
-//     and needs no transposition for K; for V two rows' bytes are interleaved
-//     (one byte permute per two columns).  fp16 queries enter as they are;
-//     bf16 ones scaled by a power of two per row into fp16's range, exactly.
-//   * Rows 8-15 would be idle: they carry what fp16 loses of the
-//     probabilities, so that P V has 22 bits of P at no extra product.
-//   * The key scale multiplies the finished score; the value scale enters P
-//     as an exponent, with a running maximum of its own (score + log2 of the
-//     scale), so that blocks of any scales combine without overflow.
+//   * S^T = K Q^T and O^T = V^T P^T: the cache's codes are the 16-row operand
+//     of both products and the query heads of a kv head (up to 8) the 8
+//     columns.  A code converts exactly to fp16, two at a time, straight into
+//     the fragment: the products' inner index and rows may be numbered at
+//     will, so a lane takes sixteen consecutive codes of a token with one load
+//     and K needs no transposition; for V two tokens' bytes are interleaved
+//     (one byte permute per two fragment registers).  fp16 queries enter as
+//     they are, bf16 ones scaled by a power of two per head into fp16's range.
+//   * Up to four heads leave four columns idle: those repeat the heads and
+//     carry what fp16 loses of the probabilities, so that P V has 22 bits of P
+//     at no extra product.  More heads take a second product for it.
+//   * The key scale multiplies the finished score, the value scale the
+//     probability, relative to the largest value scale so far: a probability
+//     enters the product as 2^(x - m) * (scale / largest) * 2^15, which fits
+//     fp16 with 24 bits to spare below it.  Where an item's value scales
+//     spread over more than 2^10, that could lose the blocks of small scales;
+//     there the reference is the running maximum of x + log2(scale) instead.
 //   * K and V tiles come by tiled TMA, swizzled; tokens are numbered within
 //     groups of eight so that the wide loads of both are free of bank
 //     conflicts (see perm_token).
@@ -55,9 +60,10 @@ namespace {
 constexpr int kTokens = 64;                 // tokens per ring stage
 constexpr int kMinBlock = 4;
 constexpr int kStageBlocks = kTokens / kMinBlock;
-constexpr int kTileHeads = 8;               // query heads per item at most
+constexpr int kTileHeads = 8;               // query heads per item at most: the products' columns
 constexpr int kLaunchSeqs = 2048;           // sequences per launch (their lengths sit in shared memory)
 constexpr int kCounters = 65536;            // merge counters of a workspace
+constexpr float kMaxSpread = 10.f;          // log2 of the largest over the least value scale, see above
 constexpr float kPExp = 15.f;               // probabilities enter the product times 2^15 (fp16 reaches 2^16)
 
 // The workspace: two ticket headers (decode; the prompt phase at 128), the
@@ -96,10 +102,10 @@ struct F8Meta {
     int flags, qbuf;
 };
 
-// Column j of a group of eight tokens is token perm_token(j) of it.  The
-// numbers make the quarter-warps of the wide loads hit distinct banks: of K,
-// columns 2i and 2i + 1 (four chunks each); of V, the four even or the four
-// odd columns (two chunks each), under the swizzle of 128- or 64-byte rows.
+// Row j of a group of eight is its token perm_token(j).  The numbers make the
+// quarter-warps of the wide loads hit distinct banks: of K, rows 2i and 2i + 1
+// (four chunks each); of V, the four even or the four odd rows (two chunks
+// each), under the swizzle of 128- or 64-byte rows.
 template <int D> __device__ __forceinline__ int perm_token(int j) {
     if (D >= 128) return j ^ ((j & 1) << 2);                              // 0 5 2 7 4 1 6 3
     const int even = ((j & 2) << 1) | (j >> 2);                           // 0 4 1 5 of columns 0 2 4 6
@@ -112,52 +118,72 @@ template <int D> __device__ __forceinline__ int chunk_at(int row, int chunk) {
     return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
+// The lane's two columns (2c and 2c + 1, c = lane % 4) of an item.  o is the
+// value sum relative to 2^(r - 15): r = m + (log2 of the largest value scale so
+// far), or above the largest x + log2(scale) where scales spread far.
 template <int D> struct F8State {
-    float o[D / 8][4];     // columns d of row lane / 4: [0], [1] from P's fp16 part, [2], [3] from its rest
-    float m, l;            // running max (log2 domain) and this lane's share of the sum of exponentials
-    float m2;              // running max of score + log2(value scale): o is relative to it
+    float o[D / 16][4];    // d = (D / 8) (lane / 4) + 2 i: [0], [1]; + 1: [2], [3]
+    float m[2], l[2];      // running max (log2 domain) and this lane's share of the sum of exponentials
+    float r[2];
+    float top, low;        // largest and least log2 of a value scale (uniform over the warp)
 };
 
 template <int D> __device__ __forceinline__ void f8_reset(F8State<D> &st) {
 #pragma unroll
-    for (int j = 0; j < D / 8; j++)
+    for (int j = 0; j < D / 16; j++)
 #pragma unroll
         for (int e = 0; e < 4; e++) st.o[j][e] = 0.f;
-    st.m = st.m2 = -INFINITY;
-    st.l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+        st.m[e] = st.r[e] = -INFINITY;
+        st.l[e] = 0.f;
+    }
+    st.top = -INFINITY;
+    st.low = INFINITY;
 }
 
-__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
-    return __byte_perm(a, b, sel);
+// 2^x: the hardware's approximation (relative error 2^-22), subnormal results flushed.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// Query row lane / 4 as A fragments.  k-step ks of lane column c covers
-// d = (ks / 4) * 64 + 16 c + 4 (ks % 4) .. + 3.  Returns the factor that undoes
-// the row's power of two.
-template <int D, typename T>
-__device__ __forceinline__ float f8_load_q(uint32_t (&qa)[D / 16][2], const T *q, int rows, int lane) {
-    const int row = lane >> 2, c = lane & 3;
+// The 8x8 matrix of 16-bit elements whose row lane / 4, columns 2c and 2c + 1
+// each lane holds, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Query head lane / 4 (of an item of `rows`; the upper four columns repeat the
+// lower ones unless WIDE) as B fragments.  k-step ks of lane column c covers
+// d = (ks / 4) * 64 + 16 c + 4 (ks % 4) .. + 3.  qf: the factors that undo the
+// powers of two of columns 2c and 2c + 1.
+template <int D, bool WIDE, typename T>
+__device__ __forceinline__ void f8_load_q(uint32_t (&qb)[D / 16][2], float (&qf)[2], const T *q, int rows, int lane) {
+    const int head = WIDE ? lane >> 2 : (lane >> 2) & 3, c = lane & 3;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ks++) {
         uint2 v = make_uint2(0u, 0u);
-        if (row < rows) v = *reinterpret_cast<const uint2 *>(q + row * D + (ks >> 2) * 64 + c * 16 + (ks & 3) * 4);
-        qa[ks][0] = v.x;
-        qa[ks][1] = v.y;
+        if (head < rows) v = *reinterpret_cast<const uint2 *>(q + head * D + (ks >> 2) * 64 + c * 16 + (ks & 3) * 4);
+        qb[ks][0] = v.x;
+        qb[ks][1] = v.y;
     }
-    if constexpr (std::is_same<T, __half>::value) {
-        return 1.f;
-    } else {
+    qf[0] = qf[1] = 1.f;
+    if constexpr (!std::is_same<T, __half>::value) {
         float amax = 0.f;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ks++)
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qa[ks][e]));
+                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qb[ks][e]));
                 amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-        // the row's largest value goes to [2^14, 2^15): bf16's 8 bits then stay exact over 31 binades below it
+        // the head's largest value goes to [2^14, 2^15): bf16's 8 bits then stay exact over 31 binades below it
         int sh = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
         sh = amax == 0.f || amax == INFINITY ? 0 : (sh > 100 ? 100 : sh);
         const float up = __uint_as_float((unsigned)(sh + 127) << 23);
@@ -165,115 +191,147 @@ __device__ __forceinline__ float f8_load_q(uint32_t (&qa)[D / 16][2], const T *q
         for (int ks = 0; ks < D / 16; ks++)
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qa[ks][e]));
-                qa[ks][e] = Mma<__half>::pack(f.x * up, f.y * up);
+                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qb[ks][e]));
+                qb[ks][e] = Mma<__half>::pack(f.x * up, f.y * up);
             }
-        return __uint_as_float((unsigned)(127 - sh) << 23);
+        const float down = __uint_as_float((unsigned)(127 - sh) << 23);
+        qf[0] = __shfl_sync(kFull, down, (2 * c) * 4);
+        qf[1] = __shfl_sync(kFull, down, (2 * c + 1) * 4);
     }
 }
 
 // Thirty-two tokens from row `base` of a stage.  sc: the stage's block scales
-// (key scale * softmax scale * log2 e, log2 of the value scale), a block per
-// 2^log2_rows tokens.
-template <int D, bool FULL>
+// (key scale * softmax scale * log2 e, value scale), a block per 2^log2_rows
+// tokens.
+template <int D, bool WIDE, bool FULL>
 __device__ __forceinline__ void f8_consume(const unsigned char *Ks, const unsigned char *Vs, const float2 *sc,
                                            int log2_rows, int base, int nvalid, int lane,
-                                           const uint32_t (&qa)[D / 16][2], float qf, F8State<D> &st) {
+                                           const uint32_t (&qb)[D / 16][2], const float (&qf)[2], F8State<D> &st) {
     const int n = lane >> 2, c = lane & 3;
     const int pn = perm_token<D>(n), pe = perm_token<D>(2 * c), po = perm_token<D>(2 * c + 1);
-    // S = Q K^T: four groups of eight tokens
-    float s[4][4];
+    // S^T = K Q^T: sixteen tokens (rows lane / 4 and + 8) at a time
+    float s[2][4];
 #pragma unroll
-    for (int nt = 0; nt < 4; nt++) {
+    for (int mt = 0; mt < 2; mt++) {
 #pragma unroll
-        for (int e = 0; e < 4; e++) s[nt][e] = 0.f;
-        const int row = base + nt * 8 + pn;
-        uint32_t w[D / 16];
+        for (int e = 0; e < 4; e++) s[mt][e] = 0.f;
+        const int row = base + mt * 16 + pn;
 #pragma unroll
         for (int k = 0; k < D / 64; k++) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(Ks + chunk_at<D>(row, c + 4 * k));
-            w[4 * k] = v.x;
-            w[4 * k + 1] = v.y;
-            w[4 * k + 2] = v.z;
-            w[4 * k + 3] = v.w;
-        }
+            const uint4 u = *reinterpret_cast<const uint4 *>(Ks + chunk_at<D>(row, c + 4 * k));
+            const uint4 v = *reinterpret_cast<const uint4 *>(Ks + chunk_at<D>(row + 8, c + 4 * k));
+            const uint32_t lo8[4] = {u.x, u.y, u.z, u.w}, hi8[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks++) {
-            const uint32_t a[4] = {qa[ks][0], 0u, qa[ks][1], 0u};
-            Mma<__half>::run(s[nt], a, e4m3x2_lo(w[ks]), e4m3x2_hi(w[ks]));
+            for (int ks = 0; ks < 4; ks++) {
+                const uint32_t a[4] = {e4m3x2_lo(lo8[ks]), e4m3x2_lo(hi8[ks]), e4m3x2_hi(lo8[ks]), e4m3x2_hi(hi8[ks])};
+                Mma<__half>::run(s[mt], a, qb[4 * k + ks][0], qb[4 * k + ks][1]);
+            }
         }
     }
-    // scores of row lane / 4, this lane's tokens 8 nt + pe and 8 nt + po
-    float x[8], x2[8];
+    // this lane's tokens g = 0 .. 3: row lane / 4 of the g-th group of eight
+    float x[4][2], vs[4];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const int tok = base + (j >> 1) * 8 + ((j & 1) ? po : pe);
+    for (int g = 0; g < 4; g++) {
+        const int tok = base + g * 8 + pn;
         const float2 f = sc[tok >> log2_rows];
-        x[j] = s[j >> 1][j & 1] * qf * f.x;
-        x2[j] = x[j] + f.y;
-        if (!FULL && tok >= nvalid) x[j] = x2[j] = -INFINITY;
-    }
-    float mx = x[0], mx2 = x2[0];
+        vs[g] = f.y;
 #pragma unroll
-    for (int j = 1; j < 8; j++) {
-        mx = fmaxf(mx, x[j]);
-        mx2 = fmaxf(mx2, x2[j]);
+        for (int e = 0; e < 2; e++) x[g][e] = s[g >> 1][(g & 1) * 2 + e] * (qf[e] * f.x);
+        if (!FULL && tok >= nvalid) {            // what stands past the context may be anything, its scales too
+            x[g][0] = x[g][1] = -INFINITY;
+            vs[g] = 0.f;
+        }
     }
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-    mx2 = fmaxf(mx2, __shfl_xor_sync(kFull, mx2, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-    mx2 = fmaxf(mx2, __shfl_xor_sync(kFull, mx2, 2));
-    const float mnew = fmaxf(st.m, mx);
-    const float m2new = fmaxf(fmaxf(st.m2, mx2), -1e30f);     // finite: value scales of zero leave -inf
-    const float alpha = exp2f(st.m - mnew), alpha2 = exp2f(st.m2 - m2new);
-    float psum = 0.f;
+    float mnew[2], alpha[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+        float mx = fmaxf(fmaxf(x[0][e], x[1][e]), fmaxf(x[2][e], x[3][e]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+        mnew[e] = fmaxf(st.m[e], mx);
+        alpha[e] = ex2(st.m[e] - mnew[e]);
+        st.m[e] = mnew[e];
+    }
+    float rnew[2], w[4][2];
+    if (st.top - st.low <= kMaxSpread) {                        // uniform over the warp
+        const float wscale = ex2(kPExp - fmaxf(st.top, -100.f));
+#pragma unroll
+        for (int g = 0; g < 4; g++) w[g][0] = w[g][1] = vs[g] * wscale;
+        rnew[0] = mnew[0] + st.top;
+        rnew[1] = mnew[1] + st.top;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            float mx = -1e30f;                                  // finite: value scales of zero leave nothing
+#pragma unroll
+            for (int g = 0; g < 4; g++)
+                if (vs[g] > 0.f && x[g][e] > -INFINITY) mx = fmaxf(mx, x[g][e] + log2f(vs[g]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+            rnew[e] = fmaxf(st.r[e], mx);
+#pragma unroll
+            for (int g = 0; g < 4; g++)
+                w[g][e] = vs[g] > 0.f ? fminf(exp2f(log2f(vs[g]) - (rnew[e] - mnew[e]) + kPExp), 0x1p100f) : 0.f;
+        }
+    }
+    // the probabilities, and P^T as B fragments
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int nt = 0; nt < 4; nt++) {
-        psum += exp2f(x[2 * nt] - mnew) + exp2f(x[2 * nt + 1] - mnew);
-        const float p0 = exp2f(x2[2 * nt] - (m2new - kPExp)), p1 = exp2f(x2[2 * nt + 1] - (m2new - kPExp));
-        hi[nt] = Mma<__half>::pack(p0, p1);
-        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[nt]));
-        lo[nt] = Mma<__half>::pack(p0 - h.x, p1 - h.y);
+    for (int g = 0; g < 4; g++) {
+        const float p0 = ex2(x[g][0] - mnew[0]), p1 = ex2(x[g][1] - mnew[1]);
+        st.l[0] = g == 0 ? fmaf(st.l[0], alpha[0], p0) : st.l[0] + p0;
+        st.l[1] = g == 0 ? fmaf(st.l[1], alpha[1], p1) : st.l[1] + p1;
+        const float w0 = p0 * w[g][0], w1 = p1 * w[g][1];
+        uint32_t h = Mma<__half>::pack(w0, w1);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        const uint32_t rest = Mma<__half>::pack(w0 - f.x, w1 - f.y);
+        if (WIDE) {
+            hi[g] = transpose8x8(h);
+            lo[g] = transpose8x8(rest);
+        } else {
+            hi[g] = transpose8x8(c < 2 ? h : rest);
+        }
     }
-    st.l = st.l * alpha + psum;
-    st.m = mnew;
-    st.m2 = m2new;
-    if (__any_sync(kFull, alpha2 != 1.f)) {
+    const float a0 = ex2(st.r[0] - rnew[0]), a1 = ex2(st.r[1] - rnew[1]);
+    st.r[0] = rnew[0];
+    st.r[1] = rnew[1];
+    if (__any_sync(kFull, a0 != 1.f || a1 != 1.f)) {
 #pragma unroll
-        for (int j = 0; j < D / 8; j++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) st.o[j][e] *= alpha2;
+        for (int i = 0; i < D / 16; i++) {
+            st.o[i][0] *= a0;
+            st.o[i][1] *= a1;
+            st.o[i][2] *= a0;
+            st.o[i][3] *= a1;
+        }
     }
-    // O += P V: sixteen tokens a step, output column (j, n) is d = (D / 8) n + j
+    // O^T += V^T P^T: sixteen tokens a step; rows lane / 4 and + 8 of tile i are d = (D / 8) (lane / 4) + 2 i and + 1
 #pragma unroll
     for (int kt = 0; kt < 2; kt++) {
-        const uint32_t pa[4] = {hi[2 * kt], lo[2 * kt], hi[2 * kt + 1], lo[2 * kt + 1]};
         const int t = base + kt * 16;
         const int rows[4] = {t + pe, t + po, t + 8 + pe, t + 8 + po};
         uint32_t v[4][D / 32];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             if constexpr (D >= 128) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(Vs + chunk_at<D>(rows[i], n));
-                v[i][0] = w.x;
-                v[i][1] = w.y;
-                v[i][2] = w.z;
-                v[i][3] = w.w;
+                const uint4 r = *reinterpret_cast<const uint4 *>(Vs + chunk_at<D>(rows[i], n));
+                v[i][0] = r.x;
+                v[i][1] = r.y;
+                v[i][2] = r.z;
+                v[i][3] = r.w;
             } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(Vs + chunk_at<D>(rows[i], n >> 1) + (n & 1) * 8);
-                v[i][0] = w.x;
-                v[i][1] = w.y;
+                const uint2 r = *reinterpret_cast<const uint2 *>(Vs + chunk_at<D>(rows[i], n >> 1) + (n & 1) * 8);
+                v[i][0] = r.x;
+                v[i][1] = r.y;
             }
         }
 #pragma unroll
-        for (int w = 0; w < D / 32; w++) {
-            const uint32_t a01 = byte_perm(v[0][w], v[1][w], 0x5140u), a23 = byte_perm(v[2][w], v[3][w], 0x5140u);
-            const uint32_t b01 = byte_perm(v[0][w], v[1][w], 0x7362u), b23 = byte_perm(v[2][w], v[3][w], 0x7362u);
-            Mma<__half>::run(st.o[4 * w], pa, e4m3x2_lo(a01), e4m3x2_lo(a23));
-            Mma<__half>::run(st.o[4 * w + 1], pa, e4m3x2_hi(a01), e4m3x2_hi(a23));
-            Mma<__half>::run(st.o[4 * w + 2], pa, e4m3x2_lo(b01), e4m3x2_lo(b23));
-            Mma<__half>::run(st.o[4 * w + 3], pa, e4m3x2_hi(b01), e4m3x2_hi(b23));
+        for (int i = 0; i < D / 16; i++) {
+            const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;   // bytes 2, 3 or 0, 1 of two tokens, interleaved
+            const uint32_t x01 = __byte_perm(v[0][i >> 1], v[1][i >> 1], sel);
+            const uint32_t x23 = __byte_perm(v[2][i >> 1], v[3][i >> 1], sel);
+            const uint32_t a[4] = {e4m3x2_lo(x01), e4m3x2_hi(x01), e4m3x2_lo(x23), e4m3x2_hi(x23)};
+            Mma<__half>::run(st.o[i], a, hi[2 * kt], hi[2 * kt + 1]);
+            if (WIDE) Mma<__half>::run(st.o[i], a, lo[2 * kt], lo[2 * kt + 1]);
         }
     }
 }
@@ -286,11 +344,10 @@ struct F8Item {
 };
 
 __device__ __forceinline__ void f8_load_scales(const F8Args &f, int g, int ent, float2 &sc) {
-    sc = make_float2(0.f, -INFINITY);
+    sc = make_float2(0.f, 0.f);
     if (ent >= 0 && ent < f.a.num_blocks) {
-        const float2 v = __ldg(f.scales + (size_t)ent * f.scale_heads + g);
-        sc.x = v.x * f.a.scale_log2;
-        sc.y = v.y > 0.f ? log2f(v.y) : -INFINITY;
+        sc = __ldg(f.scales + (size_t)ent * f.scale_heads + g);
+        sc.x *= f.a.scale_log2;
     }
 }
 
@@ -322,7 +379,8 @@ __device__ __forceinline__ void f8_decode_item(const F8Args &f, const int *pref,
     it.ent = j < it.nblk ? __ldg(a.tables + (size_t)lo * a.max_blocks + j) : -1;
 }
 
-template <int D, typename T>
+// WIDE: items of five to eight query heads.
+template <int D, bool WIDE, typename T>
 __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
     paged_attention_fp8_kernel(const F8Args f, const __grid_constant__ CUtensorMap tmk,
                                const __grid_constant__ CUtensorMap tmv) {
@@ -340,6 +398,7 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
     F8Meta *meta = reinterpret_cast<F8Meta *>(smem + L::meta);
     const int S = a.num_seqs;
     int &cta_flags = *reinterpret_cast<int *>(smem + L::misc);
+    int &consumer_warp = *(reinterpret_cast<int *>(smem + L::misc) + 1);
     int *scan_tmp = reinterpret_cast<int *>(smem + L::misc) + 32;
     int *pref = reinterpret_cast<int *>(smem + L::seqs);             // [S + 1] partitions before s
     int *ctxs = pref + S + 1;                                        // [S]
@@ -354,6 +413,12 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
             mbar_init(&empty[i], 1);
         }
         fence_mbar_init();
+        // Which of the two warps consumes.  A warp's scheduler is its slot on the SM modulo four: two-warp
+        // CTAs that all gave the work to their first warp would use two of the four schedulers.  The slot
+        // is a hint; either warp may take either role.
+        unsigned slot;
+        asm volatile("mov.u32 %0, %%warpid;" : "=r"(slot));
+        consumer_warp = (int)(slot >> 2) & 1;
     }
     pdl_trigger();
     pdl_wait();
@@ -379,7 +444,7 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
     const int B = 1 << a.log2_block;
     const int log2_rows = a.log2_block < 6 ? a.log2_block : 6;       // tokens per copy: a block or 64 of it
 
-    if (warp == 1) {
+    if (warp != consumer_warp) {
         // ---------------- producer: tickets -> items -> tiled copies ----------------
         const T *qg = static_cast<const T *>(a.q);
         const int rows_per_copy = 1 << log2_rows;
@@ -503,8 +568,8 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
     }
 
     // ---------------- consumer ----------------
-    uint32_t qa[D / 16][2];
-    float qf = 1.f;
+    uint32_t qb[D / 16][2];
+    float qf[2] = {1.f, 1.f};
     F8State<D> st;
     f8_reset(st);
     for (int k = 0;; k++) {
@@ -519,18 +584,28 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
         unsigned char *Vs = ring + (size_t)(slot * 2 + 1) * L::tensor;
         const float2 *sc = scs + slot * kStageBlocks;
         if ((md.flags & kFirst) && md.nvalid > 0)
-            qf = f8_load_q<D, T>(qa, qs + (size_t)md.qbuf * kTileHeads * D, md.rows, lane);
+            f8_load_q<D, WIDE, T>(qb, qf, qs + (size_t)md.qbuf * kTileHeads * D, md.rows, lane);
+        if (md.nvalid > 0) {
+            // the range of the stage's value scales, one block to a lane
+            const int blocks = (md.nvalid + (1 << log2_rows) - 1) >> log2_rows;
+            const float v = sc[lane < blocks ? lane : 0].y;
+            const float lv = v > 0.f ? log2f(v) : -INFINITY;
+            st.top = fmaxf(st.top, warp_max(lv));
+            st.low = fminf(st.low, -warp_max(-lv));
+        }
         if (md.nvalid == kTokens) {
-            f8_consume<D, true>(Ks, Vs, sc, log2_rows, 0, kTokens, lane, qa, qf, st);
-            f8_consume<D, true>(Ks, Vs, sc, log2_rows, 32, kTokens, lane, qa, qf, st);
+#pragma unroll 1
+            for (int base = 0; base < kTokens; base += 32)
+                f8_consume<D, WIDE, true>(Ks, Vs, sc, log2_rows, base, kTokens, lane, qb, qf, st);
         } else if (md.nvalid > 0) {
             // rows past the context may hold anything: zero them in V (0 * NaN would poison the sum)
             const int end = (md.nvalid + 31) & ~31;
             for (int v = md.nvalid * (D / 16) + lane; v < end * (D / 16); v += 32)
                 reinterpret_cast<uint4 *>(Vs)[v] = make_uint4(0u, 0u, 0u, 0u);
             __syncwarp();
+#pragma unroll 1
             for (int base = 0; base < md.nvalid; base += 32)
-                f8_consume<D, false>(Ks, Vs, sc, log2_rows, base, md.nvalid, lane, qa, qf, st);
+                f8_consume<D, WIDE, false>(Ks, Vs, sc, log2_rows, base, md.nvalid, lane, qb, qf, st);
             fence_proxy_async_smem();            // the zeroed rows, before TMA refills the slot
         }
         __syncwarp();
@@ -538,37 +613,47 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
         if (!(md.flags & kLast)) continue;
 
         // ---- the item's end: this warp holds its whole state ----
-        float l = st.l;
-        l += __shfl_xor_sync(kFull, l, 1);
-        l += __shfl_xor_sync(kFull, l, 2);
-        const int row = lane >> 2, c = lane & 3;
-        // o is relative to m2 - 15, the sum of exponentials to m
-        const float rel = l > 0.f || l != l ? exp2f(st.m2 - kPExp - st.m) : 0.f;
-        if (row < md.rows) {
-            const size_t sh = (size_t)md.s * a.num_heads + md.h0 + row;
-            constexpr int W = D / 8;             // d = W n + j; this lane's columns n = 2c and 2c + 1
-            float v[2 * W];
+        constexpr int W = D / 8;                 // this lane's d: W (lane / 4) .. + W - 1
+        const int c = lane & 3;
 #pragma unroll
-            for (int j = 0; j < W; j++) {
-                v[j] = (st.o[j][0] + st.o[j][2]) * rel;
-                v[W + j] = (st.o[j][1] + st.o[j][3]) * rel;
+        for (int e = 0; e < 2; e++) {
+            float l = st.l[e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
+            // o is relative to r - 15, the sum of exponentials to m
+            const float rel = l > 0.f || l != l ? exp2f(st.r[e] - kPExp - st.m[e]) : 0.f;
+            float v[W];
+#pragma unroll
+            for (int i = 0; i < W / 2; i++) {
+                v[2 * i] = st.o[i][e];
+                v[2 * i + 1] = st.o[i][2 + e];
+                if (!WIDE) {                     // the columns that carry the probabilities' rest
+                    v[2 * i] += __shfl_xor_sync(kFull, v[2 * i], 2);
+                    v[2 * i + 1] += __shfl_xor_sync(kFull, v[2 * i + 1], 2);
+                }
+                v[2 * i] *= rel;
+                v[2 * i + 1] *= rel;
             }
+            const int head = 2 * c + e;
+            if (head >= md.rows || (!WIDE && c >= 2)) continue;
+            const size_t sh = (size_t)md.s * a.num_heads + md.h0 + head;
+            const int d0 = W * (lane >> 2);
             if (md.nparts <= 1) {
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + sh * D + c * 2 * W);
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + sh * D + d0);
 #pragma unroll
-                for (int j = 0; j < 2 * W; j += 8)
+                for (int j = 0; j < W; j += 8)
                     dst[j / 8] = make_uint4(Mma<T>::pack(v[j] * inv, v[j + 1] * inv),
                                             Mma<T>::pack(v[j + 2] * inv, v[j + 3] * inv),
                                             Mma<T>::pack(v[j + 4] * inv, v[j + 5] * inv),
                                             Mma<T>::pack(v[j + 6] * inv, v[j + 7] * inv));
             } else {
                 const size_t sp = sh * a.max_parts + md.part;
-                float4 *dst = reinterpret_cast<float4 *>(a.ws_o + sp * D + c * 2 * W);
+                float4 *dst = reinterpret_cast<float4 *>(a.ws_o + sp * D + d0);
 #pragma unroll
-                for (int j = 0; j < 2 * W; j += 4) dst[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                if (c == 0) {
-                    a.ws_m[sp] = st.m;
+                for (int j = 0; j < W; j += 4) dst[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                if (lane < 4) {
+                    a.ws_m[sp] = st.m[e];
                     a.ws_l[sp] = l;
                 }
             }
@@ -647,8 +732,8 @@ bool encode_cache_map8(CUtensorMap *map, const void *base, int num_blocks, int H
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, typename T> cudaError_t launch_decode8(const F8Args &f, cudaStream_t stream) {
-    auto kern = paged_attention_fp8_kernel<D, T>;
+template <int D, bool WIDE, typename T> cudaError_t launch_decode8w(const F8Args &f, cudaStream_t stream) {
+    auto kern = paged_attention_fp8_kernel<D, WIDE, T>;
     const size_t smem = F8Layout<D>::bytes(f.a.num_seqs);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)F8Layout<D>::bytes(kLaunchSeqs));
@@ -664,6 +749,10 @@ template <int D, typename T> cudaError_t launch_decode8(const F8Args &f, cudaStr
     long long ctas = sm_count() * (fit < PKV_FP8_CTAS_PER_SM ? fit : (long long)PKV_FP8_CTAS_PER_SM);
     if (ctas > items) ctas = items;
     return launch(kern, dim3((unsigned)ctas), dim3(64), smem, stream, f, tmk, tmv);
+}
+
+template <int D, typename T> cudaError_t launch_decode8(const F8Args &f, cudaStream_t stream) {
+    return f.tile > 4 ? launch_decode8w<D, true, T>(f, stream) : launch_decode8w<D, false, T>(f, stream);
 }
 
 // ---- the prompt phase ------------------------------------------------------------
