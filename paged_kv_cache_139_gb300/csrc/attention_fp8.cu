@@ -30,8 +30,9 @@
 //   * K and V tiles come by tiled TMA, swizzled; tokens are numbered within
 //     groups of eight so that the wide loads of both are free of bank
 //     conflicts (see perm_token).
-// One producer and one consumer warp per CTA, several CTAs per SM, persistent
-// over (sequence, partition, head tile) items claimed by tickets.
+// A CTA is four pipelines of a producer and a consumer warp, one consumer to
+// each of the SM's schedulers, two CTAs to an SM; each pipeline is persistent
+// over (sequence, partition, head tile) items that it claims by tickets.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -47,24 +48,24 @@
 namespace pkv {
 namespace {
 
-#ifndef PKV_FP8_SLOTS_D128
-#define PKV_FP8_SLOTS_D128 2
-#endif
-#ifndef PKV_FP8_SLOTS_D64
-#define PKV_FP8_SLOTS_D64 4
+// Tuning knobs (compile-time): ring slots of a pipeline, resident CTAs per SM.
+#ifndef PKV_FP8_SLOTS
+#define PKV_FP8_SLOTS 3
 #endif
 #ifndef PKV_FP8_CTAS_PER_SM
-#define PKV_FP8_CTAS_PER_SM 6
+#define PKV_FP8_CTAS_PER_SM 2
 #endif
 
-constexpr int kTokens = 64;                 // tokens per ring stage
+constexpr int kPipes = 4;                   // pipelines of a CTA
+constexpr int kStageBytes = 4096;           // a ring stage's K, and its V: 32 tokens at head_dim 128, 64 at 64
+constexpr int kMaxTokens = kStageBytes / 64;
 constexpr int kMinBlock = 4;
-constexpr int kStageBlocks = kTokens / kMinBlock;
+constexpr int kStageBlocks = kMaxTokens / kMinBlock;
 constexpr int kTileHeads = 8;               // query heads per item at most: the products' columns
-constexpr int kLaunchSeqs = 2048;           // sequences per launch (their lengths sit in shared memory)
+constexpr int kLaunchSeqs = 1024;           // sequences per launch (their partitions are counted in shared memory)
 constexpr int kCounters = 65536;            // merge counters of a workspace
-constexpr float kMaxSpread = 10.f;          // log2 of the largest over the least value scale, see above
-constexpr float kPExp = 15.f;               // probabilities enter the product times 2^15 (fp16 reaches 2^16)
+constexpr int kMaxSpread = 10;              // log2 of the largest over the least value scale, see above
+constexpr int kPExp = 15;                   // probabilities enter the product times 2^15 (fp16 reaches 2^16)
 
 // The workspace: two ticket headers (decode; the prompt phase at 128), the
 // merge counters, then what a call needs.  The counters' place depends on no
@@ -81,26 +82,33 @@ struct F8Args {
     int tile;                    // query heads per item (the last tile of a kv head may hold fewer)
 };
 
-template <int D> struct F8Layout {
-    static constexpr int R = D >= 128 ? PKV_FP8_SLOTS_D128 : PKV_FP8_SLOTS_D64;
-    static constexpr uint32_t tensor = kTokens * D;                                // bytes of a stage's K or V
-    static constexpr uint32_t ring = 0;
-    static constexpr uint32_t q = ring + R * 2 * tensor;                            // [R][8][D] 16-bit
-    static constexpr uint32_t sc = q + R * kTileHeads * D * 2;                      // [R][kStageBlocks] float2
-    static constexpr uint32_t bars = sc + R * kStageBlocks * 8;
-    static constexpr uint32_t meta = bars + 2 * R * 8;
-    static constexpr uint32_t misc = meta + R * 32;
-    static constexpr uint32_t seqs = misc + 64 * 4;
-    static size_t bytes(int S) { return seqs + (size_t)(2 * S + 1) * sizeof(int); }
-};
-
-enum : int { kFirst = 1, kLast = 2, kStop = 4 };
-
 struct F8Meta {
     int s, h0, rows, part, nparts;   // the item: query heads h0 .. h0 + rows - 1
     int nvalid;                      // tokens of the stage
-    int flags, qbuf;
+    int flags;
+    int range;                       // value scales of the item's blocks up to here: see scale_range
 };
+
+// A pipeline's shared memory, and the CTA's.
+struct F8Layout {
+    static constexpr int R = PKV_FP8_SLOTS;
+    static constexpr uint32_t ring = 0;                                             // [R][2][kStageBytes]
+    static constexpr uint32_t q = ring + R * 2 * kStageBytes;                       // [8][<= 128] 16-bit
+    static constexpr uint32_t sc = q + kTileHeads * 128 * 2;                        // [R][kStageBlocks] float2
+    static constexpr uint32_t bars = sc + R * kStageBlocks * 8;
+    static constexpr uint32_t meta = bars + 2 * R * 8;
+    static constexpr uint32_t bytes = meta + R * sizeof(F8Meta);
+    // the 128-byte swizzle repeats every 1024 bytes: rings start on such a boundary, in front of the rest
+    static constexpr uint32_t rings = 0;
+    static constexpr uint32_t rest = kPipes * q;
+    static constexpr uint32_t rest_bytes = bytes - q;
+    static constexpr uint32_t misc = rest + kPipes * rest_bytes;
+    static constexpr uint32_t seqs = misc + 64 * 4;
+    static size_t total(int S) { return seqs + (size_t)(S + 1) * sizeof(int); }
+    static_assert(q % 1024 == 0 && rest_bytes % 16 == 0, "swizzled rings, 16-byte copies");
+};
+
+enum : int { kFirst = 1, kLast = 2, kStop = 4 };
 
 // Row j of a group of eight is its token perm_token(j).  The numbers make the
 // quarter-warps of the wide loads hit distinct banks: of K, rows 2i and 2i + 1
@@ -125,7 +133,6 @@ template <int D> struct F8State {
     float o[D / 16][4];    // d = (D / 8) (lane / 4) + 2 i: [0], [1]; + 1: [2], [3]
     float m[2], l[2];      // running max (log2 domain) and this lane's share of the sum of exponentials
     float r[2];
-    float top, low;        // largest and least log2 of a value scale (uniform over the warp)
 };
 
 template <int D> __device__ __forceinline__ void f8_reset(F8State<D> &st) {
@@ -138,8 +145,6 @@ template <int D> __device__ __forceinline__ void f8_reset(F8State<D> &st) {
         st.m[e] = st.r[e] = -INFINITY;
         st.l[e] = 0.f;
     }
-    st.top = -INFINITY;
-    st.low = INFINITY;
 }
 
 // 2^x: the hardware's approximation (relative error 2^-22), subnormal results flushed.
@@ -155,6 +160,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+
+// The largest exponent of the value scales seen (the scale is at most 2^top),
+// and whether they spread over more than 2^kMaxSpread; negative and zero
+// scales count as far below.
+__device__ __forceinline__ int scale_range(int top, int low) {
+    return top * 2 + (top - low > kMaxSpread ? 1 : 0);
+}
+// e with 2^(e - 1) < v <= 2^e.
+__device__ __forceinline__ int exponent_above(float v) {
+    if (!(v > 0.f)) return -1000;
+    const unsigned b = __float_as_uint(v);
+    return (int)(b >> 23) - 127 + ((b & 0x7fffffu) ? 1 : 0);
 }
 
 // Query head lane / 4 (of an item of `rows`; the upper four columns repeat the
@@ -206,7 +224,8 @@ __device__ __forceinline__ void f8_load_q(uint32_t (&qb)[D / 16][2], float (&qf)
 template <int D, bool WIDE, bool FULL>
 __device__ __forceinline__ void f8_consume(const unsigned char *Ks, const unsigned char *Vs, const float2 *sc,
                                            int log2_rows, int base, int nvalid, int lane,
-                                           const uint32_t (&qb)[D / 16][2], const float (&qf)[2], F8State<D> &st) {
+                                           int range, const uint32_t (&qb)[D / 16][2], const float (&qf)[2],
+                                           F8State<D> &st) {
     const int n = lane >> 2, c = lane & 3;
     const int pn = perm_token<D>(n), pe = perm_token<D>(2 * c), po = perm_token<D>(2 * c + 1);
     // S^T = K Q^T: sixteen tokens (rows lane / 4 and + 8) at a time
@@ -253,12 +272,13 @@ __device__ __forceinline__ void f8_consume(const unsigned char *Ks, const unsign
         st.m[e] = mnew[e];
     }
     float rnew[2], w[4][2];
-    if (st.top - st.low <= kMaxSpread) {                        // uniform over the warp
-        const float wscale = ex2(kPExp - fmaxf(st.top, -100.f));
+    if (!(range & 1)) {                                         // uniform over the warp
+        const int top = range >> 1 > -100 ? range >> 1 : -100;
+        const float wscale = __uint_as_float((unsigned)(kPExp - top + 127) << 23);
 #pragma unroll
         for (int g = 0; g < 4; g++) w[g][0] = w[g][1] = vs[g] * wscale;
-        rnew[0] = mnew[0] + st.top;
-        rnew[1] = mnew[1] + st.top;
+        rnew[0] = mnew[0] + (float)top;
+        rnew[1] = mnew[1] + (float)top;
     } else {
 #pragma unroll
         for (int e = 0; e < 2; e++) {
@@ -271,7 +291,7 @@ __device__ __forceinline__ void f8_consume(const unsigned char *Ks, const unsign
             rnew[e] = fmaxf(st.r[e], mx);
 #pragma unroll
             for (int g = 0; g < 4; g++)
-                w[g][e] = vs[g] > 0.f ? fminf(exp2f(log2f(vs[g]) - (rnew[e] - mnew[e]) + kPExp), 0x1p100f) : 0.f;
+                w[g][e] = vs[g] > 0.f ? fminf(exp2f(log2f(vs[g]) - (rnew[e] - mnew[e]) + (float)kPExp), 0x1p100f) : 0.f;
         }
     }
     // the probabilities, and P^T as B fragments
@@ -341,18 +361,28 @@ __device__ __forceinline__ void f8_consume(const unsigned char *Ks, const unsign
 struct F8Item {
     int s, part, nparts, g, h0, rows, tok0, ntok, nst, nblk, win, ent;
     float2 sc;
+    int top, low;              // exponents of the value scales of the window's blocks, over the warp
 };
 
-__device__ __forceinline__ void f8_load_scales(const F8Args &f, int g, int ent, float2 &sc) {
-    sc = make_float2(0.f, 0.f);
-    if (ent >= 0 && ent < f.a.num_blocks) {
-        sc = __ldg(f.scales + (size_t)ent * f.scale_heads + g);
-        sc.x *= f.a.scale_log2;
-    }
+// The scales of this lane's block, requested; f8_scale_range, when they are
+// here, folds the softmax scale in and takes the window's exponents.
+__device__ __forceinline__ float2 f8_load_scales(const F8Args &f, int g, int ent) {
+    if (ent < 0 || ent >= f.a.num_blocks) return make_float2(0.f, -1.f);
+    const float2 v = __ldg(f.scales + (size_t)ent * f.scale_heads + g);
+    return make_float2(v.x * f.a.scale_log2, fmaxf(v.y, 0.f));
 }
 
-__device__ __forceinline__ void f8_decode_item(const F8Args &f, const int *pref, const int *ctxs, int S, int tiles,
-                                               unsigned int t, int lane, F8Item &it) {
+__device__ __forceinline__ void f8_scale_range(float2 sc, int &top, int &low) {
+    const int e = exponent_above(sc.y);
+    const int t = __reduce_max_sync(kFull, e);
+    const int l = __reduce_min_sync(kFull, sc.y < 0.f ? 1000 : e);      // below zero: no block
+    top = top > t ? top : t;
+    low = low < l ? low : l;
+}
+
+template <int TOKENS>
+__device__ __forceinline__ void f8_decode_item(const F8Args &f, const int *pref, int S, int tiles, unsigned int t,
+                                               int lane, F8Item &it) {
     const AttnArgs &a = f.a;
     const int pidx = (int)(t / (unsigned int)tiles);
     const int tile = (int)(t % (unsigned int)tiles);
@@ -368,12 +398,13 @@ __device__ __forceinline__ void f8_decode_item(const F8Args &f, const int *pref,
     const int group = a.num_heads / a.num_kv_heads, first = (tile % a.head_tiles) * f.tile;
     it.h0 = it.g * group + first;
     it.rows = group - first < f.tile ? group - first : f.tile;
-    const int ctx = ctxs[lo];
+    int ctx = __ldg(a.ctx_lens + lo);
+    ctx = ctx < 0 ? 0 : ctx > a.max_ctx ? a.max_ctx : ctx;             // latched where the partitions are counted
     it.tok0 = it.part * a.partition;
     const int ntok = ctx - it.tok0 < a.partition ? ctx - it.tok0 : a.partition;
     it.ntok = ntok < 0 ? 0 : ntok;
-    it.nst = (it.ntok + kTokens - 1) / kTokens;
-    it.nblk = (ctx + (1 << a.log2_block) - 1) >> a.log2_block;
+    it.nst = (it.ntok + TOKENS - 1) / TOKENS;
+    it.nblk = (it.tok0 + it.ntok + (1 << a.log2_block) - 1) >> a.log2_block;      // blocks up to the item's end
     it.win = it.tok0 >> a.log2_block;
     const int j = it.win + lane;
     it.ent = j < it.nblk ? __ldg(a.tables + (size_t)lo * a.max_blocks + j) : -1;
@@ -381,56 +412,46 @@ __device__ __forceinline__ void f8_decode_item(const F8Args &f, const int *pref,
 
 // WIDE: items of five to eight query heads.
 template <int D, bool WIDE, typename T>
-__global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
+__global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
     paged_attention_fp8_kernel(const F8Args f, const __grid_constant__ CUtensorMap tmk,
                                const __grid_constant__ CUtensorMap tmv) {
-    using L = F8Layout<D>;
-    constexpr int R = L::R;
+    using L = F8Layout;
+    constexpr int R = L::R, TOKENS = kStageBytes / D;
     const AttnArgs &a = f.a;
-    // the 128-byte swizzle repeats every 1024 bytes: the ring starts on such a boundary
     extern __shared__ __align__(1024) unsigned char smem8[];
-    unsigned char *smem = smem8;
-    unsigned char *ring = smem + L::ring;                            // [R][2][kTokens][D]
-    T *qs = reinterpret_cast<T *>(smem + L::q);                      // [R][8][D]
-    float2 *scs = reinterpret_cast<float2 *>(smem + L::sc);          // [R][kStageBlocks]
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::bars);
-    uint64_t *empty = full + R;
-    F8Meta *meta = reinterpret_cast<F8Meta *>(smem + L::meta);
-    const int S = a.num_seqs;
-    int &cta_flags = *reinterpret_cast<int *>(smem + L::misc);
-    int &consumer_warp = *(reinterpret_cast<int *>(smem + L::misc) + 1);
-    int *scan_tmp = reinterpret_cast<int *>(smem + L::misc) + 32;
-    int *pref = reinterpret_cast<int *>(smem + L::seqs);             // [S + 1] partitions before s
-    int *ctxs = pref + S + 1;                                        // [S]
-
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pipe = warp & (kPipes - 1);
+    unsigned char *ring = smem8 + L::rings + (uint32_t)pipe * L::q;                  // [R][2][TOKENS][D]
+    unsigned char *rest = smem8 + L::rest + (uint32_t)pipe * L::rest_bytes - L::q;
+    T *qs = reinterpret_cast<T *>(rest + L::q);                      // [8][D]
+    float2 *scs = reinterpret_cast<float2 *>(rest + L::sc);          // [R][kStageBlocks]
+    uint64_t *full = reinterpret_cast<uint64_t *>(rest + L::bars);
+    uint64_t *empty = full + R;
+    F8Meta *meta = reinterpret_cast<F8Meta *>(rest + L::meta);
+    int &cta_flags = *reinterpret_cast<int *>(smem8 + L::misc);
+    int *scan_tmp = reinterpret_cast<int *>(smem8 + L::misc) + 32;
+    int *pref = reinterpret_cast<int *>(smem8 + L::seqs);            // [S + 1] partitions before s
+    const int S = a.num_seqs;
     const int tiles = a.num_kv_heads * a.head_tiles;
     WsHeader *hdr = a.hdr;
 
-    if (threadIdx.x == 0) {
+    if (warp < kPipes && lane == 0) {
         for (int i = 0; i < R; i++) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         fence_mbar_init();
-        // Which of the two warps consumes.  A warp's scheduler is its slot on the SM modulo four: two-warp
-        // CTAs that all gave the work to their first warp would use two of the four schedulers.  The slot
-        // is a hint; either warp may take either role.
-        unsigned slot;
-        asm volatile("mov.u32 %0, %%warpid;" : "=r"(slot));
-        consumer_warp = (int)(slot >> 2) & 1;
     }
     pdl_trigger();
     pdl_wait();
     if (threadIdx.x == 0)
-        cta_flags = (timed_out(a.st) ? 1 : 0) | (hdr->magic != kWsMagic8 ? 2 : 0) | ((smem_u32(smem) & 1023u) ? 4 : 0);
+        cta_flags = (timed_out(a.st) ? 1 : 0) | (hdr->magic != kWsMagic8 ? 2 : 0) | ((smem_u32(smem8) & 1023u) ? 4 : 0);
     for (int i = threadIdx.x; i < S; i += blockDim.x) {
         int c = a.ctx_lens[i];
         if (c < 0 || c > a.max_ctx) {
             if (blockIdx.x == 0) latch(a.st, kFlagBadContext, c);
             c = c < 0 ? 0 : a.max_ctx;
         }
-        ctxs[i] = c;
         pref[i + 1] = c > 0 ? (c + a.partition - 1) / a.partition : 1;
     }
     __syncthreads();
@@ -442,23 +463,26 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
     block_prefix_sum(pref, S, scan_tmp);
     const unsigned int N = (unsigned int)pref[S] * (unsigned int)tiles;
     const int B = 1 << a.log2_block;
-    const int log2_rows = a.log2_block < 6 ? a.log2_block : 6;       // tokens per copy: a block or 64 of it
+    constexpr int kLog2Tokens = TOKENS == 64 ? 6 : 5;
+    const int log2_rows = a.log2_block < kLog2Tokens ? a.log2_block : kLog2Tokens;   // tokens per copy: a block, or a stage of it
 
-    if (warp != consumer_warp) {
+    if (warp >= kPipes) {
         // ---------------- producer: tickets -> items -> tiled copies ----------------
         const T *qg = static_cast<const T *>(a.q);
         const int rows_per_copy = 1 << log2_rows;
-        const int cps = kTokens >> log2_rows;                        // blocks per stage
+        const int cps = TOKENS >> log2_rows;                         // blocks per stage
         const uint32_t copy_bytes = (uint32_t)rows_per_copy * D;
         // another head tile of the same kv head reads the same tiles next
         const uint64_t policy = a.head_tiles > 1 ? policy_evict_last() : policy_evict_first();
-        unsigned int cur_t = blockIdx.x;
+        // the first items go round the CTAs; later ones come from the counter
+        const unsigned int pipes = gridDim.x * kPipes;
+        unsigned int cur_t = (unsigned int)pipe * gridDim.x + blockIdx.x;
         F8Item cur, nx;
         if (cur_t < N) {
-            f8_decode_item(f, pref, ctxs, S, tiles, cur_t, lane, cur);
-            f8_load_scales(f, cur.g, cur.ent, cur.sc);
+            f8_decode_item<TOKENS>(f, pref, S, tiles, cur_t, lane, cur);
+            cur.sc = f8_load_scales(f, cur.g, cur.ent);
         }
-        int kk = 0, items = 0;
+        int kk = 0, first = -R;                                      // stages so far, the last item's first one
         bool dead = false;
         while (cur_t < N && !dead) {
             // The next ticket is claimed three stages before the item's last, its table entries
@@ -468,20 +492,21 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
             int step = 0;                                            // claimed, decoded, scales requested
             auto next_item = [&]() {
                 if (step == 0) {
-                    if (lane == 0) nxt_raw = gridDim.x + atomicAdd(&hdr->next, 1u);
+                    if (lane == 0) nxt_raw = pipes + atomicAdd(&hdr->next, 1u);
                 } else if (step == 1) {
                     nxt_t = __shfl_sync(kFull, nxt_raw, 0);
-                    if (nxt_t < N) f8_decode_item(f, pref, ctxs, S, tiles, nxt_t, lane, nx);
+                    if (nxt_t < N) f8_decode_item<TOKENS>(f, pref, S, tiles, nxt_t, lane, nx);
                 } else {
-                    if (nxt_t < N) f8_load_scales(f, nx.g, nx.ent, nx.sc);
+                    if (nxt_t < N) nx.sc = f8_load_scales(f, nx.g, nx.ent);
                 }
                 step++;
             };
             const int npad = cur.nst > 0 ? cur.nst : 1;              // an empty context still has a stage
             const int32_t *trow = a.tables + (size_t)cur.s * a.max_blocks;
-            const int qb = items % R;
-            int win = cur.win, ent = cur.ent;
+            const uint32_t q_bytes = (uint32_t)(cur.rows * D * 2);
+            int win = cur.win, ent = cur.ent, top = -1000, low = 1000;
             float2 sc = cur.sc;
+            f8_scale_range(sc, top, low);
             for (int i = 0; i < npad; i++, kk++) {
                 if (i >= npad - 3) next_item();
                 const int slot = kk % R;
@@ -489,16 +514,17 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
                 int nv = 0, nb = 0, off0 = 0, pj = -1;
                 float2 sj = make_float2(0.f, 0.f);
                 if (i < cur.nst) {                                   // uniform over the warp
-                    const int t_first = cur.tok0 + i * kTokens;
+                    const int t_first = cur.tok0 + i * TOKENS;
                     const int lb0 = t_first >> a.log2_block;
                     off0 = t_first & (B - 1);
-                    nv = cur.ntok - i * kTokens < kTokens ? cur.ntok - i * kTokens : kTokens;
+                    nv = cur.ntok - i * TOKENS < TOKENS ? cur.ntok - i * TOKENS : TOKENS;
                     nb = (nv + rows_per_copy - 1) >> log2_rows;
                     if (lb0 < win || lb0 + cps > win + 32) {
                         win = lb0;
                         const int j = win + lane;
                         ent = j < cur.nblk ? __ldg(trow + j) : -1;
-                        f8_load_scales(f, cur.g, ent, sc);
+                        sc = f8_load_scales(f, cur.g, ent);
+                        f8_scale_range(sc, top, low);
                     }
                     const int jl = lane >> 1;                        // this lane's block of the stage
                     const int from = (lb0 + jl - win) & 31;
@@ -513,17 +539,21 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
                         nv = nb << log2_rows;
                     }
                 }
-                if (kk >= R && !__all_sync(kFull, mbar_wait(&empty[slot], ((kk / R) - 1) & 1, kWaitLimitCycles))) {
+                bool ok = kk < R || mbar_wait(&empty[slot], ((kk / R) - 1) & 1, kWaitLimitCycles);
+                // the one query buffer: the last item's first stage (which read it) must be consumed
+                if (withq && first > kk - R) ok = ok && mbar_wait(&empty[first % R], (first / R) & 1, kWaitLimitCycles);
+                if (!__all_sync(kFull, ok)) {
                     if (lane == 0) latch(a.st, kFlagTimeout, kk);
                     dead = true;
                     break;
                 }
+                if (i == 0) first = kk;
                 if ((lane & 1) == 0 && (lane >> 1) < nb) scs[slot * kStageBlocks + (lane >> 1)] = sj;
-                const uint32_t q_bytes = (uint32_t)(cur.rows * D * 2);
                 if (lane == 0) {
                     int4 *mv = reinterpret_cast<int4 *>(&meta[slot]);
                     mv[0] = make_int4(cur.s, cur.h0, cur.rows, cur.part);
-                    mv[1] = make_int4(cur.nparts, nv, (i == 0 ? kFirst : 0) | (i == npad - 1 ? kLast : 0), qb);
+                    mv[1] = make_int4(cur.nparts, nv, (i == 0 ? kFirst : 0) | (i == npad - 1 ? kLast : 0),
+                                      scale_range(top, low));
                 }
                 __syncwarp();
                 if (lane == 0)
@@ -532,33 +562,31 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
                 // lane 2j + t moves block j's K (t = 0) or V (t = 1) tile
                 if (lane < 2 * nb) {
                     const int t = lane & 1;
-                    unsigned char *dst = ring + (size_t)(slot * 2 + t) * L::tensor + (size_t)(lane >> 1) * copy_bytes;
+                    unsigned char *dst = ring + (slot * 2 + t) * kStageBytes + (uint32_t)(lane >> 1) * copy_bytes;
                     tma_load_4d(dst, t ? (const void *)&tmv : (const void *)&tmk, 0, off0, cur.g, pj, &full[slot],
                                 policy);
                 }
                 if (withq && lane == 0)
-                    bulk_g2s(qs + (size_t)qb * kTileHeads * D, qg + ((size_t)cur.s * a.num_heads + cur.h0) * D, q_bytes,
-                             &full[slot]);
+                    bulk_g2s(qs, qg + ((size_t)cur.s * a.num_heads + cur.h0) * D, q_bytes, &full[slot]);
             }
             if (dead) break;
             while (step < 3) next_item();
-            items++;
             cur_t = nxt_t;
             cur = nx;
         }
         if (lane == 0) {
-            for (int once = 0; once < 1 && !dead; once++, kk++) {    // the stop mark
+            if (!dead) {                                             // the stop mark
                 const int slot = kk % R;
                 if (kk >= R && !mbar_wait(&empty[slot], ((kk / R) - 1) & 1, kWaitLimitCycles)) {
                     latch(a.st, kFlagTimeout, kk);
-                    break;
+                } else {
+                    meta[slot].flags = kStop;
+                    mbar_arrive_expect_tx(&full[slot], 0u);
                 }
-                meta[slot].flags = kStop;
-                mbar_arrive_expect_tx(&full[slot], 0u);
             }
-            // the last CTA to finish leaves the counters at zero for the next call
+            // the last pipeline to finish leaves the counters at zero for the next call
             __threadfence();
-            if (atomicAdd(&hdr->done, 1u) == gridDim.x - 1) {
+            if (atomicAdd(&hdr->done, 1u) == pipes - 1) {
                 hdr->next = 0;
                 hdr->done = 0;
                 __threadfence();
@@ -580,23 +608,14 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
         }
         const F8Meta md = meta[slot];
         if (md.flags & kStop) break;
-        const unsigned char *Ks = ring + (size_t)(slot * 2) * L::tensor;
-        unsigned char *Vs = ring + (size_t)(slot * 2 + 1) * L::tensor;
+        const unsigned char *Ks = ring + (slot * 2) * kStageBytes;
+        unsigned char *Vs = ring + (slot * 2 + 1) * kStageBytes;
         const float2 *sc = scs + slot * kStageBlocks;
-        if ((md.flags & kFirst) && md.nvalid > 0)
-            f8_load_q<D, WIDE, T>(qb, qf, qs + (size_t)md.qbuf * kTileHeads * D, md.rows, lane);
-        if (md.nvalid > 0) {
-            // the range of the stage's value scales, one block to a lane
-            const int blocks = (md.nvalid + (1 << log2_rows) - 1) >> log2_rows;
-            const float v = sc[lane < blocks ? lane : 0].y;
-            const float lv = v > 0.f ? log2f(v) : -INFINITY;
-            st.top = fmaxf(st.top, warp_max(lv));
-            st.low = fminf(st.low, -warp_max(-lv));
-        }
-        if (md.nvalid == kTokens) {
+        if ((md.flags & kFirst) && md.nvalid > 0) f8_load_q<D, WIDE, T>(qb, qf, qs, md.rows, lane);
+        if (md.nvalid == TOKENS) {
 #pragma unroll 1
-            for (int base = 0; base < kTokens; base += 32)
-                f8_consume<D, WIDE, true>(Ks, Vs, sc, log2_rows, base, kTokens, lane, qb, qf, st);
+            for (int base = 0; base < TOKENS; base += 32)
+                f8_consume<D, WIDE, true>(Ks, Vs, sc, log2_rows, base, TOKENS, lane, md.range, qb, qf, st);
         } else if (md.nvalid > 0) {
             // rows past the context may hold anything: zero them in V (0 * NaN would poison the sum)
             const int end = (md.nvalid + 31) & ~31;
@@ -605,7 +624,7 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
             __syncwarp();
 #pragma unroll 1
             for (int base = 0; base < md.nvalid; base += 32)
-                f8_consume<D, WIDE, false>(Ks, Vs, sc, log2_rows, base, md.nvalid, lane, qb, qf, st);
+                f8_consume<D, WIDE, false>(Ks, Vs, sc, log2_rows, base, md.nvalid, lane, md.range, qb, qf, st);
             fence_proxy_async_smem();            // the zeroed rows, before TMA refills the slot
         }
         __syncwarp();
@@ -621,7 +640,7 @@ __global__ void __launch_bounds__(64, PKV_FP8_CTAS_PER_SM)
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
             // o is relative to r - 15, the sum of exponentials to m
-            const float rel = l > 0.f || l != l ? exp2f(st.r[e] - kPExp - st.m[e]) : 0.f;
+            const float rel = l > 0.f || l != l ? exp2f(st.r[e] - (float)kPExp - st.m[e]) : 0.f;
             float v[W];
 #pragma unroll
             for (int i = 0; i < W / 2; i++) {
@@ -719,13 +738,13 @@ F8Sizes f8_sizes(int S, int H, int Hkv, int D, int max_ctx, int partition_size) 
 }
 
 // The cache [NB][Hkv][B][D] of bytes as a 4-D tensor (innermost first); a box
-// is a row by min(B, 64) tokens of one (block, kv head), swizzled over rows.
+// is whole rows of min(B, a stage's) tokens of one (block, kv head), swizzled.
 bool encode_cache_map8(CUtensorMap *map, const void *base, int num_blocks, int Hkv, int B, int D) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)B, (cuuint64_t)Hkv, (cuuint64_t)(num_blocks > 0 ? num_blocks : 1)};
     const cuuint64_t strides[3] = {(cuuint64_t)D, (cuuint64_t)B * D, (cuuint64_t)Hkv * B * D};
-    const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(B < kTokens ? B : kTokens), 1u, 1u};
+    const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(B < kStageBytes / D ? B : kStageBytes / D), 1u, 1u};
     const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -734,9 +753,9 @@ bool encode_cache_map8(CUtensorMap *map, const void *base, int num_blocks, int H
 
 template <int D, bool WIDE, typename T> cudaError_t launch_decode8w(const F8Args &f, cudaStream_t stream) {
     auto kern = paged_attention_fp8_kernel<D, WIDE, T>;
-    const size_t smem = F8Layout<D>::bytes(f.a.num_seqs);
+    const size_t smem = F8Layout::total(f.a.num_seqs);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)F8Layout<D>::bytes(kLaunchSeqs));
+                                         (int)F8Layout::total(kLaunchSeqs));
     if (e != cudaSuccess) return e;
     CUtensorMap tmk, tmv;
     const AttnArgs &a = f.a;
@@ -744,11 +763,9 @@ template <int D, bool WIDE, typename T> cudaError_t launch_decode8w(const F8Args
         !encode_cache_map8(&tmv, a.v_cache, a.num_blocks, a.num_kv_heads, 1 << a.log2_block, D))
         return cudaErrorInvalidValue;
     const long long items = (long long)a.num_seqs * a.max_parts * a.num_kv_heads * a.head_tiles;
-    // resident CTAs: the sequence table's size may allow fewer than the registers do (228 KB per SM, 1 KB per CTA)
-    const long long fit = (long long)(228 * 1024 / (smem + 1024));
-    long long ctas = sm_count() * (fit < PKV_FP8_CTAS_PER_SM ? fit : (long long)PKV_FP8_CTAS_PER_SM);
-    if (ctas > items) ctas = items;
-    return launch(kern, dim3((unsigned)ctas), dim3(64), smem, stream, f, tmk, tmv);
+    long long ctas = (long long)sm_count() * PKV_FP8_CTAS_PER_SM;
+    if (ctas > items) ctas = items;                  // few items: one to a CTA
+    return launch(kern, dim3((unsigned)ctas), dim3(kPipes * 64), smem, stream, f, tmk, tmv);
 }
 
 template <int D, typename T> cudaError_t launch_decode8(const F8Args &f, cudaStream_t stream) {
@@ -888,8 +905,8 @@ pkv_status paged_attention_decode_fp8(void *out, const void *query, const void *
     if (num_seqs < 0 || num_seqs > 65535 || max_blocks_per_seq < 0 || num_blocks < 0)
         return fail(PKV_EINVAL, "%s: bad sizes (seqs %d, table width %d, blocks %d)", what, num_seqs, max_blocks_per_seq,
                     num_blocks);
-    if (partition_size < 0 || partition_size % kTokens)
-        return fail(PKV_EINVAL, "%s: partition_size %d not a multiple of %d", what, partition_size, kTokens);
+    if (partition_size < 0 || partition_size % kMaxTokens)
+        return fail(PKV_EINVAL, "%s: partition_size %d not a multiple of %d", what, partition_size, kMaxTokens);
     if (!std::isfinite(scale)) return fail(PKV_EINVAL, "%s: scale must be finite", what);
     const int64_t table_cap = (int64_t)max_blocks_per_seq * block_size;
     if (max_context_len < 0 || max_context_len > table_cap)
