@@ -471,15 +471,12 @@ def paged_attention_prefill_fp8_workspace_size(num_seqs: int, num_kv_heads: int,
                                                                  max_context_len))
 
 
-_FP8_WS_MIN = 256 + 65536 * 4              # ticket headers and merge counters
-
-
 def make_fp8_workspace(device, nbytes: int, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """A device buffer of at least nbytes, prepared for
     paged_attention_decode_fp8 and paged_attention_prefill_fp8.  Returns once
     the preparation has finished, so any stream may use the buffer."""
     dev = torch.device(device)
-    buf = torch.empty(max(nbytes, _FP8_WS_MIN), dtype=torch.uint8, device=dev)
+    buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     with _on(buf.device):
         _ck(load().paged_attention_fp8_workspace_init(buf.data_ptr(), buf.numel(), _stream(stream, buf.device)),
             "paged_attention_fp8_workspace_init")

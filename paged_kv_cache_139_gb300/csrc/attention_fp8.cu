@@ -32,7 +32,9 @@
 //     conflicts (see perm_token).
 // A CTA is four pipelines of a producer and a consumer warp, one consumer to
 // each of the SM's schedulers, two CTAs to an SM; each pipeline is persistent
-// over (sequence, partition, head tile) items that it claims by tickets.
+// over (sequence, partition, head tile) items that it claims by tickets.  The
+// partitions of a split context are merged by a second kernel: merging in this
+// one (a fence and an atomic per item) cost more than its launch.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -48,32 +50,26 @@
 namespace pkv {
 namespace {
 
-// Tuning knobs (compile-time): ring slots of a pipeline, resident CTAs per SM.
+// Tuning knob (compile-time): ring slots of a pipeline.
 #ifndef PKV_FP8_SLOTS
 #define PKV_FP8_SLOTS 3
 #endif
-#ifndef PKV_FP8_CTAS_PER_SM
-#define PKV_FP8_CTAS_PER_SM 2
-#endif
-
 constexpr int kPipes = 4;                   // pipelines of a CTA
+constexpr int kCtasPerSm = 2;
 constexpr int kStageBytes = 4096;           // a ring stage's K, and its V: 32 tokens at head_dim 128, 64 at 64
 constexpr int kMaxTokens = kStageBytes / 64;
 constexpr int kMinBlock = 4;
 constexpr int kStageBlocks = kMaxTokens / kMinBlock;
 constexpr int kTileHeads = 8;               // query heads per item at most: the products' columns
-constexpr int kLaunchSeqs = 1024;           // sequences per launch (their partitions are counted in shared memory)
-constexpr int kCounters = 65536;            // merge counters of a workspace
+constexpr int kLaunchSeqs = 512;            // sequences per launch (their lengths sit in shared memory)
 constexpr int kMaxSpread = 10;              // log2 of the largest over the least value scale, see above
 constexpr int kPExp = 15;                   // probabilities enter the product times 2^15 (fp16 reaches 2^16)
 
-// The workspace: two ticket headers (decode; the prompt phase at 128), the
-// merge counters, then what a call needs.  The counters' place depends on no
-// size, and every call leaves them at zero: calls of any sizes, captured or
-// not, may follow one another on a workspace.
+// The workspace: two ticket headers (decode; the prompt phase at 128), then
+// what a call needs.  Every call leaves the headers ready: calls of any sizes,
+// captured or not, may follow one another on a workspace.
 constexpr size_t kPrefillHeader = 128;
-constexpr size_t kCounterOff = kWsHeaderBytes;
-constexpr size_t kBodyOff = kCounterOff + kCounters * sizeof(unsigned int);
+constexpr size_t kBodyOff = kWsHeaderBytes;
 
 struct F8Args {
     AttnArgs a;
@@ -104,7 +100,7 @@ struct F8Layout {
     static constexpr uint32_t rest_bytes = bytes - q;
     static constexpr uint32_t misc = rest + kPipes * rest_bytes;
     static constexpr uint32_t seqs = misc + 64 * 4;
-    static size_t total(int S) { return seqs + (size_t)(S + 1) * sizeof(int); }
+    static size_t total(int S) { return seqs + (size_t)(2 * S + 1) * sizeof(int); }
     static_assert(q % 1024 == 0 && rest_bytes % 16 == 0, "swizzled rings, 16-byte copies");
 };
 
@@ -218,22 +214,23 @@ __device__ __forceinline__ void f8_load_q(uint32_t (&qb)[D / 16][2], float (&qf)
     }
 }
 
-// Thirty-two tokens from row `base` of a stage.  sc: the stage's block scales
-// (key scale * softmax scale * log2 e, value scale), a block per 2^log2_rows
-// tokens.
-template <int D, bool WIDE, bool FULL>
+// TOK tokens (a multiple of 32) from row `base` of a stage.  sc: the stage's
+// block scales (key scale * softmax scale * log2 e, value scale), a block per
+// 2^log2_rows tokens.
+template <int D, int TOK, bool WIDE, bool FULL>
 __device__ __forceinline__ void f8_consume(const unsigned char *Ks, const unsigned char *Vs, const float2 *sc,
-                                           int log2_rows, int base, int nvalid, int lane,
-                                           int range, const uint32_t (&qb)[D / 16][2], const float (&qf)[2],
-                                           F8State<D> &st) {
+                                           int log2_rows, int base, int nvalid, int lane, int range,
+                                           const uint32_t (&qb)[D / 16][2], const float (&qf)[2], F8State<D> &st) {
+    constexpr int NG = TOK / 8;                  // groups of eight tokens
     const int n = lane >> 2, c = lane & 3;
     const int pn = perm_token<D>(n), pe = perm_token<D>(2 * c), po = perm_token<D>(2 * c + 1);
     // S^T = K Q^T: sixteen tokens (rows lane / 4 and + 8) at a time
-    float s[2][4];
+    float x[NG][2], vs[NG];                      // this lane's tokens: row lane / 4 of the g-th group of eight
 #pragma unroll
-    for (int mt = 0; mt < 2; mt++) {
+    for (int mt = 0; mt < NG / 2; mt++) {
+        float s[4], s2[4];                       // two sums halve the chain of dependent products
 #pragma unroll
-        for (int e = 0; e < 4; e++) s[mt][e] = 0.f;
+        for (int e = 0; e < 4; e++) s[e] = s2[e] = 0.f;
         const int row = base + mt * 16 + pn;
 #pragma unroll
         for (int k = 0; k < D / 64; k++) {
@@ -242,41 +239,42 @@ __device__ __forceinline__ void f8_consume(const unsigned char *Ks, const unsign
             const uint32_t lo8[4] = {u.x, u.y, u.z, u.w}, hi8[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int ks = 0; ks < 4; ks++) {
-                const uint32_t a[4] = {e4m3x2_lo(lo8[ks]), e4m3x2_lo(hi8[ks]), e4m3x2_hi(lo8[ks]), e4m3x2_hi(hi8[ks])};
-                Mma<__half>::run(s[mt], a, qb[4 * k + ks][0], qb[4 * k + ks][1]);
+                const uint32_t a[4] = {e4m3x2_lo(lo8[ks]), e4m3x2_lo(hi8[ks]), e4m3x2_hi(lo8[ks]),
+                                       e4m3x2_hi(hi8[ks])};
+                Mma<__half>::run((ks & 1) ? s2 : s, a, qb[4 * k + ks][0], qb[4 * k + ks][1]);
             }
         }
-    }
-    // this lane's tokens g = 0 .. 3: row lane / 4 of the g-th group of eight
-    float x[4][2], vs[4];
 #pragma unroll
-    for (int g = 0; g < 4; g++) {
-        const int tok = base + g * 8 + pn;
-        const float2 f = sc[tok >> log2_rows];
-        vs[g] = f.y;
+        for (int i = 0; i < 2; i++) {
+            const int g = 2 * mt + i, tok = base + g * 8 + pn;
+            const float2 f = sc[tok >> log2_rows];
+            vs[g] = f.y;
 #pragma unroll
-        for (int e = 0; e < 2; e++) x[g][e] = s[g >> 1][(g & 1) * 2 + e] * (qf[e] * f.x);
-        if (!FULL && tok >= nvalid) {            // what stands past the context may be anything, its scales too
-            x[g][0] = x[g][1] = -INFINITY;
-            vs[g] = 0.f;
+            for (int e = 0; e < 2; e++) x[g][e] = (s[2 * i + e] + s2[2 * i + e]) * (qf[e] * f.x);
+            if (!FULL && tok >= nvalid) {        // what stands past the context may be anything, its scales too
+                x[g][0] = x[g][1] = -INFINITY;
+                vs[g] = 0.f;
+            }
         }
     }
     float mnew[2], alpha[2];
 #pragma unroll
     for (int e = 0; e < 2; e++) {
-        float mx = fmaxf(fmaxf(x[0][e], x[1][e]), fmaxf(x[2][e], x[3][e]));
+        float mx = x[0][e];
+#pragma unroll
+        for (int g = 1; g < NG; g++) mx = fmaxf(mx, x[g][e]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
         mnew[e] = fmaxf(st.m[e], mx);
         alpha[e] = ex2(st.m[e] - mnew[e]);
         st.m[e] = mnew[e];
     }
-    float rnew[2], w[4][2];
+    float rnew[2], w[NG][2];
     if (!(range & 1)) {                                         // uniform over the warp
         const int top = range >> 1 > -100 ? range >> 1 : -100;
         const float wscale = __uint_as_float((unsigned)(kPExp - top + 127) << 23);
 #pragma unroll
-        for (int g = 0; g < 4; g++) w[g][0] = w[g][1] = vs[g] * wscale;
+        for (int g = 0; g < NG; g++) w[g][0] = w[g][1] = vs[g] * wscale;
         rnew[0] = mnew[0] + (float)top;
         rnew[1] = mnew[1] + (float)top;
     } else {
@@ -284,20 +282,20 @@ __device__ __forceinline__ void f8_consume(const unsigned char *Ks, const unsign
         for (int e = 0; e < 2; e++) {
             float mx = -1e30f;                                  // finite: value scales of zero leave nothing
 #pragma unroll
-            for (int g = 0; g < 4; g++)
+            for (int g = 0; g < NG; g++)
                 if (vs[g] > 0.f && x[g][e] > -INFINITY) mx = fmaxf(mx, x[g][e] + log2f(vs[g]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
             rnew[e] = fmaxf(st.r[e], mx);
 #pragma unroll
-            for (int g = 0; g < 4; g++)
+            for (int g = 0; g < NG; g++)
                 w[g][e] = vs[g] > 0.f ? fminf(exp2f(log2f(vs[g]) - (rnew[e] - mnew[e]) + (float)kPExp), 0x1p100f) : 0.f;
         }
     }
     // the probabilities, and P^T as B fragments
-    uint32_t hi[4], lo[4];
+    uint32_t hi[NG], lo[NG];
 #pragma unroll
-    for (int g = 0; g < 4; g++) {
+    for (int g = 0; g < NG; g++) {
         const float p0 = ex2(x[g][0] - mnew[0]), p1 = ex2(x[g][1] - mnew[1]);
         st.l[0] = g == 0 ? fmaf(st.l[0], alpha[0], p0) : st.l[0] + p0;
         st.l[1] = g == 0 ? fmaf(st.l[1], alpha[1], p1) : st.l[1] + p1;
@@ -326,7 +324,7 @@ __device__ __forceinline__ void f8_consume(const unsigned char *Ks, const unsign
     }
     // O^T += V^T P^T: sixteen tokens a step; rows lane / 4 and + 8 of tile i are d = (D / 8) (lane / 4) + 2 i and + 1
 #pragma unroll
-    for (int kt = 0; kt < 2; kt++) {
+    for (int kt = 0; kt < NG / 2; kt++) {
         const int t = base + kt * 16;
         const int rows[4] = {t + pe, t + po, t + 8 + pe, t + 8 + po};
         uint32_t v[4][D / 32];
@@ -381,8 +379,8 @@ __device__ __forceinline__ void f8_scale_range(float2 sc, int &top, int &low) {
 }
 
 template <int TOKENS>
-__device__ __forceinline__ void f8_decode_item(const F8Args &f, const int *pref, int S, int tiles, unsigned int t,
-                                               int lane, F8Item &it) {
+__device__ __forceinline__ void f8_decode_item(const F8Args &f, const int *pref, const int *ctxs, int S, int tiles,
+                                               unsigned int t, int lane, F8Item &it) {
     const AttnArgs &a = f.a;
     const int pidx = (int)(t / (unsigned int)tiles);
     const int tile = (int)(t % (unsigned int)tiles);
@@ -398,8 +396,7 @@ __device__ __forceinline__ void f8_decode_item(const F8Args &f, const int *pref,
     const int group = a.num_heads / a.num_kv_heads, first = (tile % a.head_tiles) * f.tile;
     it.h0 = it.g * group + first;
     it.rows = group - first < f.tile ? group - first : f.tile;
-    int ctx = __ldg(a.ctx_lens + lo);
-    ctx = ctx < 0 ? 0 : ctx > a.max_ctx ? a.max_ctx : ctx;             // latched where the partitions are counted
+    const int ctx = ctxs[lo];
     it.tok0 = it.part * a.partition;
     const int ntok = ctx - it.tok0 < a.partition ? ctx - it.tok0 : a.partition;
     it.ntok = ntok < 0 ? 0 : ntok;
@@ -412,7 +409,7 @@ __device__ __forceinline__ void f8_decode_item(const F8Args &f, const int *pref,
 
 // WIDE: items of five to eight query heads.
 template <int D, bool WIDE, typename T>
-__global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
+__global__ void __launch_bounds__(kPipes * 64, kCtasPerSm)
     paged_attention_fp8_kernel(const F8Args f, const __grid_constant__ CUtensorMap tmk,
                                const __grid_constant__ CUtensorMap tmv) {
     using L = F8Layout;
@@ -430,8 +427,9 @@ __global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
     F8Meta *meta = reinterpret_cast<F8Meta *>(rest + L::meta);
     int &cta_flags = *reinterpret_cast<int *>(smem8 + L::misc);
     int *scan_tmp = reinterpret_cast<int *>(smem8 + L::misc) + 32;
-    int *pref = reinterpret_cast<int *>(smem8 + L::seqs);            // [S + 1] partitions before s
     const int S = a.num_seqs;
+    int *pref = reinterpret_cast<int *>(smem8 + L::seqs);            // [S + 1] partitions before s
+    int *ctxs = pref + S + 1;                                        // [S]
     const int tiles = a.num_kv_heads * a.head_tiles;
     WsHeader *hdr = a.hdr;
 
@@ -442,25 +440,51 @@ __global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
         }
         fence_mbar_init();
     }
+    if (warp == kPipes && lane < 2) prefetch_tensor_map(lane ? &tmv : &tmk);
     pdl_trigger();
     pdl_wait();
-    if (threadIdx.x == 0)
-        cta_flags = (timed_out(a.st) ? 1 : 0) | (hdr->magic != kWsMagic8 ? 2 : 0) | ((smem_u32(smem8) & 1023u) ? 4 : 0);
-    for (int i = threadIdx.x; i < S; i += blockDim.x) {
-        int c = a.ctx_lens[i];
-        if (c < 0 || c > a.max_ctx) {
-            if (blockIdx.x == 0) latch(a.st, kFlagBadContext, c);
-            c = c < 0 ? 0 : a.max_ctx;
-        }
-        pref[i + 1] = c > 0 ? (c + a.partition - 1) / a.partition : 1;
+    // every thread counts the partitions of its sequences, neighbouring ones, and what stands before them
+    static_assert(kLaunchSeqs <= 2 * kPipes * 64, "two sequences to a thread");
+    int ctx[2], parts[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int q = 2 * (int)threadIdx.x + i;
+        ctx[i] = q < S ? a.ctx_lens[q] : 0;
     }
+    if (threadIdx.x == 0) {
+        const unsigned magic = hdr->magic;
+        cta_flags = (timed_out(a.st) ? 1 : 0) | (magic != kWsMagic8 ? 2 : 0) | ((smem_u32(smem8) & 1023u) ? 4 : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int q = 2 * (int)threadIdx.x + i;
+        if (ctx[i] < 0 || ctx[i] > a.max_ctx) {
+            if (blockIdx.x == 0) latch(a.st, kFlagBadContext, ctx[i]);
+            ctx[i] = ctx[i] < 0 ? 0 : a.max_ctx;
+        }
+        parts[i] = q >= S ? 0 : ctx[i] > 0 ? (ctx[i] + a.partition - 1) / a.partition : 1;
+        if (q < S) ctxs[q] = ctx[i];
+    }
+    int upto = parts[0] + parts[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (lane == 31) scan_tmp[warp] = upto;
     __syncthreads();
     if (cta_flags) {                                   // uniform over the CTA
         if ((cta_flags & 2) && blockIdx.x == 0 && threadIdx.x == 0) latch(a.st, kFlagBadWorkspace, hdr->magic);
         if ((cta_flags & 4) && blockIdx.x == 0 && threadIdx.x == 0) latch(a.st, kFlagTimeout, -2);
         return;
     }
-    block_prefix_sum(pref, S, scan_tmp);
+#pragma unroll
+    for (int w = 0; w < 2 * kPipes - 1; w++)
+        if (w < warp) upto += scan_tmp[w];
+    if (2 * (int)threadIdx.x < S) pref[2 * threadIdx.x + 1] = upto - parts[1];
+    if (2 * (int)threadIdx.x + 1 < S) pref[2 * threadIdx.x + 2] = upto;
+    if (threadIdx.x == 0) pref[0] = 0;
+    __syncthreads();
     const unsigned int N = (unsigned int)pref[S] * (unsigned int)tiles;
     const int B = 1 << a.log2_block;
     constexpr int kLog2Tokens = TOKENS == 64 ? 6 : 5;
@@ -468,6 +492,9 @@ __global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
 
     if (warp >= kPipes) {
         // ---------------- producer: tickets -> items -> tiled copies ----------------
+        // At head_dim 128 the consumers' four warps take registers that these four give up: 72 + 184 =
+        // 2 x 128, the launch's own (256 threads of 128, two CTAs to an SM).
+        if constexpr (D >= 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const T *qg = static_cast<const T *>(a.q);
         const int rows_per_copy = 1 << log2_rows;
         const int cps = TOKENS >> log2_rows;                         // blocks per stage
@@ -479,7 +506,7 @@ __global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
         unsigned int cur_t = (unsigned int)pipe * gridDim.x + blockIdx.x;
         F8Item cur, nx;
         if (cur_t < N) {
-            f8_decode_item<TOKENS>(f, pref, S, tiles, cur_t, lane, cur);
+            f8_decode_item<TOKENS>(f, pref, ctxs, S, tiles, cur_t, lane, cur);
             cur.sc = f8_load_scales(f, cur.g, cur.ent);
         }
         int kk = 0, first = -R;                                      // stages so far, the last item's first one
@@ -495,7 +522,7 @@ __global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
                     if (lane == 0) nxt_raw = pipes + atomicAdd(&hdr->next, 1u);
                 } else if (step == 1) {
                     nxt_t = __shfl_sync(kFull, nxt_raw, 0);
-                    if (nxt_t < N) f8_decode_item<TOKENS>(f, pref, S, tiles, nxt_t, lane, nx);
+                    if (nxt_t < N) f8_decode_item<TOKENS>(f, pref, ctxs, S, tiles, nxt_t, lane, nx);
                 } else {
                     if (nxt_t < N) nx.sc = f8_load_scales(f, nx.g, nx.ent);
                 }
@@ -596,6 +623,7 @@ __global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
     }
 
     // ---------------- consumer ----------------
+    if constexpr (D >= 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     uint32_t qb[D / 16][2];
     float qf[2] = {1.f, 1.f};
     F8State<D> st;
@@ -613,9 +641,7 @@ __global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
         const float2 *sc = scs + slot * kStageBlocks;
         if ((md.flags & kFirst) && md.nvalid > 0) f8_load_q<D, WIDE, T>(qb, qf, qs, md.rows, lane);
         if (md.nvalid == TOKENS) {
-#pragma unroll 1
-            for (int base = 0; base < TOKENS; base += 32)
-                f8_consume<D, WIDE, true>(Ks, Vs, sc, log2_rows, base, TOKENS, lane, md.range, qb, qf, st);
+            f8_consume<D, TOKENS, WIDE, true>(Ks, Vs, sc, log2_rows, 0, TOKENS, lane, md.range, qb, qf, st);
         } else if (md.nvalid > 0) {
             // rows past the context may hold anything: zero them in V (0 * NaN would poison the sum)
             const int end = (md.nvalid + 31) & ~31;
@@ -624,7 +650,7 @@ __global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
             __syncwarp();
 #pragma unroll 1
             for (int base = 0; base < md.nvalid; base += 32)
-                f8_consume<D, WIDE, false>(Ks, Vs, sc, log2_rows, base, md.nvalid, lane, md.range, qb, qf, st);
+                f8_consume<D, 32, WIDE, false>(Ks, Vs, sc, log2_rows, base, md.nvalid, lane, md.range, qb, qf, st);
             fence_proxy_async_smem();            // the zeroed rows, before TMA refills the slot
         }
         __syncwarp();
@@ -677,24 +703,25 @@ __global__ void __launch_bounds__(kPipes * 64, PKV_FP8_CTAS_PER_SM)
                 }
             }
         }
-        if (a.fused_merge && md.nparts > 1) {
-            // count this partition in; the one that completes the set merges it
-            __threadfence();
-            __syncwarp();
-            unsigned int done = 0;
-            const int g = md.h0 / (a.num_heads / a.num_kv_heads);
-            const int tile = g * a.head_tiles + (md.h0 - g * (a.num_heads / a.num_kv_heads)) / f.tile;
-            unsigned int *cnt = a.cnt + (size_t)md.s * tiles + tile;
-            if (lane == 0) done = atomicAdd(cnt, 1u);
-            done = __shfl_sync(kFull, done, 0);
-            if (done == (unsigned int)md.nparts - 1) {
-                __threadfence();
-                merge_partitions_warp<D, T>(a, md.s, md.h0, md.rows, md.nparts, lane);
-                if (lane == 0) *cnt = 0u;
-            }
-        }
         f8_reset(st);
     }
+}
+
+// Merge the partitions of split contexts, a warp to a (sequence, head); for
+// splits of up to 32 partitions (partition_reduce_kernel takes longer ones).
+constexpr int kMergeThreads = 128;
+constexpr int kMergeParts = 32;
+
+template <int D, typename T> __global__ void __launch_bounds__(kMergeThreads) fp8_merge_kernel(const AttnArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int row = (int)((blockIdx.x * (unsigned)kMergeThreads + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    if (row >= a.num_seqs * a.num_heads) return;
+    const int s = row / a.num_heads;
+    int ctx = a.ctx_lens[s];
+    ctx = ctx < 0 ? 0 : ctx > a.max_ctx ? a.max_ctx : ctx;
+    const int np = (ctx + a.partition - 1) / a.partition;
+    if (np > 1) merge_partitions_warp<D, T>(a, s, row - s * a.num_heads, 1, np, lane);
 }
 
 __global__ void fp8_workspace_init_kernel(uint4 *ws, size_t n16) {
@@ -763,13 +790,19 @@ template <int D, bool WIDE, typename T> cudaError_t launch_decode8w(const F8Args
         !encode_cache_map8(&tmv, a.v_cache, a.num_blocks, a.num_kv_heads, 1 << a.log2_block, D))
         return cudaErrorInvalidValue;
     const long long items = (long long)a.num_seqs * a.max_parts * a.num_kv_heads * a.head_tiles;
-    long long ctas = (long long)sm_count() * PKV_FP8_CTAS_PER_SM;
+    long long ctas = (long long)sm_count() * kCtasPerSm;
     if (ctas > items) ctas = items;                  // few items: one to a CTA
     return launch(kern, dim3((unsigned)ctas), dim3(kPipes * 64), smem, stream, f, tmk, tmv);
 }
 
 template <int D, typename T> cudaError_t launch_decode8(const F8Args &f, cudaStream_t stream) {
-    return f.tile > 4 ? launch_decode8w<D, true, T>(f, stream) : launch_decode8w<D, false, T>(f, stream);
+    cudaError_t e = f.tile > 4 ? launch_decode8w<D, true, T>(f, stream) : launch_decode8w<D, false, T>(f, stream);
+    if (e != cudaSuccess || f.a.max_parts <= 1) return e;
+    const unsigned rows = (unsigned)f.a.num_seqs * (unsigned)f.a.num_heads;      // <= kLaunchSeqs heads
+    if (f.a.max_parts <= kMergeParts)
+        return launch(fp8_merge_kernel<D, T>, dim3((rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32)),
+                      dim3(kMergeThreads), 0, stream, f.a);
+    return launch_reduce<T>(D, f.a, dim3((unsigned)f.a.num_heads, (unsigned)f.a.num_seqs), stream);
 }
 
 // ---- the prompt phase ------------------------------------------------------------
@@ -931,7 +964,6 @@ pkv_status paged_attention_decode_fp8(void *out, const void *query, const void *
     std::memset(&f, 0, sizeof f);
     AttnArgs &a = f.a;
     a.hdr = reinterpret_cast<WsHeader *>(ws);
-    a.cnt = reinterpret_cast<unsigned int *>(ws + kCounterOff);
     a.k_cache = key_cache;
     a.v_cache = value_cache;
     a.st = st;
@@ -960,20 +992,12 @@ pkv_status paged_attention_decode_fp8(void *out, const void *query, const void *
         a.ws_m = reinterpret_cast<float *>(ws + z.m_off) + part;
         a.ws_l = reinterpret_cast<float *>(ws + z.l_off) + part;
         a.ws_o = reinterpret_cast<float *>(ws + z.o_off) + part * head_dim;
-        a.fused_merge = z.MP > 1 && z.MP <= kFusedMaxParts &&
-                        (long long)S * num_kv_heads * z.head_tiles <= kCounters;
         cudaError_t e;
         if (head_dim == 128)
             e = dtype == PKV_F16 ? launch_decode8<128, __half>(f, stream) : launch_decode8<128, __nv_bfloat16>(f, stream);
         else
             e = dtype == PKV_F16 ? launch_decode8<64, __half>(f, stream) : launch_decode8<64, __nv_bfloat16>(f, stream);
         if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));
-        if (z.MP > 1 && !a.fused_merge) {
-            const dim3 rgrid((unsigned)num_heads, (unsigned)S);
-            e = dtype == PKV_F16 ? launch_reduce<__half>(head_dim, a, rgrid, stream)
-                                 : launch_reduce<__nv_bfloat16>(head_dim, a, rgrid, stream);
-            if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: reduce launch: %s", what, cudaGetErrorString(e));
-        }
     }
     return PKV_OK;
 }

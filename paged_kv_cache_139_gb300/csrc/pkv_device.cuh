@@ -164,6 +164,11 @@ __device__ __forceinline__ uint64_t policy_evict_last() {
 
 // ---- tiled (tensor-map) TMA copy ------------------------------------------
 
+// Requests the descriptor ahead of the first copy through it.
+__device__ __forceinline__ void prefetch_tensor_map(const void *tmap) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+
 // A 3-D box at coordinates (x, y, z) (innermost first); x * element size a
 // multiple of 16 bytes.
 __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, int x, int y, int z, uint64_t *bar,

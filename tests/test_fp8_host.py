@@ -80,7 +80,7 @@ def _decode(**over):
 @pytest.mark.parametrize("over", [
     dict(d=96), dict(d=256), dict(B=12), dict(B=2), dict(B=256), dict(H=5), dict(H=0), dict(Hkv=0), dict(part=32), dict(part=-64),
     dict(mcl=65), dict(mcl=-1), dict(dt=2), dict(S=-1), dict(S=65536), dict(NB=-1), dict(mb=-1), dict(out=None), dict(q=None),
-    dict(kc=None), dict(sc=None), dict(bt=None), dict(cl=None), dict(q=18), dict(sc=8), dict(ws=None), dict(ws=24), dict(wsb=1000),
+    dict(kc=None), dict(sc=None), dict(bt=None), dict(cl=None), dict(q=18), dict(sc=8), dict(ws=None), dict(ws=24), dict(wsb=128),
     dict(scale=float("nan")), dict(scale=float("inf")), dict(mb=1 << 24, part=64),
 ])
 def test_decode_refusals(over):
@@ -99,7 +99,7 @@ def _prefill(**over):
     dict(d=96), dict(B=12), dict(B=2), dict(B=256), dict(H=5), dict(Hkv=0), dict(dt=2), dict(S=-1), dict(S=65536), dict(T=-1),
     dict(mql=-1), dict(mcl=-1), dict(mcl=65), dict(mb=0), dict(mb=-1), dict(mb=1 << 28), dict(NB=0), dict(NB=-1), dict(scale=0.0),
     dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(out=None), dict(qst=None), dict(sc=None),
-    dict(kc=18), dict(ws=None), dict(ws=24), dict(wsb=1000),
+    dict(kc=18), dict(ws=None), dict(ws=24), dict(wsb=128),
 ])
 def test_prefill_refusals(over):
     assert _prefill(**over) == 1
@@ -107,7 +107,7 @@ def test_prefill_refusals(over):
 
 def test_workspace_sizes():
     size = pkv.paged_attention_decode_fp8_workspace_size
-    head = 256 + 4 * 65536
+    head = 256
     assert size(2, 4, 2, 128, 64, 64) == head == size(2, 4, 2, 128, 0, 0)
     r = lambda x: (x + 255) // 256 * 256  # noqa: E731
     n = 8 * 32 * (32768 // 512)

@@ -128,6 +128,14 @@ def test_decode_queries_of_all_sizes(cuda_device):
         out = c.decode(q=q, scale=2.0 ** (-3 - q_exp))
         pkv.check()
         c.check(out, q=q, scale=2.0 ** (-3 - q_exp))
+    for what in (math.inf, -math.inf, math.nan):                 # one head of one sequence: its row alone is NaN
+        q = c.q.clone()
+        q[1, 2, 7] = what
+        out = c.decode(q=q)
+        bad = out.isnan()
+        assert bool(bad[1, 2].all()) and int(bad.sum()) == c.d
+        out[1, 2] = c.decode()[1, 2]
+        c.check(out)
     z = c.decode(q=torch.zeros_like(c.q))
     c.check(z, q=torch.zeros_like(c.q))
 
@@ -209,7 +217,7 @@ def test_workspaces_of_the_other_kind_are_refused(cuda_device):
             pkv.check()
         assert e.value.status_name == "PKV_EINVAL" and "workspace" in str(e.value)
     with pytest.raises(pkv.PkvError):
-        c.decode(workspace=pkv.make_fp8_workspace(cuda_device, 0)[:1024])
+        c.decode(workspace=pkv.make_fp8_workspace(cuda_device, 0)[:128])
     # an 8-bit workspace does not serve the 16-bit calls either
     q = torch.zeros(1, 2, 64, dtype=torch.float16, device=cuda_device)
     kc = torch.zeros(8, 1, 16, 64, dtype=torch.float16, device=cuda_device)
