@@ -614,6 +614,34 @@ template <int D, int G, typename T, bool MMA> struct PLayout {
     static size_t bytes(int S) { return seqs + (size_t)(2 * S + 1) * sizeof(int); }
 };
 
+// In place: v[1..n] := inclusive prefix sums of v[1..n]; v[0] := 0.
+// warp_tot: shared scratch of one int per warp.
+__device__ __forceinline__ void block_prefix_sum(int *v, int n, int *warp_tot) {
+    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int chunk = (n + nt - 1) / nt;
+    const int b0 = tid * chunk < n ? tid * chunk : n;
+    const int b1 = b0 + chunk < n ? b0 + chunk : n;
+    int sum = 0;
+    for (int i = b0; i < b1; i++) sum += v[i + 1];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_tot[wid] = incl;
+    __syncthreads();
+    int off = 0;
+    for (int w = 0; w < wid; w++) off += warp_tot[w];
+    int run = off + incl - sum;
+    for (int i = b0; i < b1; i++) {
+        run += v[i + 1];
+        v[i + 1] = run;
+    }
+    if (tid == 0) v[0] = 0;
+    __syncthreads();
+}
+
 // A work item as the producer sees it.  ent holds, on lane j, block-table
 // entry win + j of the item's sequence (-1 past its blocks).
 struct Item {

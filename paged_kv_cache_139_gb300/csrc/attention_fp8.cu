@@ -735,12 +735,22 @@ __global__ void fp8_workspace_init_kernel(uint4 *ws, size_t n16) {
     ws[i] = v;
 }
 
-// A work item's bytes: 64 to 1024 tokens.  Long items cost less to begin and
-// leave fewer partials; short ones fill the GPU and end together.
-int choose_partition8(int partition_size, int num_seqs, int items_per_partition, int max_ctx) {
+// Tokens per partition.  A GPU of 152 SMs has 1216 pipelines.  Where that many
+// items hold everything, the shortest partitions that do so end first (1 x
+// 8,000 tokens, 8 kv heads: 11.4 us at 64 tokens, 13.9 at 256); beyond, 256
+// tokens (512 of head_dim 64) keep the items' beginnings and ends small beside
+// them and their last round short (64 x up to 2,000 tokens, 8 kv heads: 30.0 us
+// at 256, 32.5 at 128, 43.5 at 1024); and calls of so many items that rounds no
+// longer matter take longer ones, which leave fewer partials (256 x up to 4,096
+// tokens, 32 kv heads: 630 us at 1024, 659 at 256).
+int choose_partition8(int partition_size, int num_seqs, int tiles, int head_dim, int max_ctx) {
     if (partition_size > 0) return partition_size;
-    int P = 1024;
-    while (P > 128 && (long long)num_seqs * items_per_partition * parts_for(max_ctx, P) < 8192) P /= 2;
+    constexpr long long kPipelines = 1216;
+    const long long n = (long long)num_seqs * tiles;
+    for (int P = 64; P <= 256; P *= 2)
+        if (n * parts_for(max_ctx, P) <= kPipelines) return P;
+    int P = head_dim >= 128 ? 256 : 512;
+    while (P < 1024 && n * parts_for(max_ctx, 2 * P) >= 24 * kPipelines) P *= 2;
     return P;
 }
 
@@ -754,7 +764,7 @@ F8Sizes f8_sizes(int S, int H, int Hkv, int D, int max_ctx, int partition_size) 
     const int group = H / Hkv;
     z.head_tiles = (group + kTileHeads - 1) / kTileHeads;
     z.tile = (group + z.head_tiles - 1) / z.head_tiles;
-    z.P = choose_partition8(partition_size, S, Hkv * z.head_tiles, max_ctx);
+    z.P = choose_partition8(partition_size, S, Hkv * z.head_tiles, D, max_ctx);
     z.MP = parts_for(max_ctx, z.P);
     const size_t n = z.MP > 1 ? (size_t)S * H * z.MP : 0;
     z.m_off = kBodyOff;

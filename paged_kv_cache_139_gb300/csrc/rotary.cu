@@ -81,7 +81,8 @@ struct RopeArgs {
     int num_tokens, num_heads, num_kv_heads;
     int rot, num_positions, log2_block;
     int q_ctas;                    // 8-bit append: CTAs that rotate queries (after the others)
-    int tokens_per_cta, head_split;   // 8-bit append: tokens of a CTA, CTAs that share their heads
+    int head_split;                // 8-bit append of few tokens: CTAs that share a token's heads
+    int group_heads;               // 8-bit append of many: kv heads of a CTA
 };
 
 // A thread's unit of a head: sixteen elements as two 16-byte chunks that
@@ -251,79 +252,27 @@ __device__ __forceinline__ bool was_written(const Run &run, int off) {
     return (w >> (off & 31)) & 1u;
 }
 
-// The rows of run [t, t + run.n) of one kv head, keys or values, into block
-// blk, by one warp: D/16 lanes to a row.  A pass over the rows takes their
-// largest magnitude, the block gets its scale, and a second pass writes the
-// codes; a run of up to 16 rows stays in registers between the two.
-template <int D, typename T, bool INTERLEAVED>
-__device__ __forceinline__ void append8_rows(const RopeArgs &a, int t, const Run &run, int64_t blk, int h, bool isv,
-                                             int lane) {
-    constexpr int UPR = D / 16;            // lanes per row
-    constexpr int RP = 32 / UPR;           // rows side by side
-    constexpr int CH = 16 / RP;            // rows per lane and chunk of 16
+// The block's scale for new rows of magnitude up to amax (any lane's), stored;
+// the block's other rows are rounded again where it grows.  By one warp.
+template <int D>
+__device__ __forceinline__ float grow_scale(const RopeArgs &a, const Run &run, int64_t blk, int h, bool isv, float amax,
+                                            unsigned char *rows, int lane) {
+    constexpr int UPR = D / 16, RP = 32 / UPR;
     const int r = lane / UPR, u = lane % UPR;
-    const int rot = isv ? 0 : a.rot;
-    const Unit x = unit_at<INTERLEAVED>(u, rot);
-    const T *src = (isv ? static_cast<const T *>(a.v) : static_cast<const T *>(a.k)) + h * D;
-    const int64_t stride = isv ? a.v_stride : a.k_stride;
-    const int B = 1 << a.log2_block;
-    float y[CH][16];
-
-    auto load = [&](int base) {
-        uint4 ra[CH], rb[CH];
-#pragma unroll
-        for (int i = 0; i < CH; i++) {
-            const int row = base + i * RP + r;
-            ra[i] = rb[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < run.n) {
-                const T *p = src + (t + row) * stride;
-                ra[i] = *reinterpret_cast<const uint4 *>(p + x.a);
-                rb[i] = *reinterpret_cast<const uint4 *>(p + x.b);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < CH; i++) {
-            widen<T>(y[i], ra[i], rb[i]);
-            const int row = base + i * RP + r;
-            if (x.rotated && row < run.n) {
-                const int pos = a.positions[t + row];
-                if (pos >= 0 && pos < a.num_positions) {    // others are latched by the caller
-                    float4 cs[4];
-                    load_cos_sin(cs, a, pos, u);
-                    turn<INTERLEAVED>(y[i], cs);
-                }
-            }
-        }
-    };
-
-    // the largest finite magnitude; fmaxf passes NaN over
-    float amax = 0.f;
-    for (int base = 0; base < run.n; base += 16) {
-        load(base);
-#pragma unroll
-        for (int i = 0; i < CH; i++)
-#pragma unroll
-            for (int e = 0; e < 16; e++) amax = fmaxf(amax, fabsf(y[i][e]));
-    }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    amax = fminf(amax, 3.4028235e38f);
-
+    amax = fminf(amax, 3.4028235e38f);             // infinities; fmaxf has passed NaN over
     // a write at offset 0 starts the block anew; otherwise its scale can only grow
     const bool fresh = run.written[0] & 1u;
     float *sp = a.scales + ((size_t)blk * scale_heads(a.num_kv_heads) + h) * 2 + (isv ? 1 : 0);
-    const float need = pow2_scale(amax);
     const float had = fresh ? 0.f : *sp;
-    const float scale = fmaxf(had, need);
-    unsigned char *rows = static_cast<unsigned char *>(isv ? a.v_cache : a.k_cache) +
-                          ((size_t)(blk * a.num_kv_heads + h) << a.log2_block) * D;
+    const float scale = fmaxf(had, pow2_scale(amax));
     if (!fresh && scale != had) {
-        // the scale grew: the block's other rows are rounded again under it
         const float ratio = __fdiv_rn(had, scale);
-        for (int o = r; o < B; o += RP) {
+        for (int o = r; o < 1 << a.log2_block; o += RP) {
             if (was_written(run, o)) continue;
-            uint4 *p = reinterpret_cast<uint4 *>(rows + (size_t)o * D) + u;
-            const uint4 w = *p;
+            uint4 *q = reinterpret_cast<uint4 *>(rows + (size_t)o * D) + u;
+            const uint4 w = *q;
             const uint32_t in[4] = {w.x, w.y, w.z, w.w};
             uint32_t out[4];
 #pragma unroll
@@ -333,42 +282,137 @@ __device__ __forceinline__ void append8_rows(const RopeArgs &a, int t, const Run
                 const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
                 out[j] = to_e4m3x4(f.x * ratio, f.y * ratio, g.x * ratio, g.y * ratio);
             }
-            *p = make_uint4(out[0], out[1], out[2], out[3]);
+            *q = make_uint4(out[0], out[1], out[2], out[3]);
         }
     }
     __syncwarp();
     if (lane == 0) *sp = scale;
+    return scale;
+}
 
-    // the reciprocal of a power of two is exact; a caller's own scale may be another number
-    const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0u;
-    const float inv = 1.f / scale;
-    for (int base = 0; base < run.n; base += 16) {
-        if (run.n > 16) load(base);
+// A unit's codes under `scale` into its row.  The reciprocal of a power of two
+// is exact; a caller's own scale may be another number.
+__device__ __forceinline__ void store_codes(unsigned char *row, const Unit &x, float (&f)[16], float scale) {
+    if ((__float_as_uint(scale) & 0x7fffffu) == 0u && scale < 0x1p126f) {
+        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(scale));   // 2^-e
 #pragma unroll
-        for (int i = 0; i < CH; i++) {
-            const int row = base + i * RP + r;
-            if (row >= run.n) continue;
-            const int off = (int)(a.slots[t + row] & (B - 1));
-            float *f = y[i];
-            if (pow2) {
+        for (int e = 0; e < 16; e++) f[e] *= inv;
+    } else {
 #pragma unroll
-                for (int e = 0; e < 16; e++) f[e] *= inv;
-            } else {
+        for (int e = 0; e < 16; e++) f[e] = __fdiv_rn(f[e], scale);
+    }
+    *reinterpret_cast<uint2 *>(row + x.a) =
+        make_uint2(to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
+    *reinterpret_cast<uint2 *>(row + x.b) =
+        make_uint2(to_e4m3x4(f[8], f[9], f[10], f[11]), to_e4m3x4(f[12], f[13], f[14], f[15]));
+}
+
+// A lane's rows of a chunk of sixteen rows of a run: their offsets in the block
+// (-1: none) and positions (-1: not to be rotated).
+template <int CH> struct RowPlan {
+    int off[CH], pos[CH];
+};
+
+template <int RP, int CH>
+__device__ __forceinline__ void plan_rows(RowPlan<CH> &p, const RopeArgs &a, int t, int n, int base, int r) {
 #pragma unroll
-                for (int e = 0; e < 16; e++) f[e] = __fdiv_rn(f[e], scale);
-            }
-            unsigned char *p = rows + (size_t)off * D;
-            *reinterpret_cast<uint2 *>(p + x.a) =
-                make_uint2(to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
-            *reinterpret_cast<uint2 *>(p + x.b) =
-                make_uint2(to_e4m3x4(f[8], f[9], f[10], f[11]), to_e4m3x4(f[12], f[13], f[14], f[15]));
+    for (int i = 0; i < CH; i++) {
+        const int row = base + i * RP + r;
+        p.off[i] = p.pos[i] = -1;
+        if (row < n) {
+            p.off[i] = (int)(a.slots[t + row] & ((1 << a.log2_block) - 1));
+            const int pos = a.rot ? a.positions[t + row] : -1;
+            if (pos >= 0 && pos < a.num_positions) p.pos[i] = pos;    // others are latched by the caller
         }
     }
 }
 
-// The first CTAs append: each looks over tokens_per_cta tokens for those that
-// begin a run, and its warps take (run, kv head, keys or values) in turn.
-// The CTAs after them rotate queries, a thread to a unit.
+// The rows of run [t, t + run.n) of one kv head, keys or values, into block
+// blk, by one warp: D/16 lanes to a row.  A pass over the rows takes their
+// largest magnitude, the block gets its scale, and a second pass writes the
+// codes; `plan` is that of the first sixteen rows, and a run of so many stays
+// in registers between the two.
+template <int D, typename T, bool INTERLEAVED>
+__device__ __forceinline__ void append8_rows(const RopeArgs &a, int t, const Run &run,
+                                             const RowPlan<D / 32> &plan, int64_t blk, int h, bool isv, int lane) {
+    constexpr int UPR = D / 16;            // lanes per row
+    constexpr int RP = 32 / UPR;           // rows side by side
+    constexpr int CH = 16 / RP;            // rows per lane and chunk of 16
+    const int r = lane / UPR, u = lane % UPR;
+    const Unit x = unit_at<INTERLEAVED>(u, isv ? 0 : a.rot);
+    const T *src = (isv ? static_cast<const T *>(a.v) : static_cast<const T *>(a.k)) + h * D;
+    const int64_t stride = isv ? a.v_stride : a.k_stride;
+    RowPlan<CH> p = plan;
+    float y[CH][16];
+
+    auto load = [&](int base) {
+        uint4 ra[CH], rb[CH];
+#pragma unroll
+        for (int i = 0; i < CH; i++) {
+            ra[i] = rb[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.off[i] >= 0) {
+                const T *q = src + (t + base + i * RP + r) * stride;
+                ra[i] = *reinterpret_cast<const uint4 *>(q + x.a);
+                rb[i] = *reinterpret_cast<const uint4 *>(q + x.b);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CH; i++) {
+            widen<T>(y[i], ra[i], rb[i]);
+            if (x.rotated && p.pos[i] >= 0) {
+                float4 cs[4];
+                load_cos_sin(cs, a, p.pos[i], u);
+                turn<INTERLEAVED>(y[i], cs);
+            }
+        }
+    };
+
+    float amax = 0.f;
+    for (int base = 0; base < run.n; base += 16) {
+        if (base > 0) plan_rows<RP, CH>(p, a, t, run.n, base, r);
+        load(base);
+#pragma unroll
+        for (int i = 0; i < CH; i++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) amax = fmaxf(amax, fabsf(y[i][e]));
+    }
+    unsigned char *rows = static_cast<unsigned char *>(isv ? a.v_cache : a.k_cache) +
+                          ((size_t)(blk * a.num_kv_heads + h) << a.log2_block) * D;
+    const float scale = grow_scale<D>(a, run, blk, h, isv, amax, rows, lane);
+
+    for (int base = 0; base < run.n; base += 16) {
+        if (run.n > 16) {
+            plan_rows<RP, CH>(p, a, t, run.n, base, r);
+            load(base);
+        }
+#pragma unroll
+        for (int i = 0; i < CH; i++)
+            if (p.off[i] >= 0) store_codes(rows + (size_t)p.off[i] * D, x, y[i], scale);
+    }
+}
+
+// A run begins at a token in the pool whose predecessor is not of its block.
+// Returns that block, or -1.
+__device__ __forceinline__ int64_t leads_run(const RopeArgs &a, int t, bool tells) {
+    const int64_t s = a.slots[t];
+    if (s < 0) return -1;                                  // padding token
+    if (a.rot && tells) checked_position(a, t, a.num_heads == 0);
+    if (s >= a.num_slots) {
+        if (tells) latch(a.st, kFlagBadSlot, s);
+        return -1;
+    }
+    const int64_t blk = s >> a.log2_block;
+    if (t > 0) {
+        const int64_t before = a.slots[t - 1];
+        if (before >= 0 && before < a.num_slots && (before >> a.log2_block) == blk) return -1;
+    }
+    return blk;
+}
+
+// Few tokens (a decode step): the first CTAs append, head_split to a token,
+// their warps taking (kv head, keys or values) in turn; the CTAs after them
+// rotate queries, a thread to a unit.  Bound by latency: everything that a
+// token needs is requested as early as its address is known.
 template <int D, typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rotary_append8_kernel(const RopeArgs a) {
     constexpr int UPR = D / 16;
@@ -384,37 +428,245 @@ __global__ void __launch_bounds__(kRopeThreads) rotary_append8_kernel(const Rope
         const int t = (int)t64;
         const int r = (int)(i - t64 * per_token);
         const int row = r / UPR;
-        const int pos = a.rot ? checked_position(a, t, r == 0) : 0;
+        const int pos = checked_position(a, t, r == 0);
         if (pos < 0) return;
         rotate_row<T, INTERLEAVED>(a, static_cast<const T *>(a.q) + t * a.q_stride + row * D,
                                    static_cast<T *>(a.q_out) + ((size_t)t * a.num_heads + row) * D, r % UPR, pos);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x % a.head_split;
-    const int first = (int)(blockIdx.x / a.head_split) * a.tokens_per_cta;
-    const int last = first + a.tokens_per_cta < a.num_tokens ? first + a.tokens_per_cta : a.num_tokens;
-    const bool tells = split == 0 && warp == 0 && lane == 0;
-    for (int t = first; t < last; t++) {
-        const int64_t s = a.slots[t];
-        if (s < 0) continue;                               // padding token
-        if (a.rot && tells) checked_position(a, t, a.num_heads == 0);
-        if (s >= a.num_slots) {
-            if (tells) latch(a.st, kFlagBadSlot, s);
-            continue;
+    const int split = blockIdx.x % a.head_split, t = (int)(blockIdx.x / a.head_split);
+    const int64_t blk = leads_run(a, t, split == 0 && warp == 0 && lane == 0);
+    if (blk < 0) return;
+    const Run run = find_run(a, t, blk, lane);
+    RowPlan<D / 32> plan;
+    plan_rows<32 / UPR, D / 32>(plan, a, t, run.n, 0, lane / UPR);
+    for (int j = split * W + warp; j < 2 * a.num_kv_heads; j += a.head_split * W)
+        append8_rows<D, T, INTERLEAVED>(a, t, run, plan, blk, j >> 1, j & 1, lane);
+}
+
+// The largest magnitude of eight 16-bit values, NaN passed over.
+template <typename T> __device__ __forceinline__ float largest8(const uint4 &w);
+template <> __device__ __forceinline__ float largest8<__half>(const uint4 &w) {
+    const __half2 *h = reinterpret_cast<const __half2 *>(&w);
+    const __half2 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+template <> __device__ __forceinline__ float largest8<__nv_bfloat16>(const uint4 &w) {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
+// Sixteen bytes of shared memory in one load (the compiler would split it by
+// the elements that it feeds, at four times the bank accesses).
+__device__ __forceinline__ uint4 load_shared16(const void *p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem_u32(p)));
+    return v;
+}
+
+// Many tokens (prompts): a CTA looks over block_size tokens for those that
+// begin a run (about one does) and takes group_heads kv heads of it.  The run's
+// keys and values come as bulk copies of whole row pieces into shared memory,
+// 64 KB at a time with three CTAs to an SM, which keeps more bytes under way
+// than registers hold.  A thread keeps to one unit of a row, whose cosines it
+// holds, and goes through the heads twice: for the magnitudes, and, when the
+// scales are known, for the codes.  The CTAs after them rotate queries, a
+// thread to a unit of four heads.
+constexpr int kSlabBytes = 64 * 1024;
+constexpr int kMaxGroupHeads = kSlabBytes / (4 * 64 * 4);           // blocks of 4 tokens, head_dim 64
+constexpr int kQueryRows = 4;
+
+template <int D, typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(const RopeArgs a) {
+    constexpr int UPR = D / 16;
+    constexpr int W = kRopeThreads / 32;
+    constexpr int kRowsAtOnce = kRopeThreads / 2 / UPR;
+    extern __shared__ __align__(16) unsigned char slab[];           // [2][rows][group_heads][D] 16-bit
+    __shared__ uint64_t bar;
+    __shared__ int failed;
+    __shared__ unsigned top[2 * kMaxGroupHeads];                    // largest magnitudes, then scales, as bits
+    const int kv_ctas = (int)gridDim.x - a.q_ctas;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_mbar_init();
+        failed = 0;
+    }
+    __syncthreads();                       // any warp may issue the first copies
+    pdl_trigger();
+    pdl_wait();
+    if ((int)blockIdx.x >= kv_ctas) {
+        const unsigned groups = (unsigned)(a.num_heads + kQueryRows - 1) / kQueryRows;
+        const unsigned per_token = groups * UPR;
+        const unsigned long long i = (unsigned long long)(blockIdx.x - kv_ctas) * kRopeThreads + threadIdx.x;
+        const unsigned long long t64 = i / per_token;
+        if (t64 >= (unsigned)a.num_tokens) return;
+        const int t = (int)t64;
+        const int r = (int)(i - t64 * per_token);
+        const int row0 = (r / UPR) * kQueryRows, u = r % UPR;
+        const int n = a.num_heads - row0 < kQueryRows ? a.num_heads - row0 : kQueryRows;
+        const Unit x = unit_at<INTERLEAVED>(u, a.rot);
+        const T *src = static_cast<const T *>(a.q) + t * a.q_stride + row0 * D;
+        T *dst = static_cast<T *>(a.q_out) + ((size_t)t * a.num_heads + row0) * D;
+        uint4 ra[kQueryRows], rb[kQueryRows];
+#pragma unroll
+        for (int k = 0; k < kQueryRows; k++)
+            if (k < n) {
+                ra[k] = *reinterpret_cast<const uint4 *>(src + k * D + x.a);
+                rb[k] = *reinterpret_cast<const uint4 *>(src + k * D + x.b);
+            }
+        const int pos = checked_position(a, t, r == 0);
+        if (pos < 0) return;
+        float4 cs[4];
+        if (x.rotated) load_cos_sin(cs, a, pos, u);
+#pragma unroll
+        for (int k = 0; k < kQueryRows; k++)
+            if (k < n) {
+                if (x.rotated) {
+                    float f[16];
+                    widen<T>(f, ra[k], rb[k]);
+                    turn<INTERLEAVED>(f, cs);
+                    ra[k] = narrow<T>(f);
+                    rb[k] = narrow<T>(f + 8);
+                }
+                *reinterpret_cast<uint4 *>(dst + k * D + x.a) = ra[k];
+                *reinterpret_cast<uint4 *>(dst + k * D + x.b) = rb[k];
+            }
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int B = 1 << a.log2_block;
+    const int hgroups = (a.num_kv_heads + a.group_heads - 1) / a.group_heads;
+    const int h0 = (int)(blockIdx.x % hgroups) * a.group_heads;
+    const int heads = a.num_kv_heads - h0 < a.group_heads ? a.num_kv_heads - h0 : a.group_heads;
+    const int first = (int)(blockIdx.x / hgroups) * B;
+    const int last = first + B < a.num_tokens ? first + B : a.num_tokens;
+    const uint32_t piece = (uint32_t)(heads * D * sizeof(T));        // of a token's row
+    // this thread's unit of keys (the first half of the threads) or values, and its row of kRowsAtOnce
+    const bool isv = tid >= kRopeThreads / 2;
+    const int r = (tid % (kRopeThreads / 2)) / UPR, u = tid % UPR;
+    const Unit x = unit_at<INTERLEAVED>(u, isv ? 0 : a.rot);
+    if (tid == 0 && timed_out(a.st)) failed = 1;
+    uint32_t phase = 0;
+    for (int base = first; base < last; base += 32) {
+        // the tokens that begin a run, a lane to a token; every warp finds the same ones
+        const int tl = base + lane;
+        const bool mine = tl < last;
+        const int64_t sl = mine ? __ldg(a.slots + tl) : -1;
+        const int64_t before = mine && tl > 0 ? __ldg(a.slots + tl - 1) : -1;
+        const bool good = sl >= 0 && sl < a.num_slots;
+        if (h0 == 0 && warp == 0 && sl >= 0) {
+            if (a.rot) checked_position(a, tl, a.num_heads == 0);
+            if (!good) latch(a.st, kFlagBadSlot, sl);
         }
-        const int64_t blk = s >> a.log2_block;
-        if (t > 0) {
-            const int64_t before = a.slots[t - 1];
-            if (before >= 0 && before < a.num_slots && (before >> a.log2_block) == blk) continue;
+        const bool leads = good && !(before >= 0 && before < a.num_slots &&
+                                     (before >> a.log2_block) == (sl >> a.log2_block));
+        for (unsigned todo = __ballot_sync(0xffffffffu, leads); todo; todo &= todo - 1) {
+            const int src_lane = __ffs(todo) - 1, t = base + src_lane;
+            const int64_t blk = __shfl_sync(0xffffffffu, sl, src_lane) >> a.log2_block;
+            Run run = find_run(a, t, blk, lane);
+            if (run.n > B) run.n = B;                                 // slots that repeat: the slab holds a block
+            if (tid < 2 * heads) top[tid] = 0;
+            if (tid == 0) mbar_arrive_expect_tx(&bar, 2u * (uint32_t)run.n * piece);
+            // row pieces of keys, then of values, spread over the warps
+            for (int c = lane * W + warp; c < 2 * run.n; c += kRopeThreads) {
+                const bool v = c >= run.n;
+                const int row = v ? c - run.n : c;
+                const T *src = v ? static_cast<const T *>(a.v) + (t + row) * a.v_stride
+                                 : static_cast<const T *>(a.k) + (t + row) * a.k_stride;
+                bulk_g2s(slab + (size_t)c * piece, src + (size_t)h0 * D, piece, &bar);
+            }
+            // meanwhile this thread's first row: its offset in the block and its cosines
+            int off = 0;
+            bool turned = false;
+            float4 cs[4];
+            auto plan = [&](int row) {
+                turned = false;
+                if (row >= run.n) return;
+                off = (int)(__ldg(a.slots + t + row) & (B - 1));
+                if (x.rotated) {
+                    const int pos = __ldg(a.positions + t + row);
+                    turned = pos >= 0 && pos < a.num_positions;       // others have been latched
+                    if (turned) load_cos_sin(cs, a, pos, u);
+                }
+            };
+            plan(r);
+            if (!mbar_wait(&bar, phase, kWaitLimitCycles)) {
+                if (lane == 0) latch(a.st, kFlagTimeout, t);
+                failed = 1;
+            }
+            __syncthreads();
+            if (failed) {                                             // copies may still be under way
+                if (tid == 0) mbar_wait(&bar, phase, kDrainLimitCycles);
+                return;
+            }
+            phase ^= 1u;
+            const T *mine_rows = reinterpret_cast<const T *>(slab + (size_t)(isv ? run.n : 0) * piece);
+            auto unit32 = [&](float (&y)[16], int row, int h) {
+                const T *q = mine_rows + ((size_t)row * heads + h) * D;
+                widen<T>(y, load_shared16(q + x.a), load_shared16(q + x.b));
+                if (turned) turn<INTERLEAVED>(y, cs);
+            };
+            for (int row0 = 0; row0 < run.n; row0 += kRowsAtOnce) {
+                const int row = row0 + r;
+                if (row0 > 0) plan(row);
+                for (int h = 0; h < heads; h++) {
+                    float amax = 0.f;
+                    if (row < run.n) {
+                        if (turned) {
+                            float y[16];
+                            unit32(y, row, h);
+#pragma unroll
+                            for (int e = 0; e < 16; e++) amax = fmaxf(amax, fabsf(y[e]));
+                        } else {
+                            const T *q = mine_rows + ((size_t)row * heads + h) * D;
+                            amax = fmaxf(largest8<T>(load_shared16(q + x.a)), largest8<T>(load_shared16(q + x.b)));
+                        }
+                    }
+                    // magnitudes are not negative: their bits order as they do
+                    const unsigned m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+                    if (lane == 0) atomicMax(&top[2 * h + (isv ? 1 : 0)], m);
+                }
+            }
+            __syncthreads();
+            for (int j = warp; j < 2 * heads; j += W) {
+                const bool v = j & 1;
+                const int h = h0 + (j >> 1);
+                unsigned char *rows = static_cast<unsigned char *>(v ? a.v_cache : a.k_cache) +
+                                      ((size_t)(blk * a.num_kv_heads + h) << a.log2_block) * D;
+                const float scale = grow_scale<D>(a, run, blk, h, v, __uint_as_float(top[j]), rows, lane);
+                if (lane == 0) top[j] = __float_as_uint(scale);
+            }
+            __syncthreads();
+            for (int row0 = 0; row0 < run.n; row0 += kRowsAtOnce) {
+                const int row = row0 + r;
+                if (run.n > kRowsAtOnce) plan(row);
+                if (row >= run.n) continue;
+                unsigned char *dst = static_cast<unsigned char *>(isv ? a.v_cache : a.k_cache) +
+                                     (((size_t)(blk * a.num_kv_heads + h0) << a.log2_block) + off) * D;
+#pragma unroll 2
+                for (int h = 0; h < heads; h++) {
+                    float y[16];
+                    unit32(y, row, h);
+                    store_codes(dst + ((size_t)h << a.log2_block) * D, x, y, __uint_as_float(top[2 * h + (isv ? 1 : 0)]));
+                }
+            }
+            __syncthreads();                                          // the slab and the scales are free again
         }
-        const Run run = find_run(a, t, blk, lane);
-        for (int j = split * W + warp; j < 2 * a.num_kv_heads; j += a.head_split * W)
-            append8_rows<D, T, INTERLEAVED>(a, t, run, blk, j >> 1, j & 1, lane);
     }
 }
 
 // ---- host ---------------------------------------------------------------------------
+
+// From so many tokens on the copies' setup pays for itself (prompts of 32/8
+// heads: 2,000 tokens 16 us against 22, 1,000 tokens 13 against 10).  A decode
+// step of so many sequences goes the same way at twice the time: what their
+// tokens are to one another only the device sees.
+#ifndef PKV_BULK_TOKENS
+#define PKV_BULK_TOKENS 2048
+#endif
+constexpr int kBulkTokens = PKV_BULK_TOKENS;
 
 template <int D, typename T>
 cudaError_t launch_append(const RopeArgs &a, bool interleaved, bool fp8, cudaStream_t stream) {
@@ -426,18 +678,28 @@ cudaError_t launch_append(const RopeArgs &a, bool interleaved, bool fp8, cudaStr
         return launch(interleaved ? rotary_append_kernel<D, T, true> : rotary_append_kernel<D, T, false>, dim3(grid),
                       dim3(kRopeThreads), 0, stream, b);
     }
+    const int sms = sm_count() > 0 ? sm_count() : 1;
+    if (a.num_tokens >= kBulkTokens) {
+        b.group_heads = kSlabBytes / (int)((2 * sizeof(T) * D) << a.log2_block);
+        if (b.group_heads > a.num_kv_heads) b.group_heads = a.num_kv_heads;
+        const int hgroups = (a.num_kv_heads + b.group_heads - 1) / b.group_heads;
+        const unsigned long long chunks = ((unsigned long long)a.num_tokens + (1u << a.log2_block) - 1) >> a.log2_block;
+        const unsigned long long qunits =
+            (unsigned long long)a.num_tokens * ((a.num_heads + kQueryRows - 1) / kQueryRows) * UPR;
+        b.q_ctas = (int)((qunits + kRopeThreads - 1) / kRopeThreads);
+        auto kern = interleaved ? rotary_append8_bulk_kernel<D, T, true> : rotary_append8_bulk_kernel<D, T, false>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlabBytes);
+        if (e != cudaSuccess) return e;
+        const size_t smem = (size_t)b.group_heads * ((2 * sizeof(T) * D) << a.log2_block);
+        return launch(kern, dim3((unsigned)(chunks * hgroups + b.q_ctas)), dim3(kRopeThreads), smem, stream, b);
+    }
     const unsigned long long qunits = (unsigned long long)a.num_tokens * a.num_heads * UPR;
     b.q_ctas = (int)((qunits + kRopeThreads - 1) / kRopeThreads);
-    // long calls: 8 tokens to a CTA, so that most CTAs find a run; short ones: the heads of a token spread out
-    const int sms = sm_count() > 0 ? sm_count() : 1;
-    b.tokens_per_cta = a.num_tokens >= 64 * sms ? 8 : 1;
-    const int groups = (a.num_tokens + b.tokens_per_cta - 1) / b.tokens_per_cta;
     const int most = (2 * a.num_kv_heads + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
     b.head_split = 1;
-    while (b.head_split < most && groups * b.head_split < 4 * sms) b.head_split++;
-    const unsigned grid = (unsigned)(groups * b.head_split + b.q_ctas);
-    return launch(interleaved ? rotary_append8_kernel<D, T, true> : rotary_append8_kernel<D, T, false>, dim3(grid),
-                  dim3(kRopeThreads), 0, stream, b);
+    while (b.head_split < most && a.num_tokens * b.head_split < 4 * sms) b.head_split++;
+    return launch(interleaved ? rotary_append8_kernel<D, T, true> : rotary_append8_kernel<D, T, false>,
+                  dim3((unsigned)(a.num_tokens * b.head_split + b.q_ctas)), dim3(kRopeThreads), 0, stream, b);
 }
 
 pkv_status append_impl(const char *what, bool fp8, void *query_out, const void *query, const void *key,
