@@ -18,6 +18,7 @@ missing, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Sequence
 
@@ -303,44 +304,57 @@ _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
 
 
-class _on:
-    """The library launches on the current device: makes that the tensors'
-    own (a no-op when it is)."""
-
-    __slots__ = ("index", "was")
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.was = torch.cuda.current_device()
-        if self.index is not None and self.index != self.was:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.index is not None and self.index != self.was:
-            torch.cuda.set_device(self.was)
+def _raw_stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
+    """The stream's handle; the current one's without building a Stream."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
 
 
-def _one_device(what: str, device, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{what}: tensors on {t.device} and {device}")
+def _call(fn, what: str, index: int, *args) -> None:
+    """A C call on the tensors' own device: the library launches on the current one."""
+    was = torch.cuda.current_device()
+    if was == index:
+        rc = fn(*args)
+    else:
+        torch.cuda.set_device(index)
+        try:
+            rc = fn(*args)
+        finally:
+            torch.cuda.set_device(was)
+    if rc:
+        _ck(rc, what)
 
 
-def _rows(t: torch.Tensor, name: str, T: int, h: int, d: int):
+def _at(t: torch.Tensor, name: str, dtype, index: int) -> int:
+    """The address of a contiguous tensor of this type on CUDA device `index`."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    ptr = _dev(t, name, dtype)                      # says what is wrong
+    raise ValueError(f"{name} (at {ptr:#x}) is on {t.device}, other tensors on cuda:{index}")
+
+
+def _rows(t: torch.Tensor, name: str, dtype, index: int, T: int, h: int, d: int):
     """Pointer and token stride of a [T][h][d] tensor whose tokens may lie
     further apart than h * d elements (a slice of a wider projection)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
     if t.shape != (T, h, d):
         raise ValueError(f"{name} must be [{T}][{h}][{d}], got shape {tuple(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != index:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{index}")
     st, sh, sd = t.stride()
     if T <= 1:
         st = h * d
     if T and ((h > 1 and sh != d) or sd != 1 or st < h * d or st % 8):
         raise ValueError(f"{name}: a token's heads must be contiguous, tokens a multiple of 8 elements apart")
     return t.data_ptr(), st
+
+
+def _cuda_index(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
 def rotary_table(num_positions: int, rotary_dim: int, base: float = 10000.0, scaling: str = "none",
@@ -359,11 +373,10 @@ def rotary_table(num_positions: int, rotary_dim: int, base: float = 10000.0, sca
         out = torch.empty(num_positions, rotary_dim // 2, 2, dtype=torch.float32, device=device)
     elif out.shape != (num_positions, rotary_dim // 2, 2):
         raise ValueError("rotary_table: out must be [num_positions][rotary_dim / 2][2]")
-    with _on(out.device):
-        rc = load().rotary_table(_dev(out, "out", torch.float32), num_positions, rotary_dim, float(base),
-                                 _SCALINGS[scaling], float(factor), original_positions, float(low_turns),
-                                 float(high_turns), float(magnitude), _stream(stream, out.device))
-    _ck(rc, "rotary_table")
+    index = _cuda_index(out, "out")
+    _call(load().rotary_table, "rotary_table", index, _at(out, "out", torch.float32, index), num_positions, rotary_dim,
+          base, _SCALINGS[scaling], factor, original_positions, low_turns, high_turns, magnitude,
+          _raw_stream(stream, index))
     return out
 
 
@@ -378,52 +391,46 @@ def _append(what, fp8, query, key, value, cos_sin, positions, key_cache, value_c
             query_out, stream):
     if layout not in _LAYOUTS:
         raise ValueError(f"{what}: layout {layout!r} not one of {sorted(_LAYOUTS)}")
+    index = _cuda_index(key_cache, "key_cache")
     NB, Hkv, B, d = key_cache.shape
-    T = key.shape[0]
+    T, dtype = key.shape[0], key.dtype
     if value_cache.shape != key_cache.shape or slot_mapping.shape != (T,):
         raise ValueError(f"{what}: caches of different shapes, or slot_mapping not [num_tokens]")
-    if value.dtype != key.dtype or (query is not None and query.dtype != key.dtype):
-        raise TypeError(f"{what}: query, key and value must have one dtype")
-    cache_dtype = torch.float8_e4m3fn if fp8 else key.dtype
-    if key_cache.dtype != cache_dtype or value_cache.dtype != cache_dtype:
-        raise TypeError(f"{what}: caches must be {cache_dtype}")
-    dev = key_cache.device
-    _one_device(what, dev, query, key, value, cos_sin, positions, value_cache, scales, slot_mapping, query_out)
-    rot = npos = H = 0
-    cs_ptr = pos_ptr = q_ptr = qo_ptr = sc_ptr = None
-    q_stride = 0
+    code = _dtype_code(key)
+    k_ptr, k_stride = _rows(key, "key", dtype, index, T, Hkv, d)
+    v_ptr, v_stride = _rows(value, "value", dtype, index, T, Hkv, d)
+    rot = npos = H = q_stride = 0
+    cs_ptr = pos_ptr = q_ptr = qo_ptr = None
     if cos_sin is not None:
         if cos_sin.dim() != 3 or cos_sin.shape[2] != 2 or positions is None or positions.shape != (T,):
             raise ValueError(f"{what}: cos_sin must be [positions][rotary_dim / 2][2], positions [num_tokens]")
         npos, rot = cos_sin.shape[0], 2 * cos_sin.shape[1]
-        cs_ptr, pos_ptr = _dev(cos_sin, "cos_sin", torch.float32), _dev(positions, "positions", torch.int32)
+        cs_ptr = _at(cos_sin, "cos_sin", torch.float32, index)
+        pos_ptr = _at(positions, "positions", torch.int32, index)
     if query is not None:
         if cos_sin is None:
             raise ValueError(f"{what}: a query needs a table to rotate it by")
         H = query.shape[1]
-        q_ptr, q_stride = _rows(query, "query", T, H, d)
+        q_ptr, q_stride = _rows(query, "query", dtype, index, T, H, d)
         if query_out is None:
-            query_out = torch.empty(T, H, d, dtype=query.dtype, device=dev)
-        elif query_out.shape != query.shape or query_out.dtype != query.dtype:
-            raise ValueError(f"{what}: query_out must be shaped and typed like query")
-        qo_ptr = _dev(query_out, "query_out")
-    k_ptr, k_stride = _rows(key, "key", T, Hkv, d)
-    v_ptr, v_stride = _rows(value, "value", T, Hkv, d)
+            query_out = torch.empty(T, H, d, dtype=dtype, device=key_cache.device)
+        elif query_out.shape != query.shape:
+            raise ValueError(f"{what}: query_out must be shaped like query")
+        qo_ptr = _at(query_out, "query_out", dtype, index)
+    cache_dtype = torch.float8_e4m3fn if fp8 else dtype
+    caches = _at(key_cache, "key_cache", cache_dtype, index), _at(value_cache, "value_cache", cache_dtype, index)
+    slots = _at(slot_mapping, "slot_mapping", torch.int64, index)
+    L = load()
     if fp8:
         if scales.shape != (NB, Hkv + Hkv % 2, 2):
             raise ValueError(f"{what}: scales must be [num_blocks][num_kv_heads rounded up to even][2]")
-        sc_ptr = _dev(scales, "scales", torch.float32)
-    caches = (_dev(key_cache, "key_cache"), _dev(value_cache, "value_cache"))
-    slots = _dev(slot_mapping, "slot_mapping", torch.int64)
-    sizes = (T, H, Hkv, d, rot, npos, _LAYOUTS[layout], q_stride, k_stride, v_stride, B, NB, _dtype_code(key))
-    with _on(dev):
-        st = _stream(stream, dev)
-        if fp8:
-            rc = load().kv_rotary_and_cache_fp8(qo_ptr, q_ptr, k_ptr, v_ptr, *caches, sc_ptr, cs_ptr, pos_ptr, slots,
-                                                *sizes, st)
-        else:
-            rc = load().kv_rotary_and_cache(qo_ptr, q_ptr, k_ptr, v_ptr, *caches, cs_ptr, pos_ptr, slots, *sizes, st)
-    _ck(rc, what)
+        _call(L.kv_rotary_and_cache_fp8, what, index, qo_ptr, q_ptr, k_ptr, v_ptr, *caches,
+              _at(scales, "scales", torch.float32, index), cs_ptr, pos_ptr, slots, T, H, Hkv, d, rot, npos,
+              _LAYOUTS[layout], q_stride, k_stride, v_stride, B, NB, code, _raw_stream(stream, index))
+    else:
+        _call(L.kv_rotary_and_cache, what, index, qo_ptr, q_ptr, k_ptr, v_ptr, *caches, cs_ptr, pos_ptr, slots, T, H,
+              Hkv, d, rot, npos, _LAYOUTS[layout], q_stride, k_stride, v_stride, B, NB, code,
+              _raw_stream(stream, index))
     return query_out
 
 
@@ -459,12 +466,14 @@ def kv_rotary_and_cache_fp8(query: Optional[torch.Tensor], key: torch.Tensor, va
 
 # -- attention over an 8-bit cache ---------------------------------------------------
 
+@functools.lru_cache(maxsize=4096)
 def paged_attention_decode_fp8_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
                                               max_context_len: int, partition_size: int = 0) -> int:
     return int(load().paged_attention_decode_fp8_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
                                                                 max_context_len, partition_size))
 
 
+@functools.lru_cache(maxsize=4096)
 def paged_attention_prefill_fp8_workspace_size(num_seqs: int, num_kv_heads: int, head_dim: int, block_size: int,
                                                max_context_len: int) -> int:
     return int(load().paged_attention_prefill_fp8_workspace_size(num_seqs, num_kv_heads, head_dim, block_size,
@@ -475,30 +484,29 @@ def make_fp8_workspace(device, nbytes: int, stream: Optional[torch.cuda.Stream] 
     """A device buffer of at least nbytes, prepared for
     paged_attention_decode_fp8 and paged_attention_prefill_fp8.  Returns once
     the preparation has finished, so any stream may use the buffer."""
-    dev = torch.device(device)
-    buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    with _on(buf.device):
-        _ck(load().paged_attention_fp8_workspace_init(buf.data_ptr(), buf.numel(), _stream(stream, buf.device)),
-            "paged_attention_fp8_workspace_init")
-        (stream or torch.cuda.current_stream(buf.device)).synchronize()
+    buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device(device))
+    index = buf.get_device()
+    _call(load().paged_attention_fp8_workspace_init, "paged_attention_fp8_workspace_init", index, buf.data_ptr(),
+          buf.numel(), _raw_stream(stream, index))
+    (stream or torch.cuda.current_stream(buf.device)).synchronize()
     return buf
 
 
 _ws8_cache: dict = {}
 
 
-def _workspace8(device, nbytes: int) -> torch.Tensor:
+def _workspace8(index: int, nbytes: int) -> torch.Tensor:
     """The binding's own 8-bit workspace per device, as _workspace."""
-    buf = _ws8_cache.get(device)
+    buf = _ws8_cache.get(index)
     if buf is None or buf.numel() < nbytes:
         if buf is not None:
             _ws_retired.append(buf)
-        buf = make_fp8_workspace(device, nbytes)
-        _ws8_cache[device] = buf
+        buf = make_fp8_workspace(torch.device("cuda", index), nbytes)
+        _ws8_cache[index] = buf
     return buf
 
 
-def _check8(what, out, query, key_cache, value_cache, scales, block_tables, context_lens, S):
+def _check8(what, out, query, key_cache, value_cache, scales, block_tables, context_lens, S, index):
     NB, Hkv, B, d = key_cache.shape
     if query.shape[2] != d or out.shape != query.shape or value_cache.shape != key_cache.shape:
         raise ValueError(f"{what}: shape mismatch")
@@ -506,12 +514,11 @@ def _check8(what, out, query, key_cache, value_cache, scales, block_tables, cont
         raise ValueError(f"{what}: block_tables must be [S][max_blocks], context_lens [S]")
     if scales.shape != (NB, Hkv + Hkv % 2, 2):
         raise ValueError(f"{what}: scales must be [num_blocks][num_kv_heads rounded up to even][2]")
-    if query.dtype != out.dtype or key_cache.dtype != torch.float8_e4m3fn or value_cache.dtype != key_cache.dtype:
-        raise TypeError(f"{what}: out must be typed like query, caches float8_e4m3fn")
-    _one_device(what, query.device, out, key_cache, value_cache, scales, block_tables, context_lens)
-    return (_dev(out, "out"), _dev(query, "query"), _dev(key_cache, "key_cache"), _dev(value_cache, "value_cache"),
-            _dev(scales, "scales", torch.float32), _dev(block_tables, "block_tables", torch.int32),
-            _dev(context_lens, "context_lens", torch.int32))
+    f8, i32 = torch.float8_e4m3fn, torch.int32
+    return (_at(out, "out", query.dtype, index), _at(query, "query", query.dtype, index),
+            _at(key_cache, "key_cache", f8, index), _at(value_cache, "value_cache", f8, index),
+            _at(scales, "scales", torch.float32, index), _at(block_tables, "block_tables", i32, index),
+            _at(context_lens, "context_lens", i32, index))
 
 
 def paged_attention_decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -523,21 +530,18 @@ def paged_attention_decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache
     their block scales).  workspace from make_fp8_workspace, one call at a
     time; None takes the binding's own per-device buffer, which every 8-bit
     call without a workspace shares.  Returns out."""
+    what = "paged_attention_decode_fp8"
+    index = _cuda_index(query, "query")
     S, H, d = query.shape
-    ptrs = _check8("paged_attention_decode_fp8", out, query, key_cache, value_cache, scales, block_tables,
-                   context_lens, S)
+    ptrs = _check8(what, out, query, key_cache, value_cache, scales, block_tables, context_lens, S, index)
     NB, Hkv, B, _ = key_cache.shape
     mb = block_tables.shape[1]
-    dev = query.device
-    with _on(dev):
-        if workspace is None:
-            workspace = _workspace8(dev, paged_attention_decode_fp8_workspace_size(
-                S, H, Hkv, d, max_context_len if max_context_len > 0 else mb * B, partition_size))
-        rc = load().paged_attention_decode_fp8(
-            *ptrs, S, mb, max_context_len, B, NB, H, Hkv, d, float(1.0 / math.sqrt(d) if scale is None else scale),
-            partition_size, _dev(workspace, "workspace", torch.uint8), workspace.numel(), _dtype_code(query),
-            _stream(stream, dev))
-    _ck(rc, "paged_attention_decode_fp8")
+    if workspace is None:
+        workspace = _workspace8(index, paged_attention_decode_fp8_workspace_size(
+            S, H, Hkv, d, max_context_len if max_context_len > 0 else mb * B, partition_size))
+    _call(load().paged_attention_decode_fp8, what, index, *ptrs, S, mb, max_context_len, B, NB, H, Hkv, d,
+          1.0 / math.sqrt(d) if scale is None else scale, partition_size, _at(workspace, "workspace", torch.uint8, index),
+          workspace.numel(), _dtype_code(query), _raw_stream(stream, index))
     return out
 
 
@@ -550,25 +554,22 @@ def paged_attention_prefill_fp8(out: torch.Tensor, query: torch.Tensor, key_cach
     """paged_attention_prefill over an 8-bit cache.  max_context_len bounds the
     contexts and sizes the workspace (0: the whole table).  workspace as for
     paged_attention_decode_fp8.  Returns out."""
+    what = "paged_attention_prefill_fp8"
+    index = _cuda_index(query, "query")
     T, H, d = query.shape
     S = context_lens.shape[0]
-    ptrs = _check8("paged_attention_prefill_fp8", out, query, key_cache, value_cache, scales, block_tables,
-                   context_lens, S)
+    ptrs = _check8(what, out, query, key_cache, value_cache, scales, block_tables, context_lens, S, index)
     if query_start.shape != (S + 1,):
-        raise ValueError("paged_attention_prefill_fp8: query_start must be [S+1]")
-    _one_device("paged_attention_prefill_fp8", query.device, query_start)
+        raise ValueError(f"{what}: query_start must be [S+1]")
     NB, Hkv, B, _ = key_cache.shape
     mb = block_tables.shape[1]
-    dev = query.device
-    with _on(dev):
-        if workspace is None:
-            workspace = _workspace8(dev, paged_attention_prefill_fp8_workspace_size(
-                S, Hkv, d, B, max_context_len if max_context_len > 0 else mb * B))
-        rc = load().paged_attention_prefill_fp8(
-            *ptrs, _dev(query_start, "query_start", torch.int32), S, T, max_query_len, max_context_len, mb, B, NB, H,
-            Hkv, d, float(1.0 / math.sqrt(d) if scale is None else scale), _dev(workspace, "workspace", torch.uint8),
-            workspace.numel(), _dtype_code(query), _stream(stream, dev))
-    _ck(rc, "paged_attention_prefill_fp8")
+    if workspace is None:
+        workspace = _workspace8(index, paged_attention_prefill_fp8_workspace_size(
+            S, Hkv, d, B, max_context_len if max_context_len > 0 else mb * B))
+    _call(load().paged_attention_prefill_fp8, what, index, *ptrs, _at(query_start, "query_start", torch.int32, index), S,
+          T, max_query_len, max_context_len, mb, B, NB, H, Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale,
+          _at(workspace, "workspace", torch.uint8, index), workspace.numel(), _dtype_code(query),
+          _raw_stream(stream, index))
     return out
 
 

@@ -791,8 +791,8 @@ bool encode_cache_map8(CUtensorMap *map, const void *base, int num_blocks, int H
 template <int D, bool WIDE, typename T> cudaError_t launch_decode8w(const F8Args &f, cudaStream_t stream) {
     auto kern = paged_attention_fp8_kernel<D, WIDE, T>;
     const size_t smem = F8Layout::total(f.a.num_seqs);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)F8Layout::total(kLaunchSeqs));
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = allow_smem(kern, F8Layout::total(kLaunchSeqs), allowed);
     if (e != cudaSuccess) return e;
     CUtensorMap tmk, tmv;
     const AttnArgs &a = f.a;

@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "pkv.h"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -32,6 +34,19 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
     if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+// Allow `kern` `bytes` of dynamic shared memory, once per device; `done` is the
+// kernel's own record (a bit per device).
+template <typename K> cudaError_t allow_smem(K kern, size_t bytes, std::atomic<unsigned long long> &done) {
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = d < 64 ? 1ull << d : 0ull;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
 

@@ -688,7 +688,8 @@ cudaError_t launch_append(const RopeArgs &a, bool interleaved, bool fp8, cudaStr
             (unsigned long long)a.num_tokens * ((a.num_heads + kQueryRows - 1) / kQueryRows) * UPR;
         b.q_ctas = (int)((qunits + kRopeThreads - 1) / kRopeThreads);
         auto kern = interleaved ? rotary_append8_bulk_kernel<D, T, true> : rotary_append8_bulk_kernel<D, T, false>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlabBytes);
+        static std::atomic<unsigned long long> allowed[2];
+        cudaError_t e = allow_smem(kern, kSlabBytes, allowed[interleaved]);
         if (e != cudaSuccess) return e;
         const size_t smem = (size_t)b.group_heads * ((2 * sizeof(T) * D) << a.log2_block);
         return launch(kern, dim3((unsigned)(chunks * hgroups + b.q_ctas)), dim3(kRopeThreads), smem, stream, b);
