@@ -820,30 +820,32 @@ template <int D, typename T> cudaError_t launch_decode8(const F8Args &f, cudaStr
 // Logical block j of sequence s, as 16-bit values, to block s * width + j of a
 // scratch pool of the same layout; new_tables names those blocks.  A code
 // times a power of two is exact in bf16, and in fp16 within its range.  Rows
-// past the context become zeros.  One CTA per block, sixteen codes of K and of
-// V to a thread: bound by the bytes read and twice as many written.
+// past the context become zeros.  A full block that an earlier sequence holds
+// in the same place (a shared prefix) is widened there once and named by both
+// (32 requests after a shared 1000-token prefix: 358 us the whole call without
+// that).  One CTA per block, eight codes of K and of V to a load: bound by
+// the bytes read and twice as many written.
 constexpr int kWidenThreads = 256;
+constexpr int kWidenUnroll = 4;
 
-template <typename T>
-__device__ __forceinline__ void widen16(const uint4 &w, float s, uint4 (&out)[2]) {
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-    uint32_t o[8];
+template <typename T> __device__ __forceinline__ uint4 widen8(const uint2 &w, float s) {
+    const uint32_t in[2] = {w.x, w.y};
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < 2; i++) {
         const uint32_t lo = e4m3x2_lo(in[i]), hi = e4m3x2_hi(in[i]);
         const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
         const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
         o[2 * i] = Mma<T>::pack(x.x * s, x.y * s);
         o[2 * i + 1] = Mma<T>::pack(y.x * s, y.y * s);
     }
-    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kWidenThreads) widen_blocks_kernel(
     uint4 *__restrict__ k_out, uint4 *__restrict__ v_out, int32_t *__restrict__ new_tables, const WsHeader *hdr,
-    const uint4 *__restrict__ k_cache, const uint4 *__restrict__ v_cache, const float2 *__restrict__ scales,
+    const uint2 *__restrict__ k_cache, const uint2 *__restrict__ v_cache, const float2 *__restrict__ scales,
     const int32_t *__restrict__ tables, const int32_t *__restrict__ ctx_lens, int width, int max_blocks, int log2_block,
     int num_blocks, int num_kv_heads, int row_chunks, DeviceStatus *st) {
     pdl_trigger();
@@ -854,31 +856,53 @@ __global__ void __launch_bounds__(kWidenThreads) widen_blocks_kernel(
     }
     const int s = (int)(blockIdx.x / (unsigned)width), j = (int)(blockIdx.x % (unsigned)width);
     const int B = 1 << log2_block;
-    if (threadIdx.x == 0) new_tables[blockIdx.x] = (int)blockIdx.x;
     const int rows = ctx_lens[s] - (j << log2_block);                // tokens of the context in this block and after
-    if (rows <= 0 || j >= max_blocks) return;
-    const int32_t b = tables[(size_t)s * max_blocks + j];
-    if (b < 0 || b >= num_blocks) {
-        if (threadIdx.x == 0) latch(st, kFlagBadBlock, b);
-        return;
+    const bool inside = rows > 0 && j < max_blocks;
+    const int32_t b = inside ? tables[(size_t)s * max_blocks + j] : -1;
+    const bool good = b >= 0 && b < num_blocks;
+    // the first sequence that holds this block, full, in this place; every warp finds the same one
+    int owner = s;
+    if (good && rows >= B) {
+        for (int base = 0; base < s; base += 32) {
+            const int q = base + (threadIdx.x & 31);
+            const bool same = q < s && tables[(size_t)q * max_blocks + j] == b && ctx_lens[q] >= ((j + 1) << log2_block);
+            const unsigned m = __ballot_sync(kFull, same);
+            if (m) {
+                owner = base + __ffs(m) - 1;
+                break;
+            }
+        }
     }
-    const int per_head = row_chunks << log2_block;                    // sixteen-code chunks of a (block, head)
-    const int chunks = per_head * num_kv_heads;
+    if (threadIdx.x == 0) new_tables[blockIdx.x] = owner * width + j;
+    if (inside && !good && threadIdx.x == 0) latch(st, kFlagBadBlock, b);
+    if (!good || owner != s) return;
+    // eight-code chunks of a (block, head); a row's are 8 or 16
+    const int log2_row = row_chunks == 16 ? 4 : 3, log2_head = log2_row + log2_block;
+    const int chunks = num_kv_heads << log2_head;
     const float2 *sc = scales + (size_t)b * scale_heads(num_kv_heads);
-    const uint4 *kin = k_cache + (size_t)b * chunks, *vin = v_cache + (size_t)b * chunks;
-    uint4 *ko = k_out + (size_t)blockIdx.x * chunks * 2, *vo = v_out + (size_t)blockIdx.x * chunks * 2;
-    for (int i = threadIdx.x; i < chunks; i += kWidenThreads) {
-        const uint4 kw = kin[i], vw = vin[i];
-        const float2 f = sc[i / per_head];
-        uint4 k2[2], v2[2];
-        widen16<T>(kw, f.x, k2);
-        widen16<T>(vw, f.y, v2);
-        if (rows < B && (i % per_head) / row_chunks >= rows)
-            k2[0] = k2[1] = v2[0] = v2[1] = make_uint4(0u, 0u, 0u, 0u);
-        ko[2 * i] = k2[0];
-        ko[2 * i + 1] = k2[1];
-        vo[2 * i] = v2[0];
-        vo[2 * i + 1] = v2[1];
+    const uint2 *kin = k_cache + (size_t)b * chunks, *vin = v_cache + (size_t)b * chunks;
+    uint4 *ko = k_out + (size_t)blockIdx.x * chunks, *vo = v_out + (size_t)blockIdx.x * chunks;
+    // four chunks of each at a time under way
+    for (int i0 = threadIdx.x; i0 < chunks; i0 += kWidenThreads * kWidenUnroll) {
+        uint2 kw[kWidenUnroll], vw[kWidenUnroll];
+        float2 f[kWidenUnroll];
+#pragma unroll
+        for (int k = 0; k < kWidenUnroll; k++) {
+            const int i = i0 + k * kWidenThreads;
+            if (i < chunks) {
+                kw[k] = kin[i];
+                vw[k] = vin[i];
+                f[k] = sc[i >> log2_head];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kWidenUnroll; k++) {
+            const int i = i0 + k * kWidenThreads;
+            if (i >= chunks) break;
+            const bool past = rows < B && ((i & ((1 << log2_head) - 1)) >> log2_row) >= rows;
+            ko[i] = past ? make_uint4(0u, 0u, 0u, 0u) : widen8<T>(kw[k], f[k].x);
+            vo[i] = past ? make_uint4(0u, 0u, 0u, 0u) : widen8<T>(vw[k], f[k].y);
+        }
     }
 }
 
@@ -1058,10 +1082,10 @@ pkv_status paged_attention_prefill_fp8(void *out, const void *query, const void 
     auto widen = dtype == PKV_F16 ? widen_blocks_kernel<__half> : widen_blocks_kernel<__nv_bfloat16>;
     cudaError_t e = launch(widen, dim3((unsigned)blocks), dim3(kWidenThreads), 0, stream,
                            reinterpret_cast<uint4 *>(ws + z.k_off), reinterpret_cast<uint4 *>(ws + z.v_off), new_tables,
-                           reinterpret_cast<const WsHeader *>(ws), static_cast<const uint4 *>(key_cache),
-                           static_cast<const uint4 *>(value_cache), reinterpret_cast<const float2 *>(scales), block_tables,
+                           reinterpret_cast<const WsHeader *>(ws), static_cast<const uint2 *>(key_cache),
+                           static_cast<const uint2 *>(value_cache), reinterpret_cast<const float2 *>(scales), block_tables,
                            context_lens, z.width, max_blocks_per_seq, ilog2(block_size), num_blocks, num_kv_heads,
-                           head_dim / 16, st);
+                           head_dim / 8, st);
     if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));
     return paged_attention_prefill(out, query, ws + z.k_off, ws + z.v_off, new_tables, context_lens, query_start, num_seqs,
                                    num_tokens, max_query_len, z.width, block_size, blocks, num_heads, num_kv_heads,

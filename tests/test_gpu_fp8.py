@@ -326,3 +326,35 @@ def test_prefill_latches_what_does_not_fit(cuda_device):
         pkv.check()
     pkv.paged_attention_prefill_fp8(out, q, c.kc, c.vc, c.sc, c.dt_, c.dc, qs)
     pkv.check()
+
+
+def test_prefill_shared_prefix(cuda_device):
+    """Sequences that share full blocks in the same place, in another place, and a partly filled one; in a workspace that
+    held NaN."""
+    B, d, H, Hkv = 16, 64, 4, 2
+    ctx = (100, 77, 100, 52, 41)
+    c = Case8(cuda_device, ctx, H, Hkv, d, B, "f16", seed=30)
+    t = c.tables
+    t[1, :3] = t[0, :3]                       # a prefix of three blocks
+    t[2, :2] = t[0, :2]
+    t[2, 3] = t[0, 4]                         # a block of another place
+    t[3, :3] = t[1, :3]
+    t[3, 3] = t[1, 3]                         # shared, but sequence 3 ends in it (52 = 3 * 16 + 4)
+    t[4, :2] = t[0, :2]
+    t[4, 2] = t[0, 2]                         # sequence 4 ends in it
+    c.dt_ = torch.from_numpy(t).to(cuda_device)
+    new = (5, 1, 30, 7, 41)
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = torch.randn(int(start[-1]), H, d, generator=torch.Generator().manual_seed(1)).to(torch.float16)
+    ws = pkv.make_fp8_workspace(cuda_device, 1 << 22)
+    ws[256:].fill_(0xFF)
+    out = torch.empty(q.shape, dtype=q.dtype, device=cuda_device)
+    pkv.paged_attention_prefill_fp8(out, q.to(cuda_device), c.kc, c.vc, c.sc, c.dt_, c.dc,
+                                    torch.from_numpy(start).to(cuda_device), workspace=ws)
+    pkv.check()
+    got = out.double().cpu().numpy()
+    for s, n in enumerate(ctx):
+        rows = slice(int(start[s]), int(start[s + 1]))
+        want, mag, vmax = attention64(q[rows].double().numpy(), c.kvals, c.vvals, c.tables[s], n, 1 / math.sqrt(d))
+        tol = attention_tolerance(want, mag, vmax, n, d, torch.finfo(q.dtype).eps, 11)
+        assert np.all(np.abs(got[rows] - want) <= tol), (s, np.abs(got[rows] - want).max())
