@@ -32,13 +32,24 @@ struct TurnTable {
     unsigned long long turn[kMaxRotaryDim / 2];
 };
 
+// Cosine and sine of a 64-bit fraction of a turn: the nearest quarter turn
+// swaps and negates; what is left, y within pi / 4 of zero, takes the Taylor
+// series of both (to y^9 and y^10: the next terms are below 2^-29 and 2^-33),
+// a third of the instructions of a sincos that would reduce its argument again.
 __device__ __forceinline__ float2 cos_sin_of(unsigned long long turns, float magnitude) {
     const int t = (int)(turns >> 32);                      // signed fraction of a turn, 2^-32 units
     const int quarter = (int)(((unsigned)t + 0x20000000u) >> 30);   // nearest quarter turn
-    // the rest, at most an eighth of a turn, as a multiple of pi: 2^-31 units
-    const float x = (float)(int)((unsigned)t - ((unsigned)quarter << 30)) * 0x1p-31f;
-    float s, c;
-    sincospif(x, &s, &c);
+    const float y = (float)(int)((unsigned)t - ((unsigned)quarter << 30)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+    const float z = y * y;
+    float s = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+    s = fmaf(z, s, 1.f / 120.f);
+    s = fmaf(z, s, -1.f / 6.f);
+    s = fmaf(y * z, s, y);
+    float c = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+    c = fmaf(z, c, -1.f / 720.f);
+    c = fmaf(z, c, 1.f / 24.f);
+    c = fmaf(z, c, -0.5f);
+    c = fmaf(z, c, 1.f);
     const float cc = (quarter & 1) ? -s : c, ss = (quarter & 1) ? c : s;
     const float sign = (quarter & 2) ? -magnitude : magnitude;
     return make_float2(cc * sign, ss * sign);
@@ -46,7 +57,7 @@ __device__ __forceinline__ float2 cos_sin_of(unsigned long long turns, float mag
 
 // Thread t owns two neighbouring pairs (one 16-byte store) of every
 // (threads / columns)-th position of its CTA's stretch: its turns stay in
-// registers.  Bound by the writes and the two sincospif per store.
+// registers.  Bound by the writes.
 __global__ void __launch_bounds__(kRopeThreads) rotary_table_kernel(float4 *__restrict__ out,
                                                                     const __grid_constant__ TurnTable tab,
                                                                     int num_positions, int columns, int rows,
@@ -824,8 +835,11 @@ pkv_status rotary_table(float *cos_sin, int num_positions, int rotary_dim, doubl
         tab.turn[i] = (unsigned long long)std::nearbyint(theta / kTwoPi * 0x1p64);   // theta <= 1: below 2^62
     }
     const int columns = rotary_dim / 4, rows = kRopeThreads / columns;
-    // a few positions per thread, enough CTAs for every SM
-    int per_cta = rows * 4;
+    // one wave of CTAs for long tables (131,072 x 128: 12.6 us against 20.2 with 32 positions to a CTA), since
+    // fetching the turns costs each CTA about a microsecond; at least four positions to a thread in short ones
+    const int wave = (sm_count() > 0 ? sm_count() : 1) * 8;
+    int per_cta = (num_positions + wave - 1) / wave;
+    per_cta = per_cta < 4 * rows ? 4 * rows : (per_cta + rows - 1) / rows * rows;
     const long long ctas = ((long long)num_positions + per_cta - 1) / per_cta;
     cudaError_t e = launch(rotary_table_kernel, dim3((unsigned)ctas), dim3(kRopeThreads), 0, stream,
                            reinterpret_cast<float4 *>(cos_sin), tab, num_positions, columns, rows, per_cta,

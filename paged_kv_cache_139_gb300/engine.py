@@ -19,9 +19,26 @@ import torch
 import ctypes
 import math
 
-from . import (BlockAllocator, PkvError, copy_blocks, kv_reshape_and_cache, make_workspace,
-               paged_attention_decode, paged_attention_prefill, paged_attention_workspace_size, swap_blocks)
+from . import (BlockAllocator, PkvError, copy_blocks, kv_reshape_and_cache, kv_rotary_and_cache,
+               kv_rotary_and_cache_fp8, kv_scales, make_fp8_workspace, make_workspace, paged_attention_decode,
+               paged_attention_decode_fp8, paged_attention_decode_fp8_workspace_size, paged_attention_prefill,
+               paged_attention_prefill_fp8, paged_attention_prefill_fp8_workspace_size, paged_attention_workspace_size,
+               rotary_table, swap_blocks)
 from ._lib import load
+
+
+@dataclasses.dataclass
+class RotaryPositions:
+    """How a cache's queries and keys are rotated by their positions: the table
+    of rotary_table and the layout of the pairs."""
+
+    cos_sin: torch.Tensor     # float32 [positions][rotary_dim / 2][2]
+    layout: str = "half"
+
+    @classmethod
+    def make(cls, num_positions: int, rotary_dim: int, device, layout: str = "half", **scaling) -> "RotaryPositions":
+        """scaling: rotary_table's base, scaling, factor, ..."""
+        return cls(rotary_table(num_positions, rotary_dim, device=device, **scaling), layout)
 
 
 @dataclasses.dataclass
@@ -34,6 +51,11 @@ class StepPlan:
     tables: np.ndarray        # int32 [n][max_blocks]
     context_lens: np.ndarray  # int32 [n]
 
+    @property
+    def positions(self) -> np.ndarray:
+        """int32 [n]: the new tokens' positions."""
+        return (self.context_lens - 1).astype(np.int32)
+
 
 @dataclasses.dataclass
 class DeviceStep:
@@ -44,6 +66,7 @@ class DeviceStep:
     tables: torch.Tensor
     context_lens: torch.Tensor
     max_context_len: int
+    positions: Optional[torch.Tensor] = None     # int32, of a cache with rotary positions
 
 
 @dataclasses.dataclass
@@ -57,6 +80,13 @@ class PrefillPlan:
     context_lens: np.ndarray  # int32 [n]
     query_start: np.ndarray   # int32 [n + 1]
 
+    @property
+    def positions(self) -> np.ndarray:
+        """int32 [T]: the new tokens' positions."""
+        n = np.diff(self.query_start)
+        return (np.arange(int(self.query_start[-1]))
+                + np.repeat(self.context_lens - self.query_start[1:], n)).astype(np.int32)
+
 
 @dataclasses.dataclass
 class DevicePrefill:
@@ -66,6 +96,8 @@ class DevicePrefill:
     context_lens: torch.Tensor
     query_start: torch.Tensor
     max_query_len: int
+    max_context_len: int = 0
+    positions: Optional[torch.Tensor] = None     # int32, of a cache with rotary positions
 
 
 class StagedInputs:
@@ -140,21 +172,33 @@ class HostKVPool:
         shape = (num_blocks, num_kv_heads, block_size, head_dim)
         self.key_cache = torch.empty(shape, dtype=dtype, pin_memory=True)
         self.value_cache = torch.empty(shape, dtype=dtype, pin_memory=True)
+        # an 8-bit pool's block scales travel with the blocks
+        self.scales = kv_scales(num_blocks, num_kv_heads, pin_memory=True) if dtype == torch.float8_e4m3fn else None
         self.alloc = BlockAllocator(num_blocks, block_size, free_order)
         self.num_blocks, self.block_size = num_blocks, block_size
 
 
 class PagedKVCache:
+    """dtype torch.float8_e4m3fn keeps keys and values in 8 bits with a scale
+    per block and kv head (queries, keys and values come in 16 bits all the
+    same).  With `rotary`, write, decode and prefill rotate queries and keys by
+    their tokens' positions on the way."""
+
     def __init__(self, num_blocks: int, num_kv_heads: int, head_dim: int, block_size: int,
                  dtype: torch.dtype, device, max_blocks_per_seq: int,
                  free_order: Optional[Sequence[int]] = None,
-                 key_cache: Optional[torch.Tensor] = None, value_cache: Optional[torch.Tensor] = None):
+                 key_cache: Optional[torch.Tensor] = None, value_cache: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, rotary: Optional[RotaryPositions] = None):
         shape = (num_blocks, num_kv_heads, block_size, head_dim)
         self.device = torch.device(device)
         self.key_cache = key_cache if key_cache is not None else torch.empty(shape, dtype=dtype, device=self.device)
         self.value_cache = value_cache if value_cache is not None else torch.empty(shape, dtype=dtype,
                                                                                     device=self.device)
         assert tuple(self.key_cache.shape) == shape and tuple(self.value_cache.shape) == shape
+        self.fp8 = dtype == torch.float8_e4m3fn
+        self.scales = (scales if scales is not None else kv_scales(num_blocks, num_kv_heads, self.device)) if self.fp8 \
+            else None
+        self.rotary = rotary
         self.alloc = BlockAllocator(num_blocks, block_size, free_order)
         self.num_blocks, self.num_kv_heads, self.head_dim, self.block_size = shape[0], shape[1], shape[3], shape[2]
         self.max_blocks_per_seq = max_blocks_per_seq
@@ -213,7 +257,9 @@ class PagedKVCache:
             tables=torch.from_numpy(plan.tables).to(d, non_blocking=non_blocking),
             context_lens=torch.from_numpy(plan.context_lens).to(d, non_blocking=non_blocking),
             query_start=torch.from_numpy(plan.query_start).to(d, non_blocking=non_blocking),
-            max_query_len=int(n.max()) if n.size else 0)
+            max_query_len=int(n.max()) if n.size else 0,
+            max_context_len=int(plan.context_lens.max()) if plan.context_lens.size else 0,
+            positions=self._upload_positions(plan, non_blocking))
 
     def upload(self, plan: StepPlan, non_blocking: bool = False) -> DeviceStep:
         d = self.device
@@ -222,33 +268,68 @@ class PagedKVCache:
             pairs=torch.from_numpy(np.ascontiguousarray(plan.pairs)).to(d, non_blocking=non_blocking),
             tables=torch.from_numpy(plan.tables).to(d, non_blocking=non_blocking),
             context_lens=torch.from_numpy(plan.context_lens).to(d, non_blocking=non_blocking),
-            max_context_len=int(plan.context_lens.max()) if plan.context_lens.size else 0)
+            max_context_len=int(plan.context_lens.max()) if plan.context_lens.size else 0,
+            positions=self._upload_positions(plan, non_blocking) if plan.slots.size else None)
+
+    def _upload_positions(self, plan, non_blocking: bool) -> Optional[torch.Tensor]:
+        if self.rotary is None:
+            return None
+        return torch.from_numpy(plan.positions).to(self.device, non_blocking=non_blocking)
 
     # -- device steps ------------------------------------------------------------
     def workspace(self, num_seqs: int, num_heads: int, max_context_len: int, partition_size: int = 0):
-        need = paged_attention_workspace_size(num_seqs, num_heads, self.num_kv_heads, self.head_dim,
-                                              max_context_len, partition_size)
+        size = paged_attention_decode_fp8_workspace_size if self.fp8 else paged_attention_workspace_size
+        return self._workspace(size(num_seqs, num_heads, self.num_kv_heads, self.head_dim, max_context_len,
+                                    partition_size))
+
+    def _workspace(self, need: int) -> torch.Tensor:
         if self._ws is None or self._ws.numel() < need:
             if self._ws is not None:
                 self._ws_retired.append(self._ws)   # calls in flight on other streams may hold it
-            self._ws = make_workspace(self.device, need)
+            self._ws = (make_fp8_workspace if self.fp8 else make_workspace)(self.device, need)
         return self._ws
+
+    def _pools(self):
+        """What a block is made of: every pool that block copies and swaps move."""
+        return (self.key_cache, self.value_cache) + ((self.scales,) if self.fp8 else ())
 
     def copy_on_write(self, pairs: torch.Tensor) -> None:
         if pairs.numel():
-            copy_blocks(self.key_cache, pairs)
-            copy_blocks(self.value_cache, pairs)
+            for pool in self._pools():
+                copy_blocks(pool, pairs)
 
-    def write(self, key: torch.Tensor, value: torch.Tensor, slots: torch.Tensor) -> None:
-        kv_reshape_and_cache(key, value, self.key_cache, self.value_cache, slots)
+    def write(self, key: torch.Tensor, value: torch.Tensor, slots: torch.Tensor,
+              query: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+              query_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+        """The new tokens' keys and values into the cache.  Of a cache with
+        rotary positions (which must be given), returns the rotated queries,
+        in query_out if given; otherwise the queries as they are."""
+        if self.rotary is None:
+            if self.fp8:
+                kv_rotary_and_cache_fp8(None, key, value, None, None, self.key_cache, self.value_cache, self.scales, slots)
+            else:
+                kv_reshape_and_cache(key, value, self.key_cache, self.value_cache, slots)
+            return query
+        r = self.rotary
+        if self.fp8:
+            return kv_rotary_and_cache_fp8(query, key, value, r.cos_sin, positions, self.key_cache, self.value_cache,
+                                           self.scales, slots, layout=r.layout, query_out=query_out)
+        return kv_rotary_and_cache(query, key, value, r.cos_sin, positions, self.key_cache, self.value_cache, slots,
+                                   layout=r.layout, query_out=query_out)
 
     def attend(self, query: torch.Tensor, step: DeviceStep, out: Optional[torch.Tensor] = None,
                scale: Optional[float] = None, partition_size: int = 0,
                max_context_len: Optional[int] = None) -> torch.Tensor:
+        """Attention of queries as the cache's keys are: of a cache with
+        rotary positions, rotated (as write returns them)."""
         if out is None:
             out = torch.empty_like(query)
         mcl = step.max_context_len if max_context_len is None else max_context_len
         ws = self.workspace(query.shape[0], query.shape[1], mcl, partition_size)
+        if self.fp8:
+            return paged_attention_decode_fp8(out, query, self.key_cache, self.value_cache, self.scales, step.tables,
+                                              step.context_lens, scale=scale, max_context_len=mcl,
+                                              partition_size=partition_size, workspace=ws)
         return paged_attention_decode(out, query, self.key_cache, self.value_cache, step.tables,
                                       step.context_lens, scale=scale, max_context_len=mcl,
                                       partition_size=partition_size, workspace=ws)
@@ -259,7 +340,7 @@ class PagedKVCache:
         """The device half of one decode iteration: copy-on-write copies, the
         new tokens' cache write, then attention (which reads the new tokens)."""
         self.copy_on_write(step.pairs)
-        self.write(key, value, step.slots)
+        query = self.write(key, value, step.slots, query, step.positions)
         return self.attend(query, step, out, scale, partition_size)
 
     def prefill_workspace(self) -> torch.Tensor:
@@ -275,35 +356,51 @@ class PagedKVCache:
         shared prefix's partly filled last block), the new tokens' cache write,
         then causal attention of the new tokens over the paged cache."""
         if out is None:
-            out = torch.empty_like(query)
+            out = torch.empty_like(query, memory_format=torch.contiguous_format)
         self.copy_on_write(step.pairs)
-        self.write(key, value, step.slots)
+        query = self.write(key, value, step.slots, query, step.positions)
+        if self.fp8:
+            ws = self._workspace(paged_attention_prefill_fp8_workspace_size(
+                step.context_lens.shape[0], self.num_kv_heads, self.head_dim, self.block_size,
+                step.max_context_len or step.tables.shape[1] * self.block_size))
+            return paged_attention_prefill_fp8(out, query, self.key_cache, self.value_cache, self.scales, step.tables,
+                                               step.context_lens, step.query_start, scale=scale,
+                                               max_query_len=step.max_query_len, max_context_len=step.max_context_len,
+                                               workspace=ws)
         return paged_attention_prefill(out, query, self.key_cache, self.value_cache, step.tables,
                                        step.context_lens, step.query_start, scale=scale,
                                        max_query_len=step.max_query_len, workspace=self.prefill_workspace())
 
     # -- swapping ----------------------------------------------------------------
+    def _host_pools(self, host: HostKVPool):
+        """The host pool's counterparts of _pools; before anything moves."""
+        if self.fp8 != (host.scales is not None):
+            raise ValueError("swapping between an 8-bit and a 16-bit pool")
+        return (host.key_cache, host.value_cache) + ((host.scales,) if self.fp8 else ())
+
     def swap_out(self, seqs: Sequence[int], host: HostKVPool, stream=None):
         """Evict a sequence group to the host pool, all or nothing: its blocks
         move to host blocks (one swap_blocks launch for keys, one for values)
         and the GPU blocks are freed.  Returns the group's ids in the host
         pool and the (GPU block, host block) pairs."""
+        pools = self._host_pools(host)
         ids, pairs = self.alloc.move_group(host.alloc, seqs)
         if len(pairs):
             p = torch.from_numpy(pairs).pin_memory()
-            swap_blocks(host.key_cache, self.key_cache, p, stream)
-            swap_blocks(host.value_cache, self.value_cache, p, stream)
+            for theirs, ours in zip(pools, self._pools()):
+                swap_blocks(theirs, ours, p, stream)
             self._keep_pairs = p            # alive until the copies are done (next sync)
         return ids, pairs
 
     def swap_in(self, host_seqs: Sequence[int], host: HostKVPool, stream=None):
         """Bring a swapped-out group back: the reverse move and copies.
         Returns the group's GPU ids and the (host block, GPU block) pairs."""
+        pools = self._host_pools(host)
         ids, pairs = host.alloc.move_group(self.alloc, host_seqs)
         if len(pairs):
             p = torch.from_numpy(pairs).pin_memory()
-            swap_blocks(self.key_cache, host.key_cache, p, stream)
-            swap_blocks(self.value_cache, host.value_cache, p, stream)
+            for theirs, ours in zip(pools, self._pools()):
+                swap_blocks(ours, theirs, p, stream)
             self._keep_pairs = p
         return ids, pairs
 
@@ -324,39 +421,69 @@ class PagedKVCache:
         return PreparedStep(self, query, key, value, step, out, scale, partition_size, stream, fused)
 
 
+def _check_step(eng: PagedKVCache, query, key, value, step, out, extra=()) -> int:
+    """The dtype code of a prepared step's 16-bit tensors, which must be on the GPU and contiguous."""
+    d = query.shape[2]
+    assert out.shape == query.shape and out.dtype == query.dtype == key.dtype == value.dtype
+    assert eng.fp8 or query.dtype == eng.key_cache.dtype
+    assert query.dtype in (torch.float16, torch.bfloat16)
+    assert key.shape == value.shape == (step.slots.shape[0], eng.num_kv_heads, d)
+    for t in (query, key, value, out, step.slots, step.tables, step.context_lens, step.pairs, *extra):
+        assert t.is_cuda and t.is_contiguous()
+    if eng.rotary is not None:
+        assert step.positions.is_cuda and step.positions.shape == step.slots.shape and query.shape[0] == key.shape[0]
+    return 1 if query.dtype == torch.bfloat16 else 0
+
+
+def _copy_calls(eng: PagedKVCache, step, st):
+    n = step.pairs.shape[0] if step.pairs.dim() == 2 else 0
+    return [(c.data_ptr(), step.pairs.data_ptr(), n, c.numel() // c.shape[0] * c.element_size(), eng.num_blocks, st)
+            for c in eng._pools()] if n else []
+
+
+def _write_call(eng: PagedKVCache, query, query_out, key, value, step, code, st):
+    """The C call of PagedKVCache.write and its arguments."""
+    T, Hkv, d, B, NB = step.slots.shape[0], eng.num_kv_heads, eng.head_dim, eng.block_size, eng.num_blocks
+    ptrs = (key.data_ptr(), value.data_ptr(), eng.key_cache.data_ptr(), eng.value_cache.data_ptr())
+    if eng.rotary is None and not eng.fp8:
+        return "kv_reshape_and_cache", (*ptrs, step.slots.data_ptr(), T, Hkv, d, B, NB, code, st)
+    r = eng.rotary
+    H, rot, npos = (query.shape[1], 2 * r.cos_sin.shape[1], r.cos_sin.shape[0]) if r else (0, 0, 0)
+    args = (query_out.data_ptr() if r else None, query.data_ptr() if r else None, *ptrs,
+            *((eng.scales.data_ptr(),) if eng.fp8 else ()), r.cos_sin.data_ptr() if r else None,
+            step.positions.data_ptr() if r else None, step.slots.data_ptr(), T, H, Hkv, d, rot, npos,
+            ("half", "interleaved").index(r.layout) if r else 0, H * d, Hkv * d, Hkv * d, B, NB, code, st)
+    return ("kv_rotary_and_cache_fp8" if eng.fp8 else "kv_rotary_and_cache"), args
+
+
 class PreparedStep:
-    """copy_blocks, kv_reshape_and_cache and paged_attention_decode for one
-    set of buffers, their arguments checked and marshalled once: issuing the
-    step then costs three or four plain C calls.  For decode loops that run
-    the same buffers every iteration (the buffers' contents may change)."""
+    """copy_blocks, the cache write and the attention for one set of buffers,
+    their arguments checked and marshalled once: issuing the step then costs
+    three or four plain C calls.  For decode loops that run the same buffers
+    every iteration (the buffers' contents may change)."""
 
     def __init__(self, eng: PagedKVCache, query, key, value, step: DeviceStep, out, scale, partition_size, stream,
                  fused=True):
         self._L = load()
         S, H, d = query.shape
-        assert out.shape == query.shape and out.dtype == query.dtype == eng.key_cache.dtype
-        assert key.shape == value.shape == (step.slots.shape[0], eng.num_kv_heads, d)
-        for t in (query, key, value, out, step.slots, step.tables, step.context_lens, step.pairs):
-            assert t.is_cuda and t.is_contiguous()
-        code = 1 if query.dtype == torch.bfloat16 else 0
+        code = _check_step(eng, query, key, value, step, out)
         st = ctypes.c_void_p((stream or torch.cuda.current_stream(eng.device)).cuda_stream)
         ws = eng.workspace(S, H, step.max_context_len, partition_size)
-        self._keep = (query, key, value, step, out, ws)
+        q = query if eng.rotary is None else torch.empty_like(query)      # as the attention reads them
+        self._keep = (query, q, key, value, step, out, ws)
         NB, B = eng.num_blocks, eng.block_size
-        block_bytes = eng.num_kv_heads * B * d * eng.key_cache.element_size()
-        n = step.pairs.shape[0] if step.pairs.dim() == 2 else 0
-        self._copy = [(c.data_ptr(), step.pairs.data_ptr(), n, block_bytes, NB, st)
-                      for c in (eng.key_cache, eng.value_cache)] if n else []
-        T = step.slots.shape[0]
-        self._write = (key.data_ptr(), value.data_ptr(), eng.key_cache.data_ptr(), eng.value_cache.data_ptr(),
-                       step.slots.data_ptr(), T, eng.num_kv_heads, d, B, NB, code, st)
-        self._attend = (out.data_ptr(), query.data_ptr(), eng.key_cache.data_ptr(), eng.value_cache.data_ptr(),
+        self._copy = _copy_calls(eng, step, st)
+        T = self._tokens = step.slots.shape[0]
+        self._write_name, self._write = _write_call(eng, query, q, key, value, step, code, st)
+        self._attend_name = "paged_attention_decode_fp8" if eng.fp8 else "paged_attention_decode"
+        self._attend = (out.data_ptr(), q.data_ptr(), eng.key_cache.data_ptr(), eng.value_cache.data_ptr(),
+                        *((eng.scales.data_ptr(),) if eng.fp8 else ()),
                         step.tables.data_ptr(), step.context_lens.data_ptr(), S, step.tables.shape[1],
                         step.max_context_len, B, NB, H, eng.num_kv_heads, d,
                         float(1.0 / math.sqrt(d) if scale is None else scale), partition_size, ws.data_ptr(),
                         ws.numel(), code, st)
         # one new token per sequence, in sequence order: the write can ride in the attention launch
-        self._fused = fused and T == S
+        self._fused = fused and T == S and not eng.fp8 and eng.rotary is None
         self._write_attend = (out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(),
                               eng.key_cache.data_ptr(), eng.value_cache.data_ptr(), step.slots.data_ptr(),
                               step.tables.data_ptr(), step.context_lens.data_ptr(), S, step.tables.shape[1],
@@ -371,15 +498,15 @@ class PreparedStep:
                 raise PkvError(rc, "copy_blocks")
 
     def write(self) -> None:
-        if self._write[5]:
-            rc = self._L.kv_reshape_and_cache(*self._write)
+        if self._tokens:
+            rc = getattr(self._L, self._write_name)(*self._write)
             if rc:
-                raise PkvError(rc, "kv_reshape_and_cache")
+                raise PkvError(rc, self._write_name)
 
     def attend(self) -> None:
-        rc = self._L.paged_attention_decode(*self._attend)
+        rc = getattr(self._L, self._attend_name)(*self._attend)
         if rc:
-            raise PkvError(rc, "paged_attention_decode")
+            raise PkvError(rc, self._attend_name)
 
     def write_attend(self) -> None:
         """The cache write and the attention in one launch (paged_attention_decode_write)."""
@@ -406,51 +533,35 @@ class PreparedStep:
 
 
 class PreparedPrefill:
-    """copy_blocks, kv_reshape_and_cache and paged_attention_prefill for one
-    set of buffers, their arguments checked and marshalled once."""
+    """copy_blocks, the cache write and the prompt-phase attention for one set
+    of buffers, their arguments checked and marshalled once."""
 
     def __init__(self, eng: PagedKVCache, query, key, value, step: DevicePrefill, out, scale, stream):
         self._L = load()
         T, H, d = query.shape
-        assert out.shape == query.shape and out.dtype == query.dtype == eng.key_cache.dtype
-        assert key.shape == value.shape == (step.slots.shape[0], eng.num_kv_heads, d)
-        for t in (query, key, value, out, step.slots, step.tables, step.context_lens, step.query_start, step.pairs):
-            assert t.is_cuda and t.is_contiguous()
-        code = 1 if query.dtype == torch.bfloat16 else 0
+        code = _check_step(eng, query, key, value, step, out, (step.query_start,))
         st = ctypes.c_void_p((stream or torch.cuda.current_stream(eng.device)).cuda_stream)
-        ws = eng.prefill_workspace()
-        self._keep = (query, key, value, step, out, ws)
-        NB, B = eng.num_blocks, eng.block_size
-        block_bytes = eng.num_kv_heads * B * d * eng.key_cache.element_size()
-        n = step.pairs.shape[0] if step.pairs.dim() == 2 else 0
-        self._copy = [(c.data_ptr(), step.pairs.data_ptr(), n, block_bytes, NB, st)
-                      for c in (eng.key_cache, eng.value_cache)] if n else []
-        Tw = step.slots.shape[0]
-        self._write = (key.data_ptr(), value.data_ptr(), eng.key_cache.data_ptr(), eng.value_cache.data_ptr(),
-                       step.slots.data_ptr(), Tw, eng.num_kv_heads, d, B, NB, code, st)
         S = step.context_lens.shape[0]
-        self._attend = (out.data_ptr(), query.data_ptr(), eng.key_cache.data_ptr(), eng.value_cache.data_ptr(),
+        NB, B, mb = eng.num_blocks, eng.block_size, step.tables.shape[1]
+        if eng.fp8:
+            ws = eng._workspace(paged_attention_prefill_fp8_workspace_size(S, eng.num_kv_heads, d, B,
+                                                                           step.max_context_len or mb * B))
+        else:
+            ws = eng.prefill_workspace()
+        q = query if eng.rotary is None else torch.empty_like(query)
+        self._keep = (query, q, key, value, step, out, ws)
+        self._copy = _copy_calls(eng, step, st)
+        self._tokens = step.slots.shape[0]
+        self._write_name, self._write = _write_call(eng, query, q, key, value, step, code, st)
+        self._attend_name = "paged_attention_prefill_fp8" if eng.fp8 else "paged_attention_prefill"
+        self._attend = (out.data_ptr(), q.data_ptr(), eng.key_cache.data_ptr(), eng.value_cache.data_ptr(),
+                        *((eng.scales.data_ptr(),) if eng.fp8 else ()),
                         step.tables.data_ptr(), step.context_lens.data_ptr(), step.query_start.data_ptr(), S, T,
-                        step.max_query_len, step.tables.shape[1], B, NB, H, eng.num_kv_heads, d,
-                        float(1.0 / math.sqrt(d) if scale is None else scale), ws.data_ptr(), ws.numel(), code,
-                        st)
+                        step.max_query_len, *((step.max_context_len,) if eng.fp8 else ()), mb, B, NB, H,
+                        eng.num_kv_heads, d, float(1.0 / math.sqrt(d) if scale is None else scale), ws.data_ptr(),
+                        ws.numel(), code, st)
 
-    def copy(self) -> None:
-        for args in self._copy:
-            rc = self._L.copy_blocks(*args)
-            if rc:
-                raise PkvError(rc, "copy_blocks")
-
-    def write(self) -> None:
-        if self._write[5]:
-            rc = self._L.kv_reshape_and_cache(*self._write)
-            if rc:
-                raise PkvError(rc, "kv_reshape_and_cache")
-
-    def attend(self) -> None:
-        rc = self._L.paged_attention_prefill(*self._attend)
-        if rc:
-            raise PkvError(rc, "paged_attention_prefill")
+    copy, write, attend = PreparedStep.copy, PreparedStep.write, PreparedStep.attend
 
     def __call__(self) -> None:
         self.copy()

@@ -152,3 +152,13 @@ def test_reference_rotation_turns_pairs():
         dots = [float((rotate32(q, cs, [p + 7], 64, layout) * rotate32(k, cs, [p], 64, layout)).sum()) for p in (0, 11, 42)]
         assert max(dots) - min(dots) < 1e-4
         assert torch.equal(rotate32(q, cs, [0], 64, layout), q.float())
+
+
+def test_plan_positions():
+    from paged_kv_cache_139_gb300.engine import PrefillPlan, StepPlan
+    e = np.empty((0, 2), np.int32)
+    ctx = np.array([5, 1, 40], np.int32)
+    assert StepPlan(np.arange(3), np.zeros(3, np.int64), e, e, ctx).positions.tolist() == [4, 0, 39]
+    p = PrefillPlan(np.arange(4), np.zeros(9, np.int64), e, e, np.array([5, 7, 40, 3], np.int32),
+                    np.array([0, 5, 5, 8, 9], np.int32))
+    assert p.positions.tolist() == [0, 1, 2, 3, 4, 37, 38, 39, 2] and p.positions.dtype == np.int32

@@ -31,8 +31,9 @@ def _theta(rot, base, scaling, factor, orig, low, high):
 ])
 @pytest.mark.parametrize("magnitude", [1.0, -0.75, 1.2079])
 def test_table(cuda_device, n, rot, base, scaling, factor, orig, magnitude):
-    """Off by: the turn's truncation (2 pi 2^-32), its remainder's rounding to fp32 (pi / 4 * 2^-24), one step
-    of sincospif (2^-24 below 1) and the magnitude's product and own rounding (2 * 2^-24): under 2^-22."""
+    """Off by: the turn's truncation (2 pi 2^-32), its remainder's conversion to fp32 and to an angle (2 pi / 4 *
+    2^-24), the series' rounding (a step, 2^-24 below 1) and the magnitude's product and own rounding (2 * 2^-24):
+    under 2^-22."""
     t = pkv.rotary_table(n, rot, base=base, scaling=scaling, factor=factor, original_positions=orig,
                          magnitude=magnitude, device=cuda_device).double().cpu().numpy()
     pkv.check()
