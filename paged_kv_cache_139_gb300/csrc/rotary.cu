@@ -92,6 +92,7 @@ struct RopeArgs {
     int num_tokens, num_heads, num_kv_heads;
     int rot, num_positions, log2_block;
     int q_ctas;                    // 8-bit append: CTAs that rotate queries (after the others)
+    int single_ctas;               // 8-bit append of many: CTAs that append runs of one token (before those)
     int head_split;                // 8-bit append of few tokens: CTAs that share a token's heads
     int group_heads;               // 8-bit append of many: kv heads of a CTA
 };
@@ -230,43 +231,83 @@ __global__ void __launch_bounds__(kRopeThreads) rotary_append_kernel(const RopeA
 
 // ---- append to the 8-bit cache ----------------------------------------------------
 
-// Neighbouring tokens of the call that go to one block, and their offsets there.
+// Neighbouring tokens of the call that go to one block: n of them from token t.
 struct Run {
-    int n;                     // tokens
-    unsigned written[4];       // bit o: offset o of the block (block sizes up to 128)
+    int t, n;
+    bool fresh;                // one of them is the block's first row
 };
 
 // The run that begins at token t (whose slot is in block blk), by the whole warp.
 __device__ __forceinline__ Run find_run(const RopeArgs &a, int t, int64_t blk, int lane) {
     Run run;
+    run.t = t;
     run.n = 0;
-    run.written[0] = run.written[1] = run.written[2] = run.written[3] = 0u;
+    run.fresh = false;
     for (int base = t; base < a.num_tokens; base += 32) {
         const int i = base + lane;
-        const int64_t s = i < a.num_tokens ? a.slots[i] : -1;
+        const int64_t s = i < a.num_tokens ? __ldg(a.slots + i) : -1;
         const bool in = s >= 0 && s < a.num_slots && (s >> a.log2_block) == blk;
         const unsigned m = __ballot_sync(0xffffffffu, in);
         const int cnt = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-        const int off = (int)(s & ((1ll << a.log2_block) - 1));
-#pragma unroll
-        for (int w = 0; w < 4; w++)
-            run.written[w] |= __reduce_or_sync(0xffffffffu, lane < cnt && (off >> 5) == w ? 1u << (off & 31) : 0u);
+        run.fresh |= __any_sync(0xffffffffu, lane < cnt && (s & ((1ll << a.log2_block) - 1)) == 0);
         run.n += cnt;
         if (cnt < 32) break;
     }
     return run;
 }
 
-__device__ __forceinline__ bool was_written(const Run &run, int off) {
-    const unsigned w = off < 64 ? (off < 32 ? run.written[0] : run.written[1])
-                                : (off < 96 ? run.written[2] : run.written[3]);
-    return (w >> (off & 31)) & 1u;
+// The run's offsets in its block as bits (block sizes up to 128), by the whole warp.
+struct Rows {
+    unsigned bits[4];
+};
+
+__device__ __forceinline__ Rows written_rows(const RopeArgs &a, const Run &run, int lane) {
+    Rows w;
+    w.bits[0] = w.bits[1] = w.bits[2] = w.bits[3] = 0u;
+    for (int base = 0; base < run.n; base += 32) {
+        const bool in = base + lane < run.n;
+        const int off = in ? (int)(__ldg(a.slots + run.t + base + lane) & ((1ll << a.log2_block) - 1)) : 0;
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            w.bits[k] |= __reduce_or_sync(0xffffffffu, in && (off >> 5) == k ? 1u << (off & 31) : 0u);
+    }
+    return w;
+}
+
+__device__ __forceinline__ bool was_written(const Rows &w, int off) {
+    const unsigned b = off < 64 ? (off < 32 ? w.bits[0] : w.bits[1]) : (off < 96 ? w.bits[2] : w.bits[3]);
+    return (b >> (off & 31)) & 1u;
+}
+
+// Whether slot x is in the pool and in slot s's block.
+__device__ __forceinline__ bool same_block(const RopeArgs &a, int64_t x, int64_t s) {
+    return x >= 0 && x < a.num_slots && (x >> a.log2_block) == (s >> a.log2_block);
+}
+
+__device__ __forceinline__ float *scale_of(const RopeArgs &a, int64_t blk, int h, bool isv) {
+    return a.scales + ((size_t)blk * scale_heads(a.num_kv_heads) + h) * 2 + (isv ? 1 : 0);
+}
+
+// Sixteen codes under a scale 1 / ratio times as large.
+__device__ __forceinline__ void round_again(uint4 *q, float ratio) {
+    const uint4 w = *q;
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const uint32_t lo = e4m3x2_lo(in[j]), hi = e4m3x2_hi(in[j]);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+        const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        out[j] = to_e4m3x4(f.x * ratio, f.y * ratio, g.x * ratio, g.y * ratio);
+    }
+    *q = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // The block's scale for new rows of magnitude up to amax (any lane's), stored;
-// the block's other rows are rounded again where it grows.  By one warp.
+// the block's other rows are rounded again where it grows.  `had`: the scale
+// before, not looked at when the run starts the block anew.  By one warp.
 template <int D>
-__device__ __forceinline__ float grow_scale(const RopeArgs &a, const Run &run, int64_t blk, int h, bool isv, float amax,
+__device__ __forceinline__ float grow_scale(const RopeArgs &a, const Run &run, float *sp, float had, float amax,
                                             unsigned char *rows, int lane) {
     constexpr int UPR = D / 16, RP = 32 / UPR;
     const int r = lane / UPR, u = lane % UPR;
@@ -274,26 +315,14 @@ __device__ __forceinline__ float grow_scale(const RopeArgs &a, const Run &run, i
     for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     amax = fminf(amax, 3.4028235e38f);             // infinities; fmaxf has passed NaN over
     // a write at offset 0 starts the block anew; otherwise its scale can only grow
-    const bool fresh = run.written[0] & 1u;
-    float *sp = a.scales + ((size_t)blk * scale_heads(a.num_kv_heads) + h) * 2 + (isv ? 1 : 0);
-    const float had = fresh ? 0.f : *sp;
+    if (run.fresh) had = 0.f;
     const float scale = fmaxf(had, pow2_scale(amax));
-    if (!fresh && scale != had) {
+    if (!run.fresh && scale != had) {
+        const Rows written = written_rows(a, run, lane);
         const float ratio = __fdiv_rn(had, scale);
         for (int o = r; o < 1 << a.log2_block; o += RP) {
-            if (was_written(run, o)) continue;
-            uint4 *q = reinterpret_cast<uint4 *>(rows + (size_t)o * D) + u;
-            const uint4 w = *q;
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-            uint32_t out[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const uint32_t lo = e4m3x2_lo(in[j]), hi = e4m3x2_hi(in[j]);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-                const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                out[j] = to_e4m3x4(f.x * ratio, f.y * ratio, g.x * ratio, g.y * ratio);
-            }
-            *q = make_uint4(out[0], out[1], out[2], out[3]);
+            if (was_written(written, o)) continue;
+            round_again(reinterpret_cast<uint4 *>(rows + (size_t)o * D) + u, ratio);
         }
     }
     __syncwarp();
@@ -318,42 +347,47 @@ __device__ __forceinline__ void store_codes(unsigned char *row, const Unit &x, f
         make_uint2(to_e4m3x4(f[8], f[9], f[10], f[11]), to_e4m3x4(f[12], f[13], f[14], f[15]));
 }
 
-// A lane's rows of a chunk of sixteen rows of a run: their offsets in the block
+// A lane's rows of a chunk of rows of a run: their offsets in the block
 // (-1: none) and positions (-1: not to be rotated).
 template <int CH> struct RowPlan {
     int off[CH], pos[CH];
 };
 
+// pos0: the position of the lane's first row of the first chunk, if it is one.
 template <int RP, int CH>
-__device__ __forceinline__ void plan_rows(RowPlan<CH> &p, const RopeArgs &a, int t, int n, int base, int r) {
+__device__ __forceinline__ void plan_rows(RowPlan<CH> &p, const RopeArgs &a, const Run &run, int base, int r, int pos0) {
 #pragma unroll
     for (int i = 0; i < CH; i++) {
         const int row = base + i * RP + r;
         p.off[i] = p.pos[i] = -1;
-        if (row < n) {
-            p.off[i] = (int)(a.slots[t + row] & ((1 << a.log2_block) - 1));
-            const int pos = a.rot ? a.positions[t + row] : -1;
+        if (row < run.n) {
+            p.off[i] = (int)(__ldg(a.slots + run.t + row) & ((1 << a.log2_block) - 1));
+            const int pos = !a.rot ? -1 : base == 0 && i == 0 ? pos0 : __ldg(a.positions + run.t + row);
             if (pos >= 0 && pos < a.num_positions) p.pos[i] = pos;    // others are latched by the caller
         }
     }
 }
 
-// The rows of run [t, t + run.n) of one kv head, keys or values, into block
-// blk, by one warp: D/16 lanes to a row.  A pass over the rows takes their
-// largest magnitude, the block gets its scale, and a second pass writes the
-// codes; `plan` is that of the first sixteen rows, and a run of so many stays
-// in registers between the two.
+// The rows of a run of one kv head, keys or values, into block blk, by one
+// warp: D/16 lanes to a row.  A pass over the rows takes their largest
+// magnitude, the block gets its scale, and a second pass writes the codes;
+// `plan` is that of the first chunk, and a run of so few rows stays in registers
+// between the two.
+constexpr int kChunkRows = 2;              // rows per lane and chunk
+
 template <int D, typename T, bool INTERLEAVED>
-__device__ __forceinline__ void append8_rows(const RopeArgs &a, int t, const Run &run,
-                                             const RowPlan<D / 32> &plan, int64_t blk, int h, bool isv, int lane) {
+__device__ __forceinline__ void append8_rows(const RopeArgs &a, const Run &run, const RowPlan<kChunkRows> &plan,
+                                             int64_t blk, int h, bool isv, int lane) {
     constexpr int UPR = D / 16;            // lanes per row
     constexpr int RP = 32 / UPR;           // rows side by side
-    constexpr int CH = 16 / RP;            // rows per lane and chunk of 16
+    constexpr int CH = kChunkRows;
     const int r = lane / UPR, u = lane % UPR;
     const Unit x = unit_at<INTERLEAVED>(u, isv ? 0 : a.rot);
     const T *src = (isv ? static_cast<const T *>(a.v) : static_cast<const T *>(a.k)) + h * D;
     const int64_t stride = isv ? a.v_stride : a.k_stride;
     RowPlan<CH> p = plan;
+    float *sp = scale_of(a, blk, h, isv);
+    const float had = run.fresh ? 0.f : *sp;
     float y[CH][16];
 
     auto load = [&](int base) {
@@ -362,7 +396,7 @@ __device__ __forceinline__ void append8_rows(const RopeArgs &a, int t, const Run
         for (int i = 0; i < CH; i++) {
             ra[i] = rb[i] = make_uint4(0u, 0u, 0u, 0u);
             if (p.off[i] >= 0) {
-                const T *q = src + (t + base + i * RP + r) * stride;
+                const T *q = src + (run.t + base + i * RP + r) * stride;
                 ra[i] = *reinterpret_cast<const uint4 *>(q + x.a);
                 rb[i] = *reinterpret_cast<const uint4 *>(q + x.b);
             }
@@ -379,8 +413,8 @@ __device__ __forceinline__ void append8_rows(const RopeArgs &a, int t, const Run
     };
 
     float amax = 0.f;
-    for (int base = 0; base < run.n; base += 16) {
-        if (base > 0) plan_rows<RP, CH>(p, a, t, run.n, base, r);
+    for (int base = 0; base < run.n; base += CH * RP) {
+        if (base > 0) plan_rows<RP, CH>(p, a, run, base, r, -1);
         load(base);
 #pragma unroll
         for (int i = 0; i < CH; i++)
@@ -389,11 +423,11 @@ __device__ __forceinline__ void append8_rows(const RopeArgs &a, int t, const Run
     }
     unsigned char *rows = static_cast<unsigned char *>(isv ? a.v_cache : a.k_cache) +
                           ((size_t)(blk * a.num_kv_heads + h) << a.log2_block) * D;
-    const float scale = grow_scale<D>(a, run, blk, h, isv, amax, rows, lane);
+    const float scale = grow_scale<D>(a, run, sp, had, amax, rows, lane);
 
-    for (int base = 0; base < run.n; base += 16) {
-        if (run.n > 16) {
-            plan_rows<RP, CH>(p, a, t, run.n, base, r);
+    for (int base = 0; base < run.n; base += CH * RP) {
+        if (run.n > CH * RP) {
+            plan_rows<RP, CH>(p, a, run, base, r, base == 0 ? plan.pos[0] : -1);
             load(base);
         }
 #pragma unroll
@@ -402,38 +436,66 @@ __device__ __forceinline__ void append8_rows(const RopeArgs &a, int t, const Run
     }
 }
 
-// A run begins at a token in the pool whose predecessor is not of its block.
-// Returns that block, or -1.
-__device__ __forceinline__ int64_t leads_run(const RopeArgs &a, int t, bool tells) {
-    const int64_t s = a.slots[t];
-    if (s < 0) return -1;                                  // padding token
-    if (a.rot && tells) checked_position(a, t, a.num_heads == 0);
-    if (s >= a.num_slots) {
-        if (tells) latch(a.st, kFlagBadSlot, s);
-        return -1;
+// A run of one token, the usual one of a decode step: its key and value rows j
+// = j0 + lane / (D/16) (the kv heads' keys, then their values) side by side.
+template <int D, typename T, bool INTERLEAVED>
+__device__ __forceinline__ void append8_token(const RopeArgs &a, int t, int pos, int64_t slot, bool fresh, int j0,
+                                              int lane) {
+    constexpr int UPR = D / 16;
+    const int u = lane % UPR, j = j0 + lane / UPR;
+    const bool active = j < 2 * a.num_kv_heads, isv = j >= a.num_kv_heads;
+    const int h = isv ? j - a.num_kv_heads : j;
+    const int off = (int)(slot & ((1ll << a.log2_block) - 1));
+    const int64_t blk = slot >> a.log2_block;
+    const Unit x = unit_at<INTERLEAVED>(u, isv ? 0 : a.rot);
+    float y[16];
+    float amax = 0.f, had = 0.f;
+    if (active) {
+        const T *src = isv ? static_cast<const T *>(a.v) + t * a.v_stride + h * D
+                           : static_cast<const T *>(a.k) + t * a.k_stride + h * D;
+        const uint4 ra = *reinterpret_cast<const uint4 *>(src + x.a), rb = *reinterpret_cast<const uint4 *>(src + x.b);
+        if (!fresh) had = *scale_of(a, blk, h, isv);
+        widen<T>(y, ra, rb);
+        if (x.rotated && pos >= 0 && pos < a.num_positions) {
+            float4 cs[4];
+            load_cos_sin(cs, a, pos, u);
+            turn<INTERLEAVED>(y, cs);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e++) amax = fmaxf(amax, fabsf(y[e]));
     }
-    const int64_t blk = s >> a.log2_block;
-    if (t > 0) {
-        const int64_t before = a.slots[t - 1];
-        if (before >= 0 && before < a.num_slots && (before >> a.log2_block) == blk) return -1;
+#pragma unroll
+    for (int o = UPR / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (!active) return;
+    const float scale = fmaxf(had, pow2_scale(fminf(amax, 3.4028235e38f)));
+    unsigned char *rows = static_cast<unsigned char *>(isv ? a.v_cache : a.k_cache) +
+                          ((size_t)(blk * a.num_kv_heads + h) << a.log2_block) * D;
+    if (!fresh && scale != had) {
+        const float ratio = __fdiv_rn(had, scale);
+#pragma unroll 4
+        for (int o = 0; o < 1 << a.log2_block; o++)
+            if (o != off) round_again(reinterpret_cast<uint4 *>(rows + (size_t)o * D) + u, ratio);
     }
-    return blk;
+    if (u == 0) *scale_of(a, blk, h, isv) = scale;
+    store_codes(rows + (size_t)off * D, x, y, scale);
 }
 
 // Few tokens (a decode step): the first CTAs append, head_split to a token,
 // their warps taking (kv head, keys or values) in turn; the CTAs after them
 // rotate queries, a thread to a unit.  Bound by latency: everything that a
 // token needs is requested as early as its address is known.
+constexpr int kStepThreads = 128;
+
 template <int D, typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) rotary_append8_kernel(const RopeArgs a) {
-    constexpr int UPR = D / 16;
-    constexpr int W = kRopeThreads / 32;
+__global__ void __launch_bounds__(kStepThreads, 6) rotary_append8_kernel(const RopeArgs a) {
+    constexpr int UPR = D / 16, RP = 32 / UPR;
+    constexpr int W = kStepThreads / 32;
     pdl_trigger();
     pdl_wait();
     const int kv_ctas = (int)gridDim.x - a.q_ctas;
     if ((int)blockIdx.x >= kv_ctas) {
         const unsigned per_token = (unsigned)a.num_heads * UPR;
-        const unsigned long long i = (unsigned long long)(blockIdx.x - kv_ctas) * kRopeThreads + threadIdx.x;
+        const unsigned long long i = (unsigned long long)(blockIdx.x - kv_ctas) * kStepThreads + threadIdx.x;
         const unsigned long long t64 = i / per_token;
         if (t64 >= (unsigned)a.num_tokens) return;
         const int t = (int)t64;
@@ -447,13 +509,37 @@ __global__ void __launch_bounds__(kRopeThreads) rotary_append8_kernel(const Rope
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x % a.head_split, t = (int)(blockIdx.x / a.head_split);
-    const int64_t blk = leads_run(a, t, split == 0 && warp == 0 && lane == 0);
-    if (blk < 0) return;
-    const Run run = find_run(a, t, blk, lane);
-    RowPlan<D / 32> plan;
-    plan_rows<32 / UPR, D / 32>(plan, a, t, run.n, 0, lane / UPR);
+    // one round trip for what says where the token goes: the slots around it and the rows' positions
+    const int r = lane / UPR, around = t - 1 + lane;
+    const int64_t s = around >= 0 && around < a.num_tokens ? __ldg(a.slots + around) : -1;
+    const int pos0 = a.rot && t + r < a.num_tokens ? __ldg(a.positions + t + r) : -1;
+    const int64_t mine = __shfl_sync(0xffffffffu, s, 1), before = __shfl_sync(0xffffffffu, s, 0);
+    if (mine < 0) return;                                             // padding token
+    if (split == 0 && warp == 0 && lane == 0) {
+        if (a.rot && (pos0 < 0 || pos0 >= a.num_positions) && a.num_heads == 0) latch(a.st, kFlagBadPosition, pos0);
+        if (mine >= a.num_slots) latch(a.st, kFlagBadSlot, mine);
+    }
+    if (mine >= a.num_slots) return;
+    const int64_t blk = mine >> a.log2_block;
+    // a run begins at a token whose predecessor is not of its block
+    if (same_block(a, before, mine)) return;
+    const bool in = lane > 0 && same_block(a, s, mine);
+    const unsigned m = __ballot_sync(0xffffffffu, in) >> 1;
+    Run run;
+    run.t = t;
+    run.n = __ffs(~m) - 1;
+    run.fresh = __any_sync(0xffffffffu, lane > 0 && lane <= run.n && (s & ((1ll << a.log2_block) - 1)) == 0);
+    if (run.n == 31) run = find_run(a, t, blk, lane);                 // and perhaps more
+    if (run.n == 1) {
+        const int pos = __shfl_sync(0xffffffffu, pos0, 0);
+        for (int j = (split * W + warp) * RP; j < 2 * a.num_kv_heads; j += a.head_split * W * RP)
+            append8_token<D, T, INTERLEAVED>(a, t, pos, mine, run.fresh, j, lane);
+        return;
+    }
+    RowPlan<kChunkRows> plan;
+    plan_rows<RP, kChunkRows>(plan, a, run, 0, r, pos0);
     for (int j = split * W + warp; j < 2 * a.num_kv_heads; j += a.head_split * W)
-        append8_rows<D, T, INTERLEAVED>(a, t, run, plan, blk, j >> 1, j & 1, lane);
+        append8_rows<D, T, INTERLEAVED>(a, run, plan, blk, j >> 1, j & 1, lane);
 }
 
 // The largest magnitude of eight 16-bit values, NaN passed over.
@@ -483,8 +569,10 @@ __device__ __forceinline__ uint4 load_shared16(const void *p) {
 // 64 KB at a time with three CTAs to an SM, which keeps more bytes under way
 // than registers hold.  A thread keeps to one unit of a row, whose cosines it
 // holds, and goes through the heads twice: for the magnitudes, and, when the
-// scales are known, for the codes.  The CTAs after them rotate queries, a
-// thread to a unit of four heads.
+// scales are known, for the codes.  The CTAs after them look over sixteen tokens
+// each for runs of one token (all of a large decode step), a warp to rows of
+// one, and the last ones rotate queries, a thread to a unit of four heads.
+constexpr int kSingleTokens = 16;
 constexpr int kSlabBytes = 64 * 1024;
 constexpr int kMaxGroupHeads = kSlabBytes / (4 * 64 * 4);           // blocks of 4 tokens, head_dim 64
 constexpr int kQueryRows = 4;
@@ -498,7 +586,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
     __shared__ uint64_t bar;
     __shared__ int failed;
     __shared__ unsigned top[2 * kMaxGroupHeads];                    // largest magnitudes, then scales, as bits
-    const int kv_ctas = (int)gridDim.x - a.q_ctas;
+    const int first_single = (int)gridDim.x - a.q_ctas - a.single_ctas, first_q = (int)gridDim.x - a.q_ctas;
     if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
         fence_mbar_init();
@@ -507,10 +595,29 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
     __syncthreads();                       // any warp may issue the first copies
     pdl_trigger();
     pdl_wait();
-    if ((int)blockIdx.x >= kv_ctas) {
+    if ((int)blockIdx.x >= first_single && (int)blockIdx.x < first_q) {
+        const int lane = threadIdx.x & 31, base = ((int)blockIdx.x - first_single) * kSingleTokens;
+        const int around = base - 1 + lane;                           // the window and a token to either side
+        const int64_t s = lane < kSingleTokens + 2 && around >= 0 && around < a.num_tokens ? __ldg(a.slots + around) : -1;
+        const int64_t before = __shfl_up_sync(0xffffffffu, s, 1), after = __shfl_down_sync(0xffffffffu, s, 1);
+        const bool alone = lane >= 1 && lane <= kSingleTokens && s >= 0 && s < a.num_slots &&
+                           !same_block(a, before, s) && !same_block(a, after, s);
+        const int jobs = (2 * a.num_kv_heads + 32 / UPR - 1) / (32 / UPR);
+        int done = 0;                                                 // jobs of the tokens before
+        for (unsigned todo = __ballot_sync(0xffffffffu, alone); todo; todo &= todo - 1, done += jobs) {
+            const int l = __ffs(todo) - 1;
+            const int64_t slot = __shfl_sync(0xffffffffu, s, l);
+            const int pos = a.rot ? __ldg(a.positions + base - 1 + l) : -1;
+            for (int j = ((int)(threadIdx.x >> 5) - done % W + W) % W; j < jobs; j += W)
+                append8_token<D, T, INTERLEAVED>(a, base - 1 + l, pos, slot, (slot & ((1ll << a.log2_block) - 1)) == 0,
+                                                 j * (32 / UPR), lane);
+        }
+        return;
+    }
+    if ((int)blockIdx.x >= first_q) {
         const unsigned groups = (unsigned)(a.num_heads + kQueryRows - 1) / kQueryRows;
         const unsigned per_token = groups * UPR;
-        const unsigned long long i = (unsigned long long)(blockIdx.x - kv_ctas) * kRopeThreads + threadIdx.x;
+        const unsigned long long i = (unsigned long long)(blockIdx.x - first_q) * kRopeThreads + threadIdx.x;
         const unsigned long long t64 = i / per_token;
         if (t64 >= (unsigned)a.num_tokens) return;
         const int t = (int)t64;
@@ -566,14 +673,16 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
         const bool mine = tl < last;
         const int64_t sl = mine ? __ldg(a.slots + tl) : -1;
         const int64_t before = mine && tl > 0 ? __ldg(a.slots + tl - 1) : -1;
+        const int64_t after = mine && tl + 1 < a.num_tokens ? __ldg(a.slots + tl + 1) : -1;
         const bool good = sl >= 0 && sl < a.num_slots;
         if (h0 == 0 && warp == 0 && sl >= 0) {
             if (a.rot) checked_position(a, tl, a.num_heads == 0);
             if (!good) latch(a.st, kFlagBadSlot, sl);
         }
-        const bool leads = good && !(before >= 0 && before < a.num_slots &&
-                                     (before >> a.log2_block) == (sl >> a.log2_block));
-        for (unsigned todo = __ballot_sync(0xffffffffu, leads); todo; todo &= todo - 1) {
+        // but for runs of one token: the CTAs after these take them
+        const bool leads = good && !same_block(a, before, sl) && same_block(a, after, sl);
+        unsigned todo = __ballot_sync(0xffffffffu, leads);
+        for (; todo; todo &= todo - 1) {
             const int src_lane = __ffs(todo) - 1, t = base + src_lane;
             const int64_t blk = __shfl_sync(0xffffffffu, sl, src_lane) >> a.log2_block;
             Run run = find_run(a, t, blk, lane);
@@ -646,7 +755,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
                 const int h = h0 + (j >> 1);
                 unsigned char *rows = static_cast<unsigned char *>(v ? a.v_cache : a.k_cache) +
                                       ((size_t)(blk * a.num_kv_heads + h) << a.log2_block) * D;
-                const float scale = grow_scale<D>(a, run, blk, h, v, __uint_as_float(top[j]), rows, lane);
+                float *sp = scale_of(a, blk, h, v);
+                const float scale = grow_scale<D>(a, run, sp, run.fresh ? 0.f : *sp, __uint_as_float(top[j]), rows, lane);
                 if (lane == 0) top[j] = __float_as_uint(scale);
             }
             __syncthreads();
@@ -671,11 +781,11 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
 // ---- host ---------------------------------------------------------------------------
 
 // From so many tokens on the copies' setup pays for itself (prompts of 32/8
-// heads: 2,000 tokens 16 us against 22, 1,000 tokens 13 against 10).  A decode
-// step of so many sequences goes the same way at twice the time: what their
-// tokens are to one another only the device sees.
+// heads: 1,000 tokens 13 us against 18, 500 tokens 15 against 10).  What the
+// tokens are to one another only the device sees: a decode step of so many
+// sequences takes its own way through either kernel.
 #ifndef PKV_BULK_TOKENS
-#define PKV_BULK_TOKENS 2048
+#define PKV_BULK_TOKENS 1024
 #endif
 constexpr int kBulkTokens = PKV_BULK_TOKENS;
 
@@ -698,20 +808,22 @@ cudaError_t launch_append(const RopeArgs &a, bool interleaved, bool fp8, cudaStr
         const unsigned long long qunits =
             (unsigned long long)a.num_tokens * ((a.num_heads + kQueryRows - 1) / kQueryRows) * UPR;
         b.q_ctas = (int)((qunits + kRopeThreads - 1) / kRopeThreads);
+        b.single_ctas = (a.num_tokens + kSingleTokens - 1) / kSingleTokens;
         auto kern = interleaved ? rotary_append8_bulk_kernel<D, T, true> : rotary_append8_bulk_kernel<D, T, false>;
         static std::atomic<unsigned long long> allowed[2];
         cudaError_t e = allow_smem(kern, kSlabBytes, allowed[interleaved]);
         if (e != cudaSuccess) return e;
         const size_t smem = (size_t)b.group_heads * ((2 * sizeof(T) * D) << a.log2_block);
-        return launch(kern, dim3((unsigned)(chunks * hgroups + b.q_ctas)), dim3(kRopeThreads), smem, stream, b);
+        return launch(kern, dim3((unsigned)(chunks * hgroups + b.single_ctas + b.q_ctas)),
+                      dim3(kRopeThreads), smem, stream, b);
     }
     const unsigned long long qunits = (unsigned long long)a.num_tokens * a.num_heads * UPR;
-    b.q_ctas = (int)((qunits + kRopeThreads - 1) / kRopeThreads);
-    const int most = (2 * a.num_kv_heads + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    b.q_ctas = (int)((qunits + kStepThreads - 1) / kStepThreads);
+    const int most = (2 * a.num_kv_heads + kStepThreads / 32 - 1) / (kStepThreads / 32);
     b.head_split = 1;
     while (b.head_split < most && a.num_tokens * b.head_split < 4 * sms) b.head_split++;
     return launch(interleaved ? rotary_append8_kernel<D, T, true> : rotary_append8_kernel<D, T, false>,
-                  dim3((unsigned)(a.num_tokens * b.head_split + b.q_ctas)), dim3(kRopeThreads), 0, stream, b);
+                  dim3((unsigned)(a.num_tokens * b.head_split + b.q_ctas)), dim3(kStepThreads), 0, stream, b);
 }
 
 pkv_status append_impl(const char *what, bool fp8, void *query_out, const void *query, const void *key,

@@ -205,6 +205,30 @@ def test_append8_long_call(cuda_device):
     _same8(ref, kc, vc, sc, "long")
 
 
+@pytest.mark.parametrize("T,Hkv", [(1023, 1), (1024, 3), (1500, 40)])
+def test_append8_large_step(cuda_device, T, Hkv):
+    """One token for each of many sequences, some padded, some blocks begun anew, scales that grow; a few runs of two."""
+    B, d, NB = 16, 64, 1600
+    x = Inputs(cuda_device, T, 2, Hkv, d, B, "bf16", 3, 32, NB=NB)
+    rng = np.random.default_rng(4)
+    x.k, x.dk = x.k * 8, x.dk * 8
+    for pairs in (False, True):
+        slots = rng.permutation(NB)[:T].astype(np.int64) * B + rng.integers(0, B - 1, T)
+        slots[rng.random(T) < 0.1] = -1
+        if pairs:
+            slots[701], slots[31] = slots[700] + 1, slots[30] + 1
+            slots[700] = -1 if slots[700] < 0 else slots[700]
+            slots[[31, 701]] = np.where(slots[[30, 700]] < 0, -1, slots[[31, 701]])
+        k0, v0, s0 = _random_cache8(NB, Hkv, B, d, 8)
+        kc, vc, sc = k0.to(cuda_device), v0.to(cuda_device), s0.to(cuda_device)
+        q = pkv.kv_rotary_and_cache_fp8(x.dq, x.dk, x.dv, x.dcs, x.dpos, kc, vc, sc, torch.from_numpy(slots).to(cuda_device))
+        pkv.check()
+        assert torch.equal(q.cpu(), rotate32(x.q, x.cs, x.positions, 32, "half").bfloat16())
+        ref = RefCache8(k0, v0, s0)
+        ref.append(rotate32(x.k, x.cs, x.positions, 32, "half").numpy(), x.v.float().numpy(), slots)
+        _same8(ref, kc, vc, sc, "step")
+
+
 def test_append8_special_values(cuda_device):
     """Zeros, the least and the largest magnitudes, infinities and NaN: what the definition says of each."""
     B, d = 8, 64
