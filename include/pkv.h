@@ -159,7 +159,8 @@ pkv_status kv_rotary_and_cache(void *query_out_dev, const void *query_dev, const
  * above; scales_dev holds, for every block and kv head, the key scale and the
  * value scale: value = code * scale.
  *   scales  fp32 [num_blocks][Hs][2], Hs = num_kv_heads rounded up to even:
- *           [b][g][0] for the keys, [b][g][1] for the values of kv head g
+ *           [b][g][0] for the keys, [b][g][1] for the values of kv head g;
+ *           finite and not negative.  The library's own are powers of two.
  * A block's codes (num_kv_heads * block_size * head_dim bytes) and its scales
  * (8 * Hs bytes) are multiples of 16 bytes: copy_blocks and swap_blocks move
  * them (keys, values and scales, one call each).
@@ -209,8 +210,8 @@ pkv_status kv_rotary_and_cache_fp8(void *query_out_dev, const void *query_dev, c
  *                   graphs or not, may follow one another on it; calls that
  *                   may overlap on the GPU need one each.  After a call that
  *                   reported PKV_ETIMEOUT, prepare it again.
- * num_seqs <= 65535 (2048 to a launch); any number of query heads per kv head;
- * scale finite.
+ * num_seqs <= 65535 (512 to a launch); num_heads <= 65535, any number of them
+ * per kv head; scale finite.
  * ------------------------------------------------------------------------- */
 pkv_status paged_attention_decode_fp8(void *out_dev, const void *query_dev,
                                       const void *key_cache_dev, const void *value_cache_dev,
@@ -234,7 +235,8 @@ pkv_status paged_attention_fp8_workspace_init(void *workspace_dev, size_t worksp
 /* ---------------------------------------------------------------------------
  * paged_attention_prefill_fp8 -- paged_attention_prefill over the 8-bit cache.
  * The contexts' blocks are first widened to `dtype` in the workspace (exact
- * for bf16, and for fp16 where code * scale is within its range), then the
+ * for bf16, and for fp16 where code * scale is within its range; full blocks
+ * that sequences share in the same place, as a common prefix, once), then the
  * prompt-phase kernel runs on them: two launches.  Arguments as for
  * paged_attention_prefill, but:
  *   max_context_len  host-side upper bound on every context_lens[s] (0 =

@@ -596,7 +596,10 @@ __global__ void __launch_bounds__(kPipes * 64, kCtasPerSm)
                 if (withq && lane == 0)
                     bulk_g2s(qs, qg + ((size_t)cur.s * a.num_heads + cur.h0) * D, q_bytes, &full[slot]);
             }
-            if (dead) break;
+            if (dead) {                                              // copies may still be under way
+                for (int k = kk < R ? 0 : kk - R; k < kk; k++) mbar_wait(&full[k % R], (k / R) & 1, kDrainLimitCycles);
+                break;
+            }
             while (step < 3) next_item();
             cur_t = nxt_t;
             cur = nx;
@@ -632,6 +635,8 @@ __global__ void __launch_bounds__(kPipes * 64, kCtasPerSm)
         const int slot = k % R;
         if (!__all_sync(kFull, mbar_wait(&full[slot], (k / R) & 1, kWaitLimitCycles))) {
             if (lane == 0) latch(a.st, kFlagTimeout, k);
+            // what the producer has under way in the other slots
+            for (int i = 1; i < R; i++) mbar_wait(&full[(k + i) % R], ((k + i) / R) & 1, kDrainLimitCycles);
             break;
         }
         const F8Meta md = meta[slot];
@@ -929,7 +934,7 @@ pkv_status check_cache8(const char *what, int num_heads, int num_kv_heads, int h
         return fail(PKV_EINVAL, "%s: head_dim %d not supported (64 or 128)", what, head_dim);
     if (!is_pow2(block_size) || block_size < kMinBlock || block_size > 128)
         return fail(PKV_EINVAL, "%s: block_size %d not a power of two in [4, 128]", what, block_size);
-    if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads)
+    if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || num_heads > 65535)
         return fail(PKV_EINVAL, "%s: %d query heads do not group over %d kv heads", what, num_heads, num_kv_heads);
     return PKV_OK;
 }

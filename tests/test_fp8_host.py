@@ -81,7 +81,7 @@ def _decode(**over):
     dict(d=96), dict(d=256), dict(B=12), dict(B=2), dict(B=256), dict(H=5), dict(H=0), dict(Hkv=0), dict(part=32), dict(part=-64),
     dict(mcl=65), dict(mcl=-1), dict(dt=2), dict(S=-1), dict(S=65536), dict(NB=-1), dict(mb=-1), dict(out=None), dict(q=None),
     dict(kc=None), dict(sc=None), dict(bt=None), dict(cl=None), dict(q=18), dict(sc=8), dict(ws=None), dict(ws=24), dict(wsb=128),
-    dict(scale=float("nan")), dict(scale=float("inf")), dict(mb=1 << 24, part=64),
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(mb=1 << 24, part=64), dict(H=65536),
 ])
 def test_decode_refusals(over):
     assert _decode(**over) == 1 and "paged_attention_decode_fp8" in _message()

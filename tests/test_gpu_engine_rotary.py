@@ -152,3 +152,82 @@ def test_an_8_bit_cache_does_not_swap_with_a_16_bit_pool(cuda_device):
     with pytest.raises(ValueError):
         eng.swap_out([s], HostKVPool(8, 2, 64, 16, torch.float16))
     assert eng.alloc.seq_len(s) == 5
+
+
+def test_a_captured_step_replays(cuda_device):
+    """The prepared calls of a step (rotating 8-bit write, attention) captured once and replayed over changing inputs and
+    lengths give what the eager calls give."""
+    H, Hkv, d, B, S = 8, 2, 64, 16, 5
+    rotary = RotaryPositions.make(512, 64, cuda_device)
+    engines = [PagedKVCache(80, Hkv, d, B, F8, cuda_device, 16, rotary=rotary) for _ in range(2)]
+    for e in engines:
+        for pool in e._pools():
+            pool.zero_()
+    seqs = [[e.new_sequence(0) for _ in range(S)] for e in engines]
+    g = torch.Generator().manual_seed(2)
+    q, k, v = (torch.empty(S, h, d, dtype=torch.bfloat16, device=cuda_device) for h in (H, Hkv, Hkv))
+    out = [torch.empty_like(q) for _ in engines]
+    fixed = graph = None
+    for i in range(40):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, generator=g) * (1 + i % 3))
+        steps = [e.upload(e.plan_step(s)) for e, s in zip(engines, seqs)]
+        engines[0].prepare(q, k, v, steps[0], out[0])()
+        if graph is None:
+            fixed = steps[1]
+            fixed.max_context_len = 256
+            stream = torch.cuda.Stream()
+            prep = engines[1].prepare(q, k, v, fixed, out[1], stream=stream)
+            torch.cuda.synchronize()
+            prep()                                   # kernels are set up outside capture
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                prep()
+        else:
+            for name in ("slots", "tables", "context_lens", "positions"):
+                getattr(fixed, name).copy_(getattr(steps[1], name))
+            graph.replay()
+        torch.cuda.synchronize()
+        pkv.check()
+        for a, b in zip(engines[0]._pools(), engines[1]._pools()):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        # another partition size (the captured call's bound is larger) sums in another order
+        assert torch.allclose(out[0].float(), out[1].float(), rtol=2.0 ** -7, atol=2.0 ** -12 * float(v.abs().max()))
+
+
+def test_bindings_refuse_what_does_not_fit(cuda_device):
+    dev = cuda_device
+    kc = torch.zeros(4, 2, 16, 64, dtype=F8, device=dev)
+    sc = pkv.kv_scales(4, 2, dev)
+    k = torch.zeros(3, 2, 64, dtype=torch.float16, device=dev)
+    q = torch.zeros(3, 4, 64, dtype=torch.float16, device=dev)
+    cs = pkv.rotary_table(32, 64, device=dev)
+    pos = torch.zeros(3, dtype=torch.int32, device=dev)
+    slots = torch.arange(3, device=dev)
+    call = lambda **o: pkv.kv_rotary_and_cache_fp8(*(dict(dict(q=q, k=k, v=k, cs=cs, pos=pos, kc=kc, vc=kc.clone(), sc=sc, s=slots), **o)[n]  # noqa: E731
+                                                     for n in ("q", "k", "v", "cs", "pos", "kc", "vc", "sc", "s")))
+    call()
+    for o in (dict(k=k.bfloat16()), dict(v=k.float()), dict(q=q.cpu()), dict(kc=kc.view(torch.uint8)), dict(pos=pos.long()),
+              dict(s=slots.int()), dict(sc=sc.double()), dict(k=k.float(), v=k.float(), q=q.float())):
+        with pytest.raises(TypeError):
+            call(**o)
+    for o in (dict(k=k[:, :1]), dict(k=k[:, :, ::2]), dict(v=k.expand(1, 3, 2, 64)[0].transpose(0, 1)), dict(pos=pos[:2]),
+              dict(sc=sc[:, :1]), dict(s=slots[:2]), dict(cs=cs[..., 0]), dict(cs=None, pos=None), dict(k=k[:1].expand(3, 2, 64)),
+              dict(pos=None)):
+        with pytest.raises(ValueError):
+            call(**o)
+    with pytest.raises(ValueError):
+        pkv.kv_rotary_and_cache_fp8(q, k, k, cs, pos, kc, kc.clone(), sc, slots, layout="pairs")
+    with pytest.raises(pkv.PkvError):                      # a table wider than the head
+        call(cs=pkv.rotary_table(32, 128, device=dev))
+    with pytest.raises(ValueError):
+        pkv.rotary_table(32, 64, scaling="ntk", device=dev)
+    out = torch.empty_like(q)
+    bt, cl = torch.zeros(3, 1, dtype=torch.int32, device=dev), torch.ones(3, dtype=torch.int32, device=dev)
+    pkv.paged_attention_decode_fp8(out, q, kc, kc, sc, bt, cl)
+    for o in (dict(out=out.bfloat16()), dict(q=q.float()), dict(kc=kc.half()), dict(bt=bt.long()), dict(cl=cl.cpu())):
+        a = dict(dict(out=out, q=q, kc=kc, bt=bt, cl=cl), **o)
+        with pytest.raises((TypeError, ValueError)):
+            pkv.paged_attention_decode_fp8(a["out"], a["q"], a["kc"], kc, sc, a["bt"], a["cl"])
+    pkv.check()
