@@ -124,7 +124,9 @@ __device__ __forceinline__ void load_cos_sin(float4 (&cs)[4], const RopeArgs &a,
 // x[0..7] = chunk a, x[8..15] = chunk b, turned in place.  The products and
 // their sum are rounded one by one (no fused multiply-add), so that the
 // result is that of the formula in 32 bits, whoever evaluates it: a value on
-// the border between two 8-bit codes then falls the same way.
+// the border between two 8-bit codes then falls the same way.  (Instructions
+// on two numbers at once do not serve: the assembler fuses their products and
+// sums.)
 template <bool INTERLEAVED> __device__ __forceinline__ void turn(float (&x)[16], const float4 (&cs)[4]) {
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -336,7 +338,11 @@ __device__ __forceinline__ void store_codes(unsigned char *row, const Unit &x, f
     if ((__float_as_uint(scale) & 0x7fffffu) == 0u && scale < 0x1p126f) {
         const float inv = __uint_as_float(0x7f000000u - __float_as_uint(scale));   // 2^-e
 #pragma unroll
-        for (int e = 0; e < 16; e++) f[e] *= inv;
+        for (int e = 0; e < 16; e += 2) {
+            const unsigned long long y = mul2(pack2(f[e], f[e + 1]), pack2(inv, inv));
+            f[e] = lo2(y);
+            f[e + 1] = hi2(y);
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < 16; e++) f[e] = __fdiv_rn(f[e], scale);
