@@ -358,3 +358,47 @@ def test_prefill_shared_prefix(cuda_device):
         want, mag, vmax = attention64(q[rows].double().numpy(), c.kvals, c.vvals, c.tables[s], n, 1 / math.sqrt(d))
         tol = attention_tolerance(want, mag, vmax, n, d, torch.finfo(q.dtype).eps, 11)
         assert np.all(np.abs(got[rows] - want) <= tol), (s, np.abs(got[rows] - want).max())
+
+
+def test_decode_very_long_context(cuda_device):
+    """More than a thousand partitions of one sequence beside a short one."""
+    c = Case8(cuda_device, (300001, 7), 2, 1, 64, 64, "f16", seed=31)
+    out = c.decode()
+    pkv.check()
+    c.check(out)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_pools_past_32_bits(cuda_device, fp8):
+    """Writes, decode and prompt phase at the end of pools whose offsets pass 2^32 give what a small pool gives."""
+    Hkv, H, B, d, T = 8, 16, 128, 128, 150
+    dt = torch.bfloat16
+    far = (1 << 32) // (Hkv * B * d) + 40
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(T, h, d, generator=g).to(dt).to(cuda_device) for h in (H, Hkv, Hkv))
+    cs = pkv.rotary_table(512, d, device=cuda_device)
+    pos = torch.arange(T, dtype=torch.int32, device=cuda_device)
+    got = []
+    for NB, blocks in ((3, (2, 0)), (far, (far - 1, far - 9))):
+        pool = lambda: torch.empty(NB, Hkv, B, d, dtype=torch.float8_e4m3fn if fp8 else dt, device=cuda_device)  # noqa: E731
+        kc, vc = pool(), pool()
+        slots = torch.tensor([blocks[t // B] * B + t % B for t in range(T)], device=cuda_device)
+        table = torch.tensor([blocks], dtype=torch.int32, device=cuda_device)
+        ctx = torch.tensor([T], dtype=torch.int32, device=cuda_device)
+        start = torch.tensor([0, T], dtype=torch.int32, device=cuda_device)
+        if fp8:
+            sc = pkv.kv_scales(NB, Hkv, cuda_device)
+            r = pkv.kv_rotary_and_cache_fp8(q, k, v, cs, pos, kc, vc, sc, slots)
+            a = pkv.paged_attention_decode_fp8(torch.empty_like(r[-1:]), r[-1:].contiguous(), kc, vc, sc, table, ctx)
+            b = pkv.paged_attention_prefill_fp8(torch.empty_like(r), r, kc, vc, sc, table, ctx, start)
+            got.append([r, a, b, sc[list(blocks)]])
+        else:
+            r = pkv.kv_rotary_and_cache(q, k, v, cs, pos, kc, vc, slots)
+            a = pkv.paged_attention_decode(torch.empty_like(r[-1:]), r[-1:].contiguous(), kc, vc, table, ctx)
+            got.append([r, a])
+        pkv.check()
+        got[-1] += [kc[list(blocks)].view(torch.uint8)[0], vc[blocks[1], :, :T - B].view(torch.uint8)]
+        del kc, vc
+        torch.cuda.empty_cache()
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
