@@ -32,32 +32,38 @@ struct TurnTable {
     unsigned long long turn[kMaxRotaryDim / 2];
 };
 
-// Cosine and sine of a 64-bit fraction of a turn: the nearest quarter turn
-// swaps and negates; what is left, y within pi / 4 of zero, takes the Taylor
-// series of both (to y^9 and y^10: the next terms are below 2^-29 and 2^-33),
-// a third of the instructions of a sincos that would reduce its argument again.
-__device__ __forceinline__ float2 cos_sin_of(unsigned long long turns, float magnitude) {
-    const int t = (int)(turns >> 32);                      // signed fraction of a turn, 2^-32 units
-    const int quarter = (int)(((unsigned)t + 0x20000000u) >> 30);   // nearest quarter turn
-    const float y = (float)(int)((unsigned)t - ((unsigned)quarter << 30)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
-    const float z = y * y;
-    float s = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
-    s = fmaf(z, s, 1.f / 120.f);
-    s = fmaf(z, s, -1.f / 6.f);
-    s = fmaf(y * z, s, y);
-    float c = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
-    c = fmaf(z, c, -1.f / 720.f);
-    c = fmaf(z, c, 1.f / 24.f);
-    c = fmaf(z, c, -0.5f);
-    c = fmaf(z, c, 1.f);
-    const float cc = (quarter & 1) ? -s : c, ss = (quarter & 1) ? c : s;
-    const float sign = (quarter & 2) ? -magnitude : magnitude;
-    return make_float2(cc * sign, ss * sign);
+// Cosines and sines of two 64-bit fractions of a turn, (cos, sin, cos, sin): the
+// nearest quarter turn swaps and negates; what is left, y within pi / 4 of zero,
+// takes the Taylor series of both (to y^9 and y^10: the next terms are below
+// 2^-29 and 2^-33), the two angles in one instruction each.
+__device__ __forceinline__ float4 cos_sin_of(unsigned long long turns0, unsigned long long turns1, float magnitude) {
+    const unsigned t0 = (unsigned)(turns0 >> 32), t1 = (unsigned)(turns1 >> 32);    // fractions of a turn, 2^-32 units
+    const unsigned q0 = (t0 + 0x20000000u) >> 30, q1 = (t1 + 0x20000000u) >> 30;    // nearest quarter turns
+    const auto both = [](float x) { return pack2(x, x); };
+    const unsigned long long y = mul2(pack2((float)(int)(t0 - (q0 << 30)), (float)(int)(t1 - (q1 << 30))),
+                                      both(1.4629180792671596e-9f));                // 2 pi / 2^32
+    const unsigned long long z = mul2(y, y);
+    unsigned long long s = fma2(z, both(1.f / 362880.f), both(-1.f / 5040.f));
+    s = fma2(z, s, both(1.f / 120.f));
+    s = fma2(z, s, both(-1.f / 6.f));
+    s = fma2(mul2(y, z), s, y);
+    unsigned long long c = fma2(z, both(-1.f / 3628800.f), both(1.f / 40320.f));
+    c = fma2(z, c, both(-1.f / 720.f));
+    c = fma2(z, c, both(1.f / 24.f));
+    c = fma2(z, c, both(-0.5f));
+    c = fma2(z, c, both(1.f));
+    s = mul2(s, both(magnitude));
+    c = mul2(c, both(magnitude));
+    // quarter turns 1 and 3 swap; the cosine changes its sign in 1 and 2, the sine in 2 and 3
+    const float c0 = (q0 & 1) ? lo2(s) : lo2(c), s0 = (q0 & 1) ? lo2(c) : lo2(s);
+    const float c1 = (q1 & 1) ? hi2(s) : hi2(c), s1 = (q1 & 1) ? hi2(c) : hi2(s);
+    const auto flip = [](float x, unsigned q) { return __uint_as_float(__float_as_uint(x) ^ ((q & 2u) << 30)); };
+    return make_float4(flip(c0, q0 + 1u), flip(s0, q0), flip(c1, q1 + 1u), flip(s1, q1));
 }
 
 // Thread t owns two neighbouring pairs (one 16-byte store) of every
 // (threads / columns)-th position of its CTA's stretch: its turns stay in
-// registers.  131,072 x 128: 12.7 us, 5.3 TB/s written; 64 % of the issue slots.
+// registers.  131,072 x 128: 11.5 us, 5.9 TB/s written.
 __global__ void __launch_bounds__(kRopeThreads) rotary_table_kernel(float4 *__restrict__ out,
                                                                     const __grid_constant__ TurnTable tab,
                                                                     int num_positions, int columns, int rows,
@@ -70,9 +76,8 @@ __global__ void __launch_bounds__(kRopeThreads) rotary_table_kernel(float4 *__re
     const int begin = blockIdx.x * per_cta;
     const int end = begin + per_cta < num_positions ? begin + per_cta : num_positions;
     for (int p = begin + r; p < end; p += rows) {
-        const float2 a = cos_sin_of(t0 * (unsigned long long)p, magnitude);
-        const float2 b = cos_sin_of(t1 * (unsigned long long)p, magnitude);
-        out[(size_t)p * columns + c] = make_float4(a.x, a.y, b.x, b.y);
+        out[(size_t)p * columns + c] =
+            cos_sin_of(t0 * (unsigned long long)p, t1 * (unsigned long long)p, magnitude);
     }
 }
 
@@ -957,8 +962,8 @@ pkv_status rotary_table(float *cos_sin, int num_positions, int rotary_dim, doubl
         tab.turn[i] = (unsigned long long)std::nearbyint(theta / kTwoPi * 0x1p64);   // theta <= 1: below 2^62
     }
     const int columns = rotary_dim / 4, rows = kRopeThreads / columns;
-    // one wave of CTAs for long tables (131,072 x 128: 12.6 us against 20.2 with 32 positions to a CTA), since
-    // fetching the turns costs each CTA about a microsecond; at least four positions to a thread in short ones
+    // one wave of CTAs for long tables, since fetching the turns costs each CTA about a microsecond (131,072 x 128:
+    // 7 us more with 32 positions to a CTA); at least four positions to a thread in short ones
     const int wave = (sm_count() > 0 ? sm_count() : 1) * 8;
     int per_cta = (num_positions + wave - 1) / wave;
     per_cta = per_cta < 4 * rows ? 4 * rows : (per_cta + rows - 1) / rows * rows;
