@@ -109,8 +109,9 @@ pkv_status kv_reshape_and_cache(const void *key_dev, const void *value_dev,
  *              angle, slow ones are stretched.
  * magnitude (usually 1) scales queries and keys alike.
  *   cos_sin_dev   fp32 [num_positions][rotary_dim / 2][2], written whole
- * rotary_dim a multiple of 16 up to 256; base > 1; factor >= 1 (ignored when
- * UNSCALED); BY_PARTS: original_positions > 0, low_turns < high_turns.
+ * num_positions up to 2^30; rotary_dim a multiple of 16 up to 256; base > 1;
+ * magnitude finite in fp32; factor >= 1 (ignored when UNSCALED); BY_PARTS:
+ * original_positions > 0, low_turns < high_turns.
  * ------------------------------------------------------------------------- */
 pkv_status rotary_table(float *cos_sin_dev, int num_positions, int rotary_dim, double base,
                         pkv_rotary_scaling scaling, double factor, int original_positions,
@@ -200,7 +201,8 @@ pkv_status kv_rotary_and_cache_fp8(void *query_out_dev, const void *query_dev, c
  * the same attention with K_t = key code * scales[b][g][0] and
  * V_t = value code * scales[b][g][1].  dtype is that of query and out.  The
  * codes enter the products exactly; fp16 queries too, bf16 ones too unless
- * they lie 2^31 below their row's largest; probabilities carry 22 bits.
+ * they lie 2^31 below their row's largest; probabilities carry 22 bits, and
+ * those below 2^-126 of their row's largest count as zero.
  * Arguments as for paged_attention_decode, but:
  *   partition_size  0 (the library chooses) or a multiple of 64.
  *   workspace_dev   at least paged_attention_decode_fp8_workspace_size(...)

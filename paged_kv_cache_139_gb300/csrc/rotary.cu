@@ -10,6 +10,7 @@
 // The append kernels rotate the queries into query_out and the keys into the
 // cache, and copy the values, in one launch: each element is read once and
 // written once, which is what bounds them.
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -20,6 +21,7 @@ namespace pkv {
 namespace {
 
 constexpr int kMaxRotaryDim = 256;
+constexpr int kMaxPositions = 1 << 30;      // of a table: positions and strides past its end stay in 31 bits
 constexpr int kRopeThreads = 256;
 
 // ---- the table ---------------------------------------------------------------
@@ -928,11 +930,12 @@ pkv_status rotary_table(float *cos_sin, int num_positions, int rotary_dim, doubl
                         double factor, int original_positions, double low_turns, double high_turns, double magnitude,
                         struct CUstream_st *stream) {
     using namespace pkv;
-    if (num_positions < 0 || rotary_dim <= 0 || rotary_dim % 16 || rotary_dim > kMaxRotaryDim)
-        return fail(PKV_EINVAL, "rotary_table: bad sizes (%d positions, rotary_dim %d: a multiple of 16 up to %d)",
-                    num_positions, rotary_dim, kMaxRotaryDim);
-    if (!(base > 1.0) || !std::isfinite(base) || !std::isfinite(magnitude))
-        return fail(PKV_EINVAL, "rotary_table: base %g must be above 1, magnitude %g finite", base, magnitude);
+    if (num_positions < 0 || num_positions > kMaxPositions || rotary_dim <= 0 || rotary_dim % 16 ||
+        rotary_dim > kMaxRotaryDim)
+        return fail(PKV_EINVAL, "rotary_table: bad sizes (%d positions: up to %d, rotary_dim %d: a multiple of 16 up to %d)",
+                    num_positions, kMaxPositions, rotary_dim, kMaxRotaryDim);
+    if (!(base > 1.0) || !std::isfinite(base) || !(std::fabs(magnitude) <= (double)FLT_MAX))
+        return fail(PKV_EINVAL, "rotary_table: base %g must be above 1, magnitude %g finite in fp32", base, magnitude);
     if (scaling != PKV_ROTARY_UNSCALED && scaling != PKV_ROTARY_LINEAR && scaling != PKV_ROTARY_BY_PARTS)
         return fail(PKV_EINVAL, "rotary_table: bad scaling %d", (int)scaling);
     if (scaling != PKV_ROTARY_UNSCALED && (!(factor >= 1.0) || !std::isfinite(factor)))

@@ -33,6 +33,12 @@ def test_table_refusals(over):
     assert _call("rotary_table", TABLE, TABLE, over) == 1 and "rotary_table" in _message()
 
 
+@pytest.mark.parametrize("over", [dict(n=2 ** 30 + 1), dict(n=2 ** 31 - 1), dict(mag=1e39), dict(mag=-float("inf"))])
+def test_table_limits(over):
+    """Positions past the end of the table's stretches have to fit 31 bits, the magnitude fp32."""
+    assert _call("rotary_table", TABLE, TABLE, over) == 1 and "rotary_table" in _message()
+
+
 def test_empty_calls_are_ok():
     assert _call("rotary_table", TABLE, TABLE, dict(n=0)) == 0
     assert _append(False, T=0) == 0 and _append(True, T=0) == 0
