@@ -98,10 +98,10 @@ struct RopeArgs {
     int64_t num_slots;
     int num_tokens, num_heads, num_kv_heads;
     int rot, num_positions, log2_block;
-    int q_ctas;                    // 8-bit append: CTAs that rotate queries (after the others)
-    int single_ctas;               // 8-bit append of many: CTAs that append runs of one token (before those)
-    int head_split;                // 8-bit append of few tokens: CTAs that share a token's heads
-    int group_heads;               // 8-bit append of many: kv heads of a CTA
+    // 8-bit append: see rotary_append8_kernel
+    int single_ctas, single_tokens, single_parts;
+    int run_ctas, run_tokens, group_heads;
+    unsigned long long run_share;  // 2^32 times the share of run_ctas in the CTAs that they are mixed into
 };
 
 // A thread's unit of a head: sixteen elements as two 16-byte chunks that
@@ -313,7 +313,7 @@ __device__ __forceinline__ void round_again(uint4 *q, float ratio) {
     *q = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// The block's scale for new rows of magnitude up to amax (any lane's), stored;
+// The block's scale for new rows of magnitude up to amax, stored;
 // the block's other rows are rounded again where it grows.  `had`: the scale
 // before, not looked at when the run starts the block anew.  By one warp.
 template <int D>
@@ -321,8 +321,6 @@ __device__ __forceinline__ float grow_scale(const RopeArgs &a, const Run &run, f
                                             unsigned char *rows, int lane) {
     constexpr int UPR = D / 16, RP = 32 / UPR;
     const int r = lane / UPR, u = lane % UPR;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     amax = fminf(amax, 3.4028235e38f);             // infinities; fmaxf has passed NaN over
     // a write at offset 0 starts the block anew; otherwise its scale can only grow
     if (run.fresh) had = 0.f;
@@ -361,104 +359,16 @@ __device__ __forceinline__ void store_codes(unsigned char *row, const Unit &x, f
         make_uint2(to_e4m3x4(f[8], f[9], f[10], f[11]), to_e4m3x4(f[12], f[13], f[14], f[15]));
 }
 
-// A lane's rows of a chunk of rows of a run: their offsets in the block
-// (-1: none) and positions (-1: not to be rotated).
-template <int CH> struct RowPlan {
-    int off[CH], pos[CH];
-};
-
-// pos0: the position of the lane's first row of the first chunk, if it is one.
-template <int RP, int CH>
-__device__ __forceinline__ void plan_rows(RowPlan<CH> &p, const RopeArgs &a, const Run &run, int base, int r, int pos0) {
-#pragma unroll
-    for (int i = 0; i < CH; i++) {
-        const int row = base + i * RP + r;
-        p.off[i] = p.pos[i] = -1;
-        if (row < run.n) {
-            p.off[i] = (int)(__ldg(a.slots + run.t + row) & ((1 << a.log2_block) - 1));
-            const int pos = !a.rot ? -1 : base == 0 && i == 0 ? pos0 : __ldg(a.positions + run.t + row);
-            if (pos >= 0 && pos < a.num_positions) p.pos[i] = pos;    // others are latched by the caller
-        }
-    }
-}
-
-// The rows of a run of one kv head, keys or values, into block blk, by one
-// warp: D/16 lanes to a row.  A pass over the rows takes their largest
-// magnitude, the block gets its scale, and a second pass writes the codes;
-// `plan` is that of the first chunk, and a run of so few rows stays in registers
-// between the two.
-constexpr int kChunkRows = 2;              // rows per lane and chunk
-
-template <int D, typename T, bool INTERLEAVED>
-__device__ __forceinline__ void append8_rows(const RopeArgs &a, const Run &run, const RowPlan<kChunkRows> &plan,
-                                             int64_t blk, int h, bool isv, int lane) {
-    constexpr int UPR = D / 16;            // lanes per row
-    constexpr int RP = 32 / UPR;           // rows side by side
-    constexpr int CH = kChunkRows;
-    const int r = lane / UPR, u = lane % UPR;
-    const Unit x = unit_at<INTERLEAVED>(u, isv ? 0 : a.rot);
-    const T *src = (isv ? static_cast<const T *>(a.v) : static_cast<const T *>(a.k)) + h * D;
-    const int64_t stride = isv ? a.v_stride : a.k_stride;
-    RowPlan<CH> p = plan;
-    float *sp = scale_of(a, blk, h, isv);
-    const float had = run.fresh ? 0.f : *sp;
-    float y[CH][16];
-
-    auto load = [&](int base) {
-        uint4 ra[CH], rb[CH];
-#pragma unroll
-        for (int i = 0; i < CH; i++) {
-            ra[i] = rb[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (p.off[i] >= 0) {
-                const T *q = src + (run.t + base + i * RP + r) * stride;
-                ra[i] = *reinterpret_cast<const uint4 *>(q + x.a);
-                rb[i] = *reinterpret_cast<const uint4 *>(q + x.b);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < CH; i++) {
-            widen<T>(y[i], ra[i], rb[i]);
-            if (x.rotated && p.pos[i] >= 0) {
-                float4 cs[4];
-                load_cos_sin(cs, a, p.pos[i], u);
-                turn<INTERLEAVED>(y[i], cs);
-            }
-        }
-    };
-
-    float amax = 0.f;
-    for (int base = 0; base < run.n; base += CH * RP) {
-        if (base > 0) plan_rows<RP, CH>(p, a, run, base, r, -1);
-        load(base);
-#pragma unroll
-        for (int i = 0; i < CH; i++)
-#pragma unroll
-            for (int e = 0; e < 16; e++) amax = fmaxf(amax, fabsf(y[i][e]));
-    }
-    unsigned char *rows = static_cast<unsigned char *>(isv ? a.v_cache : a.k_cache) +
-                          ((size_t)(blk * a.num_kv_heads + h) << a.log2_block) * D;
-    const float scale = grow_scale<D>(a, run, sp, had, amax, rows, lane);
-
-    for (int base = 0; base < run.n; base += CH * RP) {
-        if (run.n > CH * RP) {
-            plan_rows<RP, CH>(p, a, run, base, r, base == 0 ? plan.pos[0] : -1);
-            load(base);
-        }
-#pragma unroll
-        for (int i = 0; i < CH; i++)
-            if (p.off[i] >= 0) store_codes(rows + (size_t)p.off[i] * D, x, y[i], scale);
-    }
-}
-
 // A run of one token, the usual one of a decode step: its key and value rows j
-// = j0 + lane / (D/16) (the kv heads' keys, then their values) side by side.
+// = j0 + lane / (D/16) (the keys of `heads` kv heads from h0 on, then their
+// values) side by side.
 template <int D, typename T, bool INTERLEAVED>
-__device__ __forceinline__ void append8_token(const RopeArgs &a, int t, int pos, int64_t slot, bool fresh, int j0,
-                                              int lane) {
+__device__ __forceinline__ void append8_token(const RopeArgs &a, int t, int pos, int64_t slot, bool fresh, int h0,
+                                              int heads, int j0, int lane) {
     constexpr int UPR = D / 16;
     const int u = lane % UPR, j = j0 + lane / UPR;
-    const bool active = j < 2 * a.num_kv_heads, isv = j >= a.num_kv_heads;
-    const int h = isv ? j - a.num_kv_heads : j;
+    const bool active = j < 2 * heads, isv = j >= heads;
+    const int h = h0 + (isv ? j - heads : j);
     const int off = (int)(slot & ((1ll << a.log2_block) - 1));
     const int64_t blk = slot >> a.log2_block;
     const Unit x = unit_at<INTERLEAVED>(u, isv ? 0 : a.rot);
@@ -494,69 +404,6 @@ __device__ __forceinline__ void append8_token(const RopeArgs &a, int t, int pos,
     store_codes(rows + (size_t)off * D, x, y, scale);
 }
 
-// Few tokens (a decode step): the first CTAs append, head_split to a token,
-// their warps taking (kv head, keys or values) in turn; the CTAs after them
-// rotate queries, a thread to a unit.  Bound by latency: everything that a
-// token needs is requested as early as its address is known.  256 tokens of
-// 32/8 heads: 3.4 us (6.3 with a warp to each key or value row).
-constexpr int kStepThreads = 128;
-
-template <int D, typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kStepThreads, 6) rotary_append8_kernel(const RopeArgs a) {
-    constexpr int UPR = D / 16, RP = 32 / UPR;
-    constexpr int W = kStepThreads / 32;
-    pdl_trigger();
-    pdl_wait();
-    const int kv_ctas = (int)gridDim.x - a.q_ctas;
-    if ((int)blockIdx.x >= kv_ctas) {
-        const unsigned per_token = (unsigned)a.num_heads * UPR;
-        const unsigned long long i = (unsigned long long)(blockIdx.x - kv_ctas) * kStepThreads + threadIdx.x;
-        const unsigned long long t64 = i / per_token;
-        if (t64 >= (unsigned)a.num_tokens) return;
-        const int t = (int)t64;
-        const int r = (int)(i - t64 * per_token);
-        const int row = r / UPR;
-        const int pos = checked_position(a, t, r == 0);
-        if (pos < 0) return;
-        rotate_row<T, INTERLEAVED>(a, static_cast<const T *>(a.q) + t * a.q_stride + row * D,
-                                   static_cast<T *>(a.q_out) + ((size_t)t * a.num_heads + row) * D, r % UPR, pos);
-        return;
-    }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x % a.head_split, t = (int)(blockIdx.x / a.head_split);
-    // one round trip for what says where the token goes: the slots around it and the rows' positions
-    const int r = lane / UPR, around = t - 1 + lane;
-    const int64_t s = around >= 0 && around < a.num_tokens ? __ldg(a.slots + around) : -1;
-    const int pos0 = a.rot && t + r < a.num_tokens ? __ldg(a.positions + t + r) : -1;
-    const int64_t mine = __shfl_sync(0xffffffffu, s, 1), before = __shfl_sync(0xffffffffu, s, 0);
-    if (mine < 0) return;                                             // padding token
-    if (split == 0 && warp == 0 && lane == 0) {
-        if (a.rot && (pos0 < 0 || pos0 >= a.num_positions) && a.num_heads == 0) latch(a.st, kFlagBadPosition, pos0);
-        if (mine >= a.num_slots) latch(a.st, kFlagBadSlot, mine);
-    }
-    if (mine >= a.num_slots) return;
-    const int64_t blk = mine >> a.log2_block;
-    // a run begins at a token whose predecessor is not of its block
-    if (same_block(a, before, mine)) return;
-    const bool in = lane > 0 && same_block(a, s, mine);
-    const unsigned m = __ballot_sync(0xffffffffu, in) >> 1;
-    Run run;
-    run.t = t;
-    run.n = __ffs(~m) - 1;
-    run.fresh = __any_sync(0xffffffffu, lane > 0 && lane <= run.n && (s & ((1ll << a.log2_block) - 1)) == 0);
-    if (run.n == 31) run = find_run(a, t, blk, lane);                 // and perhaps more
-    if (run.n == 1) {
-        const int pos = __shfl_sync(0xffffffffu, pos0, 0);
-        for (int j = (split * W + warp) * RP; j < 2 * a.num_kv_heads; j += a.head_split * W * RP)
-            append8_token<D, T, INTERLEAVED>(a, t, pos, mine, run.fresh, j, lane);
-        return;
-    }
-    RowPlan<kChunkRows> plan;
-    plan_rows<RP, kChunkRows>(plan, a, run, 0, r, pos0);
-    for (int j = split * W + warp; j < 2 * a.num_kv_heads; j += a.head_split * W)
-        append8_rows<D, T, INTERLEAVED>(a, run, plan, blk, j >> 1, j & 1, lane);
-}
-
 // The largest magnitude of eight 16-bit values, NaN passed over.
 template <typename T> __device__ __forceinline__ float largest8(const uint4 &w);
 template <> __device__ __forceinline__ float largest8<__half>(const uint4 &w) {
@@ -578,32 +425,39 @@ __device__ __forceinline__ uint4 load_shared16(const void *p) {
     return v;
 }
 
-// Many tokens (prompts): a CTA looks over block_size tokens for those that
-// begin a run (about one does) and takes group_heads kv heads of it.  The run's
-// keys and values come as bulk copies of whole row pieces into shared memory,
-// 64 KB at a time with three CTAs to an SM, which keeps more bytes under way
-// than registers hold.  A thread keeps to one unit of a row, whose cosines it
-// holds, and goes through the heads twice: for the magnitudes, and, when the
-// scales are known, for the codes.  The CTAs after them look over sixteen tokens
-// each for runs of one token (all of a large decode step), a warp to rows of
-// one, and the last ones rotate queries, a thread to a unit of four heads.
-// 16,381 tokens of 32/32 heads: 133 us, 5.1 TB/s (200 with two passes of loads
-// into registers); half the issue slots are taken, by the two passes.
-constexpr int kSingleTokens = 16;
-constexpr int kSlabBytes = 64 * 1024;
+// CTAs of three kinds.
+//  * Runs of one token (a decode step's): a CTA looks over single_tokens tokens
+//    for them, a warp to key and value rows of one side by side; in small calls
+//    single_parts CTAs share a token's heads.  Bound by latency: everything
+//    that a token needs is requested as soon as its slot is known.
+//  * Longer runs (prompts): a CTA looks over run_tokens tokens for those that
+//    begin a run (about one of block_size does) and takes group_heads kv heads of
+//    it.  The run's keys and values come as bulk copies of whole row pieces into
+//    shared memory, 32 KB at a time with five CTAs to an SM, which keeps more
+//    bytes under way than registers hold.  A thread keeps to one unit of a row,
+//    whose cosines it holds, and goes through the heads' keys and values twice:
+//    for the magnitudes, and, when the scales are known, for the codes.
+//  * Queries: a thread to a unit of four heads.  These wait for memory while the
+//    second kind computes, so the two are mixed in the grid (16,381 tokens of
+//    32/32 heads: 124 us with the queries last, 114 so; of 32/8: 68 and 59).
+// 16,381 tokens of 32/32 heads: 114 us, 6.0 TB/s (200 with two passes of loads
+// into registers, 133 with 64 KB and 256 threads to a CTA, half on keys and half
+// on values); a step of 256 tokens of 32/8 heads: 3.0 us.
+constexpr int kAppend8Threads = 128;
+constexpr int kAppend8Ctas = 5;                                     // to an SM
+constexpr int kSlabBytes = 32 * 1024;                               // one head of a block of 128 takes twice that
 constexpr int kMaxGroupHeads = kSlabBytes / (4 * 64 * 4);           // blocks of 4 tokens, head_dim 64
 constexpr int kQueryRows = 4;
+static_assert(2 * kMaxGroupHeads <= kAppend8Threads, "a thread clears a magnitude");
 
 template <int D, typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kAppend8Threads, kAppend8Ctas) rotary_append8_kernel(const RopeArgs a) {
     constexpr int UPR = D / 16;
-    constexpr int W = kRopeThreads / 32;
-    constexpr int kRowsAtOnce = kRopeThreads / 2 / UPR;
+    constexpr int W = kAppend8Threads / 32;
     extern __shared__ __align__(16) unsigned char slab[];           // [2][rows][group_heads][D] 16-bit
     __shared__ uint64_t bar;
     __shared__ int failed;
     __shared__ unsigned top[2 * kMaxGroupHeads];                    // largest magnitudes, then scales, as bits
-    const int first_single = (int)gridDim.x - a.q_ctas - a.single_ctas, first_q = (int)gridDim.x - a.q_ctas;
     if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
         fence_mbar_init();
@@ -612,29 +466,34 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
     __syncthreads();                       // any warp may issue the first copies
     pdl_trigger();
     pdl_wait();
-    if ((int)blockIdx.x >= first_single && (int)blockIdx.x < first_q) {
-        const int lane = threadIdx.x & 31, base = ((int)blockIdx.x - first_single) * kSingleTokens;
+    if (blockIdx.x < (unsigned)a.single_ctas) {
+        const int lane = threadIdx.x & 31, part = (int)blockIdx.x % a.single_parts;
+        const int base = (int)blockIdx.x / a.single_parts * a.single_tokens;
         const int around = base - 1 + lane;                           // the window and a token to either side
-        const int64_t s = lane < kSingleTokens + 2 && around >= 0 && around < a.num_tokens ? __ldg(a.slots + around) : -1;
+        const int64_t s = lane < a.single_tokens + 2 && around >= 0 && around < a.num_tokens ? __ldg(a.slots + around) : -1;
+        const int p = a.rot && around >= 0 && around < a.num_tokens ? __ldg(a.positions + around) : -1;
         const int64_t before = __shfl_up_sync(0xffffffffu, s, 1), after = __shfl_down_sync(0xffffffffu, s, 1);
-        const bool alone = lane >= 1 && lane <= kSingleTokens && s >= 0 && s < a.num_slots &&
+        const bool alone = lane >= 1 && lane <= a.single_tokens && s >= 0 && s < a.num_slots &&
                            !same_block(a, before, s) && !same_block(a, after, s);
         const int jobs = (2 * a.num_kv_heads + 32 / UPR - 1) / (32 / UPR);
         int done = 0;                                                 // jobs of the tokens before
         for (unsigned todo = __ballot_sync(0xffffffffu, alone); todo; todo &= todo - 1, done += jobs) {
             const int l = __ffs(todo) - 1;
             const int64_t slot = __shfl_sync(0xffffffffu, s, l);
-            const int pos = a.rot ? __ldg(a.positions + base - 1 + l) : -1;
-            for (int j = ((int)(threadIdx.x >> 5) - done % W + W) % W; j < jobs; j += W)
+            const int pos = __shfl_sync(0xffffffffu, p, l);
+            for (int j = part * W + ((int)(threadIdx.x >> 5) + W - done % W) % W; j < jobs; j += a.single_parts * W)
                 append8_token<D, T, INTERLEAVED>(a, base - 1 + l, pos, slot, (slot & ((1ll << a.log2_block) - 1)) == 0,
-                                                 j * (32 / UPR), lane);
+                                                 0, a.num_kv_heads, j * (32 / UPR), lane);
         }
         return;
     }
-    if ((int)blockIdx.x >= first_q) {
+    // this CTA's number among those that append runs, or those that rotate queries
+    const unsigned cta = blockIdx.x - a.single_ctas;
+    const int runs_before = min((int)((cta * a.run_share) >> 32), a.run_ctas);
+    if (runs_before == a.run_ctas || (int)(((cta + 1) * a.run_share) >> 32) == runs_before) {
         const unsigned groups = (unsigned)(a.num_heads + kQueryRows - 1) / kQueryRows;
         const unsigned per_token = groups * UPR;
-        const unsigned long long i = (unsigned long long)(blockIdx.x - first_q) * kRopeThreads + threadIdx.x;
+        const unsigned long long i = (unsigned long long)(cta - runs_before) * kAppend8Threads + threadIdx.x;
         const unsigned long long t64 = i / per_token;
         if (t64 >= (unsigned)a.num_tokens) return;
         const int t = (int)t64;
@@ -673,15 +532,15 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = 1 << a.log2_block;
     const int hgroups = (a.num_kv_heads + a.group_heads - 1) / a.group_heads;
-    const int h0 = (int)(blockIdx.x % hgroups) * a.group_heads;
+    const int h0 = (runs_before % hgroups) * a.group_heads;
     const int heads = a.num_kv_heads - h0 < a.group_heads ? a.num_kv_heads - h0 : a.group_heads;
-    const int first = (int)(blockIdx.x / hgroups) * B;
-    const int last = first + B < a.num_tokens ? first + B : a.num_tokens;
+    const int first = (runs_before / hgroups) * a.run_tokens;
+    const int last = first + a.run_tokens < a.num_tokens ? first + a.run_tokens : a.num_tokens;
     const uint32_t piece = (uint32_t)(heads * D * sizeof(T));        // of a token's row
-    // this thread's unit of keys (the first half of the threads) or values, and its row of kRowsAtOnce
-    const bool isv = tid >= kRopeThreads / 2;
-    const int r = (tid % (kRopeThreads / 2)) / UPR, u = tid % UPR;
-    const Unit x = unit_at<INTERLEAVED>(u, isv ? 0 : a.rot);
+    // this thread's unit, its row of rows_at_once (whole warps of them), and its first head of every head_step-th
+    const int rows_at_once = min(max(B, 32 / UPR), kAppend8Threads / UPR), head_step = kAppend8Threads / UPR / rows_at_once;
+    const int r = tid / UPR % rows_at_once, u = tid % UPR, head0 = tid / UPR / rows_at_once;
+    const Unit xk = unit_at<INTERLEAVED>(u, a.rot), xv = unit_at<INTERLEAVED>(u, 0);
     if (tid == 0 && timed_out(a.st)) failed = 1;
     uint32_t phase = 0;
     for (int base = first; base < last; base += 32) {
@@ -696,10 +555,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
             if (a.rot) checked_position(a, tl, a.num_heads == 0);
             if (!good) latch(a.st, kFlagBadSlot, sl);
         }
-        // but for runs of one token: the CTAs after these take them
+        // but for runs of one token: other CTAs take them
         const bool leads = good && !same_block(a, before, sl) && same_block(a, after, sl);
-        unsigned todo = __ballot_sync(0xffffffffu, leads);
-        for (; todo; todo &= todo - 1) {
+        for (unsigned todo = __ballot_sync(0xffffffffu, leads); todo; todo &= todo - 1) {
             const int src_lane = __ffs(todo) - 1, t = base + src_lane;
             const int64_t blk = __shfl_sync(0xffffffffu, sl, src_lane) >> a.log2_block;
             Run run = find_run(a, t, blk, lane);
@@ -707,7 +565,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
             if (tid < 2 * heads) top[tid] = 0;
             if (tid == 0) mbar_arrive_expect_tx(&bar, 2u * (uint32_t)run.n * piece);
             // row pieces of keys, then of values, spread over the warps
-            for (int c = lane * W + warp; c < 2 * run.n; c += kRopeThreads) {
+            for (int c = lane * W + warp; c < 2 * run.n; c += kAppend8Threads) {
                 const bool v = c >= run.n;
                 const int row = v ? c - run.n : c;
                 const T *src = v ? static_cast<const T *>(a.v) + (t + row) * a.v_stride
@@ -722,7 +580,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
                 turned = false;
                 if (row >= run.n) return;
                 off = (int)(__ldg(a.slots + t + row) & (B - 1));
-                if (x.rotated) {
+                if (xk.rotated) {
                     const int pos = __ldg(a.positions + t + row);
                     turned = pos >= 0 && pos < a.num_positions;       // others have been latched
                     if (turned) load_cos_sin(cs, a, pos, u);
@@ -739,31 +597,34 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
                 return;
             }
             phase ^= 1u;
-            const T *mine_rows = reinterpret_cast<const T *>(slab + (size_t)(isv ? run.n : 0) * piece);
-            auto unit32 = [&](float (&y)[16], int row, int h) {
-                const T *q = mine_rows + ((size_t)row * heads + h) * D;
-                widen<T>(y, load_shared16(q + x.a), load_shared16(q + x.b));
+            const T *keys = reinterpret_cast<const T *>(slab), *values = keys + (size_t)run.n * heads * D;
+            auto key32 = [&](float (&y)[16], int row, int h) {
+                const T *q = keys + (row * heads + h) * D;
+                widen<T>(y, load_shared16(q + xk.a), load_shared16(q + xk.b));
                 if (turned) turn<INTERLEAVED>(y, cs);
             };
-            for (int row0 = 0; row0 < run.n; row0 += kRowsAtOnce) {
+            for (int row0 = 0; row0 < run.n; row0 += rows_at_once) {
                 const int row = row0 + r;
                 if (row0 > 0) plan(row);
-                for (int h = 0; h < heads; h++) {
-                    float amax = 0.f;
+                for (int h = head0; h < heads; h += head_step) {
+                    float kmax = 0.f, vmax = 0.f;
                     if (row < run.n) {
+                        const T *q = values + (row * heads + h) * D;
+                        vmax = fmaxf(largest8<T>(load_shared16(q + xv.a)), largest8<T>(load_shared16(q + xv.b)));
                         if (turned) {
                             float y[16];
-                            unit32(y, row, h);
+                            key32(y, row, h);
 #pragma unroll
-                            for (int e = 0; e < 16; e++) amax = fmaxf(amax, fabsf(y[e]));
+                            for (int e = 0; e < 16; e++) kmax = fmaxf(kmax, fabsf(y[e]));
                         } else {
-                            const T *q = mine_rows + ((size_t)row * heads + h) * D;
-                            amax = fmaxf(largest8<T>(load_shared16(q + x.a)), largest8<T>(load_shared16(q + x.b)));
+                            q = keys + (row * heads + h) * D;
+                            kmax = fmaxf(largest8<T>(load_shared16(q + xk.a)), largest8<T>(load_shared16(q + xk.b)));
                         }
                     }
                     // magnitudes are not negative: their bits order as they do
-                    const unsigned m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-                    if (lane == 0) atomicMax(&top[2 * h + (isv ? 1 : 0)], m);
+                    const unsigned km = __reduce_max_sync(0xffffffffu, __float_as_uint(kmax));
+                    const unsigned vm = __reduce_max_sync(0xffffffffu, __float_as_uint(vmax));
+                    if (lane < 2) atomicMax(&top[2 * h + lane], lane ? vm : km);
                 }
             }
             __syncthreads();
@@ -777,17 +638,19 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
                 if (lane == 0) top[j] = __float_as_uint(scale);
             }
             __syncthreads();
-            for (int row0 = 0; row0 < run.n; row0 += kRowsAtOnce) {
+            for (int row0 = 0; row0 < run.n; row0 += rows_at_once) {
                 const int row = row0 + r;
-                if (run.n > kRowsAtOnce) plan(row);
+                if (run.n > rows_at_once) plan(row);
                 if (row >= run.n) continue;
-                unsigned char *dst = static_cast<unsigned char *>(isv ? a.v_cache : a.k_cache) +
-                                     (((size_t)(blk * a.num_kv_heads + h0) << a.log2_block) + off) * D;
-#pragma unroll 2
-                for (int h = 0; h < heads; h++) {
+                const size_t dst = (((size_t)(blk * a.num_kv_heads + h0) << a.log2_block) + off) * D;
+                for (int h = head0; h < heads; h += head_step) {
+                    const size_t at = dst + ((size_t)h << a.log2_block) * D;
                     float y[16];
-                    unit32(y, row, h);
-                    store_codes(dst + ((size_t)h << a.log2_block) * D, x, y, __uint_as_float(top[2 * h + (isv ? 1 : 0)]));
+                    key32(y, row, h);
+                    store_codes(static_cast<unsigned char *>(a.k_cache) + at, xk, y, __uint_as_float(top[2 * h]));
+                    const T *q = values + (row * heads + h) * D;
+                    widen<T>(y, load_shared16(q + xv.a), load_shared16(q + xv.b));
+                    store_codes(static_cast<unsigned char *>(a.v_cache) + at, xv, y, __uint_as_float(top[2 * h + 1]));
                 }
             }
             __syncthreads();                                          // the slab and the scales are free again
@@ -797,14 +660,12 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rotary_append8_bulk_kernel(co
 
 // ---- host ---------------------------------------------------------------------------
 
-// From so many tokens on the copies' setup pays for itself (prompts of 32/8
-// heads: 1,000 tokens 13 us against 18, 500 tokens 15 against 10).  What the
-// tokens are to one another only the device sees: a decode step of so many
-// sequences takes its own way through either kernel.
-#ifndef PKV_BULK_TOKENS
-#define PKV_BULK_TOKENS 1024
-#endif
-constexpr int kBulkTokens = PKV_BULK_TOKENS;
+// CTAs of a small 8-bit append at least: for runs, by fewer heads and then by
+// fewer tokens to a CTA, until they do (one prompt of 1,000 tokens of 32/8
+// heads: 7.0 us, 9.8 with four heads throughout; 64 sequences of four tokens:
+// 7.4, 10.9 with whole blocks; more than these only delay what a decode step
+// does in the CTAs after them), and for single tokens.
+constexpr int kRunCtasByHeads = 256, kRunCtasByTokens = 152, kSingleCtas = 512;
 
 template <int D, typename T>
 cudaError_t launch_append(const RopeArgs &a, bool interleaved, bool fp8, cudaStream_t stream) {
@@ -816,31 +677,37 @@ cudaError_t launch_append(const RopeArgs &a, bool interleaved, bool fp8, cudaStr
         return launch(interleaved ? rotary_append_kernel<D, T, true> : rotary_append_kernel<D, T, false>, dim3(grid),
                       dim3(kRopeThreads), 0, stream, b);
     }
-    const int sms = sm_count() > 0 ? sm_count() : 1;
-    if (a.num_tokens >= kBulkTokens) {
-        b.group_heads = kSlabBytes / (int)((2 * sizeof(T) * D) << a.log2_block);
-        if (b.group_heads > a.num_kv_heads) b.group_heads = a.num_kv_heads;
-        const int hgroups = (a.num_kv_heads + b.group_heads - 1) / b.group_heads;
-        const unsigned long long chunks = ((unsigned long long)a.num_tokens + (1u << a.log2_block) - 1) >> a.log2_block;
-        const unsigned long long qunits =
-            (unsigned long long)a.num_tokens * ((a.num_heads + kQueryRows - 1) / kQueryRows) * UPR;
-        b.q_ctas = (int)((qunits + kRopeThreads - 1) / kRopeThreads);
-        b.single_ctas = (a.num_tokens + kSingleTokens - 1) / kSingleTokens;
-        auto kern = interleaved ? rotary_append8_bulk_kernel<D, T, true> : rotary_append8_bulk_kernel<D, T, false>;
-        static std::atomic<unsigned long long> allowed[2];
-        cudaError_t e = allow_smem(kern, kSlabBytes, allowed[interleaved]);
-        if (e != cudaSuccess) return e;
-        const size_t smem = (size_t)b.group_heads * ((2 * sizeof(T) * D) << a.log2_block);
-        return launch(kern, dim3((unsigned)(chunks * hgroups + b.single_ctas + b.q_ctas)),
-                      dim3(kRopeThreads), smem, stream, b);
-    }
-    const unsigned long long qunits = (unsigned long long)a.num_tokens * a.num_heads * UPR;
-    b.q_ctas = (int)((qunits + kStepThreads - 1) / kStepThreads);
-    const int most = (2 * a.num_kv_heads + kStepThreads / 32 - 1) / (kStepThreads / 32);
-    b.head_split = 1;
-    while (b.head_split < most && a.num_tokens * b.head_split < 4 * sms) b.head_split++;
-    return launch(interleaved ? rotary_append8_kernel<D, T, true> : rotary_append8_kernel<D, T, false>,
-                  dim3((unsigned)(a.num_tokens * b.head_split + b.q_ctas)), dim3(kStepThreads), 0, stream, b);
+    // single tokens
+    b.single_tokens = a.num_tokens > 16 * kSingleCtas ? 16 : (a.num_tokens + kSingleCtas - 1) / kSingleCtas;
+    constexpr int kRowsAtOnce = kAppend8Threads / UPR;
+    b.single_parts = 1;
+    while (b.single_parts * kRowsAtOnce < 2 * a.num_kv_heads && (long long)a.num_tokens * (b.single_parts + 1) <= kSingleCtas)
+        b.single_parts++;
+    b.single_ctas = ((a.num_tokens - 1) / b.single_tokens + 1) * b.single_parts;
+    // longer runs
+    const size_t head_bytes = (2 * sizeof(T) * D) << a.log2_block;   // of a block's keys and values
+    b.group_heads = head_bytes < (size_t)kSlabBytes ? (int)(kSlabBytes / head_bytes) : 1;
+    if (b.group_heads > a.num_kv_heads) b.group_heads = a.num_kv_heads;
+    b.run_tokens = 1 << a.log2_block;
+    const auto run_ctas = [&]() {
+        return ((long long)a.num_tokens + b.run_tokens - 1) / b.run_tokens *
+               ((a.num_kv_heads + b.group_heads - 1) / b.group_heads);
+    };
+    while (b.group_heads > 1 && run_ctas() < kRunCtasByHeads) b.group_heads = (b.group_heads + 1) / 2;
+    while (b.run_tokens > 2 && run_ctas() < kRunCtasByTokens) b.run_tokens /= 2;
+    b.run_ctas = (int)run_ctas();
+    // queries, the runs mixed into the first half of them: what takes longest does not begin last
+    const unsigned long long qunits =
+        (unsigned long long)a.num_tokens * ((a.num_heads + kQueryRows - 1) / kQueryRows) * UPR;
+    const unsigned long long q_ctas = (qunits + kAppend8Threads - 1) / kAppend8Threads;
+    const unsigned long long among = b.run_ctas + q_ctas / 2;
+    b.run_share = (((unsigned long long)b.run_ctas << 32) + among - 1) / among;
+    auto kern = interleaved ? rotary_append8_kernel<D, T, true> : rotary_append8_kernel<D, T, false>;
+    static std::atomic<unsigned long long> allowed[2];
+    cudaError_t e = allow_smem(kern, 2 * kSlabBytes, allowed[interleaved]);
+    if (e != cudaSuccess) return e;
+    return launch(kern, dim3((unsigned)(b.single_ctas + b.run_ctas + q_ctas)), dim3(kAppend8Threads),
+                  b.group_heads * head_bytes, stream, b);
 }
 
 pkv_status append_impl(const char *what, bool fp8, void *query_out, const void *query, const void *key,

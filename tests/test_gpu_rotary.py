@@ -229,6 +229,29 @@ def test_append8_large_step(cuda_device, T, Hkv):
         _same8(ref, kc, vc, sc, "step")
 
 
+@pytest.mark.parametrize("T,H,Hkv,B,d", [(5, 2, 2, 128, 128), (40, 8, 8, 16, 128), (200, 2, 40, 16, 64), (300, 7, 1, 4, 64),
+                                         (700, 4, 2, 32, 128), (2100, 6, 3, 16, 64), (9000, 2, 1, 8, 64)])
+def test_append8_short_runs(cuda_device, T, H, Hkv, B, d):
+    """A few tokens for each of many sequences, runs of one among them, padding between."""
+    x = Inputs(cuda_device, T, H, Hkv, d, B, "f16", T, d, NB=T + 8)
+    x.k, x.dk = x.k * 4, x.dk * 4
+    rng = np.random.default_rng(T)
+    slots, free = [], list(rng.permutation(T + 8))
+    while len(slots) < T:
+        n = int(rng.integers(1, min(6, B + 1)))
+        lo = 0 if rng.random() < 0.3 else int(rng.integers(0, B - n + 1))
+        slots += list(free.pop() * B + lo + np.arange(n)) + [-1] * int(rng.random() < 0.1)
+    slots = np.array(slots[:T], np.int64)
+    k0, v0, s0 = _random_cache8(T + 8, Hkv, B, d, 9)
+    kc, vc, sc = k0.to(cuda_device), v0.to(cuda_device), s0.to(cuda_device)
+    q = pkv.kv_rotary_and_cache_fp8(x.dq, x.dk, x.dv, x.dcs, x.dpos, kc, vc, sc, torch.from_numpy(slots).to(cuda_device))
+    pkv.check()
+    assert torch.equal(q.cpu(), rotate32(x.q, x.cs, x.positions, d, "half").half())
+    ref = RefCache8(k0, v0, s0)
+    ref.append(rotate32(x.k, x.cs, x.positions, d, "half").numpy(), x.v.float().numpy(), slots)
+    _same8(ref, kc, vc, sc, "short runs")
+
+
 def test_append8_special_values(cuda_device):
     """Zeros, the least and the largest magnitudes, infinities and NaN: what the definition says of each."""
     B, d = 8, 64
