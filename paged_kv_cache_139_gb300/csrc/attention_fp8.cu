@@ -706,9 +706,9 @@ __global__ void __launch_bounds__(kPipes * 64, kCtasPerSm)
                 float4 *dst = reinterpret_cast<float4 *>(a.ws_o + sp * D + d0);
 #pragma unroll
                 for (int j = 0; j < W; j += 4) dst[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                if (lane < 4) {
-                    a.ws_m[sp] = st.m[e];
-                    a.ws_l[sp] = l;
+                if (lane < 4) {                  // the merge takes a sum that is NaN for an empty one: v says it
+                    a.ws_m[sp] = l != l ? 0.f : st.m[e];
+                    a.ws_l[sp] = l != l ? 1.f : l;
                 }
             }
         }

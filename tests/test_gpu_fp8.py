@@ -151,6 +151,22 @@ def test_decode_nan_in_the_context_shows_and_beyond_it_does_not(cuda_device):
     assert bool(out[2, 1, 9].isnan()) and int(out[2].isnan().sum()) == 1
 
 
+@pytest.mark.parametrize("H,ctx,parts", [(2, 700, 64), (12, 700, 256), (2, 5000, 64)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_nan_in_a_split_context_shows(cuda_device, H, ctx, parts, d):
+    """In one of its partitions, or all through one."""
+    c = Case8(cuda_device, (ctx, ctx, ctx), H, 2, d, 16, seed=14)
+    keys = c.kc.view(torch.uint8)
+    keys[int(c.tables[1, 20]), 0, 3, 5] = NAN_CODE
+    keys[torch.from_numpy(c.tables[2, parts // 16:parts // 8].astype(np.int64)).to(cuda_device), 1] = NAN_CODE
+    out = c.decode(partition_size=parts)
+    pkv.check()
+    c.check(out, seqs=[0])
+    g = H // 2
+    assert bool(out[1, :g].isnan().all()) and not bool(out[1, g:].isnan().any())
+    assert bool(out[2, g:].isnan().all()) and not bool(out[2, :g].isnan().any())
+
+
 def test_decode_zero_scales_are_zeros(cuda_device):
     c = Case8(cuda_device, (100,), 2, 1, 128, 16, seed=10)
     c.sc[int(c.tables[0, 0])] = 0.0
