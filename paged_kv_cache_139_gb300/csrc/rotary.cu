@@ -321,7 +321,7 @@ __device__ __forceinline__ float grow_scale(const RopeArgs &a, const Run &run, f
                                             unsigned char *rows, int lane) {
     constexpr int UPR = D / 16, RP = 32 / UPR;
     const int r = lane / UPR, u = lane % UPR;
-    amax = fminf(amax, 3.4028235e38f);             // infinities; fmaxf has passed NaN over
+    amax = fminf(amax, 3.4028235e38f);             // infinities; NaN does not come this far
     // a write at offset 0 starts the block anew; otherwise its scale can only grow
     if (run.fresh) had = 0.f;
     const float scale = fmaxf(had, pow2_scale(amax));
@@ -404,17 +404,18 @@ __device__ __forceinline__ void append8_token(const RopeArgs &a, int t, int pos,
     store_codes(rows + (size_t)off * D, x, y, scale);
 }
 
-// The largest magnitude of eight 16-bit values, NaN passed over.
+// The largest magnitude of eight 16-bit values, NaN passed over (zero if all are NaN: a
+// NaN's bits would win the maximum that is taken over bits after this).
 template <typename T> __device__ __forceinline__ float largest8(const uint4 &w);
 template <> __device__ __forceinline__ float largest8<__half>(const uint4 &w) {
     const __half2 *h = reinterpret_cast<const __half2 *>(&w);
     const __half2 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
-    return fmaxf(__low2float(m), __high2float(m));
+    return fmaxf(0.f, fmaxf(__low2float(m), __high2float(m)));
 }
 template <> __device__ __forceinline__ float largest8<__nv_bfloat16>(const uint4 &w) {
     const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&w);
     const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
-    return fmaxf(__low2float(m), __high2float(m));
+    return fmaxf(0.f, fmaxf(__low2float(m), __high2float(m)));
 }
 
 // Sixteen bytes of shared memory in one load (the compiler would split it by
