@@ -17,6 +17,7 @@ missing, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -96,6 +97,12 @@ def _stream(stream: Optional[torch.cuda.Stream], device) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream: Optional[torch.cuda.Stream]):
+    """Where memory is made for a call on `stream`: taken from the current
+    stream's, work still queued there could be using it while the call writes."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 # -- the three device calls -------------------------------------------------------
 
 def kv_reshape_and_cache(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor,
@@ -134,7 +141,8 @@ def make_workspace(device, nbytes: int, stream: Optional[torch.cuda.Stream] = No
     and paged_attention_prefill (paged_attention_workspace_init).  Returns
     once the preparation has finished, so any stream may use the buffer."""
     dev = torch.device(device)
-    buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    with _on(stream):
+        buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     st = _stream(stream, dev)
     _ck(load().paged_attention_workspace_init(buf.data_ptr(), buf.numel(), st), "paged_attention_workspace_init")
     (stream or torch.cuda.current_stream(dev)).synchronize()
@@ -366,11 +374,12 @@ def rotary_table(num_positions: int, rotary_dim: int, base: float = 10000.0, sca
     contexts: "none", "linear" (theta / factor), or "by_parts" (pairs that turn
     at least high_turns times over original_positions keep their angle, those
     below low_turns are divided by factor, a ramp between).  Written into out
-    when given."""
+    when given, else into a tensor allocated on the call's stream."""
     if scaling not in _SCALINGS:
         raise ValueError(f"rotary_table: scaling {scaling!r} not one of {sorted(_SCALINGS)}")
     if out is None:
-        out = torch.empty(num_positions, rotary_dim // 2, 2, dtype=torch.float32, device=device)
+        with _on(stream):
+            out = torch.empty(num_positions, rotary_dim // 2, 2, dtype=torch.float32, device=device)
     elif out.shape != (num_positions, rotary_dim // 2, 2):
         raise ValueError("rotary_table: out must be [num_positions][rotary_dim / 2][2]")
     index = _cuda_index(out, "out")
@@ -413,7 +422,8 @@ def _append(what, fp8, query, key, value, cos_sin, positions, key_cache, value_c
         H = query.shape[1]
         q_ptr, q_stride = _rows(query, "query", dtype, index, T, H, d)
         if query_out is None:
-            query_out = torch.empty(T, H, d, dtype=dtype, device=key_cache.device)
+            with _on(stream):
+                query_out = torch.empty(T, H, d, dtype=dtype, device=key_cache.device)
         elif query_out.shape != query.shape:
             raise ValueError(f"{what}: query_out must be shaped like query")
         qo_ptr = _at(query_out, "query_out", dtype, index)
@@ -443,7 +453,8 @@ def kv_rotary_and_cache(query: Optional[torch.Tensor], key: torch.Tensor, value:
     in one launch.  cos_sin comes from rotary_table; layout "half" pairs (i,
     i + rotary_dim / 2), "interleaved" (2i, 2i + 1).  query, key and value may
     be slices of one projection's rows.  Returns the rotated queries
-    (query_out, which may be a contiguous query itself)."""
+    (query_out, which may be a contiguous query itself; without it, a tensor
+    allocated on the call's stream)."""
     if cos_sin is None:
         raise ValueError("kv_rotary_and_cache: needs a table (kv_reshape_and_cache writes without rotation)")
     return _append("kv_rotary_and_cache", False, query, key, value, cos_sin, positions, key_cache, value_cache, None,
@@ -484,7 +495,8 @@ def make_fp8_workspace(device, nbytes: int, stream: Optional[torch.cuda.Stream] 
     """A device buffer of at least nbytes, prepared for
     paged_attention_decode_fp8 and paged_attention_prefill_fp8.  Returns once
     the preparation has finished, so any stream may use the buffer."""
-    buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device(device))
+    with _on(stream):
+        buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device(device))
     index = buf.get_device()
     _call(load().paged_attention_fp8_workspace_init, "paged_attention_fp8_workspace_init", index, buf.data_ptr(),
           buf.numel(), _raw_stream(stream, index))

@@ -19,7 +19,7 @@ import torch
 import ctypes
 import math
 
-from . import (BlockAllocator, PkvError, copy_blocks, kv_reshape_and_cache, kv_rotary_and_cache,
+from . import (BlockAllocator, PkvError, _on, copy_blocks, kv_reshape_and_cache, kv_rotary_and_cache,
                kv_rotary_and_cache_fp8, kv_scales, make_fp8_workspace, make_workspace, paged_attention_decode,
                paged_attention_decode_fp8, paged_attention_decode_fp8_workspace_size, paged_attention_prefill,
                paged_attention_prefill_fp8, paged_attention_prefill_fp8_workspace_size, paged_attention_workspace_size,
@@ -435,6 +435,19 @@ def _check_step(eng: PagedKVCache, query, key, value, step, out, extra=()) -> in
     return 1 if query.dtype == torch.bfloat16 else 0
 
 
+def _scratch_queries(eng: PagedKVCache, query, ws, stream):
+    """The queries as a prepared step's attention reads them: with rotary
+    positions a tensor of the step's own, on its stream.  The workspace was
+    made on another one: neither goes back to its stream before the step's
+    work is done, if the step is dropped while that runs."""
+    if stream is not None:
+        ws.record_stream(stream)
+    if eng.rotary is None:
+        return query
+    with _on(stream):
+        return torch.empty_like(query)
+
+
 def _copy_calls(eng: PagedKVCache, step, st):
     n = step.pairs.shape[0] if step.pairs.dim() == 2 else 0
     return [(c.data_ptr(), step.pairs.data_ptr(), n, c.numel() // c.shape[0] * c.element_size(), eng.num_blocks, st)
@@ -469,7 +482,7 @@ class PreparedStep:
         code = _check_step(eng, query, key, value, step, out)
         st = ctypes.c_void_p((stream or torch.cuda.current_stream(eng.device)).cuda_stream)
         ws = eng.workspace(S, H, step.max_context_len, partition_size)
-        q = query if eng.rotary is None else torch.empty_like(query)      # as the attention reads them
+        q = _scratch_queries(eng, query, ws, stream)
         self._keep = (query, q, key, value, step, out, ws)
         NB, B = eng.num_blocks, eng.block_size
         self._copy = _copy_calls(eng, step, st)
@@ -548,7 +561,7 @@ class PreparedPrefill:
                                                                            step.max_context_len or mb * B))
         else:
             ws = eng.prefill_workspace()
-        q = query if eng.rotary is None else torch.empty_like(query)
+        q = _scratch_queries(eng, query, ws, stream)
         self._keep = (query, q, key, value, step, out, ws)
         self._copy = _copy_calls(eng, step, st)
         self._tokens = step.slots.shape[0]

@@ -1,0 +1,139 @@
+"""On which stream the bindings take the memory that they give to a call (CPU:
+streams, allocations and the library are stood in for)."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+import paged_kv_cache_139_gb300 as pkv
+from paged_kv_cache_139_gb300 import engine
+
+STREAM = types.SimpleNamespace(cuda_stream=77, synchronize=lambda: None)
+
+
+class Library:
+    """Every call succeeds and is written down."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def world(monkeypatch):
+    """Tensors on the CPU pass for CUDA ones; made: (size, current stream) of every uninitialised tensor."""
+    stack, made = [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        stack.append(stream)
+        yield
+        stack.pop()
+
+    def watched(make):
+        def empty(*args, **kw):
+            kw.pop("device", None)
+            t = make(*args, **kw)
+            made.append((tuple(t.shape), stack[-1]))
+            return t
+        return empty
+
+    lib = Library()
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch, "empty", watched(torch.empty))
+    monkeypatch.setattr(torch, "empty_like", watched(torch.empty_like))
+    monkeypatch.setattr(pkv, "load", lambda: lib)
+    monkeypatch.setattr(engine, "load", lambda: lib)
+    monkeypatch.setattr(pkv, "_cuda_index", lambda t, name: t.get_device())
+    monkeypatch.setattr(pkv, "_call", lambda fn, what, index, *args: fn(*args))
+    return types.SimpleNamespace(made=made, lib=lib)
+
+
+def _tokens():
+    z = lambda *shape: torch.zeros(*shape, dtype=torch.float16)  # noqa: E731
+    return z(3, 4, 64), z(3, 2, 64), z(3, 2, 64)
+
+
+@pytest.mark.parametrize("stream", [None, STREAM])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rotated_queries_are_made_on_the_calls_stream(world, monkeypatch, stream, fp8):
+    monkeypatch.setattr(pkv, "_raw_stream", lambda s, index: 0 if s is None else s.cuda_stream)
+    q, k, v = _tokens()
+    cs, pos, slots = torch.zeros(10, 32, 2), torch.zeros(3, dtype=torch.int32), torch.arange(3)
+    kc = torch.zeros(4, 2, 16, 64, dtype=torch.float8_e4m3fn if fp8 else torch.float16)
+    if fp8:
+        out = pkv.kv_rotary_and_cache_fp8(q, k, v, cs, pos, kc, kc.clone(), torch.zeros(4, 2, 2), slots, stream=stream)
+    else:
+        out = pkv.kv_rotary_and_cache(q, k, v, cs, pos, kc, kc.clone(), slots, stream=stream)
+    assert out.shape == q.shape and world.made == [((3, 4, 64), stream)]
+    assert world.lib.calls[0][1][-1] == (77 if stream else 0)
+
+
+@pytest.mark.parametrize("stream", [None, STREAM])
+def test_tables_and_workspaces_are_made_on_the_calls_stream(world, monkeypatch, stream):
+    monkeypatch.setattr(pkv, "_raw_stream", lambda s, index: 0 if s is None else s.cuda_stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=0, synchronize=lambda: None))
+    pkv.rotary_table(10, 64, device="cpu", stream=stream)
+    pkv.make_workspace("cpu", 1000, stream=stream)
+    pkv.make_fp8_workspace("cpu", 2000, stream=stream)
+    assert world.made == [((10, 32, 2), stream), ((1000,), stream), ((2000,), stream)]
+
+
+class Workspace(torch.Tensor):
+    """A workspace that writes down which streams it is kept from."""
+
+    @staticmethod
+    def make(n):
+        w = torch.zeros(n, dtype=torch.uint8).as_subclass(Workspace)
+        w.recorded = []
+        return w
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+
+def _engine(monkeypatch, fp8, rotary):
+    monkeypatch.setattr(engine, "_check_step", lambda *a, **k: 0)
+    ws = Workspace.make(1 << 16)
+    monkeypatch.setattr(engine.PagedKVCache, "_workspace", lambda self, need: ws)
+    monkeypatch.setattr(engine.PagedKVCache, "workspace", lambda self, *a: ws)
+    monkeypatch.setattr(engine.PagedKVCache, "prefill_workspace", lambda self: ws)
+    monkeypatch.setattr(engine, "BlockAllocator", lambda *a: None)
+    monkeypatch.setattr(engine, "paged_attention_prefill_fp8_workspace_size", lambda *a: 0)
+    cs = engine.RotaryPositions(torch.zeros(10, 32, 2)) if rotary else None
+    eng = engine.PagedKVCache(4, 2, 64, 16, torch.float8_e4m3fn if fp8 else torch.float16, "cpu", 4, rotary=cs)
+    return eng, ws
+
+
+def _step(kind):
+    e = torch.zeros(0, 2, dtype=torch.int32)
+    common = dict(slots=torch.arange(3), pairs=e, tables=torch.zeros(3, 4, dtype=torch.int32),
+                  context_lens=torch.ones(3, dtype=torch.int32), positions=torch.zeros(3, dtype=torch.int32), max_context_len=1)
+    if kind == "prefill":
+        return engine.DevicePrefill(query_start=torch.arange(4, dtype=torch.int32), max_query_len=1, **common)
+    return engine.DeviceStep(**common)
+
+
+def _prepare(eng, kind, stream=STREAM):
+    q, k, v = _tokens()
+    out = torch.zeros_like(q)
+    prepare = eng.prepare_prefill if kind == "prefill" else eng.prepare
+    return prepare(q, k, v, _step(kind), out, stream=stream)
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_prepared_step_takes_its_queries_scratch_on_its_stream(world, monkeypatch, kind, fp8):
+    eng, ws = _engine(monkeypatch, fp8, rotary=True)
+    world.made.clear()
+    step = _prepare(eng, kind)
+    assert world.made == [((3, 4, 64), STREAM)] and ws.recorded == [STREAM]
+    assert dict(world.lib.calls) == {}
+    step()
+    assert len(world.lib.calls) == 2
