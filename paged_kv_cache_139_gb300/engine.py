@@ -435,13 +435,22 @@ def _check_step(eng: PagedKVCache, query, key, value, step, out, extra=()) -> in
     return 1 if query.dtype == torch.bfloat16 else 0
 
 
-def _scratch_queries(eng: PagedKVCache, query, ws, stream):
-    """The queries as a prepared step's attention reads them: with rotary
-    positions a tensor of the step's own, on its stream.  The workspace was
-    made on another one: neither goes back to its stream before the step's
-    work is done, if the step is dropped while that runs."""
+def _held(eng: PagedKVCache, ws, stream):
+    """The cache's own tensors whose addresses a prepared step holds: it keeps
+    them, since the cache may be given others (a longer table, a larger
+    workspace) or go.  Made on other streams than the step's, their memory is
+    not used again before the step's work is done, if the step is dropped
+    while that runs."""
+    held = (ws, *eng._pools(), *((eng.rotary.cos_sin,) if eng.rotary else ()))
     if stream is not None:
-        ws.record_stream(stream)
+        for t in held:
+            t.record_stream(stream)
+    return held
+
+
+def _scratch_queries(eng: PagedKVCache, query, stream):
+    """The queries as a prepared step's attention reads them: with rotary
+    positions a tensor of the step's own, made on its stream."""
     if eng.rotary is None:
         return query
     with _on(stream):
@@ -482,8 +491,8 @@ class PreparedStep:
         code = _check_step(eng, query, key, value, step, out)
         st = ctypes.c_void_p((stream or torch.cuda.current_stream(eng.device)).cuda_stream)
         ws = eng.workspace(S, H, step.max_context_len, partition_size)
-        q = _scratch_queries(eng, query, ws, stream)
-        self._keep = (query, q, key, value, step, out, ws)
+        q = _scratch_queries(eng, query, stream)
+        self._keep = (query, q, key, value, step, out, _held(eng, ws, stream))
         NB, B = eng.num_blocks, eng.block_size
         self._copy = _copy_calls(eng, step, st)
         T = self._tokens = step.slots.shape[0]
@@ -561,8 +570,8 @@ class PreparedPrefill:
                                                                            step.max_context_len or mb * B))
         else:
             ws = eng.prefill_workspace()
-        q = _scratch_queries(eng, query, ws, stream)
-        self._keep = (query, q, key, value, step, out, ws)
+        q = _scratch_queries(eng, query, stream)
+        self._keep = (query, q, key, value, step, out, _held(eng, ws, stream))
         self._copy = _copy_calls(eng, step, st)
         self._tokens = step.slots.shape[0]
         self._write_name, self._write = _write_call(eng, query, q, key, value, step, code, st)

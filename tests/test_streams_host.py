@@ -1,7 +1,9 @@
 """On which stream the bindings take the memory that they give to a call (CPU:
 streams, allocations and the library are stood in for)."""
 import contextlib
+import gc
 import types
+import weakref
 
 import pytest
 import torch
@@ -28,7 +30,7 @@ class Library:
 @pytest.fixture
 def world(monkeypatch):
     """Tensors on the CPU pass for CUDA ones; made: (size, current stream) of every uninitialised tensor."""
-    stack, made = [None], []
+    stack, made, recorded = [None], [], []
 
     @contextlib.contextmanager
     def on(stream):
@@ -46,13 +48,14 @@ def world(monkeypatch):
 
     lib = Library()
     monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s)))
     monkeypatch.setattr(torch, "empty", watched(torch.empty))
     monkeypatch.setattr(torch, "empty_like", watched(torch.empty_like))
     monkeypatch.setattr(pkv, "load", lambda: lib)
     monkeypatch.setattr(engine, "load", lambda: lib)
     monkeypatch.setattr(pkv, "_cuda_index", lambda t, name: t.get_device())
     monkeypatch.setattr(pkv, "_call", lambda fn, what, index, *args: fn(*args))
-    return types.SimpleNamespace(made=made, lib=lib)
+    return types.SimpleNamespace(made=made, lib=lib, recorded=recorded)
 
 
 def _tokens():
@@ -85,22 +88,9 @@ def test_tables_and_workspaces_are_made_on_the_calls_stream(world, monkeypatch, 
     assert world.made == [((10, 32, 2), stream), ((1000,), stream), ((2000,), stream)]
 
 
-class Workspace(torch.Tensor):
-    """A workspace that writes down which streams it is kept from."""
-
-    @staticmethod
-    def make(n):
-        w = torch.zeros(n, dtype=torch.uint8).as_subclass(Workspace)
-        w.recorded = []
-        return w
-
-    def record_stream(self, stream):
-        self.recorded.append(stream)
-
-
 def _engine(monkeypatch, fp8, rotary):
     monkeypatch.setattr(engine, "_check_step", lambda *a, **k: 0)
-    ws = Workspace.make(1 << 16)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
     monkeypatch.setattr(engine.PagedKVCache, "_workspace", lambda self, need: ws)
     monkeypatch.setattr(engine.PagedKVCache, "workspace", lambda self, *a: ws)
     monkeypatch.setattr(engine.PagedKVCache, "prefill_workspace", lambda self: ws)
@@ -133,7 +123,28 @@ def test_a_prepared_step_takes_its_queries_scratch_on_its_stream(world, monkeypa
     eng, ws = _engine(monkeypatch, fp8, rotary=True)
     world.made.clear()
     step = _prepare(eng, kind)
-    assert world.made == [((3, 4, 64), STREAM)] and ws.recorded == [STREAM]
+    assert world.made == [((3, 4, 64), STREAM)] and (ws.data_ptr(), STREAM) in world.recorded
     assert dict(world.lib.calls) == {}
     step()
     assert len(world.lib.calls) == 2
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+@pytest.mark.parametrize("fp8,rotary", [(False, False), (False, True), (True, False), (True, True)])
+def test_a_prepared_step_keeps_what_it_reads(world, monkeypatch, kind, fp8, rotary):
+    """The pools, the scales and the table that its calls address, whatever the cache holds by then."""
+    eng, _ = _engine(monkeypatch, fp8, rotary)
+    step = _prepare(eng, kind)
+    tensors = [t for t in (eng.key_cache, eng.value_cache, eng.scales, eng.rotary and eng.rotary.cos_sin) if t is not None]
+    assert all((t.data_ptr(), STREAM) in world.recorded for t in tensors)
+    held = [weakref.ref(t) for t in tensors]
+    del tensors
+    if rotary:
+        eng.rotary = engine.RotaryPositions(torch.zeros(20, 32, 2))
+    eng.key_cache = eng.value_cache = eng.scales = None
+    del eng
+    gc.collect()
+    assert len(held) == 2 + fp8 + rotary and all(r() is not None for r in held)
+    del step
+    gc.collect()
+    assert all(r() is None for r in held)
