@@ -504,14 +504,17 @@ class PreparedStep:
                         step.max_context_len, B, NB, H, eng.num_kv_heads, d,
                         float(1.0 / math.sqrt(d) if scale is None else scale), partition_size, ws.data_ptr(),
                         ws.numel(), code, st)
-        # one new token per sequence, in sequence order: the write can ride in the attention launch
-        self._fused = fused and T == S and not eng.fp8 and eng.rotary is None
-        self._write_attend = (out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(),
-                              eng.key_cache.data_ptr(), eng.value_cache.data_ptr(), step.slots.data_ptr(),
-                              step.tables.data_ptr(), step.context_lens.data_ptr(), S, step.tables.shape[1],
-                              step.max_context_len, B, NB, H, eng.num_kv_heads, d,
-                              float(1.0 / math.sqrt(d) if scale is None else scale), partition_size, ws.data_ptr(),
-                              ws.numel(), code, st)
+        # one new token per sequence, in sequence order, written as it is in 16 bits: the write can ride in the
+        # attention launch
+        self._write_attend = None
+        if T == S and not eng.fp8 and eng.rotary is None:
+            self._write_attend = (out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(),
+                                  eng.key_cache.data_ptr(), eng.value_cache.data_ptr(), step.slots.data_ptr(),
+                                  step.tables.data_ptr(), step.context_lens.data_ptr(), S, step.tables.shape[1],
+                                  step.max_context_len, B, NB, H, eng.num_kv_heads, d,
+                                  float(1.0 / math.sqrt(d) if scale is None else scale), partition_size, ws.data_ptr(),
+                                  ws.numel(), code, st)
+        self._fused = fused and self._write_attend is not None
 
     def copy(self) -> None:
         for args in self._copy:
@@ -531,7 +534,11 @@ class PreparedStep:
             raise PkvError(rc, self._attend_name)
 
     def write_attend(self) -> None:
-        """The cache write and the attention in one launch (paged_attention_decode_write)."""
+        """The cache write and the attention in one launch (paged_attention_decode_write): of a 16-bit cache without
+        rotary positions, for a step of one token per sequence."""
+        if self._write_attend is None:
+            raise ValueError("write_attend: only a 16-bit cache without rotary positions, one new token per sequence, is "
+                             "written in the attention launch")
         rc = self._L.paged_attention_decode_write(*self._write_attend)
         if rc:
             raise PkvError(rc, "paged_attention_decode_write")

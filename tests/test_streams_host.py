@@ -148,3 +148,33 @@ def test_a_prepared_step_keeps_what_it_reads(world, monkeypatch, kind, fp8, rota
     del step
     gc.collect()
     assert all(r() is None for r in held)
+
+
+@pytest.mark.parametrize("fp8,rotary", [(False, True), (True, False), (True, True)])
+def test_the_fused_write_serves_plain_16_bit_caches_only(world, monkeypatch, fp8, rotary):
+    eng, _ = _engine(monkeypatch, fp8, rotary)
+    step = _prepare(eng, "decode")
+    with pytest.raises(ValueError):
+        step.write_attend()
+    assert world.lib.calls == []
+    step()
+    assert [name for name, _ in world.lib.calls] == [
+        "kv_rotary_and_cache" + ("_fp8" if fp8 else ""),
+        "paged_attention_decode" + ("_fp8" if fp8 else "")]
+
+
+def test_the_fused_write_takes_a_token_for_each_sequence(world, monkeypatch):
+    """A plan without new tokens has no keys, values and slots for the fused call to read."""
+    eng, _ = _engine(monkeypatch, False, False)
+    step = _prepare(eng, "decode")
+    step.write_attend()
+    assert world.lib.calls[-1][0] == "paged_attention_decode_write"
+    q, k, v = _tokens()
+    none = _step("decode")
+    none.slots = none.slots[:0]
+    step = eng.prepare(q, k[:0], v[:0], none, torch.zeros_like(q), stream=STREAM)
+    world.lib.calls.clear()
+    with pytest.raises(ValueError):
+        step.write_attend()
+    step()
+    assert [name for name, _ in world.lib.calls] == ["paged_attention_decode"]
