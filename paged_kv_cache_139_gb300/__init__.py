@@ -34,7 +34,7 @@ __all__ = ["PkvError", "PkvOOM", "kv_reshape_and_cache", "paged_attention_decode
            "paged_attention_partition_size", "copy_blocks",
            "rotary_table", "kv_rotary_and_cache", "kv_rotary_and_cache_fp8", "kv_scales",
            "paged_attention_decode_fp8", "paged_attention_decode_fp8_workspace_size",
-           "paged_attention_prefill_fp8", "paged_attention_prefill_fp8_workspace_size", "make_fp8_workspace",
+           "paged_attention_prefill_fp8", "paged_attention_prefill_fp8_workspace_size", "make_fp8_workspace", "GrowingWorkspace",
            "validate_copy_pairs", "swap_blocks", "check", "launch_count", "version", "BlockAllocator", "library_path"]
 
 PKV_F16, PKV_BF16 = 0, 1
@@ -504,18 +504,66 @@ def make_fp8_workspace(device, nbytes: int, stream: Optional[torch.cuda.Stream] 
     return buf
 
 
+def _capturing(stream: Optional[torch.cuda.Stream]) -> bool:
+    """Whether the call's stream (or the current one, which the call may be forked from) is being captured."""
+    if torch.cuda.is_current_stream_capturing():
+        return True
+    if stream is None:
+        return False
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+class GrowingWorkspace:
+    """One workspace for 8-bit calls that follow one another, made by
+    make(nbytes) and grown as they need.  The prompt phase keeps whole contexts
+    in it, and a prompt in chunks asks for a little more each time: it grows by
+    half at least, and the smaller one is let go when the device has done all
+    that may still use it.  One that a CUDA graph has captured is kept, since
+    the graph holds its address."""
+
+    def __init__(self, make):
+        self._make = make
+        self._buf: Optional[torch.Tensor] = None
+        self._captured = False
+        self._kept: list = []
+
+    def get(self, nbytes: int, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """At least nbytes, for a call on `stream` (default the current one)."""
+        capturing = _capturing(stream)
+        if self._buf is None or self._buf.numel() < nbytes:
+            if capturing:
+                raise RuntimeError(f"a workspace of {nbytes} bytes cannot be made during a stream capture: make the call "
+                                   "once before, or give it a workspace")
+            self._grow(nbytes)
+        self._captured |= capturing
+        return self._buf
+
+    def _grow(self, nbytes: int) -> None:
+        want = nbytes
+        if self._buf is not None:
+            want = max(nbytes, self._buf.numel() * 3 // 2)
+            if self._captured:
+                self._kept.append(self._buf)
+            else:
+                torch.cuda.synchronize(self._buf.device)
+            self._buf, self._captured = None, False           # before the larger one is made
+        try:
+            self._buf = self._make(want)
+        except torch.OutOfMemoryError:
+            if want == nbytes:
+                raise
+            self._buf = self._make(nbytes)
+
+
 _ws8_cache: dict = {}
 
 
-def _workspace8(index: int, nbytes: int) -> torch.Tensor:
-    """The binding's own 8-bit workspace per device, as _workspace."""
-    buf = _ws8_cache.get(index)
-    if buf is None or buf.numel() < nbytes:
-        if buf is not None:
-            _ws_retired.append(buf)
-        buf = make_fp8_workspace(torch.device("cuda", index), nbytes)
-        _ws8_cache[index] = buf
-    return buf
+def _workspace8(index: int, nbytes: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """The binding's own 8-bit workspace per device."""
+    if index not in _ws8_cache:
+        _ws8_cache[index] = GrowingWorkspace(functools.partial(make_fp8_workspace, torch.device("cuda", index)))
+    return _ws8_cache[index].get(nbytes, stream)
 
 
 def _check8(what, out, query, key_cache, value_cache, scales, block_tables, context_lens, S, index):
@@ -541,7 +589,8 @@ def paged_attention_decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache
     """paged_attention_decode over an 8-bit cache (float8_e4m3fn caches and
     their block scales).  workspace from make_fp8_workspace, one call at a
     time; None takes the binding's own per-device buffer, which every 8-bit
-    call without a workspace shares.  Returns out."""
+    call without a workspace shares and which grows as they need (waiting for
+    the device then; it cannot grow during a stream capture).  Returns out."""
     what = "paged_attention_decode_fp8"
     index = _cuda_index(query, "query")
     S, H, d = query.shape
@@ -550,7 +599,7 @@ def paged_attention_decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache
     mb = block_tables.shape[1]
     if workspace is None:
         workspace = _workspace8(index, paged_attention_decode_fp8_workspace_size(
-            S, H, Hkv, d, max_context_len if max_context_len > 0 else mb * B, partition_size))
+            S, H, Hkv, d, max_context_len if max_context_len > 0 else mb * B, partition_size), stream)
     _call(load().paged_attention_decode_fp8, what, index, *ptrs, S, mb, max_context_len, B, NB, H, Hkv, d,
           1.0 / math.sqrt(d) if scale is None else scale, partition_size, _at(workspace, "workspace", torch.uint8, index),
           workspace.numel(), _dtype_code(query), _raw_stream(stream, index))
@@ -564,7 +613,8 @@ def paged_attention_prefill_fp8(out: torch.Tensor, query: torch.Tensor, key_cach
                                 workspace: Optional[torch.Tensor] = None,
                                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """paged_attention_prefill over an 8-bit cache.  max_context_len bounds the
-    contexts and sizes the workspace (0: the whole table).  workspace as for
+    contexts (0: the whole table) and sizes the workspace, which holds that
+    many tokens of every sequence in 16 bits.  workspace as for
     paged_attention_decode_fp8.  Returns out."""
     what = "paged_attention_prefill_fp8"
     index = _cuda_index(query, "query")
@@ -577,7 +627,7 @@ def paged_attention_prefill_fp8(out: torch.Tensor, query: torch.Tensor, key_cach
     mb = block_tables.shape[1]
     if workspace is None:
         workspace = _workspace8(index, paged_attention_prefill_fp8_workspace_size(
-            S, Hkv, d, B, max_context_len if max_context_len > 0 else mb * B))
+            S, Hkv, d, B, max_context_len if max_context_len > 0 else mb * B), stream)
     _call(load().paged_attention_prefill_fp8, what, index, *ptrs, _at(query_start, "query_start", torch.int32, index), S,
           T, max_query_len, max_context_len, mb, B, NB, H, Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale,
           _at(workspace, "workspace", torch.uint8, index), workspace.numel(), _dtype_code(query),

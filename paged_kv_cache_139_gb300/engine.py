@@ -11,6 +11,7 @@ the native allocator; the four device steps run in libpkv's kernels.
 from __future__ import annotations
 
 import dataclasses
+import functools
 from typing import Optional, Sequence
 
 import numpy as np
@@ -19,7 +20,7 @@ import torch
 import ctypes
 import math
 
-from . import (BlockAllocator, PkvError, _on, copy_blocks, kv_reshape_and_cache, kv_rotary_and_cache,
+from . import (BlockAllocator, GrowingWorkspace, PkvError, _on, copy_blocks, kv_reshape_and_cache, kv_rotary_and_cache,
                kv_rotary_and_cache_fp8, kv_scales, make_fp8_workspace, make_workspace, paged_attention_decode,
                paged_attention_decode_fp8, paged_attention_decode_fp8_workspace_size, paged_attention_prefill,
                paged_attention_prefill_fp8, paged_attention_prefill_fp8_workspace_size, paged_attention_workspace_size,
@@ -204,6 +205,7 @@ class PagedKVCache:
         self.max_blocks_per_seq = max_blocks_per_seq
         self._ws: Optional[torch.Tensor] = None
         self._ws_retired: list = []
+        self._ws8 = GrowingWorkspace(functools.partial(make_fp8_workspace, self.device)) if self.fp8 else None
 
     # -- host bookkeeping ------------------------------------------------------
     def new_sequence(self, length: int) -> int:
@@ -283,10 +285,12 @@ class PagedKVCache:
                                     partition_size))
 
     def _workspace(self, need: int) -> torch.Tensor:
+        if self.fp8:
+            return self._ws8.get(need)
         if self._ws is None or self._ws.numel() < need:
             if self._ws is not None:
                 self._ws_retired.append(self._ws)   # calls in flight on other streams may hold it
-            self._ws = (make_fp8_workspace if self.fp8 else make_workspace)(self.device, need)
+            self._ws = make_workspace(self.device, need)
         return self._ws
 
     def _pools(self):
@@ -482,7 +486,9 @@ class PreparedStep:
     """copy_blocks, the cache write and the attention for one set of buffers,
     their arguments checked and marshalled once: issuing the step then costs
     three or four plain C calls.  For decode loops that run the same buffers
-    every iteration (the buffers' contents may change)."""
+    every iteration (the buffers' contents may change).  The step holds its
+    rotated queries and its workspace: a CUDA graph that has captured its
+    calls is replayed only while it lives."""
 
     def __init__(self, eng: PagedKVCache, query, key, value, step: DeviceStep, out, scale, partition_size, stream,
                  fused=True):

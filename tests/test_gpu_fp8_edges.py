@@ -7,6 +7,7 @@ import torch
 
 import paged_kv_cache_139_gb300 as pkv
 from fp8_reference import F8, RefCache8, rotate32
+from paged_kv_cache_139_gb300.engine import PagedKVCache
 from test_gpu_rotary import DT, Inputs, _random_cache8, _same8
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +43,66 @@ def test_append8_nan_rows_do_not_count(cuda_device, dtype, B, d, rot, layout):
     ref = RefCache8(k0, v0, s0)
     ref.append(rotate32(k, x.cs, x.positions, rot, layout).numpy(), v.float().numpy(), slots)
     _same8(ref, kc, vc, sc, "NaN rows")
+
+
+def test_chunks_of_a_long_prompt_hold_a_bounded_workspace(cuda_device):
+    H, Hkv, d, B, chunk, n = 4, 2, 64, 16, 128, 64
+    eng = PagedKVCache(n * chunk // B, Hkv, d, B, F8, cuda_device, n * chunk // B)
+    seq = eng.new_sequence(0)
+    g = torch.Generator().manual_seed(0)
+    q, k, v = (torch.randn(chunk, h, d, generator=g).half().to(cuda_device) for h in (H, Hkv, Hkv))
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for _ in range(n):
+        eng.prefill(q, k, v, eng.upload_prefill(eng.plan_prefill([seq], [chunk])), out=out)
+    pkv.check()
+    need = pkv.paged_attention_prefill_fp8_workspace_size(1, Hkv, d, B, n * chunk)
+    assert torch.cuda.memory_allocated() - before <= 2 * need
+
+
+def test_growing_calls_without_a_workspace_hold_a_bounded_one(cuda_device):
+    H, Hkv, d, B, NB = 2, 2, 128, 16, 2048
+    kc, vc = (torch.zeros(NB, Hkv, B, d, device=cuda_device).to(F8) for _ in range(2))
+    sc = pkv.kv_scales(NB, Hkv, cuda_device)
+    q = torch.randn(8, H, d, device=cuda_device).half()
+    out = torch.empty_like(q)
+    bt = torch.arange(NB, dtype=torch.int32, device=cuda_device)[None]
+    start = torch.tensor([0, 8], dtype=torch.int32, device=cuda_device)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for n in range(512, NB * B + 1, 512):
+        pkv.paged_attention_prefill_fp8(out, q, kc, vc, sc, bt, torch.tensor([n], dtype=torch.int32, device=cuda_device), start,
+                                        max_context_len=n)
+    pkv.check()
+    need = pkv.paged_attention_prefill_fp8_workspace_size(1, Hkv, d, B, NB * B)
+    assert torch.cuda.memory_allocated() - before <= 2 * need
+
+
+def test_a_captured_call_keeps_its_workspace(cuda_device):
+    """A graph replays into the workspace that it was captured with, after larger calls have taken another."""
+    eng = PagedKVCache(600, 2, 64, 16, F8, cuda_device, 300)
+    for pool in eng._pools():
+        pool.zero_()
+    g = torch.Generator().manual_seed(1)
+    seqs = [eng.new_sequence(0), eng.new_sequence(0)]
+    new = lambda n: [torch.randn(n, h, 64, generator=g).half().to(cuda_device) for h in (4, 2, 2)]  # noqa: E731
+    small = eng.upload_prefill(eng.plan_prefill(seqs, [70, 50]))
+    q, k, v = new(120)
+    eng.prefill(q, k, v, small)
+    small.pairs = small.pairs[:0]
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        eng.prefill(q, k, v, small, out=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    first = out.clone()
+    eng.prefill(*new(4000), eng.upload_prefill(eng.plan_prefill([eng.new_sequence(0)], [4000])))
+    junk = [torch.full((1 << 18,), 0xFF, dtype=torch.uint8, device=cuda_device) for _ in range(64)]
+    out.fill_(5.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    pkv.check()
+    assert torch.equal(out, first) and all(bool((x == 0xFF).all()) for x in junk)

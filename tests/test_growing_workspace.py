@@ -1,0 +1,104 @@
+"""How the 8-bit calls' own workspaces grow and let go (CPU: buffers of host
+memory, the device's synchronisation and capture state stood in for)."""
+import gc
+import weakref
+
+import pytest
+import torch
+
+import paged_kv_cache_139_gb300 as pkv
+
+
+class World:
+    def __init__(self, monkeypatch):
+        self.capturing, self.synced, self.refs, self.most, self.room = False, 0, [], 0, 1 << 62
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.capturing)
+        monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: setattr(self, "synced", self.synced + 1))
+        self.ws = pkv.GrowingWorkspace(self.make)
+
+    def make(self, n):
+        if self.held() + n > self.room:
+            raise torch.OutOfMemoryError("no room")
+        buf = torch.empty(n, dtype=torch.uint8)
+        self.refs.append(weakref.ref(buf))
+        self.most = max(self.most, self.held())
+        return buf
+
+    def held(self):
+        gc.collect()
+        return sum(r().numel() for r in self.refs if r() is not None)
+
+
+@pytest.fixture
+def world(monkeypatch):
+    return World(monkeypatch)
+
+
+def test_a_prompt_in_chunks_holds_one_workspace(world):
+    for n in range(8000, 512001, 8000):
+        assert world.ws.get(n).numel() >= n
+    assert world.held() <= 512000 * 3 // 2 and world.most <= 512000 * 3 // 2
+    made = len(world.refs)
+    assert made <= 12 and world.synced == made - 1                # 1.5 ** 11 > 64
+    world.ws.get(100)
+    assert len(world.refs) == made
+
+
+def test_a_single_call_takes_what_it_needs(world):
+    assert world.ws.get(1000).numel() == 1000 and world.synced == 0
+
+
+def test_a_step_that_uses_the_old_one_keeps_it(world):
+    old = world.ws.get(1000)
+    new = world.ws.get(2000)
+    assert old.numel() == 1000 and new.numel() == 2000 and old is not new
+
+
+def test_a_captured_workspace_stays(world):
+    world.ws.get(1000)
+    world.capturing = True
+    first = weakref.ref(world.ws.get(900))
+    world.capturing = False
+    for n in (2000, 4000, 9000):
+        world.ws.get(n)
+    gc.collect()
+    assert first() is not None and sum(r() is not None for r in world.refs) == 2
+
+
+def test_it_does_not_grow_during_a_capture(world):
+    world.ws.get(1000)
+    world.capturing = True
+    with pytest.raises(RuntimeError, match="capture"):
+        world.ws.get(1001)
+    assert world.ws.get(1000).numel() == 1000
+    world.capturing = False
+    assert world.ws.get(1001).numel() == 1500
+
+
+def test_short_of_memory_it_grows_by_what_is_needed(world):
+    world.ws.get(1000)
+    world.room = 1200
+    assert world.ws.get(1100).numel() == 1100
+    with pytest.raises(torch.OutOfMemoryError):
+        world.ws.get(1201)
+    world.room = 5000
+    assert world.ws.get(3000).numel() == 3000
+
+
+def test_another_streams_capture_counts(world, monkeypatch):
+    import contextlib
+
+    @contextlib.contextmanager
+    def on(stream):
+        was, world.capturing = world.capturing, stream == "captured"
+        yield
+        world.capturing = was
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    world.ws.get(1000, stream="plain")
+    with pytest.raises(RuntimeError):
+        world.ws.get(2000, stream="captured")
+    kept = weakref.ref(world.ws.get(1000, stream="captured"))
+    world.ws.get(2000)
+    gc.collect()
+    assert kept() is not None
