@@ -183,13 +183,19 @@ class PagedKVCache:
     """dtype torch.float8_e4m3fn keeps keys and values in 8 bits with a scale
     per block and kv head (queries, keys and values come in 16 bits all the
     same).  With `rotary`, write, decode and prefill rotate queries and keys by
-    their tokens' positions on the way."""
+    their tokens' positions on the way.
+
+    The 8-bit prompt phase's workspace holds the step's contexts in 16 bits.
+    Caches whose calls follow one another on the GPU, as those of a model's
+    layers do, need one between them: give the first layer's cache as
+    `workspace_of` to the others."""
 
     def __init__(self, num_blocks: int, num_kv_heads: int, head_dim: int, block_size: int,
                  dtype: torch.dtype, device, max_blocks_per_seq: int,
                  free_order: Optional[Sequence[int]] = None,
                  key_cache: Optional[torch.Tensor] = None, value_cache: Optional[torch.Tensor] = None,
-                 scales: Optional[torch.Tensor] = None, rotary: Optional[RotaryPositions] = None):
+                 scales: Optional[torch.Tensor] = None, rotary: Optional[RotaryPositions] = None,
+                 workspace_of: Optional["PagedKVCache"] = None):
         shape = (num_blocks, num_kv_heads, block_size, head_dim)
         self.device = torch.device(device)
         self.key_cache = key_cache if key_cache is not None else torch.empty(shape, dtype=dtype, device=self.device)
@@ -205,7 +211,13 @@ class PagedKVCache:
         self.max_blocks_per_seq = max_blocks_per_seq
         self._ws: Optional[torch.Tensor] = None
         self._ws_retired: list = []
-        self._ws8 = GrowingWorkspace(functools.partial(make_fp8_workspace, self.device)) if self.fp8 else None
+        self._ws8: Optional[GrowingWorkspace] = None
+        if workspace_of is not None:
+            if not (self.fp8 and workspace_of.fp8 and self.device == workspace_of.device):
+                raise ValueError("workspace_of: 8-bit caches of one device share a workspace")
+            self._ws8 = workspace_of._ws8
+        elif self.fp8:
+            self._ws8 = GrowingWorkspace(functools.partial(make_fp8_workspace, self.device))
 
     # -- host bookkeeping ------------------------------------------------------
     def new_sequence(self, length: int) -> int:

@@ -106,3 +106,23 @@ def test_a_captured_call_keeps_its_workspace(cuda_device):
     torch.cuda.synchronize()
     pkv.check()
     assert torch.equal(out, first) and all(bool((x == 0xFF).all()) for x in junk)
+
+
+def test_layers_that_share_a_workspace_give_what_they_give_alone(cuda_device):
+    g = torch.Generator().manual_seed(2)
+    make = lambda **kw: PagedKVCache(64, 2, 64, 16, F8, cuda_device, 32, **kw)  # noqa: E731
+    first = make()
+    shared, alone = [first, make(workspace_of=first)], [make(), make()]
+    new = lambda n: [torch.randn(n, h, 64, generator=g).half().to(cuda_device) for h in (4, 2, 2)]  # noqa: E731
+    seqs = [c.new_sequence(0) for c in shared + alone]
+    for n in (40, 300, 1):
+        inputs = [new(n), new(n)]                           # of the two layers
+        outs = []
+        for i, c in enumerate(shared + alone):
+            if n == 1:
+                outs.append(c.decode(*inputs[i % 2], c.upload(c.plan_step([seqs[i]]))))
+            else:
+                outs.append(c.prefill(*inputs[i % 2], c.upload_prefill(c.plan_prefill([seqs[i]], [n]))))
+        pkv.check()
+        assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+    assert shared[1]._workspace(0) is first._workspace(0)

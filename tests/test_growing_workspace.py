@@ -102,3 +102,34 @@ def test_another_streams_capture_counts(world, monkeypatch):
     world.ws.get(2000)
     gc.collect()
     assert kept() is not None
+
+
+F8 = torch.float8_e4m3fn
+
+
+def _cache(dtype=F8, device="cpu", **kw):
+    from paged_kv_cache_139_gb300.engine import PagedKVCache
+    return PagedKVCache(4, 2, 64, 16, dtype, device, 4, **kw)
+
+
+def test_the_caches_of_a_models_layers_share_a_workspace(world):
+    first = _cache()
+    first._ws8 = world.ws
+    layers = [first] + [_cache(workspace_of=first) for _ in range(3)]
+    for n in (1000, 5000):
+        bufs = [layer._workspace(n) for layer in layers]
+        assert all(b is bufs[0] for b in bufs)
+        del bufs
+    assert world.held() == 5000
+    assert _cache()._ws8 is not first._ws8
+
+
+def test_what_cannot_share_a_workspace_is_refused():
+    with pytest.raises(ValueError):
+        _cache(workspace_of=_cache(torch.float16))
+    with pytest.raises(ValueError):
+        _cache(torch.float16, workspace_of=_cache())
+    with pytest.raises(ValueError):
+        _cache(torch.float16, workspace_of=_cache(torch.float16))
+    with pytest.raises(ValueError):
+        _cache(device="meta", workspace_of=_cache())
