@@ -236,15 +236,26 @@ pkv_status paged_attention_fp8_workspace_init(void *workspace_dev, size_t worksp
 
 /* ---------------------------------------------------------------------------
  * paged_attention_prefill_fp8 -- paged_attention_prefill over the 8-bit cache.
- * The contexts' blocks are first widened to `dtype` in the workspace (exact
- * for bf16, and for fp16 where code * scale is within its range; full blocks
- * that sequences share in the same place, as a common prefix, once), then the
- * prompt-phase kernel runs on them: two launches.  Arguments as for
- * paged_attention_prefill, but:
+ * The contexts' blocks are first widened to `dtype` in the workspace (full
+ * blocks that sequences share in the same place, as a common prefix, once),
+ * then the prompt-phase kernel runs on them: two launches.  Widened numbers are
+ * code * scale rounded to `dtype`:
+ *   bf16  exact where the scale is a power of two, as the library's own are
+ *   fp16  exact likewise, but what lies below 2^-24 (of keys 2^-23) is rounded to
+ *         a multiple of it, and values above 65,504 and keys above 131,008 in
+ *         magnitude count as those
+ * and the probabilities enter the product with 11 bits in fp16, with 16 in
+ * bf16 (22 in paged_attention_decode_fp8, which rounds no key or value).
+ * As in paged_attention_prefill, a value that is NaN may also reach rows up to
+ * 255 tokens before it in its sequence (its probability there is 0, and 0 x NaN
+ * is NaN).
+ * Arguments as for paged_attention_prefill, but:
  *   max_context_len  host-side upper bound on every context_lens[s] (0 =
  *                    max_blocks_per_seq * block_size); a context beyond its
  *                    ceil(max_context_len / block_size) blocks latches
- *                    PKV_EINDEX.  It sizes the workspace.
+ *                    PKV_EINDEX.  It sizes the workspace, which holds that
+ *                    many tokens' keys and values of every sequence in 16 bits.
+ *   scale            for fp16 at most half the largest fp32 number
  *   workspace_dev    as for paged_attention_decode_fp8, at least
  *                    paged_attention_prefill_fp8_workspace_size(...) bytes.
  * ------------------------------------------------------------------------- */

@@ -828,14 +828,31 @@ template <int D, typename T> cudaError_t launch_decode8(const F8Args &f, cudaStr
 
 // Logical block j of sequence s, as 16-bit values, to block s * width + j of a
 // scratch pool of the same layout; new_tables names those blocks.  A code
-// times a power of two is exact in bf16, and in fp16 within its range.  Rows
-// past the context become zeros.  A full block that an earlier sequence holds
+// times a power of two is exact in bf16, and in fp16 within its range (times
+// another scale it is rounded).  Rows past the context become zeros.  A full block that an earlier sequence holds
 // in the same place (a shared prefix) is widened there once and named by both
 // (32 requests after a shared 1000-token prefix: 358 us the whole call without
 // that).  One CTA per block, eight codes of K and of V to a load: bound by
 // the bytes read and twice as many written.
 constexpr int kWidenThreads = 256;
 constexpr int kWidenUnroll = 4;
+
+// Keys enter fp16 at half their size (the softmax scale makes up for it), so that
+// rotated keys of fp16 inputs, up to 65504 sqrt(2), stay in its range.
+template <typename T> constexpr float kKeyFactor = std::is_same<T, __half>::value ? 0.5f : 1.f;
+
+// Two fp32 to one register of two 16-bit numbers (x in the low half), to nearest
+// even, clamped at the largest number, NaN to NaN: what is finite in the cache
+// stays finite (an fp16 value of 65504 is 65536 in 8 bits).  An infinite value would
+// give NaN in earlier rows of its key tile, where its probability is 0.
+template <typename T> __device__ __forceinline__ uint32_t pack_finite(float x, float y) {
+    uint32_t d;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
+    else
+        asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
+    return d;
+}
 
 template <typename T> __device__ __forceinline__ uint4 widen8(const uint2 &w, float s) {
     const uint32_t in[2] = {w.x, w.y};
@@ -845,8 +862,8 @@ template <typename T> __device__ __forceinline__ uint4 widen8(const uint2 &w, fl
         const uint32_t lo = e4m3x2_lo(in[i]), hi = e4m3x2_hi(in[i]);
         const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
         const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-        o[2 * i] = Mma<T>::pack(x.x * s, x.y * s);
-        o[2 * i + 1] = Mma<T>::pack(y.x * s, y.y * s);
+        o[2 * i] = pack_finite<T>(x.x * s, x.y * s);
+        o[2 * i + 1] = pack_finite<T>(y.x * s, y.y * s);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -909,7 +926,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_blocks_kernel(
             const int i = i0 + k * kWidenThreads;
             if (i >= chunks) break;
             const bool past = rows < B && ((i & ((1 << log2_head) - 1)) >> log2_row) >= rows;
-            ko[i] = past ? make_uint4(0u, 0u, 0u, 0u) : widen8<T>(kw[k], f[k].x);
+            ko[i] = past ? make_uint4(0u, 0u, 0u, 0u) : widen8<T>(kw[k], f[k].x * kKeyFactor<T>);
             vo[i] = past ? make_uint4(0u, 0u, 0u, 0u) : widen8<T>(vw[k], f[k].y);
         }
     }
@@ -1064,7 +1081,9 @@ pkv_status paged_attention_prefill_fp8(void *out, const void *query, const void 
     if (num_seqs < 0 || num_seqs > 65535 || num_tokens < 0 || max_query_len < 0 || num_blocks < 0)
         return fail(PKV_EINVAL, "%s: bad sizes (seqs %d, tokens %d, max query length %d, blocks %d)", what, num_seqs,
                     num_tokens, max_query_len, num_blocks);
-    if (!(scale > 0.f) || scale == INFINITY) return fail(PKV_EINVAL, "%s: scale must be positive and finite", what);
+    const float wide_scale = scale / (dtype == PKV_F16 ? kKeyFactor<__half> : kKeyFactor<__nv_bfloat16>);
+    if (!(scale > 0.f) || wide_scale == INFINITY)
+        return fail(PKV_EINVAL, "%s: scale must be positive and finite (for fp16 twice as well)", what);
     const int64_t table_cap = (int64_t)max_blocks_per_seq * block_size;
     if (max_blocks_per_seq < 0 || table_cap > INT_MAX || max_context_len < 0 || max_context_len > table_cap)
         return fail(PKV_EINVAL, "%s: max_context_len %d beyond the table (%lld tokens)", what, max_context_len,
@@ -1098,7 +1117,7 @@ pkv_status paged_attention_prefill_fp8(void *out, const void *query, const void 
     if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));
     return paged_attention_prefill(out, query, ws + z.k_off, ws + z.v_off, new_tables, context_lens, query_start, num_seqs,
                                    num_tokens, max_query_len, z.width, block_size, blocks, num_heads, num_kv_heads,
-                                   head_dim, scale, ws + kPrefillHeader, kWsHeaderBytes, dtype, stream);
+                                   head_dim, wide_scale, ws + kPrefillHeader, kWsHeaderBytes, dtype, stream);
 }
 
 }  // extern "C"

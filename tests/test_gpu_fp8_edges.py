@@ -6,8 +6,9 @@ import pytest
 import torch
 
 import paged_kv_cache_139_gb300 as pkv
-from fp8_reference import F8, RefCache8, rotate32
+from fp8_reference import F8, RefCache8, attention64, attention_tolerance, rotate32
 from paged_kv_cache_139_gb300.engine import PagedKVCache
+from test_gpu_fp8 import Case8
 from test_gpu_rotary import DT, Inputs, _random_cache8, _same8
 
 pytestmark = pytest.mark.gpu
@@ -126,3 +127,84 @@ def test_layers_that_share_a_workspace_give_what_they_give_alone(cuda_device):
         pkv.check()
         assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
     assert shared[1]._workspace(0) is first._workspace(0)
+
+
+def test_prefill_of_large_fp16_numbers(cuda_device):
+    """Cached numbers past fp16's range (65,504 in 8 bits is 65,536; a turned pair of them reaches 92,682) leave earlier
+    rows of the same tiles as they are, and keys keep their scores: the prompt phase gives what the definition gives."""
+    H, Hkv, d, B, T = 2, 1, 64, 16, 100
+    g = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(T, Hkv, d, generator=g).half() for _ in range(2))
+    q = (torch.randn(T, H, d, generator=g) * 2.0 ** -10).half()
+    # rows 40 and 70 turn by an eighth of a turn: (65504, 65504) becomes (0, 92637)
+    cs = torch.zeros(2, d // 2, 2)
+    cs[0, :, 0] = 1.0
+    cs[1] = math.sqrt(0.5)
+    pos = torch.zeros(T, dtype=torch.int32)
+    pos[[40, 70]] = 1
+    k[40] = 0
+    k[40, 0, 3] = k[40, 0, 3 + d // 2] = 65504
+    k[70] = 0
+    k[70, 0, 5] = k[70, 0, 5 + d // 2] = -65504
+    v[50, 0, 7], v[60, 0, 8], v[70, 0, :4] = 65504, -65504, 64000
+    dev = cuda_device
+    kc, vc = (torch.zeros(8, Hkv, B, d, device=dev).to(F8) for _ in range(2))
+    sc = pkv.kv_scales(8, Hkv, dev)
+    pkv.kv_rotary_and_cache_fp8(None, k.to(dev), v.to(dev), cs.to(dev), pos.to(dev), kc, vc, sc, torch.arange(T, device=dev))
+    ref = RefCache8(kc, vc, sc)
+    assert np.abs(ref.values(0)).max() > 85000 and np.abs(ref.values(1)).max() == 65536
+    out = torch.empty(T, H, d, dtype=torch.float16, device=dev)
+    tables = np.arange(8, dtype=np.int32)[None, :7]
+    pkv.paged_attention_prefill_fp8(out, q.to(dev), kc, vc, sc, torch.from_numpy(tables).to(dev),
+                                    torch.tensor([T], dtype=torch.int32, device=dev),
+                                    torch.tensor([0, T], dtype=torch.int32, device=dev))
+    pkv.check()
+    got = out.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    for lo, hi in ((0, 40), (40, 50), (50, T)):             # rows by the numbers that they may see
+        want, mag, vmax = attention64(q[lo:hi].double().numpy(), ref.values(0), ref.values(1), tables[0], hi, 1 / math.sqrt(d))
+        # beside the probabilities' 11 bits, 65,536 itself is off by half a step of fp16 (2^-11)
+        tol = attention_tolerance(want, mag, vmax, hi, d, torch.finfo(q.dtype).eps, 10)
+        assert np.all(np.abs(got[lo:hi] - want) <= tol), (lo, np.abs(got[lo:hi] - want).max())
+
+
+def _prefill(c, new, dtype, seed=1):
+    """The prompt phase over a Case8 of the last new[s] tokens of each sequence: outputs, queries and where they start."""
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = torch.randn(int(start[-1]), c.H, c.d, generator=torch.Generator().manual_seed(seed)).to(DT[dtype])
+    out = torch.empty(q.shape, dtype=q.dtype, device=c.dev)
+    pkv.paged_attention_prefill_fp8(out, q.to(c.dev), c.kc, c.vc, c.sc, c.dt_, c.dc, torch.from_numpy(start).to(c.dev))
+    pkv.check()
+    return out.double().cpu().numpy(), q.double().numpy(), start
+
+
+@pytest.mark.parametrize("dtype,scale_exp,free", [("bf16", (-11, -8), True), ("f16", (-11, -8), True), ("f16", (-20, -14), False),
+                                                  ("bf16", (-40, -14), False)])
+def test_prefill_rounds_what_16_bits_do_not_hold(cuda_device, dtype, scale_exp, free):
+    """Scales that are no powers of two, and in fp16 scales whose least codes lie below its range."""
+    new, ctx = (3, 40, 150), (30, 40, 400)
+    c = Case8(cuda_device, ctx, 4, 2, 64, 16, dtype, seed=40, scale_exp=scale_exp, free_scales=free)
+    got, q, start = _prefill(c, new, dtype)
+    eps, s = torch.finfo(DT[dtype]).eps, 1 / math.sqrt(64)
+    for i, n in enumerate(ctx):
+        rows = slice(int(start[i]), int(start[i + 1]))
+        want, mag, vmax = attention64(q[rows], c.kvals, c.vvals, c.tables[i], n, s)
+        # each key and value off by half a step of 16 bits: eps / 2 of itself, or in fp16 half of 2^-23 and 2^-24
+        dx = (eps / 2 * mag if free else 0) + (2.0 ** -24 * s * np.abs(q[rows]).sum(-1).max() if dtype == "f16" else 0)
+        dv = (eps / 2 * vmax if free else 0) + (2.0 ** -25 if dtype == "f16" else 0)
+        tol = attention_tolerance(want, mag, vmax, n, 64, eps, 11 if dtype == "f16" else 15) + vmax * math.expm1(2 * dx) + dv
+        tol = tol + (2.0 ** -25 if dtype == "f16" else 0)                     # the output's own least step
+        assert np.all(np.abs(got[rows] - want) <= tol), (i, np.abs(got[rows] - want).max())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_prefill_nan_in_the_context_shows(cuda_device, dtype):
+    """In the rows that see it and in no other sequence or kv head."""
+    c = Case8(cuda_device, (200, 200, 200), 4, 2, 64, 16, dtype, seed=41)
+    c.kc.view(torch.uint8)[int(c.tables[0, 3]), 0, 2, 5] = 0x7F            # token 50
+    c.vc.view(torch.uint8)[int(c.tables[1, 3]), 1, 2, 9] = 0x7F
+    got, _, start = _prefill(c, (100, 100, 100), dtype)
+    nan = np.isnan(got)
+    assert nan[:100, :2].all() and not nan[:100, 2:].any()
+    assert nan[100:200, 2:, 9].all() and nan[100:200].sum() == 2 * 100
+    assert not nan[200:].any()
