@@ -1099,6 +1099,10 @@ pkv_status paged_attention_prefill_fp8(void *out, const void *query, const void 
     const WidenSizes z = widen_sizes(num_seqs, num_kv_heads, head_dim, block_size, max_ctx);
     if ((long long)num_seqs * z.width > INT_MAX)
         return fail(PKV_EINVAL, "%s: %lld blocks of context", what, (long long)num_seqs * z.width);
+    // all that the second call would refuse is refused here, before the first one launches
+    const long long items = prefill_items(num_seqs, num_tokens, max_query_len, num_heads, num_kv_heads);
+    if (items > kMaxPrefillItems)
+        return fail(PKV_EINVAL, "%s: %lld work items (query tile pairs x heads x sequences) above 2^30", what, items);
     if (!workspace || workspace_bytes < z.bytes || !aligned16(workspace))
         return fail(PKV_EINVAL, "%s: workspace of %zu bytes needed, %zu given", what, z.bytes,
                     workspace ? workspace_bytes : (size_t)0);

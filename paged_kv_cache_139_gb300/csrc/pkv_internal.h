@@ -23,4 +23,9 @@ void count_launches(int n);
 // is prepared again whenever this number changes.
 unsigned int timeout_epoch();
 
+// Work items of the prompt-phase attention for these sizes (query heads that
+// share a kv head in pairs, or pairs of row tiles), which one call limits.
+constexpr long long kMaxPrefillItems = (1ll << 30) - 1;
+long long prefill_items(int num_seqs, int num_tokens, int max_query_len, int num_heads, int num_kv_heads);
+
 }  // namespace pkv

@@ -919,7 +919,22 @@ cudaError_t launch_prefill(const PrefillArgs &a, const void *query, const void *
     return launch(kern, dim3((unsigned)(ctas > 0 ? ctas : 1)), dim3(kThreads), L::alloc, stream, a, tmq, tmk, tmv);
 }
 
+// Grouped query heads share their kv head's tiles: items pair the heads, not the rows.
+bool pairs_heads(int num_heads, int num_kv_heads) { return num_heads / num_kv_heads % 2 == 0; }
+
+long long row_pairs(int num_tokens, int max_query_len, bool head_pairs) {
+    const long long longest = max_query_len == 0 || max_query_len > num_tokens ? num_tokens : max_query_len;
+    const int rows_per_item = head_pairs ? kRows : kTiles * kRows;
+    return (longest + rows_per_item - 1) / rows_per_item;
+}
+
 }  // namespace
+
+long long prefill_items(int num_seqs, int num_tokens, int max_query_len, int num_heads, int num_kv_heads) {
+    const bool head_pairs = pairs_heads(num_heads, num_kv_heads);
+    return row_pairs(num_tokens, max_query_len, head_pairs) * (head_pairs ? num_heads / 2 : num_heads) * num_seqs;
+}
+
 }  // namespace pkv
 
 using namespace pkv;
@@ -960,13 +975,10 @@ extern "C" pkv_status paged_attention_prefill(void *out, const void *query, cons
     if (workspace && (!aligned16(workspace) || workspace_bytes < kWsHeaderBytes))
         return fail(PKV_EINVAL, "paged_attention_prefill: workspace must be 16-byte aligned and at least %zu bytes",
                     kWsHeaderBytes);
-    // grouped query heads share their kv head's tiles: pair the heads, not the rows
-    const int group = num_heads / num_kv_heads;
-    const bool head_pairs = group % 2 == 0;
-    const int rows_per_item = head_pairs ? kRows : kTiles * kRows;
-    const long long num_pairs = ((long long)max_query_len + rows_per_item - 1) / rows_per_item;
-    const long long num_items = num_pairs * (head_pairs ? num_heads / 2 : num_heads) * num_seqs;
-    if (num_items > INT_MAX / 2)
+    const bool head_pairs = pairs_heads(num_heads, num_kv_heads);
+    const long long num_pairs = row_pairs(num_tokens, max_query_len, head_pairs);
+    const long long num_items = prefill_items(num_seqs, num_tokens, max_query_len, num_heads, num_kv_heads);
+    if (num_items > kMaxPrefillItems)
         return fail(PKV_EINVAL, "paged_attention_prefill: %lld work items (query tile pairs x heads x sequences) "
                                 "above 2^30", num_items);
     DeviceStatus *st = status_ptr();

@@ -21,3 +21,16 @@ def test_prefill_refuses_scales_that_it_cannot_double(over):
 def test_prefill_takes_the_largest_scales():
     _without_a_gpu()
     assert _prefill(dt=0, scale=1.7e38) == NO_DEVICE and _prefill(dt=1, scale=3.4e38) == NO_DEVICE
+
+
+@pytest.mark.parametrize("over", [dict(S=1000, T=1 << 20, H=4096, Hkv=1), dict(S=65535, T=1 << 20, H=129, Hkv=1),
+                                  dict(S=60000, T=2 ** 31 - 1, mql=12800, H=360, Hkv=2)])
+def test_prefill_refuses_too_many_work_items_before_it_widens(over):
+    """What the prompt-phase kernel would refuse is refused before anything is launched."""
+    assert _prefill(wsb=1 << 50, **over) == 1 and "work items" in _message() and "prefill_fp8" in _message()
+
+
+def test_prefill_takes_as_many_work_items_as_the_kernel():
+    _without_a_gpu()
+    sizes = dict(T=1 << 23, mql=256 * 256, H=256, Hkv=256, wsb=1 << 50)                 # 2^16 items a sequence
+    assert _prefill(S=(1 << 14) - 1, **sizes) == NO_DEVICE and _prefill(S=1 << 14, **sizes) == 1
