@@ -213,7 +213,8 @@ pkv_status kv_rotary_and_cache_fp8(void *query_out_dev, const void *query_dev, c
  *                   may overlap on the GPU need one each.  After a call that
  *                   reported PKV_ETIMEOUT, prepare it again.
  * num_seqs <= 65535 (512 to a launch); num_heads <= 65535, any number of them
- * per kv head; scale finite.
+ * per kv head; scale finite; contexts below 2^30 tokens (longer ones latch
+ * PKV_EINDEX).
  * ------------------------------------------------------------------------- */
 pkv_status paged_attention_decode_fp8(void *out_dev, const void *query_dev,
                                       const void *key_cache_dev, const void *value_cache_dev,

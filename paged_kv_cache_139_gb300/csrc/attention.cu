@@ -1386,7 +1386,7 @@ pkv_status decode_impl(void *out, const void *query, const void *key_cache, cons
     a.num_heads = num_heads;
     a.num_kv_heads = num_kv_heads;
     a.head_tiles = group / G;
-    a.partition = P;
+    a.partition = kernel_partition(P, max_ctx, kStageRows);
     a.max_parts = MP;
     a.scale_log2 = scale * kLog2e;
     a.fused_merge = persistent && MP > 1 && MP <= kFusedMaxParts;

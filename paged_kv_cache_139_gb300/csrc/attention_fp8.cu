@@ -1006,7 +1006,9 @@ pkv_status paged_attention_decode_fp8(void *out, const void *query, const void *
         return fail(PKV_EINVAL, "%s: max_context_len %d beyond the table (%lld tokens)", what, max_context_len,
                     (long long)table_cap);
     if (num_seqs == 0) return PKV_OK;
-    const int max_ctx = max_context_len > 0 ? max_context_len : (int)(table_cap > INT32_MAX / 2 ? INT32_MAX / 2 : table_cap);
+    // contexts of 2^30 tokens and more are latched as beyond their bound: the kernel rounds lengths up in 31 bits
+    const int64_t bound = max_context_len > 0 ? max_context_len : table_cap;
+    const int max_ctx = (int)(bound > INT32_MAX / 2 ? INT32_MAX / 2 : bound);
     if (!out || !query || !key_cache || !value_cache || !scales || !block_tables || !context_lens)
         return fail(PKV_EINVAL, "%s: NULL pointer", what);
     if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) || !aligned16(scales))
@@ -1034,7 +1036,7 @@ pkv_status paged_attention_decode_fp8(void *out, const void *query, const void *
     a.num_heads = num_heads;
     a.num_kv_heads = num_kv_heads;
     a.head_tiles = z.head_tiles;
-    a.partition = z.P;
+    a.partition = kernel_partition(z.P, max_ctx, kMaxTokens);
     a.max_parts = z.MP;
     a.scale_log2 = scale * kLog2e;
     f.scales = reinterpret_cast<const float2 *>(scales);

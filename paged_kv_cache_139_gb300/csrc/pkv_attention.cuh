@@ -217,7 +217,15 @@ template <typename T> cudaError_t launch_reduce(int D, const AttnArgs &a, dim3 g
     return launch(partition_reduce_kernel<128, T>, grid, dim3(kReduceThreads), 0, st, a);
 }
 
-inline int parts_for(int max_ctx, int P) { return max_ctx > 0 ? (max_ctx + P - 1) / P : 1; }
+inline int parts_for(int max_ctx, int P) { return max_ctx > 0 ? (int)(((long long)max_ctx + P - 1) / P) : 1; }
+
+// P as the kernels take it: they round lengths up to it in 31 bits, so one that is
+// longer than every context becomes the least multiple of `step` that holds them.
+inline int kernel_partition(int P, int max_ctx, int step) {
+    const long long all = ((long long)max_ctx + step - 1) / step * step;
+    const long long most = all < step ? step : all > (1 << 30) ? 1 << 30 : all;
+    return P < most ? P : (int)most;
+}
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 

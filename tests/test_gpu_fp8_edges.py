@@ -208,3 +208,27 @@ def test_prefill_nan_in_the_context_shows(cuda_device, dtype):
     assert nan[:100, :2].all() and not nan[:100, 2:].any()
     assert nan[100:200, 2:, 9].all() and nan[100:200].sum() == 2 * 100
     assert not nan[200:].any()
+
+
+def test_decode_in_one_huge_partition(cuda_device):
+    """Partition sizes up to the largest number are one partition."""
+    c = Case8(cuda_device, (1, 100, 700), 4, 2, 64, 16, seed=3)
+    one = c.decode(partition_size=1 << 20)
+    for P in (1 << 30, 2 ** 31 - 64):
+        assert torch.equal(c.decode(partition_size=P), one)
+        pkv.check()
+    c.check(one)
+
+
+def test_16_bit_decode_in_one_huge_partition(cuda_device):
+    S, H, Hkv, d, B = 2, 4, 2, 64, 16
+    g = torch.Generator().manual_seed(0)
+    kc, vc = (torch.randn(20, Hkv, B, d, generator=g).half().to(cuda_device) for _ in range(2))
+    q = torch.randn(S, H, d, generator=g).half().to(cuda_device)
+    bt = torch.arange(20, dtype=torch.int32, device=cuda_device).view(2, 10)
+    cl = torch.tensor([3, 150], dtype=torch.int32, device=cuda_device)
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    pkv.paged_attention_decode(a, q, kc, vc, bt, cl, partition_size=1 << 20)
+    pkv.paged_attention_decode(b, q, kc, vc, bt, cl, partition_size=2 ** 31 - 32)
+    pkv.check()
+    assert torch.equal(a, b)
