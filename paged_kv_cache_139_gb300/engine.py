@@ -341,6 +341,7 @@ class PagedKVCache:
         if out is None:
             out = torch.empty_like(query)
         mcl = step.max_context_len if max_context_len is None else max_context_len
+        mcl = mcl or _table_tokens(self, step)
         ws = self.workspace(query.shape[0], query.shape[1], mcl, partition_size)
         if self.fp8:
             return paged_attention_decode_fp8(out, query, self.key_cache, self.value_cache, self.scales, step.tables,
@@ -378,7 +379,7 @@ class PagedKVCache:
         if self.fp8:
             ws = self._workspace(paged_attention_prefill_fp8_workspace_size(
                 step.context_lens.shape[0], self.num_kv_heads, self.head_dim, self.block_size,
-                step.max_context_len or step.tables.shape[1] * self.block_size))
+                step.max_context_len or _table_tokens(self, step)))
             return paged_attention_prefill_fp8(out, query, self.key_cache, self.value_cache, self.scales, step.tables,
                                                step.context_lens, step.query_start, scale=scale,
                                                max_query_len=step.max_query_len, max_context_len=step.max_context_len,
@@ -435,6 +436,12 @@ class PagedKVCache:
         launch (paged_attention_decode_write) when the step has one new token
         per sequence."""
         return PreparedStep(self, query, key, value, step, out, scale, partition_size, stream, fused)
+
+
+def _table_tokens(eng: PagedKVCache, step) -> int:
+    """What bounds a step's contexts when nothing else does (a bound of 0, as of
+    sequences without tokens, is none to the calls); it sizes the workspace."""
+    return step.tables.shape[1] * eng.block_size
 
 
 def _check_step(eng: PagedKVCache, query, key, value, step, out, extra=()) -> int:
@@ -508,7 +515,8 @@ class PreparedStep:
         S, H, d = query.shape
         code = _check_step(eng, query, key, value, step, out)
         st = ctypes.c_void_p((stream or torch.cuda.current_stream(eng.device)).cuda_stream)
-        ws = eng.workspace(S, H, step.max_context_len, partition_size)
+        mcl = step.max_context_len or _table_tokens(eng, step)
+        ws = eng.workspace(S, H, mcl, partition_size)
         q = _scratch_queries(eng, query, stream)
         self._keep = (query, q, key, value, step, out, _held(eng, ws, stream))
         NB, B = eng.num_blocks, eng.block_size
@@ -519,7 +527,7 @@ class PreparedStep:
         self._attend = (out.data_ptr(), q.data_ptr(), eng.key_cache.data_ptr(), eng.value_cache.data_ptr(),
                         *((eng.scales.data_ptr(),) if eng.fp8 else ()),
                         step.tables.data_ptr(), step.context_lens.data_ptr(), S, step.tables.shape[1],
-                        step.max_context_len, B, NB, H, eng.num_kv_heads, d,
+                        mcl, B, NB, H, eng.num_kv_heads, d,
                         float(1.0 / math.sqrt(d) if scale is None else scale), partition_size, ws.data_ptr(),
                         ws.numel(), code, st)
         # one new token per sequence, in sequence order, written as it is in 16 bits: the write can ride in the
@@ -529,7 +537,7 @@ class PreparedStep:
             self._write_attend = (out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(),
                                   eng.key_cache.data_ptr(), eng.value_cache.data_ptr(), step.slots.data_ptr(),
                                   step.tables.data_ptr(), step.context_lens.data_ptr(), S, step.tables.shape[1],
-                                  step.max_context_len, B, NB, H, eng.num_kv_heads, d,
+                                  mcl, B, NB, H, eng.num_kv_heads, d,
                                   float(1.0 / math.sqrt(d) if scale is None else scale), partition_size, ws.data_ptr(),
                                   ws.numel(), code, st)
         self._fused = fused and self._write_attend is not None
@@ -591,8 +599,8 @@ class PreparedPrefill:
         S = step.context_lens.shape[0]
         NB, B, mb = eng.num_blocks, eng.block_size, step.tables.shape[1]
         if eng.fp8:
-            ws = eng._workspace(paged_attention_prefill_fp8_workspace_size(S, eng.num_kv_heads, d, B,
-                                                                           step.max_context_len or mb * B))
+            ws = eng._workspace(paged_attention_prefill_fp8_workspace_size(
+                S, eng.num_kv_heads, d, B, step.max_context_len or _table_tokens(eng, step)))
         else:
             ws = eng.prefill_workspace()
         q = _scratch_queries(eng, query, stream)

@@ -232,3 +232,19 @@ def test_16_bit_decode_in_one_huge_partition(cuda_device):
     pkv.paged_attention_decode(b, q, kc, vc, bt, cl, partition_size=2 ** 31 - 32)
     pkv.check()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_sequences_without_tokens_attend_to_nothing(cuda_device, fp8):
+    eng = PagedKVCache(70, 2, 64, 16, F8 if fp8 else torch.float16, cuda_device, 64)
+    seqs = [eng.new_sequence(0) for _ in range(3)]
+    step = eng.upload(eng.plan_tables(seqs))
+    q = torch.ones(3, 4, 64, dtype=torch.float16, device=cuda_device)
+    out = eng.attend(q, step, out=torch.full_like(q, 5.0))
+    pkv.check()
+    assert not bool(out.any())
+    kv = torch.zeros(0, 2, 64, dtype=torch.float16, device=cuda_device)
+    out.fill_(5.0)
+    eng.prepare(q, kv, kv, step, out)()
+    pkv.check()
+    assert not bool(out.any())
