@@ -205,6 +205,10 @@ class PagedKVCache:
         self.fp8 = dtype == torch.float8_e4m3fn
         self.scales = (scales if scales is not None else kv_scales(num_blocks, num_kv_heads, self.device)) if self.fp8 \
             else None
+        if self.fp8:                     # prepared steps and block copies go by their address
+            assert self.scales.shape == (num_blocks, num_kv_heads + num_kv_heads % 2, 2)
+            assert self.scales.dtype == torch.float32 and self.key_cache.dtype == self.value_cache.dtype == dtype
+            assert all(t.is_contiguous() for t in (self.scales, self.key_cache, self.value_cache))
         self.rotary = rotary
         self.alloc = BlockAllocator(num_blocks, block_size, free_order)
         self.num_blocks, self.num_kv_heads, self.head_dim, self.block_size = shape[0], shape[1], shape[3], shape[2]
@@ -454,7 +458,12 @@ def _check_step(eng: PagedKVCache, query, key, value, step, out, extra=()) -> in
     for t in (query, key, value, out, step.slots, step.tables, step.context_lens, step.pairs, *extra):
         assert t.is_cuda and t.is_contiguous()
     if eng.rotary is not None:
-        assert step.positions.is_cuda and step.positions.shape == step.slots.shape and query.shape[0] == key.shape[0]
+        assert query.shape[0] == key.shape[0], "rotary positions: a query for each new token"
+        pos, cs = step.positions, eng.rotary.cos_sin
+        assert pos is not None and pos.shape == step.slots.shape
+        assert cs.dim() == 3 and cs.shape[2] == 2 and eng.rotary.layout in ("half", "interleaved")
+        for t, dtype in ((pos, torch.int32), (cs, torch.float32)):
+            assert t.dtype == dtype and t.device == query.device and t.is_contiguous()
     return 1 if query.dtype == torch.bfloat16 else 0
 
 

@@ -178,3 +178,44 @@ def test_the_fused_write_takes_a_token_for_each_sequence(world, monkeypatch):
         step.write_attend()
     step()
     assert [name for name, _ in world.lib.calls] == ["paged_attention_decode"]
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+@pytest.mark.parametrize("wrong", [lambda x: x.long(), lambda x: x[:2], lambda x: None, lambda x: x.repeat_interleave(2)[::2]])
+def test_prepared_steps_refuse_positions_that_are_not_32_bit_ones(monkeypatch, kind, wrong):
+    """The eager calls refuse them; a prepared step hands on addresses and would read other numbers."""
+    check = engine._check_step
+    eng, _ = _engine(monkeypatch, False, True)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True), raising=False)
+    q, k, v = _tokens()
+    step = _step(kind)
+    assert check(eng, q, k, v, step, torch.zeros_like(q)) == 0
+    step.positions = wrong(step.positions)
+    with pytest.raises(AssertionError):
+        check(eng, q, k, v, step, torch.zeros_like(q))
+
+
+@pytest.mark.parametrize("table", [torch.zeros(10, 32, 2).double(), torch.zeros(10, 64), torch.zeros(10, 32, 4)[..., :2],
+                                   torch.zeros(10, 32, 2, device="meta")])
+def test_prepared_steps_refuse_tables_of_another_kind(monkeypatch, table):
+    check = engine._check_step
+    eng, _ = _engine(monkeypatch, False, True)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True), raising=False)
+    eng.rotary = engine.RotaryPositions(table)
+    q, k, v = _tokens()
+    with pytest.raises(AssertionError):
+        check(eng, q, k, v, _step("decode"), torch.zeros_like(q))
+
+
+def test_caches_refuse_scales_and_pools_of_another_kind():
+    f8 = torch.float8_e4m3fn
+    pool = torch.zeros(4, 3, 16, 64).to(f8)
+    make = lambda **kw: engine.PagedKVCache(4, 3, 64, 16, f8, "cpu", 4, **kw)  # noqa: E731
+    make(key_cache=pool, value_cache=pool.clone(), scales=torch.zeros(4, 4, 2))
+    for bad in (torch.zeros(4, 3, 2), torch.zeros(3, 4, 2), torch.zeros(4, 4, 2).double(), torch.zeros(4, 2, 4).transpose(1, 2)):
+        with pytest.raises(AssertionError):
+            make(scales=bad)
+    with pytest.raises(AssertionError):
+        make(key_cache=torch.zeros(4, 3, 16, 64, dtype=torch.float16))
+    with pytest.raises(AssertionError):
+        make(value_cache=torch.zeros(4, 3, 64, 16).to(f8).transpose(2, 3))
