@@ -215,6 +215,7 @@ class PagedKVCache:
         self.max_blocks_per_seq = max_blocks_per_seq
         self._ws: Optional[torch.Tensor] = None
         self._ws_retired: list = []
+        self._swaps: list = []                        # (event after the copies, their pairs)
         self._ws8: Optional[GrowingWorkspace] = None
         if workspace_of is not None:
             if not (self.fp8 and workspace_of.fp8 and self.device == workspace_of.device):
@@ -399,6 +400,13 @@ class PagedKVCache:
             raise ValueError("swapping between an 8-bit and a 16-bit pool")
         return (host.key_cache, host.value_cache) + ((host.scales,) if self.fp8 else ())
 
+    def _keep_until_copied(self, pairs: torch.Tensor, stream) -> None:
+        """The copies read the pairs from host memory, which would otherwise be
+        given to the next swap's pairs while they run."""
+        done = torch.cuda.Event()
+        done.record(stream if stream is not None else torch.cuda.current_stream(self.device))
+        self._swaps = [(e, p) for e, p in self._swaps if not e.query()] + [(done, pairs)]
+
     def swap_out(self, seqs: Sequence[int], host: HostKVPool, stream=None):
         """Evict a sequence group to the host pool, all or nothing: its blocks
         move to host blocks (one swap_blocks launch for keys, one for values)
@@ -410,7 +418,7 @@ class PagedKVCache:
             p = torch.from_numpy(pairs).pin_memory()
             for theirs, ours in zip(pools, self._pools()):
                 swap_blocks(theirs, ours, p, stream)
-            self._keep_pairs = p            # alive until the copies are done (next sync)
+            self._keep_until_copied(p, stream)
         return ids, pairs
 
     def swap_in(self, host_seqs: Sequence[int], host: HostKVPool, stream=None):
@@ -422,7 +430,7 @@ class PagedKVCache:
             p = torch.from_numpy(pairs).pin_memory()
             for theirs, ours in zip(pools, self._pools()):
                 swap_blocks(ours, theirs, p, stream)
-            self._keep_pairs = p
+            self._keep_until_copied(p, stream)
         return ids, pairs
 
     def prepare_prefill(self, query: torch.Tensor, key: torch.Tensor, value: torch.Tensor, step: DevicePrefill,

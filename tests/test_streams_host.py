@@ -219,3 +219,38 @@ def test_caches_refuse_scales_and_pools_of_another_kind():
         make(key_cache=torch.zeros(4, 3, 16, 64, dtype=torch.float16))
     with pytest.raises(AssertionError):
         make(value_cache=torch.zeros(4, 3, 64, 16).to(f8).transpose(2, 3))
+
+
+def test_swaps_keep_their_pairs_until_their_copies_are_done(monkeypatch):
+    """Several swaps may be issued before the first one's copies have read their pairs."""
+    import numpy as np
+    events = []
+
+    class Event:
+        def __init__(self):
+            self.done, self.stream = False, None
+            events.append(self)
+
+        def record(self, stream):
+            self.stream = stream
+
+        def query(self):
+            return self.done
+
+    alive, copied = [], []
+    monkeypatch.setattr(torch.cuda, "Event", Event)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+    monkeypatch.setattr(torch.Tensor, "pin_memory", lambda t: alive.append(weakref.ref(c := t.clone())) or c)
+    monkeypatch.setattr(engine, "swap_blocks", lambda dst, src, pairs, stream: copied.append(pairs.data_ptr()))
+    eng = engine.PagedKVCache(4, 2, 64, 16, torch.float8_e4m3fn, "cpu", 4)
+    move = lambda *a: ([0], np.zeros((2, 2), np.int32))  # noqa: E731
+    eng.alloc = types.SimpleNamespace(move_group=move)
+    host = types.SimpleNamespace(key_cache=None, value_cache=None, scales=torch.zeros(1), alloc=eng.alloc)
+    held = lambda: gc.collect() and None or [r() is not None for r in alive]  # noqa: E731
+    eng.swap_out([0], host)
+    eng.swap_in([0], host, stream=STREAM)
+    eng.swap_out([0], host)
+    assert held() == [True] * 3 and [e.stream for e in events] == ["current", STREAM, "current"] and len(copied) == 9
+    events[0].done = events[1].done = True
+    eng.swap_in([0], host)
+    assert held() == [False, False, True, True]
