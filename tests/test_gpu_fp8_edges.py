@@ -248,3 +248,53 @@ def test_sequences_without_tokens_attend_to_nothing(cuda_device, fp8):
     eng.prepare(q, kv, kv, step, out)()
     pkv.check()
     assert not bool(out.any())
+
+
+@pytest.mark.parametrize("parts", [31, 32, 33])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_merges_on_both_sides_of_its_two_kernels(cuda_device, parts, d):
+    """Splits of up to 32 partitions take a warp each, longer ones a CTA; shorter contexts beside them."""
+    c = Case8(cuda_device, (64 * parts, 64 * parts - 63, 64 * parts - 64, 65, 64, 0), 8, 2, d, 16, "bf16", seed=parts)
+    out = c.decode(partition_size=64)
+    pkv.check()
+    c.check(out)
+
+
+def test_decode_launches_of_512_sequences(cuda_device):
+    """Split contexts at the last and first sequences of the launches that a large batch takes."""
+    rng = np.random.default_rng(5)
+    ctx = rng.integers(0, 20, 1200)
+    at = [0, 1, 510, 511, 512, 513, 1022, 1023, 1024, 1025, 1199]
+    ctx[at] = rng.integers(100, 900, len(at))
+    c = Case8(cuda_device, ctx, 4, 2, 64, 8, seed=12)
+    out = c.decode(partition_size=64)
+    pkv.check()
+    c.check(out, seqs=at + [2, 509, 514, 1021, 1026, 1198])
+
+
+@pytest.mark.parametrize("n,rot", [(33, 48), (1, 16), (2049, 128), (5000, 256)])
+def test_table_rows_are_on_the_unit_circle_and_nothing_else_is_written(cuda_device, n, rot):
+    """Cosine and sine are each off by under 2^-22 (see test_gpu_rotary's test_table), so their squares' sum by under
+    2 sqrt(2) times that and its own rounding."""
+    buf = torch.full((n + 7, rot // 2, 2), 7.0, device=cuda_device)
+    pkv.rotary_table(n, rot, out=buf[:n])
+    pkv.check()
+    off = (buf[:n].double().square().sum(-1) - 1).abs()
+    assert float(off.max()) < 3 * 2.0 ** -22 and bool((buf[n:] == 7.0).all())
+    assert bool((buf[0, :, 0] == 1).all()) and bool((buf[0, :, 1] == 0).all())
+
+
+def test_a_plain_8_bit_cache_takes_slices_of_keys_and_values(cuda_device):
+    """Without rotary positions the queries go to the attention as they are, which takes them contiguous."""
+    eng = PagedKVCache(16, 2, 64, 16, F8, cuda_device, 8)
+    seq = eng.new_sequence(0)
+    qkv = torch.randn(20, 8, 64, generator=torch.Generator().manual_seed(3)).half().to(cuda_device)
+    q, k, v = qkv[:, :4], qkv[:, 4:6], qkv[:, 6:]
+    step = eng.upload_prefill(eng.plan_prefill([seq], [20]))
+    out = eng.prefill(q.contiguous(), k, v, step)
+    with pytest.raises(ValueError, match="contiguous"):
+        eng.prefill(q, k, v, step)
+    other = PagedKVCache(16, 2, 64, 16, F8, cuda_device, 8)
+    step2 = other.upload_prefill(other.plan_prefill([other.new_sequence(0)], [20]))
+    assert torch.equal(out, other.prefill(q.contiguous(), k.contiguous(), v.contiguous(), step2))
+    pkv.check()
