@@ -482,9 +482,8 @@ def _held(eng: PagedKVCache, ws, stream):
     not used again before the step's work is done, if the step is dropped
     while that runs."""
     held = (ws, *eng._pools(), *((eng.rotary.cos_sin,) if eng.rotary else ()))
-    if stream is not None:
-        for t in held:
-            t.record_stream(stream)
+    for t in held:
+        t.record_stream(stream)
     return held
 
 
@@ -531,7 +530,8 @@ class PreparedStep:
         self._L = load()
         S, H, d = query.shape
         code = _check_step(eng, query, key, value, step, out)
-        st = ctypes.c_void_p((stream or torch.cuda.current_stream(eng.device)).cuda_stream)
+        stream = stream if stream is not None else torch.cuda.current_stream(eng.device)
+        st = ctypes.c_void_p(stream.cuda_stream)
         mcl = step.max_context_len or _table_tokens(eng, step)
         ws = eng.workspace(S, H, mcl, partition_size)
         q = _scratch_queries(eng, query, stream)
@@ -612,7 +612,8 @@ class PreparedPrefill:
         self._L = load()
         T, H, d = query.shape
         code = _check_step(eng, query, key, value, step, out, (step.query_start,))
-        st = ctypes.c_void_p((stream or torch.cuda.current_stream(eng.device)).cuda_stream)
+        stream = stream if stream is not None else torch.cuda.current_stream(eng.device)
+        st = ctypes.c_void_p(stream.cuda_stream)
         S = step.context_lens.shape[0]
         NB, B, mb = eng.num_blocks, eng.block_size, step.tables.shape[1]
         if eng.fp8:

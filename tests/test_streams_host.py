@@ -254,3 +254,14 @@ def test_swaps_keep_their_pairs_until_their_copies_are_done(monkeypatch):
     events[0].done = events[1].done = True
     eng.swap_in([0], host)
     assert held() == [False, False, True, True]
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_a_prepared_step_marks_what_it_holds_on_the_current_stream(world, monkeypatch, kind):
+    """Without a stream of its own; the pools and the workspace may come from another."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: STREAM)
+    eng, ws = _engine(monkeypatch, True, True)
+    _prepare(eng, kind, stream=None)()
+    held = {t.data_ptr() for t in (ws, eng.key_cache, eng.value_cache, eng.scales, eng.rotary.cos_sin)}
+    assert {p for p, s in world.recorded if s is STREAM} == held
+    assert all(args[-1].value == 77 for _, args in world.lib.calls)
