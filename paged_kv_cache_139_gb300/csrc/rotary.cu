@@ -746,6 +746,8 @@ pkv_status append_impl(const char *what, bool fp8, void *query_out, const void *
         return fail(PKV_EINVAL, "%s: token strides must be multiples of 8 elements that hold all heads "
                                 "(query %lld, key %lld, value %lld)",
                     what, (long long)query_stride, (long long)key_stride, (long long)value_stride);
+    if (num_heads > 0 && query_out == query && num_tokens > 1 && query_stride != (int64_t)num_heads * head_dim)
+        return fail(PKV_EINVAL, "%s: queries %lld elements apart cannot be rotated in place", what, (long long)query_stride);
     // one CTA or thread per token and unit: the launch's grid is a 31-bit number
     const unsigned long long units =
         (unsigned long long)num_tokens * (num_heads + 2ull * num_kv_heads) * (unsigned)(head_dim / 16);

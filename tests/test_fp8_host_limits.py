@@ -1,7 +1,7 @@
 """Arguments of the 8-bit calls at the ends of their ranges (CPU: nothing is launched)."""
 import pytest
 
-from test_fp8_host import _message, _prefill
+from test_fp8_host import P, _append, _message, _prefill
 
 NO_DEVICE = 4           # PKV_ECUDA: the arguments were taken, and there is no GPU here to launch on
 
@@ -34,3 +34,12 @@ def test_prefill_takes_as_many_work_items_as_the_kernel():
     _without_a_gpu()
     sizes = dict(T=1 << 23, mql=256 * 256, H=256, Hkv=256, wsb=1 << 50)                 # 2^16 items a sequence
     assert _prefill(S=(1 << 14) - 1, **sizes) == NO_DEVICE and _prefill(S=1 << 14, **sizes) == 1
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_refuses_to_rotate_strided_queries_in_place(fp8):
+    """query_out is contiguous: its rows would lie over other tokens' queries that are still to be read."""
+    assert _append(fp8, qs=768) == 1 and "in place" in _message()
+    _without_a_gpu()
+    assert _append(fp8, qs=768, qo=2 * P) == NO_DEVICE and _append(fp8, qs=768, T=1) == NO_DEVICE
+    assert _append(fp8) == NO_DEVICE
