@@ -21,6 +21,8 @@ import contextlib
 import ctypes
 import functools
 import math
+import re
+import weakref
 from typing import Optional, Sequence
 
 import numpy as np
@@ -146,7 +148,29 @@ def make_workspace(device, nbytes: int, stream: Optional[torch.cuda.Stream] = No
     st = _stream(stream, dev)
     _ck(load().paged_attention_workspace_init(buf.data_ptr(), buf.numel(), st), "paged_attention_workspace_init")
     (stream or torch.cuda.current_stream(dev)).synchronize()
+    return _made(buf, "paged_attention_workspace_init")
+
+
+_workspaces: list = []
+
+
+def _made(buf: torch.Tensor, init: str) -> torch.Tensor:
+    """Remembers a workspace, for as long as it lives, and the call that prepares it."""
+    _workspaces[:] = [(ref, name) for ref, name in _workspaces if ref() is not None]
+    _workspaces.append((weakref.ref(buf), init))
     return buf
+
+
+def _prepare_again(index: int) -> None:
+    """Every workspace made here for this device: a call that gave up waiting
+    leaves the counters of its own mid-count, and later calls on it would skip
+    work."""
+    torch.cuda.synchronize(index)
+    for ref, init in _workspaces:
+        buf = ref()
+        if buf is not None and buf.get_device() == index:
+            _call(getattr(load(), init), init, index, buf.data_ptr(), buf.numel(), _raw_stream(None, index))
+    torch.cuda.synchronize(index)
 
 
 _ws_cache: dict = {}
@@ -501,7 +525,7 @@ def make_fp8_workspace(device, nbytes: int, stream: Optional[torch.cuda.Stream] 
     _call(load().paged_attention_fp8_workspace_init, "paged_attention_fp8_workspace_init", index, buf.data_ptr(),
           buf.numel(), _raw_stream(stream, index))
     (stream or torch.cuda.current_stream(buf.device)).synchronize()
-    return buf
+    return _made(buf, "paged_attention_fp8_workspace_init")
 
 
 def _capturing(stream: Optional[torch.cuda.Stream]) -> bool:
@@ -682,11 +706,22 @@ def swap_blocks(dst_pool: torch.Tensor, src_pool: torch.Tensor, pairs: torch.Ten
     _ck(rc, "swap_blocks")
 
 
+_FLAG_TIMEOUT = 8          # kFlagTimeout of the device's status word
+
+
 def check(stream: Optional[torch.cuda.Stream] = None, device=None) -> None:
     """Synchronise the stream and raise if the device latched an index error
-    or a wait timeout since the last check."""
+    or a wait timeout since the last check.  After a timeout the workspaces made
+    here (make_workspace, make_fp8_workspace, the bindings' and the engine's
+    own) have been prepared again, once the device had finished its work."""
     s = stream if stream is not None else torch.cuda.current_stream(device)
-    _ck(load().pkv_check(ctypes.c_void_p(s.cuda_stream)), "pkv_check")
+    try:
+        _ck(load().pkv_check(ctypes.c_void_p(s.cuda_stream)), "pkv_check")
+    except PkvError as e:
+        flags = re.search(r"device error flags 0x([0-9a-f]+)", str(e))
+        if flags and int(flags[1], 16) & _FLAG_TIMEOUT:
+            _prepare_again(torch.cuda.current_device())
+        raise
 
 
 # -- host block allocator ---------------------------------------------------------

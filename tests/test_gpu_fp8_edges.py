@@ -298,3 +298,44 @@ def test_a_plain_8_bit_cache_takes_slices_of_keys_and_values(cuda_device):
     step2 = other.upload_prefill(other.plan_prefill([other.new_sequence(0)], [20]))
     assert torch.equal(out, other.prefill(q.contiguous(), k.contiguous(), v.contiguous(), step2))
     pkv.check()
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_steps_after_a_reported_timeout_are_whole(cuda_device, fp8):
+    """A call that gives up waiting may leave its workspace's counters mid-count (written here by hand, with the self-test's
+    timeout beside them): once check has reported it, the engine's and the bindings' own workspaces serve again."""
+    S, H, Hkv, d, B, n = 40, 4, 2, 64, 16, 700
+    g = torch.Generator().manual_seed(4)
+    eng = PagedKVCache(S * 45, Hkv, d, B, F8 if fp8 else torch.float16, cuda_device, 45)
+    seqs = [eng.new_sequence(0) for _ in range(S)]
+    new = [torch.randn(S * n, h, d, generator=g).half().to(cuda_device) for h in (H, Hkv, Hkv)]
+    eng.prefill(*new, eng.upload_prefill(eng.plan_prefill(seqs, [n] * S)))
+    step = eng.upload(eng.plan_tables(seqs))
+    q = torch.randn(S, H, d, generator=g).half().to(cuda_device)
+    out = torch.empty_like(q)
+    none = new[1][:0]
+    prep = eng.prepare(q, none, none, step, out, partition_size=64)
+    if fp8:
+        own = lambda o: pkv.paged_attention_decode_fp8(o, q, eng.key_cache, eng.value_cache, eng.scales, step.tables,  # noqa: E731
+                                                       step.context_lens, partition_size=64)
+    else:
+        own = lambda o: pkv.paged_attention_decode(o, q, eng.key_cache, eng.value_cache, step.tables, step.context_lens,  # noqa: E731
+                                                   partition_size=64)
+    prep()
+    want = out.clone()
+    assert torch.equal(own(torch.empty_like(q)), want)
+    pkv.check()
+    bindings = pkv._ws8_cache[0]._buf if fp8 else pkv._ws_cache[torch.device("cuda", 0)]
+    for ws in (eng._workspace(0), bindings):
+        ws[:8].view(torch.int32).copy_(torch.tensor([50, 3], dtype=torch.int32))         # tickets taken, pipelines done
+    torch.cuda.synchronize()
+    L = pkv.load()
+    assert L.pkv_selftest_wait_timeout(100000, torch.cuda.current_stream().cuda_stream) == 0
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.check()
+    assert e.value.status_name == "PKV_ETIMEOUT"
+    out.fill_(5.0)
+    prep()
+    mine = own(torch.full_like(q, 5.0))
+    pkv.check()
+    assert torch.equal(out, want) and torch.equal(mine, want)

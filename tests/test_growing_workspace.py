@@ -133,3 +133,44 @@ def test_what_cannot_share_a_workspace_is_refused():
         _cache(torch.float16, workspace_of=_cache(torch.float16))
     with pytest.raises(ValueError):
         _cache(device="meta", workspace_of=_cache())
+
+
+class Library:
+    """pkv_check fails once with these flags; preparations are written down."""
+
+    def __init__(self, flags):
+        self.flags, self.prepared = flags, []
+
+    def pkv_check(self, stream):
+        return 5 if self.flags == 8 else 3
+
+    def pkv_last_error_string(self):
+        return b"device error flags 0x%x; first: something (value 1)" % self.flags
+
+    def _init(self, ptr, nbytes, stream):
+        self.prepared.append((ptr, nbytes))
+        return 0
+
+    paged_attention_workspace_init = paged_attention_fp8_workspace_init = _init
+
+
+@pytest.mark.parametrize("flags,again", [(8, True), (8 | 2, True), (2, False), (128, False)])
+def test_after_a_timeout_all_workspaces_are_prepared_again(monkeypatch, flags, again):
+    import types
+    stream = types.SimpleNamespace(cuda_stream=0, synchronize=lambda: None)
+    synced = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)         # where the CPU's tensors say that they are
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: synced.append(len(lib.prepared)))
+    monkeypatch.setattr(pkv, "_raw_stream", lambda s, index: 0)
+    monkeypatch.setattr(pkv, "_workspaces", [])
+    lib = Library(flags)
+    monkeypatch.setattr(pkv, "load", lambda: lib)
+    kept = [pkv.make_workspace("cpu", 1000), pkv.make_fp8_workspace("cpu", 2000)]
+    pkv.make_fp8_workspace("cpu", 3000)                                   # gone
+    lib.prepared.clear()
+    gc.collect()
+    with pytest.raises(pkv.PkvError):
+        pkv.check()
+    assert lib.prepared == ([(w.data_ptr(), w.numel()) for w in kept] if again else [])
+    assert synced == ([0, 2] if again else [])
