@@ -36,9 +36,11 @@
 // partitions of a split context are merged by a second kernel: merging in this
 // one (a fence and an atomic per item) cost more than its launch.
 //
-// Measured: 256 x uniform[1, 4096] tokens of 32 heads x 128 (4.5 GB) 630 us, 7.1
-// TB/s; 64 sequences of 40 heads, 288 MB, 51.5 us; 8 x 32,768 tokens of 8 kv
-// heads, 538 MB, 90.6 us with 6 us of merging.
+// Measured: 256 x uniform[1, 4096] tokens of 32 heads x 128 (4.5 GB) 632 us, 7.1
+// TB/s; 64 sequences of 40 heads, 288 MB, 52 us; 8 x 32,768 tokens of 8 kv heads,
+// 538 MB, 90 us with 6 us of merging.  More than eight query heads per kv head take a
+// head tile each, which reads and converts its tiles again: 537 MB in 94 us at 32/4
+// heads, in 167 us at 32/2.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -744,7 +746,9 @@ __global__ void fp8_workspace_init_kernel(uint4 *ws, size_t n16) {
     ws[i] = v;
 }
 
-// Tokens per partition.  A GPU of 152 SMs has 1216 pipelines.  Where that many
+// Tokens per partition.  A GPU of 152 SMs has 1216 pipelines (152 x kCtasPerSm x
+// kPipes; the number is written down, since the workspace's size is asked for
+// without a GPU and has to be the call's).  Where that many
 // items hold everything, the shortest partitions that do so end first (1 x
 // 8,000 tokens, 8 kv heads: 11.4 us at 64 tokens, 13.9 at 256); beyond, 256
 // tokens (512 of head_dim 64) keep the items' beginnings and ends small beside
@@ -754,7 +758,7 @@ __global__ void fp8_workspace_init_kernel(uint4 *ws, size_t n16) {
 // tokens, 32 kv heads: 630 us at 1024, 659 at 256).
 int choose_partition8(int partition_size, int num_seqs, int tiles, int head_dim, int max_ctx) {
     if (partition_size > 0) return partition_size;
-    constexpr long long kPipelines = 1216;
+    constexpr long long kPipelines = 152 * kCtasPerSm * kPipes;
     const long long n = (long long)num_seqs * tiles;
     for (int P = 64; P <= 256; P *= 2)
         if (n * parts_for(max_ctx, P) <= kPipelines) return P;

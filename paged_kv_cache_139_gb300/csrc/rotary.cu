@@ -65,7 +65,7 @@ __device__ __forceinline__ float4 cos_sin_of(unsigned long long turns0, unsigned
 
 // Thread t owns two neighbouring pairs (one 16-byte store) of every
 // (threads / columns)-th position of its CTA's stretch: its turns stay in
-// registers.  131,072 x 128: 11.5 us, 5.9 TB/s written.
+// registers.  131,072 x 128: 11.2 us, 6.0 TB/s written.
 __global__ void __launch_bounds__(kRopeThreads) rotary_table_kernel(float4 *__restrict__ out,
                                                                     const __grid_constant__ TurnTable tab,
                                                                     int num_positions, int columns, int rows,
@@ -193,7 +193,7 @@ __device__ __forceinline__ void rotate_row(const RopeArgs &a, const T *src, T *d
 
 // One thread per unit of a row; the rows of a token are its query heads, its
 // key heads and its value heads.  16,381 tokens of 32/8 heads: 62.4 us, 6.5 TB/s,
-// the rate of a copy; 256 tokens of 32/32 heads: 4.3 us.
+// the rate of a copy; 256 tokens of 32/32 heads: 4.3 us in a captured graph.
 template <int D, typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rotary_append_kernel(const RopeArgs a) {
     constexpr int UPR = D / 16;
@@ -443,7 +443,7 @@ __device__ __forceinline__ uint4 load_shared16(const void *p) {
 //    32/32 heads: 124 us with the queries last, 114 so; of 32/8: 68 and 59).
 // 16,381 tokens of 32/32 heads: 114 us, 6.0 TB/s (200 with two passes of loads
 // into registers, 133 with 64 KB and 256 threads to a CTA, half on keys and half
-// on values); a step of 256 tokens of 32/8 heads: 3.0 us.
+// on values); a step of 256 tokens of 32/8 heads: 2.8 us in a captured graph.
 constexpr int kAppend8Threads = 128;
 constexpr int kAppend8Ctas = 5;                                     // to an SM
 constexpr int kSlabBytes = 32 * 1024;                               // one head of a block of 128 takes twice that
