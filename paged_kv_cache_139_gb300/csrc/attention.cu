@@ -1298,8 +1298,9 @@ size_t paged_attention_workspace_size(int num_seqs, int num_heads, int num_kv_he
     if (num_seqs <= 0 || num_heads <= 0 || head_dim <= 0 || max_context_len < 0 || partition_size < 0)
         return 0;
     if (max_context_len == 0) return pkv::kWsHeaderBytes;
-    const int P = paged_attention_partition_size(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len,
-                                                 partition_size);
+    const int P = pkv::kernel_partition(paged_attention_partition_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                                       max_context_len, partition_size),
+                                        max_context_len, pkv::kStageRows);
     return pkv::ws_layout(num_seqs, num_heads, head_dim, pkv::parts_for(max_context_len, P)).bytes;
 }
 
@@ -1338,7 +1339,8 @@ pkv_status decode_impl(void *out, const void *query, const void *key_cache, cons
         return fail(PKV_EINVAL, "paged_attention_decode: NULL pointer");
     if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache))
         return fail(PKV_EINVAL, "paged_attention_decode: pointers must be 16-byte aligned");
-    const int P = choose_partition(partition_size, num_seqs, num_kv_heads, head_dim, max_ctx);
+    const int P = kernel_partition(choose_partition(partition_size, num_seqs, num_kv_heads, head_dim, max_ctx), max_ctx,
+                                   kStageRows);
     const int MP = parts_for(max_ctx, P);
     if (MP > 65535) return fail(PKV_EINVAL, "paged_attention_decode: %d partitions per sequence", MP);
     const WsLayout wl = ws_layout(num_seqs, num_heads, head_dim, MP);
@@ -1386,7 +1388,7 @@ pkv_status decode_impl(void *out, const void *query, const void *key_cache, cons
     a.num_heads = num_heads;
     a.num_kv_heads = num_kv_heads;
     a.head_tiles = group / G;
-    a.partition = kernel_partition(P, max_ctx, kStageRows);
+    a.partition = P;
     a.max_parts = MP;
     a.scale_log2 = scale * kLog2e;
     a.fused_merge = persistent && MP > 1 && MP <= kFusedMaxParts;

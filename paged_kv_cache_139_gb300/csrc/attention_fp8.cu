@@ -777,7 +777,7 @@ F8Sizes f8_sizes(int S, int H, int Hkv, int D, int max_ctx, int partition_size) 
     const int group = H / Hkv;
     z.head_tiles = (group + kTileHeads - 1) / kTileHeads;
     z.tile = (group + z.head_tiles - 1) / z.head_tiles;
-    z.P = choose_partition8(partition_size, S, Hkv * z.head_tiles, D, max_ctx);
+    z.P = kernel_partition(choose_partition8(partition_size, S, Hkv * z.head_tiles, D, max_ctx), max_ctx, kMaxTokens);
     z.MP = parts_for(max_ctx, z.P);
     const size_t n = z.MP > 1 ? (size_t)S * H * z.MP : 0;
     z.m_off = kBodyOff;
@@ -1040,7 +1040,7 @@ pkv_status paged_attention_decode_fp8(void *out, const void *query, const void *
     a.num_heads = num_heads;
     a.num_kv_heads = num_kv_heads;
     a.head_tiles = z.head_tiles;
-    a.partition = kernel_partition(z.P, max_ctx, kMaxTokens);
+    a.partition = z.P;
     a.max_parts = z.MP;
     a.scale_log2 = scale * kLog2e;
     f.scales = reinterpret_cast<const float2 *>(scales);

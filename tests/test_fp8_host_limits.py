@@ -43,3 +43,17 @@ def test_append_refuses_to_rotate_strided_queries_in_place(fp8):
     _without_a_gpu()
     assert _append(fp8, qs=768, qo=2 * P) == NO_DEVICE and _append(fp8, qs=768, T=1) == NO_DEVICE
     assert _append(fp8) == NO_DEVICE
+
+
+def test_workspaces_hold_the_partitions_that_the_kernels_make():
+    """The kernels take partitions of 2^30 tokens at most: contexts past that are two, whatever size was asked for."""
+    import paged_kv_cache_139_gb300 as pkv
+    size = pkv.paged_attention_workspace_size
+    n = 2 ** 31 - 1
+    for P in (1 << 30, 2 ** 31 - 32):
+        assert size(1, 1, 1, 64, n, P) == size(1, 1, 1, 64, 600, 512) > 256
+        assert size(1, 1, 1, 64, 1 << 30, P) == 256
+    assert size(1, 1, 1, 64, 2 ** 31 - 64, 2 ** 31 - 32) == size(1, 1, 1, 64, 600, 512)
+    assert size(3, 4, 2, 64, 1000, 2 ** 31 - 32) == size(3, 4, 2, 64, 1000, 1024) == 256
+    size8 = pkv.paged_attention_decode_fp8_workspace_size
+    assert size8(3, 4, 2, 64, 1000, 2 ** 31 - 64) == size8(3, 4, 2, 64, 1000, 1024) == 256
