@@ -453,6 +453,109 @@ pkv_status paged_attention_prefill(void *out_dev, const void *query_dev,
                                    float scale, void *workspace_dev, size_t workspace_bytes,
                                    pkv_dtype dtype, struct CUstream_st *stream);
 
+/* ---------------------------------------------------------------------------
+ * paged_attention_decode_window -- paged_attention_decode with a sliding window
+ * and first tokens that stay visible.  The pages have no counterpart: models
+ * that bound what a token sees attend this way over the same cache.
+ *
+ * The query of sequence s, n = context_lens[s], sees the tokens t < n with
+ *   t >= n - window  or  t < num_sinks,
+ * its own token (t = n - 1) always among them; x_t and out as for
+ * paged_attention_decode, over those tokens only.  n = 0 gives zeros.
+ * Table entries of blocks that hold no visible token are not read: such blocks
+ * may be freed and their entries hold anything.  What invisible tokens of other
+ * blocks hold has no effect (NaN included).  Probabilities enter the product
+ * with 22 bits for fp16 and 16 for bf16.
+ *   window     at least 1;  num_sinks  at least 0
+ * Needs no workspace, keeps nothing between calls and does not depend on what
+ * else runs: calls may overlap on the GPU.  The result of a sequence does not
+ * change from call to call of the same sizes.  num_seqs <= 65535;
+ * num_heads <= 65535, any number of them per kv head; scale finite; contexts
+ * (max_context_len, or the table's capacity) up to 2^30 tokens.  Other arguments
+ * as for paged_attention_decode.
+ * ------------------------------------------------------------------------- */
+pkv_status paged_attention_decode_window(void *out_dev, const void *query_dev,
+                                         const void *key_cache_dev, const void *value_cache_dev,
+                                         const int32_t *block_tables_dev,
+                                         const int32_t *context_lens_dev, int num_seqs,
+                                         int max_blocks_per_seq, int max_context_len,
+                                         int block_size, int num_blocks, int num_heads,
+                                         int num_kv_heads, int head_dim, float scale, int window,
+                                         int num_sinks, pkv_dtype dtype, struct CUstream_st *stream);
+
+/* ---------------------------------------------------------------------------
+ * paged_attention_prefill_window -- paged_attention_prefill with a sliding
+ * window and first tokens that stay visible: the new token at position p of its
+ * sequence sees the tokens t <= p with
+ *   t > p - window  or  t < num_sinks.
+ * Table entries of blocks that no new token of the sequence sees are not read.
+ * As in paged_attention_prefill, a value that is NaN may also reach rows that do
+ * not see it: here up to 255 tokens before it, and up to 255 tokens after the
+ * last one whose window holds it.
+ *   window     at least 1;  num_sinks  at least 0
+ * Other arguments, and the workspace, as for paged_attention_prefill.
+ * ------------------------------------------------------------------------- */
+pkv_status paged_attention_prefill_window(void *out_dev, const void *query_dev,
+                                          const void *key_cache_dev, const void *value_cache_dev,
+                                          const int32_t *block_tables_dev,
+                                          const int32_t *context_lens_dev,
+                                          const int32_t *query_start_dev, int num_seqs, int num_tokens,
+                                          int max_query_len, int max_blocks_per_seq, int block_size,
+                                          int num_blocks, int num_heads, int num_kv_heads,
+                                          int head_dim, float scale, int window, int num_sinks,
+                                          void *workspace_dev, size_t workspace_bytes,
+                                          pkv_dtype dtype, struct CUstream_st *stream);
+
+/* ---------------------------------------------------------------------------
+ * paged_attention_decode_shared -- paged_attention_decode of a batch in which
+ * groups of sequences begin with the same blocks (forks of one prompt, requests
+ * after one instruction; "vLLM & PagedAttention" §VII): the shared tokens are read
+ * and multiplied once for a group instead of once per sequence.
+ *
+ * Group g is the sequences group_start[g] .. group_start[g + 1] - 1.  The first
+ * prefix_lens[s] tokens of sequence s -- the same number throughout a group --
+ * are read through the table of the group's first sequence, the others
+ * through the sequence's own; the result is that of paged_attention_decode where
+ * the tables agree.  A prefix may have any length up to the context, 0 included.
+ *   group_start_dev  int32 [num_groups + 1], from 0 to num_seqs, non-decreasing
+ *   prefix_lens_dev  int32 [num_seqs]
+ *   max_group_size   host-side upper bound on a group's sequences (0 = num_seqs)
+ *   max_prefix_len   host-side upper bound on every prefix (0 = max_context_len,
+ *                    or the table's capacity when that is 0 too); both bounds
+ *                    size the workspace and the grid
+ *   max_suffix_len   about how many tokens follow a prefix at most (0 = not
+ *                    known): decides how the work is split, never the result
+ *   workspace_dev    scratch of at least
+ *                    paged_attention_decode_shared_workspace_size(...) bytes; it
+ *                    needs no preparation and holds nothing between calls.  Calls
+ *                    that may overlap on the GPU need one each.
+ * Groups that leave sequences out, that exceed max_group_size or whose
+ * prefix_lens differ latch PKV_EINDEX, as do prefixes beyond max_prefix_len or
+ * the context.
+ * Probabilities over a prefix enter the product with 11 bits for fp16 where the
+ * group has more than 16 query rows per kv head (sequences x heads), with 22
+ * otherwise; with 16 for bf16.  A NaN among a group's first tokens reaches all of
+ * its sequences.  Two launches.  num_seqs <= 65535; up to 128 query heads per kv
+ * head; scale > 0; contexts up to 2^30 tokens.  Other arguments as for
+ * paged_attention_decode.
+ * ------------------------------------------------------------------------- */
+pkv_status paged_attention_decode_shared(void *out_dev, const void *query_dev,
+                                         const void *key_cache_dev, const void *value_cache_dev,
+                                         const int32_t *block_tables_dev,
+                                         const int32_t *context_lens_dev,
+                                         const int32_t *group_start_dev,
+                                         const int32_t *prefix_lens_dev, int num_seqs,
+                                         int num_groups, int max_group_size, int max_prefix_len,
+                                         int max_suffix_len, int max_blocks_per_seq,
+                                         int max_context_len, int block_size, int num_blocks,
+                                         int num_heads, int num_kv_heads, int head_dim, float scale,
+                                         void *workspace_dev, size_t workspace_bytes,
+                                         pkv_dtype dtype, struct CUstream_st *stream);
+
+size_t paged_attention_decode_shared_workspace_size(int num_seqs, int num_groups, int num_heads,
+                                                    int num_kv_heads, int head_dim,
+                                                    int max_prefix_len, int max_group_size);
+
 /* Bytes of workspace paged_attention_decode needs for these sizes: 256 for
  * the counters, plus the partition partials when a context can span more
  * than one partition.  partition_size as above. */

@@ -14,6 +14,8 @@ missing, the first call raises.
     rotary_table             cosines and sines of the rotary positions
     kv_rotary_and_cache      the K/V write with the rotary rotation on the way
     *_fp8                    the K/V write and the attention of an 8-bit cache
+    *_window                 decode and prompt-phase attention with a sliding window and sinks
+    paged_attention_decode_shared   decode attention that reads shared prefixes once
 """
 from __future__ import annotations
 
@@ -37,6 +39,8 @@ __all__ = ["PkvError", "PkvOOM", "kv_reshape_and_cache", "paged_attention_decode
            "rotary_table", "kv_rotary_and_cache", "kv_rotary_and_cache_fp8", "kv_scales",
            "paged_attention_decode_fp8", "paged_attention_decode_fp8_workspace_size",
            "paged_attention_prefill_fp8", "paged_attention_prefill_fp8_workspace_size", "make_fp8_workspace", "GrowingWorkspace",
+           "paged_attention_decode_window", "paged_attention_prefill_window", "paged_attention_decode_shared",
+           "paged_attention_decode_shared_workspace_size",
            "validate_copy_pairs", "swap_blocks", "check", "launch_count", "version", "BlockAllocator", "library_path"]
 
 PKV_F16, PKV_BF16 = 0, 1
@@ -654,6 +658,108 @@ def paged_attention_prefill_fp8(out: torch.Tensor, query: torch.Tensor, key_cach
             S, Hkv, d, B, max_context_len if max_context_len > 0 else mb * B), stream)
     _call(load().paged_attention_prefill_fp8, what, index, *ptrs, _at(query_start, "query_start", torch.int32, index), S,
           T, max_query_len, max_context_len, mb, B, NB, H, Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale,
+          _at(workspace, "workspace", torch.uint8, index), workspace.numel(), _dtype_code(query),
+          _raw_stream(stream, index))
+    return out
+
+
+# -- sliding windows and shared prefixes ------------------------------------------------
+
+def _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S, index):
+    if query.shape[2] != key_cache.shape[3] or out.shape != query.shape or value_cache.shape != key_cache.shape:
+        raise ValueError(f"{what}: shape mismatch")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError(f"{what}: block_tables must be [S][max_blocks], context_lens [S]")
+    dt, i32 = query.dtype, torch.int32
+    return (_at(out, "out", dt, index), _at(query, "query", dt, index), _at(key_cache, "key_cache", dt, index),
+            _at(value_cache, "value_cache", dt, index), _at(block_tables, "block_tables", i32, index),
+            _at(context_lens, "context_lens", i32, index))
+
+
+def paged_attention_decode_window(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                  value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                  window: int, num_sinks: int = 0, scale: Optional[float] = None,
+                                  max_context_len: int = 0,
+                                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_attention_decode over the last `window` tokens of each context (the
+    newest among them) and its first num_sinks ones.  Table entries of blocks
+    without a visible token are not read.  No workspace; calls may overlap.
+    Returns out."""
+    what = "paged_attention_decode_window"
+    index = _cuda_index(query, "query")
+    S, H, d = query.shape
+    ptrs = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S, index)
+    NB, Hkv, B, _ = key_cache.shape
+    _call(load().paged_attention_decode_window, what, index, *ptrs, S, block_tables.shape[1], max_context_len, B, NB, H,
+          Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale, window, num_sinks, _dtype_code(query),
+          _raw_stream(stream, index))
+    return out
+
+
+def paged_attention_prefill_window(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                   value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                   query_start: torch.Tensor, window: int, num_sinks: int = 0,
+                                   scale: Optional[float] = None, max_query_len: int = 0,
+                                   workspace: Optional[torch.Tensor] = None,
+                                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_attention_prefill in which the new token at position p sees the
+    tokens after p - window up to itself and the first num_sinks ones.  workspace:
+    from make_workspace (its counter balances the work over the SMs), one call at
+    a time; None: each SM takes a fixed share, and calls may overlap.  Returns out."""
+    what = "paged_attention_prefill_window"
+    index = _cuda_index(query, "query")
+    T, H, d = query.shape
+    S = context_lens.shape[0]
+    ptrs = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S, index)
+    if query_start.shape != (S + 1,):
+        raise ValueError(f"{what}: query_start must be [S+1]")
+    NB, Hkv, B, _ = key_cache.shape
+    ws = (None, 0) if workspace is None else (_at(workspace, "workspace", torch.uint8, index), workspace.numel())
+    _call(load().paged_attention_prefill_window, what, index, *ptrs,
+          _at(query_start, "query_start", torch.int32, index), S, T, max_query_len, block_tables.shape[1], B, NB, H, Hkv,
+          d, 1.0 / math.sqrt(d) if scale is None else scale, window, num_sinks, *ws, _dtype_code(query),
+          _raw_stream(stream, index))
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def paged_attention_decode_shared_workspace_size(num_seqs: int, num_groups: int, num_heads: int, num_kv_heads: int,
+                                                 head_dim: int, max_prefix_len: int, max_group_size: int = 0) -> int:
+    return int(load().paged_attention_decode_shared_workspace_size(num_seqs, num_groups, num_heads, num_kv_heads,
+                                                                   head_dim, max_prefix_len, max_group_size))
+
+
+def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                  value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                  group_start: torch.Tensor, prefix_lens: torch.Tensor,
+                                  scale: Optional[float] = None, max_context_len: int = 0, max_prefix_len: int = 0,
+                                  max_group_size: int = 0, max_suffix_len: int = 0,
+                                  workspace: Optional[torch.Tensor] = None,
+                                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_attention_decode of groups of sequences that begin with the same
+    blocks, which are read once for a group.  group_start int32 [G+1]: group g is
+    the sequences from group_start[g] on; prefix_lens int32 [S]: how many of its
+    first tokens a sequence shares with its group, which are read through the
+    table of the group's first sequence.  The max_* bounds (0: as large as the
+    batch allows) size the workspace and the split of the work.  workspace: uint8
+    scratch of paged_attention_decode_shared_workspace_size bytes, in no
+    particular state; None takes memory for the call on its stream.  Returns out."""
+    what = "paged_attention_decode_shared"
+    index = _cuda_index(query, "query")
+    S, H, d = query.shape
+    ptrs = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S, index)
+    if group_start.dim() != 1 or not group_start.shape[0] or prefix_lens.shape != (S,):
+        raise ValueError(f"{what}: group_start must be [G+1], prefix_lens [S]")
+    NB, Hkv, B, _ = key_cache.shape
+    G, mb = group_start.shape[0] - 1, block_tables.shape[1]
+    if workspace is None:
+        need = paged_attention_decode_shared_workspace_size(
+            S, G, H, Hkv, d, max_prefix_len or max_context_len or mb * B, max_group_size)
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    _call(load().paged_attention_decode_shared, what, index, *ptrs, _at(group_start, "group_start", torch.int32, index),
+          _at(prefix_lens, "prefix_lens", torch.int32, index), S, G, max_group_size, max_prefix_len, max_suffix_len, mb,
+          max_context_len, B, NB, H, Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale,
           _at(workspace, "workspace", torch.uint8, index), workspace.numel(), _dtype_code(query),
           _raw_stream(stream, index))
     return out

@@ -18,7 +18,7 @@ LIBDIR = PKG / "lib"
 LIB = LIBDIR / "libpkv.so"
 
 CUDA_SOURCES = ["runtime.cu", "cache_ops.cu", "attention.cu", "attention_noalloc.cu", "prefill.cu",
-                "rotary.cu", "attention_fp8.cu"]
+                "rotary.cu", "attention_fp8.cu", "attention_span.cu", "prefill_window.cu", "shared_prefix.cu"]
 CXX_SOURCES = ["allocator.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,0 +1,857 @@
+// Decode attention over spans of a paged context: a sliding window with first
+// tokens that stay visible (sinks), and sequences that share a prefix.
+//
+// What it computes.  A query row sees a set of its context's tokens; with
+// x_t = scale * q . K_t over them,  out = sum_t softmax(x)_t V_t.
+//   window  a sequence of n tokens sees [0, min(sinks, n)) and [n - window, n)
+//   shared  it sees all n, in two halves: its own tokens [prefix, n), and the
+//           prefix, computed once for all sequences of its group.  Each half is
+//           (m, l, o) = (max x, sum 2^(x - m), sum 2^(x - m) V) in the log2
+//           domain, and halves join as M = max m, sum l 2^(m - M), sum o 2^(m - M).
+//
+// What bounds it: HBM, at 2 d operations per key and query row against 2 d
+// bytes.  So the work goes by (sequence or group, kv head): every key and value
+// is read once for all query rows that see it.
+//
+// How (sm_103a):
+//   * One CTA of four warps per (sequence, kv head), with 8 or 16 query heads as
+//     the columns of S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16): the
+//     tokens are the 16-row operand, so one head or eight cost the same.  The
+//     fifth-generation tensor cores would want 64 rows of queries; four heads
+//     do not fill them, and at 48 products per 16 KB they are not what bounds.
+//   * Each warp streams stages of 16 tokens through a ring of its own, two or
+//     three deep: it issues its tiled TMA copies itself and refills a slot as
+//     soon as it has read it, so no warp waits for another before the end.
+//   * Probabilities enter the second product as a rounded part and its
+//     remainder (22 bits in fp16, 16 in bf16): rounded once they would add an
+//     error as large as the output's own rounding.
+//   * Invisible tokens of a stage (past the context, before the window, between
+//     sinks and window) get -inf scores and zeroed value fragments; blocks that
+//     hold none but those are not read, nor are their table entries.
+//   * Few sequences are spread over the GPU by clusters of 2 to 16 CTAs per
+//     (sequence, kv head), which join through distributed shared memory: no
+//     workspace, no second launch, no counters.
+//   * The shared form's second launch overlaps the first: own tokens are
+//     attended to before it waits for the prefix's partial results.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "pkv_attention.cuh"
+#include "pkv_host.cuh"
+#include "pkv_span.cuh"
+#include "pkv_tmap.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kSpanThreads = kWarps * 32;
+constexpr int kTok = 16;                       // tokens of a stage: the rows of one product
+constexpr int kMaxCluster = 16;
+
+enum SpanMode { kSpanWindow, kSpanSuffix, kSpanPrefix };
+
+struct SpanArgs {
+    void *out;                   // [S][H][D]
+    const void *q;               // [S][H][D]
+    const int32_t *tables;       // [S][max_blocks]
+    const int32_t *ctx_lens;     // [S]
+    const int32_t *prefix_lens;  // [S]     shared
+    const int32_t *group_start;  // [groups + 1]
+    DeviceStatus *st;
+    int num_seqs, num_groups, max_blocks, max_ctx, max_prefix, max_group;
+    int log2_block, num_blocks, num_heads, num_kv_heads;
+    int group;                   // query heads per kv head
+    int head_tiles, tile_heads;  // a kv head's query heads in tiles of at most 8 NT
+    int window, sinks;
+    float scale_log2;
+    PrefixParts parts;
+};
+
+// R ring slots per warp, CTAS resident CTAs per SM.
+template <int D, int NT> struct SpanConf {
+    static constexpr int HALVES = D / 64;
+    static constexpr uint32_t HALF_BYTES = kTok * 128;                 // 16 tokens x 64 elements
+    static constexpr uint32_t TENSOR_BYTES = HALVES * HALF_BYTES;
+    static constexpr uint32_t STAGE_BYTES = 2 * TENSOR_BYTES;
+    static constexpr int R = D == 128 ? 2 : 4;
+    static constexpr int CTAS = NT == 1 ? 3 : 2;
+    static constexpr int COLS = 8 * NT;
+    static constexpr int LD = D + 4;                                   // fp32 row of an output: 8 columns apart on 8 banks
+    static constexpr uint32_t ring = 0;
+    static constexpr uint32_t comb = kWarps * R * STAGE_BYTES;         // the CTA's o [COLS][LD], then m, l [COLS]
+    static constexpr uint32_t ml = comb + COLS * LD * 4;
+    static constexpr uint32_t wml = ml + 2 * COLS * 4;                 // the warps' m, l [kWarps][2][COLS]
+    static constexpr uint32_t bars = wml + kWarps * 2 * COLS * 4;
+    static constexpr uint32_t bytes = bars + kWarps * R * 8;
+    static_assert(COLS * LD * 4 <= R * STAGE_BYTES, "a warp's outputs fit its ring");
+    static_assert(ml % 16 == 0 && bars % 8 == 0, "alignment");
+};
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// A 2^x that is never slower than its one instruction; 2^-inf = 0.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two fp32 as a rounded 16-bit pair and the pair of what the rounding left.
+template <typename T> __device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint32_t &lo);
+template <> __device__ __forceinline__ void split_pair<__half>(float x, float y, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = Mma<__half>::pack(x - f.x, y - f.y);
+}
+template <> __device__ __forceinline__ void split_pair<__nv_bfloat16>(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = Mma<__nv_bfloat16>::pack(x, y);
+    lo = Mma<__nv_bfloat16>::pack(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// The shared address of CTA `rank` of the cluster that corresponds to this CTA's `addr`.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_cluster1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// A running (m, l, o) of four output elements, and another part joined to it.
+struct Joined {
+    float m, l;
+    float4 o;
+    __device__ __forceinline__ void add(float m2, float l2, const float4 &o2) {
+        // (parts that saw no token have weight 0 and values 0; a NaN score leaves m alone and shows in l and o)
+        const float M = fmaxf(m, m2), z = M == -INFINITY ? 0.f : M;
+        const float a = ex2(m - z), b = ex2(m2 - z);
+        m = M;
+        l = l * a + l2 * b;
+        o.x = o.x * a + o2.x * b;
+        o.y = o.y * a + o2.y * b;
+        o.z = o.z * a + o2.z * b;
+        o.w = o.w * a + o2.w * b;
+    }
+};
+
+template <int D, int NT, typename T, int MODE>
+__global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
+    span_attention_kernel(const SpanArgs a, const __grid_constant__ CUtensorMap tmk,
+                          const __grid_constant__ CUtensorMap tmv) {
+    using C = SpanConf<D, NT>;
+    constexpr int R = C::R, HALVES = C::HALVES, COLS = C::COLS, LD = C::LD;
+    // the 128-byte swizzle repeats every 1024 bytes: the ring starts on such a boundary
+    extern __shared__ __align__(1024) unsigned char smem_span[];
+    unsigned char *sm = smem_span;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t nrank = MODE == kSpanPrefix ? 1u : cluster_size(), rank = MODE == kSpanPrefix ? 0u : cluster_rank();
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::bars) + warp * R;      // this warp's own
+    unsigned char *ring = sm + C::ring + warp * R * C::STAGE_BYTES;
+    if (lane == 0) {
+        for (int i = 0; i < R; i++) mbar_init(&full[i], 1);
+        fence_mbar_init();
+        if (warp == 0) {
+            prefetch_tensor_map(&tmk);
+            prefetch_tensor_map(&tmv);
+        }
+    }
+    __syncwarp();
+    // The suffix half starts while the prefix half runs.  That one began after every grid before it
+    // had finished (it waits for them before it lets this one start), so queries, lengths, tables and
+    // caches are in place; only its partial results are not, and the wait for those comes below.
+    // (Loads here go past L1.)
+    if constexpr (MODE != kSpanSuffix) pdl_wait();
+    pdl_trigger();
+    bool dead = __any_sync(kFull, timed_out(a.st));     // an earlier wait gave up: no copies, nothing waited for
+    if (smem_u32(sm) & 1023u) {
+        if (tid == 0) latch(a.st, kFlagTimeout, -2);
+        dead = true;
+    }
+
+    // ---- this CTA's rows and tokens ----
+    const int B = 1 << a.log2_block;
+    const int item = blockIdx.x / nrank;
+    const int tile = item % a.head_tiles, g = item / a.head_tiles % a.num_kv_heads, unit = item / a.head_tiles / a.num_kv_heads;
+    int s = unit;                                       // whose table is read
+    int first = 0, low = 0, ctx = 0, prefix = 0;        // visible: [0, first) and [low, ctx)
+    int cols = min(a.tile_heads, a.group - tile * a.tile_heads);
+    int row0 = unit * a.num_heads + g * a.group + tile * a.tile_heads;     // rows are numbered sequence * heads + head
+    if constexpr (MODE == kSpanPrefix) {
+        const int b = __ldcg(a.group_start + unit), e = __ldcg(a.group_start + unit + 1);
+        const bool edge = (unit == 0 && b != 0) || (unit == a.num_groups - 1 && e != a.num_seqs);
+        if (b < 0 || e < b || e > a.num_seqs || e - b > a.max_group || edge) {
+            if (tid == 0 && g == 0 && blockIdx.y == 0) latch(a.st, kFlagBadGroup, unit);
+            if (b < 0 || e < b || e > a.num_seqs || e - b > a.max_group) return;
+        }
+        if (e == b) return;
+        prefix = __ldcg(a.prefix_lens + b);
+        if (g == 0 && blockIdx.y == 0)
+            for (int i = b + tid; i < e; i += kSpanThreads)
+                if (__ldcg(a.prefix_lens + i) != prefix) latch(a.st, kFlagBadGroup, unit);
+        if (prefix < 0 || prefix > a.max_prefix) return;           // the suffix half reports it
+        low = blockIdx.y * a.parts.part;
+        if (low >= prefix) return;
+        ctx = min(prefix, low + a.parts.part);
+        s = b;
+        cols = (e - b) * a.group;
+        row0 = b * a.num_heads + g * a.group;
+    } else {
+        ctx = __ldcg(a.ctx_lens + s);
+        if (ctx < 0 || ctx > a.max_ctx) {
+            if (tid == 0 && g == 0 && tile == 0 && rank == 0) latch(a.st, kFlagBadContext, ctx);
+            ctx = ctx < 0 ? 0 : a.max_ctx;
+        }
+        if constexpr (MODE == kSpanWindow) {
+            low = max(0, ctx - a.window);
+            first = min(a.sinks, low);
+        } else {
+            prefix = __ldcg(a.prefix_lens + s);
+            if (prefix < 0 || prefix > ctx || prefix > a.max_prefix) {
+                if (tid == 0 && g == 0 && tile == 0 && rank == 0) latch(a.st, kFlagBadContext, prefix);
+                prefix = prefix < 0 ? 0 : min(ctx, a.max_prefix);
+            }
+            low = prefix;
+        }
+    }
+    // row of column c (a group's columns run over its sequences, each with its heads of kv head g)
+    auto row_of = [&](int c) -> size_t {
+        if constexpr (MODE == kSpanPrefix) return (size_t)row0 + (size_t)(c / a.group) * a.num_heads + c % a.group;
+        else return (size_t)row0 + c;
+    };
+    // stages: those of the sinks, then those of [low, ctx); a stage that holds both counts once
+    const int from = low / kTok;
+    int nsink = (first + kTok - 1) / kTok;
+    if (nsink > from) nsink = from;
+    const int nst = low < ctx ? nsink + (ctx + kTok - 1) / kTok - from : 0;
+    const int st0 = (int)((long long)nst * rank / nrank), st1 = (int)((long long)nst * (rank + 1) / nrank);
+    const int mine = dead ? 0 : max(0, (st1 - st0 - warp + kWarps - 1) / kWarps);
+    auto token0 = [&](int i) {                          // first token of this warp's stage i
+        const int v = st0 + warp + kWarps * i;
+        return (v < nsink ? v : v - nsink + from) * kTok;
+    };
+
+    // ---- copies ----
+    const int lcps = a.log2_block >= 4 ? 0 : 4 - a.log2_block;       // blocks per stage (log2)
+    const int rows_per_copy = B < kTok ? B : kTok;
+    const int per_load = 32 >> lcps;                                 // stages whose table entries one load brings
+    const int32_t *table = a.tables + (size_t)s * a.max_blocks;
+    auto seen_block = [&](int t) { return t < ctx && (t < first || t + rows_per_copy > low); };
+    auto load_entries = [&](int base) -> int {
+        const int i = base + (lane >> lcps);
+        if (i >= mine) return -1;
+        const int t = token0(i) + (lane & ((1 << lcps) - 1)) * rows_per_copy;
+        return seen_block(t) ? __ldcg(table + (t >> a.log2_block)) : -1;
+    };
+    const uint64_t policy = policy_evict_first();
+    int ent = load_entries(0), base = 0;
+    int ent_next = load_entries(per_load);
+    // copy of this lane: half h of block j's keys (t = 0) or values (t = 1)
+    const int ct = lane & 1, ch = (lane >> 1) % HALVES, cj = (lane >> 1) / HALVES;
+    auto issue = [&](int i) {
+        if (i == base + per_load) {
+            base = i;
+            ent = ent_next;
+            ent_next = load_entries(base + per_load);
+        }
+        const int p = __shfl_sync(kFull, ent, (((i - base) << lcps) + cj) & 31);
+        const int t0 = token0(i), t = t0 + cj * rows_per_copy;
+        bool go = cj < (1 << lcps) && seen_block(t);
+        const bool bad = go && (p < 0 || p >= a.num_blocks);
+        const unsigned badm = __ballot_sync(kFull, bad);
+        if (badm) {
+            if (lane == __ffs(badm) - 1) latch(a.st, kFlagBadBlock, p);
+            go = go && !bad;
+        }
+        const unsigned n = __popc(__ballot_sync(kFull, go));
+        const int slot = i % R;
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], n * (uint32_t)rows_per_copy * 128u);
+        __syncwarp();
+        if (go) {
+            unsigned char *dst = ring + slot * C::STAGE_BYTES + ct * C::TENSOR_BYTES + ch * C::HALF_BYTES +
+                                 cj * rows_per_copy * 128;
+            tma_load_4d(dst, ct ? (const void *)&tmv : (const void *)&tmk, ch * 64, t & (B - 1), g, p, &full[slot], policy);
+        }
+    };
+    for (int i = 0; i < R && i < mine; i++) issue(i);
+
+    // ---- queries: B fragments, column lane / 4 of each column tile, elements 2 (lane % 4) and + 8 of each step ----
+    const int cq = lane & 3, r0 = lane >> 2;
+    uint32_t qf[NT][D / 16][2];
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+        const int c = 8 * n + r0;
+        const bool there = c < cols && mine > 0;
+        const uint32_t *qp = reinterpret_cast<const uint32_t *>(static_cast<const T *>(a.q) + (there ? row_of(c) : 0) * D) + cq;
+#pragma unroll
+        for (int k = 0; k < D / 16; k++) {
+            qf[n][k][0] = there ? __ldcg(qp + 8 * k) : 0u;
+            qf[n][k][1] = there ? __ldcg(qp + 8 * k + 4) : 0u;
+        }
+    }
+
+    float o[NT][D / 16][4];                             // O^T: elements 16 i + r0 (+ 8), columns 2 cq, 2 cq + 1
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+#pragma unroll
+        for (int i = 0; i < D / 16; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[n][i][e] = 0.f;
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+    }
+
+    // 16-byte chunk `chunk` of token row `row` in a tensor's stage (swizzled)
+    auto chunk_at = [&](const unsigned char *t, int row, int chunk) {
+        return t + (chunk >> 3) * C::HALF_BYTES + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+    };
+
+    int i = 0;
+    for (; i < mine; i++) {
+        const int slot = i % R;
+        if (!__all_sync(kFull, mbar_wait(&full[slot], (i / R) & 1, kWaitLimitCycles))) {
+            if (lane == 0) latch(a.st, kFlagTimeout, i);
+            dead = true;
+            break;
+        }
+        const unsigned char *ks = ring + slot * C::STAGE_BYTES, *vs = ks + C::TENSOR_BYTES;
+        const int t0 = token0(i);
+        // S^T = K Q^T (even and odd steps apart: half the chain)
+        float x[NT][4], y[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[n][e] = y[n][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 16; k += 2) {
+            uint32_t f[4], h[4];
+            ldmatrix_x4(f, chunk_at(ks, lane & 15, 2 * k + (lane >> 4)));
+            ldmatrix_x4(h, chunk_at(ks, lane & 15, 2 * k + 2 + (lane >> 4)));
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                Mma<T>::run(x[n], f, qf[n][k][0], qf[n][k][1]);
+                Mma<T>::run(y[n], h, qf[n][k + 1][0], qf[n][k + 1][1]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[n][e] = (x[n][e] + y[n][e]) * a.scale_log2;
+        // tokens of the stage that the rows see (the same for every row)
+        const bool whole = t0 + kTok <= ctx && (t0 >= low || t0 + kTok <= first);
+        uint32_t vm0 = ~0u, vm1 = ~0u;                  // value fragments: tokens 2 cq, 2 cq + 1, and those + 8
+        if (!whole) {
+            auto seen = [&](int t) { return t0 + t < ctx && (t0 + t >= low || t0 + t < first); };
+            if (!seen(r0)) {
+#pragma unroll
+                for (int n = 0; n < NT; n++) x[n][0] = x[n][1] = -INFINITY;
+            }
+            if (!seen(r0 + 8)) {
+#pragma unroll
+                for (int n = 0; n < NT; n++) x[n][2] = x[n][3] = -INFINITY;
+            }
+            vm0 = (seen(2 * cq) ? 0xffffu : 0u) | (seen(2 * cq + 1) ? 0xffff0000u : 0u);
+            vm1 = (seen(2 * cq + 8) ? 0xffffu : 0u) | (seen(2 * cq + 9) ? 0xffff0000u : 0u);
+        }
+        // running maximum and sum; P^T as the second product's B operand
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            float m0 = fmaxf(x[n][0], x[n][2]), m1 = fmaxf(x[n][1], x[n][3]);
+#pragma unroll
+            for (int d = 4; d <= 16; d <<= 1) {
+                m0 = fmaxf(m0, __shfl_xor_sync(kFull, m0, d));
+                m1 = fmaxf(m1, __shfl_xor_sync(kFull, m1, d));
+            }
+            if (__any_sync(kFull, m0 > m[n][0] || m1 > m[n][1])) {
+                m0 = fmaxf(m[n][0], m0);
+                m1 = fmaxf(m[n][1], m1);
+                const float a0 = m0 == -INFINITY ? 1.f : ex2(m[n][0] - m0), a1 = m1 == -INFINITY ? 1.f : ex2(m[n][1] - m1);
+                m[n][0] = m0;
+                m[n][1] = m1;
+                l[n][0] *= a0;
+                l[n][1] *= a1;
+#pragma unroll
+                for (int j = 0; j < D / 16; j++) {
+                    o[n][j][0] *= a0;
+                    o[n][j][1] *= a1;
+                    o[n][j][2] *= a0;
+                    o[n][j][3] *= a1;
+                }
+            }
+            const float z0 = m[n][0] == -INFINITY ? 0.f : m[n][0], z1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+            const float p0 = ex2(x[n][0] - z0), p1 = ex2(x[n][1] - z1), p2 = ex2(x[n][2] - z0), p3 = ex2(x[n][3] - z1);
+            l[n][0] += p0 + p2;
+            l[n][1] += p1 + p3;
+            uint32_t hi0, lo0, hi1, lo1;
+            split_pair<T>(p0, p1, hi0, lo0);
+            split_pair<T>(p2, p3, hi1, lo1);
+            ph[n][0] = movmatrix_trans(hi0);
+            ph[n][1] = movmatrix_trans(hi1);
+            pl[n][0] = movmatrix_trans(lo0);
+            pl[n][1] = movmatrix_trans(lo1);
+        }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int j = 0; j < D / 16; j++) {
+            uint32_t f[4];
+            ldmatrix_x4_trans(f, chunk_at(vs, (lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1)));
+            if (!whole) {
+                f[0] &= vm0;
+                f[1] &= vm0;
+                f[2] &= vm1;
+                f[3] &= vm1;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                Mma<T>::run(o[n][j], f, ph[n][0], ph[n][1]);
+                Mma<T>::run(o[n][j], f, pl[n][0], pl[n][1]);
+            }
+        }
+        __syncwarp();                                   // the slot has been read
+        if (i + R < mine) issue(i + R);
+    }
+    if (dead)                                           // copies in flight land before their memory is reused
+        for (int k = i; k < min(i + R, mine); k++) mbar_wait(&full[k % R], (k / R) & 1, kDrainLimitCycles);
+    __syncwarp();
+
+    // ---- the warps' parts, through their rings ----
+    float *wo = reinterpret_cast<float *>(ring);
+    float *wml = reinterpret_cast<float *>(sm + C::wml) + warp * 2 * COLS;
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) {
+            l[n][0] += __shfl_xor_sync(kFull, l[n][0], d);
+            l[n][1] += __shfl_xor_sync(kFull, l[n][1], d);
+        }
+        const int c = 8 * n + 2 * cq;
+        if (r0 == 0) {
+            wml[c] = m[n][0];
+            wml[c + 1] = m[n][1];
+            wml[COLS + c] = l[n][0];
+            wml[COLS + c + 1] = l[n][1];
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; j++) {
+            wo[c * LD + 16 * j + r0] = o[n][j][0];
+            wo[(c + 1) * LD + 16 * j + r0] = o[n][j][1];
+            wo[c * LD + 16 * j + r0 + 8] = o[n][j][2];
+            wo[(c + 1) * LD + 16 * j + r0 + 8] = o[n][j][3];
+        }
+    }
+    __syncthreads();
+    const float *all_ml = reinterpret_cast<const float *>(sm + C::wml);
+    auto join_warps = [&](int c, int e) {
+        Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll
+        for (int w = 0; w < kWarps; w++)
+            r.add(all_ml[w * 2 * COLS + c], all_ml[w * 2 * COLS + COLS + c],
+                  *reinterpret_cast<const float4 *>(sm + C::ring + w * R * C::STAGE_BYTES + (c * LD + e) * 4));
+        return r;
+    };
+    constexpr int UPR = D / 4;                          // units of four elements per row
+    auto store_out = [&](int c, int e, const Joined &r) {
+        const float inv = r.l > 0.f ? 1.f / r.l : 0.f;
+        uint2 w;
+        w.x = Mma<T>::pack(r.o.x * inv, r.o.y * inv);
+        w.y = Mma<T>::pack(r.o.z * inv, r.o.w * inv);
+        *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row_of(c) * D + e) = w;
+    };
+    if constexpr (MODE == kSpanPrefix) {
+        for (int u = tid; u < cols * UPR; u += kSpanThreads) {
+            const int c = u / UPR, e = u % UPR * 4;
+            const Joined r = join_warps(c, e);
+            const size_t at = row_of(c) * a.parts.max_parts + blockIdx.y;
+            *reinterpret_cast<float4 *>(a.parts.o + at * D + e) = r.o;
+            if (e == 0) {
+                a.parts.m[at] = r.m;
+                a.parts.l[at] = r.l;
+            }
+        }
+    } else {
+        if constexpr (MODE == kSpanSuffix) pdl_wait();              // the prefix half's results
+        const int np = MODE == kSpanSuffix ? (prefix + a.parts.part - 1) / a.parts.part : 0;
+        auto join_prefix = [&](int c, int e, Joined &r) {
+            const size_t at = row_of(c) * a.parts.max_parts;
+            for (int p0 = 0; p0 < np; p0 += 4) {                    // four parts to a round trip
+                float pm[4], pl2[4];
+                float4 po[4];
+#pragma unroll
+                for (int p = 0; p < 4; p++) {
+                    const bool there = p0 + p < np;
+                    pm[p] = there ? __ldcg(a.parts.m + at + p0 + p) : -INFINITY;
+                    pl2[p] = there ? __ldcg(a.parts.l + at + p0 + p) : 0.f;
+                    po[p] = there ? __ldcg(reinterpret_cast<const float4 *>(a.parts.o + (at + p0 + p) * D + e))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int p = 0; p < 4; p++) r.add(pm[p], pl2[p], po[p]);
+            }
+        };
+        if (nrank == 1) {
+            for (int u = tid; u < cols * UPR; u += kSpanThreads) {
+                const int c = u / UPR, e = u % UPR * 4;
+                Joined r = join_warps(c, e);
+                if constexpr (MODE == kSpanSuffix) join_prefix(c, e, r);
+                store_out(c, e, r);
+            }
+        } else {
+            // the CTA's part into its own shared memory, then every CTA joins its share of the
+            // elements over all CTAs of the cluster
+            float *comb = reinterpret_cast<float *>(sm + C::comb), *cml = reinterpret_cast<float *>(sm + C::ml);
+            for (int u = tid; u < cols * UPR; u += kSpanThreads) {
+                const int c = u / UPR, e = u % UPR * 4;
+                const Joined r = join_warps(c, e);
+                *reinterpret_cast<float4 *>(comb + c * LD + e) = r.o;
+                if (e == 0) {
+                    cml[c] = r.m;
+                    cml[COLS + c] = r.l;
+                }
+            }
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            const uint32_t comb_s = smem_u32(comb), cml_s = smem_u32(cml);
+            for (int u = tid * nrank + rank; u < cols * UPR; u += kSpanThreads * nrank) {
+                const int c = u / UPR, e = u % UPR * 4;
+                Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+                for (uint32_t k0 = 0; k0 < nrank; k0 += 4) {
+                    float pm[4], pl2[4];
+                    float4 po[4];
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; k++) {
+                        const bool there = k0 + k < nrank;
+                        const uint32_t from_rank = there ? k0 + k : rank;
+                        pm[k] = there ? ld_cluster1(map_rank(cml_s + c * 4, from_rank)) : -INFINITY;
+                        pl2[k] = ld_cluster1(map_rank(cml_s + (COLS + c) * 4, from_rank));
+                        po[k] = ld_cluster4(map_rank(comb_s + (c * LD + e) * 4, from_rank));
+                    }
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; k++)
+                        if (k0 + k < nrank) r.add(pm[k], pl2[k], po[k]);
+                }
+                if constexpr (MODE == kSpanSuffix) join_prefix(c, e, r);
+                store_out(c, e, r);
+            }
+            __syncwarp();
+            cluster_arrive();                            // no CTA leaves while others read its memory
+            cluster_wait();
+        }
+    }
+}
+
+// The cache [NB][Hkv][B][D] as a 4-D tensor (innermost first); a box is 64
+// elements of d by min(B, 16) tokens of one (block, kv head).
+bool encode_span_map(CUtensorMap *map, const void *base, int num_blocks, int Hkv, int B, int D, bool bf16) {
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)B, (cuuint64_t)Hkv, (cuuint64_t)(num_blocks > 0 ? num_blocks : 1)};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)B * D * 2, (cuuint64_t)Hkv * B * D * 2};
+    const cuuint32_t box[4] = {64u, (cuuint32_t)(B < kTok ? B : kTok), 1u, 1u};
+    return encode_tiled16(map, base, 4, dims, strides, box, bf16);
+}
+
+struct SpanMaps {
+    CUtensorMap k, v;
+};
+
+template <int D, int NT, typename T, int MODE>
+cudaError_t launch_span_kernel(const SpanArgs &a, const SpanMaps &maps, long long items, int parts, int cluster,
+                               cudaStream_t st) {
+    auto kern = span_attention_kernel<D, NT, T, MODE>;
+    constexpr size_t smem = SpanConf<D, NT>::bytes;
+    static std::atomic<unsigned long long> sized{0}, wide{0};
+    cudaError_t e = allow_smem(kern, smem, sized);
+    if (e != cudaSuccess) return e;
+    if (cluster > 8) {                                   // more than the portable size, once per device
+        int d = 0;
+        if ((e = cudaGetDevice(&d)) != cudaSuccess) return e;
+        const unsigned long long bit = d < 64 ? 1ull << d : 0ull;
+        if (!(wide.load(std::memory_order_acquire) & bit)) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            wide.fetch_or(bit, std::memory_order_release);
+        }
+    }
+    return launch_clusters(kern, dim3((unsigned)(items * cluster), (unsigned)parts), dim3(kSpanThreads), (unsigned)cluster,
+                           smem, st, a, maps.k, maps.v);
+}
+
+template <int MODE>
+cudaError_t launch_span(int D, int NT, bool bf16, const SpanArgs &a, const SpanMaps &maps, long long items, int parts,
+                        int cluster, cudaStream_t st) {
+    if (D == 128) {
+        if (NT == 1)
+            return bf16 ? launch_span_kernel<128, 1, __nv_bfloat16, MODE>(a, maps, items, parts, cluster, st)
+                        : launch_span_kernel<128, 1, __half, MODE>(a, maps, items, parts, cluster, st);
+        return bf16 ? launch_span_kernel<128, 2, __nv_bfloat16, MODE>(a, maps, items, parts, cluster, st)
+                    : launch_span_kernel<128, 2, __half, MODE>(a, maps, items, parts, cluster, st);
+    }
+    if (NT == 1)
+        return bf16 ? launch_span_kernel<64, 1, __nv_bfloat16, MODE>(a, maps, items, parts, cluster, st)
+                    : launch_span_kernel<64, 1, __half, MODE>(a, maps, items, parts, cluster, st);
+    return bf16 ? launch_span_kernel<64, 2, __nv_bfloat16, MODE>(a, maps, items, parts, cluster, st)
+                : launch_span_kernel<64, 2, __half, MODE>(a, maps, items, parts, cluster, st);
+}
+
+int resident_ctas(int NT) { return sm_count() * (NT == 1 ? SpanConf<128, 1>::CTAS : SpanConf<128, 2>::CTAS); }
+
+// CTAs per (sequence, kv head): as a rule one, since a cluster's CTAs start and
+// end together; more while the whole batch would leave resident CTAs idle, but at
+// least a stage for every warp.
+int choose_cluster(long long items, long long max_tokens, int resident) {
+    const long long stages = (max_tokens + kTok - 1) / kTok;
+    int c = 1;
+    while (c < kMaxCluster && items * c * 2 <= resident && stages >= (long long)kWarps * c * 2) c *= 2;
+    return c;
+}
+
+struct SpanCall {
+    const char *what;
+    const void *out, *query, *key_cache, *value_cache;
+    const int32_t *block_tables, *context_lens;
+    int num_seqs, max_blocks, max_context_len, block_size, num_blocks, num_heads, num_kv_heads, head_dim;
+    float scale;
+    pkv_dtype dtype;
+};
+
+// The checks that both calls share; fills what the kernels need of them.
+pkv_status check_span(const SpanCall &c, SpanArgs &a, SpanMaps &maps) {
+    if (c.dtype != PKV_F16 && c.dtype != PKV_BF16) return fail(PKV_EINVAL, "%s: bad dtype %d", c.what, (int)c.dtype);
+    if (c.num_seqs < 0 || c.num_seqs > 65535 || c.max_blocks < 0 || c.num_blocks < 0)
+        return fail(PKV_EINVAL, "%s: bad sizes (seqs %d, table width %d, blocks %d)", c.what, c.num_seqs, c.max_blocks,
+                    c.num_blocks);
+    if (c.head_dim != 64 && c.head_dim != 128)
+        return fail(PKV_EINVAL, "%s: head_dim %d not supported (64 or 128)", c.what, c.head_dim);
+    if (!is_pow2(c.block_size) || c.block_size < 4 || c.block_size > 128)
+        return fail(PKV_EINVAL, "%s: block_size %d not a power of two in [4, 128]", c.what, c.block_size);
+    if (c.num_heads <= 0 || c.num_kv_heads <= 0 || c.num_heads % c.num_kv_heads || c.num_heads > 65535)
+        return fail(PKV_EINVAL, "%s: %d query heads do not group over %d kv heads (at most 65535)", c.what, c.num_heads,
+                    c.num_kv_heads);
+    if (!std::isfinite(c.scale)) return fail(PKV_EINVAL, "%s: scale must be finite", c.what);
+    const int64_t cap = (int64_t)c.max_blocks * c.block_size;
+    if (c.max_context_len < 0 || c.max_context_len > cap)
+        return fail(PKV_EINVAL, "%s: max_context_len %d beyond the table (%lld tokens)", c.what, c.max_context_len,
+                    (long long)cap);
+    const int64_t most = c.max_context_len > 0 ? c.max_context_len : cap;
+    if (most > (1 << 30)) return fail(PKV_EINVAL, "%s: contexts of more than 2^30 tokens", c.what);
+    if (c.num_seqs == 0) return PKV_OK;
+    if (!c.out || !c.query || !c.key_cache || !c.value_cache || !c.block_tables || !c.context_lens)
+        return fail(PKV_EINVAL, "%s: NULL pointer", c.what);
+    if (!aligned16(c.out) || !aligned16(c.query) || !aligned16(c.key_cache) || !aligned16(c.value_cache))
+        return fail(PKV_EINVAL, "%s: pointers must be 16-byte aligned", c.what);
+    a.st = status_ptr();
+    if (!a.st) return fail(PKV_ECUDA, "%s: no device status word", c.what);
+    a.out = const_cast<void *>(c.out);
+    a.q = c.query;
+    a.tables = c.block_tables;
+    a.ctx_lens = c.context_lens;
+    a.num_seqs = c.num_seqs;
+    a.max_blocks = c.max_blocks;
+    a.max_ctx = (int)most;
+    a.log2_block = ilog2(c.block_size);
+    a.num_blocks = c.num_blocks;
+    a.num_heads = c.num_heads;
+    a.num_kv_heads = c.num_kv_heads;
+    a.group = c.num_heads / c.num_kv_heads;
+    a.head_tiles = (a.group + 15) / 16;
+    a.tile_heads = (a.group + a.head_tiles - 1) / a.head_tiles;
+    a.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
+    const bool bf16 = c.dtype == PKV_BF16;
+    std::memset(&maps, 0, sizeof maps);
+    if (!encode_span_map(&maps.k, c.key_cache, c.num_blocks, c.num_kv_heads, c.block_size, c.head_dim, bf16) ||
+        !encode_span_map(&maps.v, c.value_cache, c.num_blocks, c.num_kv_heads, c.block_size, c.head_dim, bf16))
+        return fail(PKV_ECUDA, "%s: no tensor map of the cache", c.what);
+    return PKV_OK;
+}
+
+// ---- sequences that share a prefix -------------------------------------------
+
+// Groups of up to this many query rows per kv head (sequences x heads) fit the
+// columns of the kernel above; larger ones go to the tcgen05 kernel.
+constexpr int kFewRows = 16;
+
+// Tokens of a prefix's partition: a multiple of 128 that spreads the prefixes
+// over the GPU.
+int prefix_partition(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int max_prefix, int max_group) {
+    const int group = num_heads / num_kv_heads;
+    const bool few = (long long)max_group * group <= kFewRows;
+    // (group, row tile pair, kv head) units that a prefix is read for
+    const long long per_unit = few ? max_group : 2 * (128 / (group < 128 ? group : 128));
+    long long units = ((long long)num_seqs + per_unit - 1) / per_unit;
+    if (units < num_groups) units = num_groups;
+    units *= num_kv_heads;
+    const int tiles = (max_prefix + 127) / 128;
+    const int sms = sm_count() > 0 ? sm_count() : 152;   // (a size asked for where there is no GPU)
+    const long long slots = few ? 2ll * sms : sms;
+    // cost of a split into np partitions, in key tiles of one SM: its waves, each with a start of two
+    // tiles' time, and the partial results
+    int best = tiles > 0 ? tiles : 1;
+    double least = 1e300;
+    for (int np = 1; np <= tiles && np <= 64; np++) {
+        const int per = (tiles + np - 1) / np;
+        const long long waves = (units * ((tiles + per - 1) / per) + slots - 1) / slots;
+        const double cost = (double)waves * (per + 2.0) + 0.02 * np;
+        if (cost < least) {
+            least = cost;
+            best = per;
+        }
+    }
+    return best * 128;
+}
+
+struct SharedLayout {
+    size_t m_off, l_off, o_off, bytes;
+    int part, max_parts;
+};
+
+SharedLayout shared_layout(int S, int groups, int H, int Hkv, int D, int max_prefix, int max_group) {
+    SharedLayout w{};
+    w.part = prefix_partition(S, groups, H, Hkv, max_prefix, max_group);
+    w.max_parts = max_prefix > w.part ? (max_prefix + w.part - 1) / w.part : 1;    // (one where no prefix is: the
+                                                                                   // first launch is always made)
+    const size_t n = (size_t)S * H * w.max_parts;
+    w.l_off = align256(n * sizeof(float));
+    w.o_off = w.l_off + align256(n * sizeof(float));
+    w.bytes = w.o_off + align256(n * D * sizeof(float));
+    return w;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+pkv_status paged_attention_decode_window(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                         const int32_t *block_tables, const int32_t *context_lens, int num_seqs,
+                                         int max_blocks_per_seq, int max_context_len, int block_size, int num_blocks,
+                                         int num_heads, int num_kv_heads, int head_dim, float scale, int window,
+                                         int num_sinks, pkv_dtype dtype, struct CUstream_st *stream) {
+    using namespace pkv;
+    const char *what = "paged_attention_decode_window";
+    if (window < 1 || num_sinks < 0)
+        return fail(PKV_EINVAL, "%s: window %d (at least 1), %d sinks (at least 0)", what, window, num_sinks);
+    SpanArgs a = {};
+    SpanMaps maps;
+    const pkv_status rc = check_span({what, out, query, key_cache, value_cache, block_tables, context_lens, num_seqs,
+                                      max_blocks_per_seq, max_context_len, block_size, num_blocks, num_heads,
+                                      num_kv_heads, head_dim, scale, dtype}, a, maps);
+    if (rc != PKV_OK || num_seqs == 0) return rc;
+    a.window = window;
+    a.sinks = num_sinks;
+    const int NT = a.tile_heads > 8 ? 2 : 1;
+    const long long items = (long long)num_seqs * num_kv_heads * a.head_tiles;
+    const long long tokens = std::min<long long>(a.max_ctx, (long long)window + num_sinks);
+    const int cluster = choose_cluster(items, tokens, resident_ctas(NT));
+    const cudaError_t e = launch_span<kSpanWindow>(head_dim, NT, dtype == PKV_BF16, a, maps, items, 1, cluster, stream);
+    if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+    return PKV_OK;
+}
+
+size_t paged_attention_decode_shared_workspace_size(int num_seqs, int num_groups, int num_heads, int num_kv_heads,
+                                                    int head_dim, int max_prefix_len, int max_group_size) {
+    using namespace pkv;
+    if (num_seqs <= 0 || num_groups <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
+        head_dim <= 0 || max_prefix_len < 0 || max_group_size < 0)
+        return 0;
+    if (max_group_size == 0 || max_group_size > num_seqs) max_group_size = num_seqs;
+    return shared_layout(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_prefix_len, max_group_size).bytes;
+}
+
+pkv_status paged_attention_decode_shared(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                         const int32_t *block_tables, const int32_t *context_lens,
+                                         const int32_t *group_start, const int32_t *prefix_lens, int num_seqs,
+                                         int num_groups, int max_group_size, int max_prefix_len, int max_suffix_len,
+                                         int max_blocks_per_seq, int max_context_len, int block_size, int num_blocks,
+                                         int num_heads, int num_kv_heads, int head_dim, float scale, void *workspace,
+                                         size_t workspace_bytes, pkv_dtype dtype, struct CUstream_st *stream) {
+    using namespace pkv;
+    const char *what = "paged_attention_decode_shared";
+    if (num_groups < 0 || max_group_size < 0 || max_prefix_len < 0 || max_suffix_len < 0)
+        return fail(PKV_EINVAL, "%s: negative size (groups %d, largest group %d, prefix %d, suffix %d)", what, num_groups,
+                    max_group_size, max_prefix_len, max_suffix_len);
+    if (num_groups > num_seqs && num_seqs >= 0)
+        return fail(PKV_EINVAL, "%s: %d groups of %d sequences", what, num_groups, num_seqs);
+    if (!(scale > 0.f)) return fail(PKV_EINVAL, "%s: scale must be positive", what);
+    SpanArgs a = {};
+    SpanMaps maps;
+    const pkv_status rc = check_span({what, out, query, key_cache, value_cache, block_tables, context_lens, num_seqs,
+                                      max_blocks_per_seq, max_context_len, block_size, num_blocks, num_heads,
+                                      num_kv_heads, head_dim, scale, dtype}, a, maps);
+    if (rc != PKV_OK || num_seqs == 0) return rc;
+    if (num_groups == 0) return fail(PKV_EINVAL, "%s: no groups", what);
+    if (!group_start || !prefix_lens) return fail(PKV_EINVAL, "%s: NULL pointer", what);
+    if (a.group > 128) return fail(PKV_EINVAL, "%s: %d query heads per kv head (at most 128)", what, a.group);
+    if (max_prefix_len > a.max_ctx)
+        return fail(PKV_EINVAL, "%s: max_prefix_len %d beyond the contexts (%d tokens)", what, max_prefix_len, a.max_ctx);
+    const int max_prefix = max_prefix_len > 0 ? max_prefix_len : a.max_ctx;
+    const int max_group = max_group_size == 0 || max_group_size > num_seqs ? num_seqs : max_group_size;
+    a.prefix_lens = prefix_lens;
+    a.group_start = group_start;
+    a.num_groups = num_groups;
+    a.max_prefix = max_prefix;
+    a.max_group = max_group;
+    const bool bf16 = dtype == PKV_BF16;
+    a.parts.part = 128;
+    cudaError_t e = cudaSuccess;
+    const SharedLayout w = shared_layout(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_prefix, max_group);
+    if (!workspace || workspace_bytes < w.bytes || !aligned16(workspace))
+        return fail(PKV_EINVAL, "%s: workspace of %zu bytes needed, %zu given", what, w.bytes,
+                    workspace ? workspace_bytes : (size_t)0);
+    if (w.max_parts > 65535) return fail(PKV_EINVAL, "%s: %d partitions of a prefix", what, w.max_parts);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    a.parts = {reinterpret_cast<float *>(ws + w.m_off), reinterpret_cast<float *>(ws + w.l_off),
+               reinterpret_cast<float *>(ws + w.o_off), w.part, w.max_parts};
+    // the prefix half
+    const long long rows = (long long)max_group * a.group;
+    if (rows <= kFewRows) {
+        SpanArgs p = a;
+        p.head_tiles = 1;
+        e = launch_span<kSpanPrefix>(head_dim, rows > 8 ? 2 : 1, bf16, p, maps, (long long)num_groups * num_kv_heads,
+                                     w.max_parts, 1, stream);
+    } else {
+        e = launch_shared_prefix(query, key_cache, value_cache, block_tables, group_start, prefix_lens, num_groups, num_seqs,
+                                 max_group, max_prefix, max_blocks_per_seq, block_size, num_blocks, num_heads,
+                                 num_kv_heads, head_dim, a.scale_log2, a.parts, bf16, stream);
+    }
+    if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: prefix launch: %s", what, cudaGetErrorString(e));
+    // the sequences' own tokens, and the join
+    const int NT = a.tile_heads > 8 ? 2 : 1;
+    const long long items = (long long)num_seqs * num_kv_heads * a.head_tiles;
+    const long long tokens = max_suffix_len > 0 ? std::min(max_suffix_len, a.max_ctx) : a.max_ctx;
+    const int cluster = choose_cluster(items, tokens, resident_ctas(NT));
+    e = launch_span<kSpanSuffix>(head_dim, NT, bf16, a, maps, items, 1, cluster, stream);
+    if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));
+    return PKV_OK;
+}
+
+}  // extern "C"

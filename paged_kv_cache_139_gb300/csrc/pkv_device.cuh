@@ -30,6 +30,7 @@ enum : unsigned int {
     kFlagBadWorkspace = 32u,   // attention workspace not initialised
     kFlagSlotNotLast = 64u,    // fused decode write: slot is not position context_len - 1 of its table
     kFlagBadPosition = 128u,   // rotary position outside the table
+    kFlagBadGroup = 256u,      // shared decode: groups that do not cover the sequences, or prefixes that differ in one
 };
 
 __device__ __forceinline__ void latch(DeviceStatus *st, unsigned int flag, long long value) {

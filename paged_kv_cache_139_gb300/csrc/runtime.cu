@@ -121,6 +121,8 @@ pkv_status pkv_check(struct CUstream_st *stream) {
                        : (h.first_flag & pkv::kFlagBadPair)    ? "copy pair outside the pool"
                        : (h.first_flag & pkv::kFlagBadContext) ? "context length outside the table"
                        : (h.first_flag & pkv::kFlagBadPosition) ? "rotary position outside the table"
+                       : (h.first_flag & pkv::kFlagBadGroup)
+                           ? "group of sequences outside the batch, or prefix lengths that differ in a group"
                        : (h.first_flag & pkv::kFlagSlotNotLast)
                            ? "decode slot is not position context_len - 1 of its sequence's block table"
                        : (h.first_flag & pkv::kFlagTimeout)    ? "device wait timed out"
