@@ -535,7 +535,7 @@ pkv_status paged_attention_prefill_window(void *out_dev, const void *query_dev,
  * Probabilities over a prefix enter the product with 11 bits for fp16 where the
  * group has more than 16 query rows per kv head (sequences x heads), with 22
  * otherwise; with 16 for bf16.  A NaN among a group's first tokens reaches all of
- * its sequences.  Two launches.  num_seqs <= 65535; up to 128 query heads per kv
+ * its sequences.  Two launches, three for groups of more than 16 query rows.  num_seqs <= 65535; up to 128 query heads per kv
  * head; scale > 0; contexts up to 2^30 tokens.  Other arguments as for
  * paged_attention_decode.
  * ------------------------------------------------------------------------- */
@@ -552,9 +552,12 @@ pkv_status paged_attention_decode_shared(void *out_dev, const void *query_dev,
                                          void *workspace_dev, size_t workspace_bytes,
                                          pkv_dtype dtype, struct CUstream_st *stream);
 
+/* The bounds as given to the call; max_context_len not 0 (the table's capacity
+ * where the call is given 0).  Asked on the device of the call. */
 size_t paged_attention_decode_shared_workspace_size(int num_seqs, int num_groups, int num_heads,
                                                     int num_kv_heads, int head_dim,
-                                                    int max_prefix_len, int max_group_size);
+                                                    int max_context_len, int max_prefix_len,
+                                                    int max_group_size, int max_suffix_len);
 
 /* Bytes of workspace paged_attention_decode needs for these sizes: 256 for
  * the counters, plus the partition partials when a context can span more

@@ -24,6 +24,7 @@ import ctypes
 import functools
 import math
 import re
+import threading
 import weakref
 from typing import Optional, Sequence
 
@@ -666,14 +667,33 @@ def paged_attention_prefill_fp8(out: torch.Tensor, query: torch.Tensor, key_cach
 # -- sliding windows and shared prefixes ------------------------------------------------
 
 def _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S, index):
-    if query.shape[2] != key_cache.shape[3] or out.shape != query.shape or value_cache.shape != key_cache.shape:
+    qs, ks, dt, i32 = query.shape, key_cache.shape, query.dtype, torch.int32
+    if out.shape != qs or value_cache.shape != ks or len(ks) != 4 or qs[2] != ks[3]:
         raise ValueError(f"{what}: shape mismatch")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
         raise ValueError(f"{what}: block_tables must be [S][max_blocks], context_lens [S]")
-    dt, i32 = query.dtype, torch.int32
     return (_at(out, "out", dt, index), _at(query, "query", dt, index), _at(key_cache, "key_cache", dt, index),
             _at(value_cache, "value_cache", dt, index), _at(block_tables, "block_tables", i32, index),
             _at(context_lens, "context_lens", i32, index))
+
+
+_scratches = threading.local()
+
+
+def _scratch(index: int, nbytes: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Uninitialised scratch of one call.  Kept per thread and stream, where calls
+    follow one another (two threads may interleave their launches on one stream);
+    a captured call takes memory of its own, which its graph keeps."""
+    key = (index, _raw_stream(stream, index))
+    held = _scratches.__dict__
+    buf = held.get(key)
+    if buf is not None and buf.numel() >= nbytes and not _capturing(stream):
+        return buf
+    with _on(stream):
+        buf = torch.empty(max(nbytes, 1 << 16), dtype=torch.uint8, device=torch.device("cuda", index))
+    if not _capturing(stream):
+        held[key] = buf
+    return buf
 
 
 def paged_attention_decode_window(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -724,9 +744,11 @@ def paged_attention_prefill_window(out: torch.Tensor, query: torch.Tensor, key_c
 
 @functools.lru_cache(maxsize=4096)
 def paged_attention_decode_shared_workspace_size(num_seqs: int, num_groups: int, num_heads: int, num_kv_heads: int,
-                                                 head_dim: int, max_prefix_len: int, max_group_size: int = 0) -> int:
+                                                 head_dim: int, max_context_len: int, max_prefix_len: int = 0,
+                                                 max_group_size: int = 0, max_suffix_len: int = 0) -> int:
     return int(load().paged_attention_decode_shared_workspace_size(num_seqs, num_groups, num_heads, num_kv_heads,
-                                                                   head_dim, max_prefix_len, max_group_size))
+                                                                   head_dim, max_context_len, max_prefix_len,
+                                                                   max_group_size, max_suffix_len))
 
 
 def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -743,7 +765,8 @@ def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_ca
     table of the group's first sequence.  The max_* bounds (0: as large as the
     batch allows) size the workspace and the split of the work.  workspace: uint8
     scratch of paged_attention_decode_shared_workspace_size bytes, in no
-    particular state; None takes memory for the call on its stream.  Returns out."""
+    particular state, for one call at a time; None takes the binding's own, kept
+    for the calling thread and stream.  Returns out."""
     what = "paged_attention_decode_shared"
     index = _cuda_index(query, "query")
     S, H, d = query.shape
@@ -753,10 +776,9 @@ def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_ca
     NB, Hkv, B, _ = key_cache.shape
     G, mb = group_start.shape[0] - 1, block_tables.shape[1]
     if workspace is None:
-        need = paged_attention_decode_shared_workspace_size(
-            S, G, H, Hkv, d, max_prefix_len or max_context_len or mb * B, max_group_size)
-        with _on(stream):
-            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+        need = paged_attention_decode_shared_workspace_size(S, G, H, Hkv, d, max_context_len or mb * B, max_prefix_len,
+                                                            max_group_size, max_suffix_len)
+        workspace = _scratch(index, need, stream)
     _call(load().paged_attention_decode_shared, what, index, *ptrs, _at(group_start, "group_start", torch.int32, index),
           _at(prefix_lens, "prefix_lens", torch.int32, index), S, G, max_group_size, max_prefix_len, max_suffix_len, mb,
           max_context_len, B, NB, H, Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale,

@@ -47,7 +47,7 @@ SIGNATURES = {
                                             _p, _sz, _i, _p]),
     "paged_attention_decode_shared": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
                                            _f, _p, _sz, _i, _p]),
-    "paged_attention_decode_shared_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "paged_attention_decode_shared_workspace_size": (_sz, [_i] * 9),
     "copy_blocks": (_i, [_p, _p, _i, _i64, _i, _p]),
     "swap_blocks": (_i, [_p, _p, _p, _i, _i64, _i, _i, _p]),
     "pkv_validate_copy_pairs": (_i, [_p, _i, _i]),

@@ -14,14 +14,14 @@
 // is read once for all query rows that see it.
 //
 // How (sm_103a):
-//   * One CTA of four warps per (sequence, kv head), with 8 or 16 query heads as
+//   * One CTA of two or four warps per (sequence, kv head), with 8 or 16 query heads as
 //     the columns of S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16): the
 //     tokens are the 16-row operand, so one head or eight cost the same.  The
 //     fifth-generation tensor cores would want 64 rows of queries; four heads
 //     do not fill them, and at 48 products per 16 KB they are not what bounds.
-//   * Each warp streams stages of 16 tokens through a ring of its own, two or
-//     three deep: it issues its tiled TMA copies itself and refills a slot as
-//     soon as it has read it, so no warp waits for another before the end.
+//   * Each warp streams stages of 16 tokens through a ring of its own (16 KB): it
+//     issues its tiled TMA copies itself and refills a slot as soon as it has
+//     read it, so no warp waits for another before the end.
 //   * Probabilities enter the second product as a rounded part and its
 //     remainder (22 bits in fp16, 16 in bf16): rounded once they would add an
 //     error as large as the output's own rounding.
@@ -31,8 +31,11 @@
 //   * Few sequences are spread over the GPU by clusters of 2 to 16 CTAs per
 //     (sequence, kv head), which join through distributed shared memory: no
 //     workspace, no second launch, no counters.
-//   * The shared form's second launch overlaps the first: own tokens are
-//     attended to before it waits for the prefix's partial results.
+//   * The shared form: groups of up to 16 query rows per kv head take their
+//     prefix through this kernel too, and the launch for own tokens overlaps
+//     that one's end, joining the two halves itself.  Larger groups go to the
+//     tcgen05 kernel, which takes some of the SMs while own tokens, bound by
+//     memory, take the others; a third launch joins.
 #include <cuda.h>
 
 #include <algorithm>
@@ -47,12 +50,12 @@
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kSpanThreads = kWarps * 32;
 constexpr int kTok = 16;                       // tokens of a stage: the rows of one product
 constexpr int kMaxCluster = 16;
 
-enum SpanMode { kSpanWindow, kSpanSuffix, kSpanPrefix };
+// What a launch computes: a window; a prefix (to memory); own tokens, joined with the prefix's parts at
+// the end; or own tokens as one part more, which a third launch joins with the others.
+enum SpanMode { kSpanWindow, kSpanPrefix, kSpanSuffix, kSpanOwn };
 
 struct SpanArgs {
     void *out;                   // [S][H][D]
@@ -71,24 +74,25 @@ struct SpanArgs {
     PrefixParts parts;
 };
 
-// R ring slots per warp, CTAS resident CTAs per SM.
-template <int D, int NT> struct SpanConf {
+// W warps per CTA (2 or 4), R ring slots per warp, CTAS resident CTAs per SM.
+template <int D, int NT, int W> struct SpanConf {
+    static constexpr int THREADS = W * 32;
     static constexpr int HALVES = D / 64;
     static constexpr uint32_t HALF_BYTES = kTok * 128;                 // 16 tokens x 64 elements
     static constexpr uint32_t TENSOR_BYTES = HALVES * HALF_BYTES;
     static constexpr uint32_t STAGE_BYTES = 2 * TENSOR_BYTES;
     static constexpr int R = D == 128 ? 2 : 4;
-    static constexpr int CTAS = NT == 1 ? 3 : 2;
+    static constexpr int CTAS = (NT == 1 ? 12 : 8) / W;
     static constexpr int COLS = 8 * NT;
     static constexpr int LD = D + 4;                                   // fp32 row of an output: 8 columns apart on 8 banks
     static constexpr uint32_t ring = 0;
-    static constexpr uint32_t comb = kWarps * R * STAGE_BYTES;         // the CTA's o [COLS][LD], then m, l [COLS]
-    static constexpr uint32_t ml = comb + COLS * LD * 4;
-    static constexpr uint32_t wml = ml + 2 * COLS * 4;                 // the warps' m, l [kWarps][2][COLS]
-    static constexpr uint32_t bars = wml + kWarps * 2 * COLS * 4;
-    static constexpr uint32_t bytes = bars + kWarps * R * 8;
+    static constexpr uint32_t wml = W * R * STAGE_BYTES;               // the warps' m, l [W][2][COLS]
+    static constexpr uint32_t bars = wml + W * 2 * COLS * 4;
+    static constexpr uint32_t ml = bars + W * R * 8;                   // the CTA's m, l [COLS] and o [COLS][LD], for its
+    static constexpr uint32_t comb = ml + 2 * COLS * 4;                // cluster (CTAs of four warps)
+    static constexpr uint32_t bytes = W == 4 ? comb + COLS * LD * 4 : ml;
     static_assert(COLS * LD * 4 <= R * STAGE_BYTES, "a warp's outputs fit its ring");
-    static_assert(ml % 16 == 0 && bars % 8 == 0, "alignment");
+    static_assert(comb % 16 == 0 && bars % 8 == 0, "alignment");
 };
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
@@ -164,17 +168,18 @@ struct Joined {
     }
 };
 
-template <int D, int NT, typename T, int MODE>
-__global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
+template <int D, int NT, int W, typename T, int MODE>
+__global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W>::CTAS)
     span_attention_kernel(const SpanArgs a, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv) {
-    using C = SpanConf<D, NT>;
+    using C = SpanConf<D, NT, W>;
+    constexpr bool kClusters = W == 4 && (MODE == kSpanWindow || MODE == kSpanSuffix);
     constexpr int R = C::R, HALVES = C::HALVES, COLS = C::COLS, LD = C::LD;
     // the 128-byte swizzle repeats every 1024 bytes: the ring starts on such a boundary
     extern __shared__ __align__(1024) unsigned char smem_span[];
     unsigned char *sm = smem_span;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t nrank = MODE == kSpanPrefix ? 1u : cluster_size(), rank = MODE == kSpanPrefix ? 0u : cluster_rank();
+    const uint32_t nrank = kClusters ? cluster_size() : 1u, rank = kClusters ? cluster_rank() : 0u;
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::bars) + warp * R;      // this warp's own
     unsigned char *ring = sm + C::ring + warp * R * C::STAGE_BYTES;
     if (lane == 0) {
@@ -190,7 +195,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
     // had finished (it waits for them before it lets this one start), so queries, lengths, tables and
     // caches are in place; only its partial results are not, and the wait for those comes below.
     // (Loads here go past L1.)
-    if constexpr (MODE != kSpanSuffix) pdl_wait();
+    if constexpr (MODE == kSpanWindow || MODE == kSpanPrefix) pdl_wait();
     pdl_trigger();
     bool dead = __any_sync(kFull, timed_out(a.st));     // an earlier wait gave up: no copies, nothing waited for
     if (smem_u32(sm) & 1023u) {
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
         if (e == b) return;
         prefix = __ldcg(a.prefix_lens + b);
         if (g == 0 && blockIdx.y == 0)
-            for (int i = b + tid; i < e; i += kSpanThreads)
+            for (int i = b + tid; i < e; i += C::THREADS)
                 if (__ldcg(a.prefix_lens + i) != prefix) latch(a.st, kFlagBadGroup, unit);
         if (prefix < 0 || prefix > a.max_prefix) return;           // the suffix half reports it
         low = blockIdx.y * a.parts.part;
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
     } else {
         ctx = __ldcg(a.ctx_lens + s);
         if (ctx < 0 || ctx > a.max_ctx) {
-            if (tid == 0 && g == 0 && tile == 0 && rank == 0) latch(a.st, kFlagBadContext, ctx);
+            if (tid == 0 && g == 0 && tile == 0 && rank == 0 && blockIdx.y == 0) latch(a.st, kFlagBadContext, ctx);
             ctx = ctx < 0 ? 0 : a.max_ctx;
         }
         if constexpr (MODE == kSpanWindow) {
@@ -237,10 +242,14 @@ __global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
         } else {
             prefix = __ldcg(a.prefix_lens + s);
             if (prefix < 0 || prefix > ctx || prefix > a.max_prefix) {
-                if (tid == 0 && g == 0 && tile == 0 && rank == 0) latch(a.st, kFlagBadContext, prefix);
+                if (tid == 0 && g == 0 && tile == 0 && rank == 0 && blockIdx.y == 0) latch(a.st, kFlagBadContext, prefix);
                 prefix = prefix < 0 ? 0 : min(ctx, a.max_prefix);
             }
             low = prefix;
+            if constexpr (MODE == kSpanOwn) {           // this CTA's partition of them (the first one reports for all)
+                low = (int)min((long long)ctx, prefix + (long long)blockIdx.y * a.parts.own);
+                if (blockIdx.y + 1 < gridDim.y) ctx = low + min(ctx - low, a.parts.own);      // the last takes the rest
+            }
         }
     }
     // row of column c (a group's columns run over its sequences, each with its heads of kv head g)
@@ -254,9 +263,9 @@ __global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
     if (nsink > from) nsink = from;
     const int nst = low < ctx ? nsink + (ctx + kTok - 1) / kTok - from : 0;
     const int st0 = (int)((long long)nst * rank / nrank), st1 = (int)((long long)nst * (rank + 1) / nrank);
-    const int mine = dead ? 0 : max(0, (st1 - st0 - warp + kWarps - 1) / kWarps);
+    const int mine = dead ? 0 : max(0, (st1 - st0 - warp + W - 1) / W);
     auto token0 = [&](int i) {                          // first token of this warp's stage i
-        const int v = st0 + warp + kWarps * i;
+        const int v = st0 + warp + W * i;
         return (v < nsink ? v : v - nsink + from) * kTok;
     };
 
@@ -475,7 +484,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
     auto join_warps = [&](int c, int e) {
         Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
-        for (int w = 0; w < kWarps; w++)
+        for (int w = 0; w < W; w++)
             r.add(all_ml[w * 2 * COLS + c], all_ml[w * 2 * COLS + COLS + c],
                   *reinterpret_cast<const float4 *>(sm + C::ring + w * R * C::STAGE_BYTES + (c * LD + e) * 4));
         return r;
@@ -488,22 +497,28 @@ __global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
         w.y = Mma<T>::pack(r.o.z * inv, r.o.w * inv);
         *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row_of(c) * D + e) = w;
     };
-    if constexpr (MODE == kSpanPrefix) {
-        for (int u = tid; u < cols * UPR; u += kSpanThreads) {
-            const int c = u / UPR, e = u % UPR * 4;
-            const Joined r = join_warps(c, e);
-            const size_t at = row_of(c) * a.parts.max_parts + blockIdx.y;
-            *reinterpret_cast<float4 *>(a.parts.o + at * D + e) = r.o;
-            if (e == 0) {
-                a.parts.m[at] = r.m;
-                a.parts.l[at] = r.l;
-            }
+    auto store_part = [&](int c, int e, const Joined &r) {
+        const size_t at = row_of(c) * a.parts.slots + (MODE == kSpanPrefix ? 0 : a.parts.max_parts) + blockIdx.y;
+        *reinterpret_cast<float4 *>(a.parts.o + at * D + e) = r.o;
+        if (e == 0) {
+            a.parts.m[at] = r.m;
+            a.parts.l[at] = r.l;
         }
+    };
+    if constexpr (MODE == kSpanPrefix || MODE == kSpanOwn) {
+        if (nst > 0)
+            for (int u = tid; u < cols * UPR; u += C::THREADS) {
+                const int c = u / UPR, e = u % UPR * 4;
+                store_part(c, e, join_warps(c, e));
+            }
+        // what follows the own tokens' grid waits for it alone: it may not end before the prefix half
+        if constexpr (MODE == kSpanOwn)
+            if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) pdl_wait();
     } else {
         if constexpr (MODE == kSpanSuffix) pdl_wait();              // the prefix half's results
         const int np = MODE == kSpanSuffix ? (prefix + a.parts.part - 1) / a.parts.part : 0;
         auto join_prefix = [&](int c, int e, Joined &r) {
-            const size_t at = row_of(c) * a.parts.max_parts;
+            const size_t at = row_of(c) * a.parts.slots;
             for (int p0 = 0; p0 < np; p0 += 4) {                    // four parts to a round trip
                 float pm[4], pl2[4];
                 float4 po[4];
@@ -519,18 +534,18 @@ __global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
                 for (int p = 0; p < 4; p++) r.add(pm[p], pl2[p], po[p]);
             }
         };
-        if (nrank == 1) {
-            for (int u = tid; u < cols * UPR; u += kSpanThreads) {
+        if (!kClusters || nrank == 1) {
+            for (int u = tid; u < cols * UPR; u += C::THREADS) {
                 const int c = u / UPR, e = u % UPR * 4;
                 Joined r = join_warps(c, e);
                 if constexpr (MODE == kSpanSuffix) join_prefix(c, e, r);
                 store_out(c, e, r);
             }
-        } else {
+        } else if constexpr (kClusters) {
             // the CTA's part into its own shared memory, then every CTA joins its share of the
             // elements over all CTAs of the cluster
             float *comb = reinterpret_cast<float *>(sm + C::comb), *cml = reinterpret_cast<float *>(sm + C::ml);
-            for (int u = tid; u < cols * UPR; u += kSpanThreads) {
+            for (int u = tid; u < cols * UPR; u += C::THREADS) {
                 const int c = u / UPR, e = u % UPR * 4;
                 const Joined r = join_warps(c, e);
                 *reinterpret_cast<float4 *>(comb + c * LD + e) = r.o;
@@ -543,7 +558,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
             cluster_arrive();
             cluster_wait();
             const uint32_t comb_s = smem_u32(comb), cml_s = smem_u32(cml);
-            for (int u = tid * nrank + rank; u < cols * UPR; u += kSpanThreads * nrank) {
+            for (int u = tid * nrank + rank; u < cols * UPR; u += C::THREADS * nrank) {
                 const int c = u / UPR, e = u % UPR * 4;
                 Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
                 for (uint32_t k0 = 0; k0 < nrank; k0 += 4) {
@@ -571,6 +586,66 @@ __global__ void __launch_bounds__(kSpanThreads, SpanConf<D, NT>::CTAS)
     }
 }
 
+// Joins a row's parts, those of its prefix and of its own tokens: a warp per row,
+// four parts to a round trip.
+constexpr int kJoinWarps = 8;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    span_join_kernel(T *out, const int32_t *ctx_lens, const int32_t *prefix_lens, int rows, int num_heads, int max_ctx,
+                     int max_prefix, PrefixParts parts) {
+    constexpr int E = D / 32;
+    pdl_wait();
+    pdl_trigger();
+    const int row = blockIdx.x * kJoinWarps + threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const int s = row / num_heads;
+    const int ctx = min(max(__ldcg(ctx_lens + s), 0), max_ctx), prefix = min(max(__ldcg(prefix_lens + s), 0), min(ctx, max_prefix));
+    const int np = (prefix + parts.part - 1) / parts.part;
+    const int n = np + min((ctx - prefix + parts.own - 1) / parts.own, parts.slots - parts.max_parts);
+    const int skip = parts.max_parts - np;                                       // own parts come last
+    const size_t at = (size_t)row * parts.slots;
+    float M = -INFINITY, L = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; e++) o[e] = 0.f;
+    for (int p0 = 0; p0 < n; p0 += 4) {
+        float pm[4], pl[4], po[4][E];
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+            const bool there = p0 + p < n;
+            const size_t k = at + p0 + p + (p0 + p < np ? 0 : skip);
+            pm[p] = there ? __ldcg(parts.m + k) : -INFINITY;
+            pl[p] = there ? __ldcg(parts.l + k) : 0.f;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 v = there ? __ldcg(reinterpret_cast<const float2 *>(parts.o + k * D + lane * E + e))
+                                       : make_float2(0.f, 0.f);
+                po[p][e] = v.x;
+                po[p][e + 1] = v.y;
+            }
+        }
+        float Mn = M;
+#pragma unroll
+        for (int p = 0; p < 4; p++) Mn = fmaxf(Mn, pm[p]);
+        const float z = Mn == -INFINITY ? 0.f : Mn, a = ex2(M - z);
+        M = Mn;
+        L *= a;
+#pragma unroll
+        for (int e = 0; e < E; e++) o[e] *= a;
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+            const float w = ex2(pm[p] - z);
+            L = fmaf(pl[p], w, L);
+#pragma unroll
+            for (int e = 0; e < E; e++) o[e] = fmaf(po[p][e], w, o[e]);
+        }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(out + (size_t)row * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = Mma<T>::pack(o[e] * inv, o[e + 1] * inv);
+}
+
 // The cache [NB][Hkv][B][D] as a 4-D tensor (innermost first); a box is 64
 // elements of d by min(B, 16) tokens of one (block, kv head).
 bool encode_span_map(CUtensorMap *map, const void *base, int num_blocks, int Hkv, int B, int D, bool bf16) {
@@ -584,13 +659,13 @@ struct SpanMaps {
     CUtensorMap k, v;
 };
 
-template <int D, int NT, typename T, int MODE>
+template <int D, int NT, int W, typename T, int MODE>
 cudaError_t launch_span_kernel(const SpanArgs &a, const SpanMaps &maps, long long items, int parts, int cluster,
                                cudaStream_t st) {
-    auto kern = span_attention_kernel<D, NT, T, MODE>;
-    constexpr size_t smem = SpanConf<D, NT>::bytes;
+    auto kern = span_attention_kernel<D, NT, W, T, MODE>;
+    using C = SpanConf<D, NT, W>;
     static std::atomic<unsigned long long> sized{0}, wide{0};
-    cudaError_t e = allow_smem(kern, smem, sized);
+    cudaError_t e = allow_smem(kern, C::bytes, sized);
     if (e != cudaSuccess) return e;
     if (cluster > 8) {                                   // more than the portable size, once per device
         int d = 0;
@@ -602,37 +677,57 @@ cudaError_t launch_span_kernel(const SpanArgs &a, const SpanMaps &maps, long lon
             wide.fetch_or(bit, std::memory_order_release);
         }
     }
-    return launch_clusters(kern, dim3((unsigned)(items * cluster), (unsigned)parts), dim3(kSpanThreads), (unsigned)cluster,
-                           smem, st, a, maps.k, maps.v);
+    return launch_clusters(kern, dim3((unsigned)(items * cluster), (unsigned)parts), dim3(C::THREADS), (unsigned)cluster,
+                           C::bytes, st, a, maps.k, maps.v);
+}
+
+// How a launch is spread: warps per CTA, CTAs per cluster.
+struct Spread {
+    int warps, cluster;
+};
+
+// (prefixes go by CTAs of four warps, own tokens in partitions by CTAs of two; the others by either)
+template <int D, int NT, typename T, int MODE>
+cudaError_t launch_span_warps(const SpanArgs &a, const SpanMaps &maps, long long items, int parts, Spread w, cudaStream_t st) {
+    if constexpr (MODE != kSpanPrefix)
+        if (MODE == kSpanOwn || w.warps == 2) return launch_span_kernel<D, NT, 2, T, MODE>(a, maps, items, parts, 1, st);
+    if constexpr (MODE != kSpanOwn) return launch_span_kernel<D, NT, 4, T, MODE>(a, maps, items, parts, w.cluster, st);
 }
 
 template <int MODE>
 cudaError_t launch_span(int D, int NT, bool bf16, const SpanArgs &a, const SpanMaps &maps, long long items, int parts,
-                        int cluster, cudaStream_t st) {
-    if (D == 128) {
-        if (NT == 1)
-            return bf16 ? launch_span_kernel<128, 1, __nv_bfloat16, MODE>(a, maps, items, parts, cluster, st)
-                        : launch_span_kernel<128, 1, __half, MODE>(a, maps, items, parts, cluster, st);
-        return bf16 ? launch_span_kernel<128, 2, __nv_bfloat16, MODE>(a, maps, items, parts, cluster, st)
-                    : launch_span_kernel<128, 2, __half, MODE>(a, maps, items, parts, cluster, st);
-    }
+                        Spread w, cudaStream_t st) {
+    using B = __nv_bfloat16;
+    using F = __half;
+    if (D == 128 && NT == 1)
+        return bf16 ? launch_span_warps<128, 1, B, MODE>(a, maps, items, parts, w, st)
+                    : launch_span_warps<128, 1, F, MODE>(a, maps, items, parts, w, st);
+    if (D == 128)
+        return bf16 ? launch_span_warps<128, 2, B, MODE>(a, maps, items, parts, w, st)
+                    : launch_span_warps<128, 2, F, MODE>(a, maps, items, parts, w, st);
     if (NT == 1)
-        return bf16 ? launch_span_kernel<64, 1, __nv_bfloat16, MODE>(a, maps, items, parts, cluster, st)
-                    : launch_span_kernel<64, 1, __half, MODE>(a, maps, items, parts, cluster, st);
-    return bf16 ? launch_span_kernel<64, 2, __nv_bfloat16, MODE>(a, maps, items, parts, cluster, st)
-                : launch_span_kernel<64, 2, __half, MODE>(a, maps, items, parts, cluster, st);
+        return bf16 ? launch_span_warps<64, 1, B, MODE>(a, maps, items, parts, w, st)
+                    : launch_span_warps<64, 1, F, MODE>(a, maps, items, parts, w, st);
+    return bf16 ? launch_span_warps<64, 2, B, MODE>(a, maps, items, parts, w, st)
+                : launch_span_warps<64, 2, F, MODE>(a, maps, items, parts, w, st);
 }
 
-int resident_ctas(int NT) { return sm_count() * (NT == 1 ? SpanConf<128, 1>::CTAS : SpanConf<128, 2>::CTAS); }
-
-// CTAs per (sequence, kv head): as a rule one, since a cluster's CTAs start and
-// end together; more while the whole batch would leave resident CTAs idle, but at
-// least a stage for every warp.
-int choose_cluster(long long items, long long max_tokens, int resident) {
+// Work items (sequence, kv head) of up to max_tokens tokens over the GPU.  CTAs are
+// of two warps where those of four would come in a second, nearly empty wave or
+// the items are short and many (each item's start and end then weighs more than
+// its stream): 512 items of 512 tokens 25.1 against 30.6 us, of 2,048 tokens 83 against
+// 97, 8,192 of 64 tokens 59 against 74; but 2,048 of 1,024 tokens 163 against 157.
+// Clusters split items while they leave SMs without one, or with one and long
+// streams: 8 items of 4,096 tokens 27, 15.8, 10.8, 9.7 us for 2, 4, 8, 16 CTAs each;
+// 128 of 512 tokens 10.1 us unsplit, 10.9 in two.  (head_dim 128, bf16.)
+Spread choose_spread(long long items, long long max_tokens, int NT) {
+    const long long sms = sm_count(), four = sms * (NT == 1 ? 3 : 2);      // CTAs of four warps that fit at once
     const long long stages = (max_tokens + kTok - 1) / kTok;
+    if (items > four) return {items <= 2 * four || stages <= 32 ? 2 : 4, 1};
     int c = 1;
-    while (c < kMaxCluster && items * c * 2 <= resident && stages >= (long long)kWarps * c * 2) c *= 2;
-    return c;
+    while (c < kMaxCluster && items * c * 2 <= 2 * sms && stages >= (items * c * 2 <= sms ? 16 : 32) * c * 2) c *= 2;
+    if (c == 1 && stages >= 128) c = 2;                  // few and long: the SMs' shares differ by less
+    return {4, c};
 }
 
 struct SpanCall {
@@ -700,50 +795,75 @@ pkv_status check_span(const SpanCall &c, SpanArgs &a, SpanMaps &maps) {
 // columns of the kernel above; larger ones go to the tcgen05 kernel.
 constexpr int kFewRows = 16;
 
-// Tokens of a prefix's partition: a multiple of 128 that spreads the prefixes
-// over the GPU.
-int prefix_partition(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int max_prefix, int max_group) {
-    const int group = num_heads / num_kv_heads;
-    const bool few = (long long)max_group * group <= kFewRows;
-    // (group, row tile pair, kv head) units that a prefix is read for
-    const long long per_unit = few ? max_group : 2 * (128 / (group < 128 ? group : 128));
-    long long units = ((long long)num_seqs + per_unit - 1) / per_unit;
-    if (units < num_groups) units = num_groups;
-    units *= num_kv_heads;
-    const int tiles = (max_prefix + 127) / 128;
-    const int sms = sm_count() > 0 ? sm_count() : 152;   // (a size asked for where there is no GPU)
-    const long long slots = few ? 2ll * sms : sms;
-    // cost of a split into np partitions, in key tiles of one SM: its waves, each with a start of two
-    // tiles' time, and the partial results
-    int best = tiles > 0 ? tiles : 1;
-    double least = 1e300;
-    for (int np = 1; np <= tiles && np <= 64; np++) {
-        const int per = (tiles + np - 1) / np;
-        const long long waves = (units * ((tiles + per - 1) / per) + slots - 1) / slots;
-        const double cost = (double)waves * (per + 2.0) + 0.02 * np;
-        if (cost < least) {
-            least = cost;
-            best = per;
-        }
-    }
-    return best * 128;
-}
-
-struct SharedLayout {
+// How a call is split.
+struct SharedPlan {
+    bool few;                    // every group fits the columns of the kernel above
+    int part, max_parts;         // tokens of a prefix's partition (a multiple of 128), partitions
+    int own, own_parts;          // of a sequence's own tokens, where the join is a launch of its own
+    int prefix_ctas;             // SMs for the prefixes, where own tokens run beside them
     size_t m_off, l_off, o_off, bytes;
-    int part, max_parts;
 };
 
-SharedLayout shared_layout(int S, int groups, int H, int Hkv, int D, int max_prefix, int max_group) {
-    SharedLayout w{};
-    w.part = prefix_partition(S, groups, H, Hkv, max_prefix, max_group);
-    w.max_parts = max_prefix > w.part ? (max_prefix + w.part - 1) / w.part : 1;    // (one where no prefix is: the
-                                                                                   // first launch is always made)
-    const size_t n = (size_t)S * H * w.max_parts;
+SharedPlan plan_shared(int S, int groups, int H, int Hkv, int D, int max_prefix, int max_group, int max_suffix) {
+    SharedPlan w{};
+    const int group = H / Hkv, tiles = (max_prefix + 127) / 128;
+    const int sms = sm_count() > 0 ? sm_count() : 152;   // (a size asked for where there is no GPU)
+    w.few = (long long)max_group * group <= kFewRows;
+    int per = tiles > 0 ? tiles : 1;                     // key tiles of a partition
+    if (w.few) {
+        // enough partitions to fill the GPU
+        const long long units = (long long)groups * Hkv;
+        const long long parts = std::min<long long>(per, (2ll * sms + units - 1) / units);
+        per = (int)((per + parts - 1) / parts);
+    } else {
+        // The prefixes are bound by the tensor cores and run on n SMs; own tokens are bound by memory
+        // and run on the others, then on all.  Times in us, measured on the kernels: a key tile of 256
+        // rows 2.0, of 128 or fewer 1.4 (between fp16's and bf16's), an item's start and end 6; an SM
+        // reads up to 85 KB/us, all of them 6.6 MB/us; parts pass through L2 at 8 MB/us.
+        const int seqs = 2 * (128 / group);
+        const double t = (long long)S * group > 128ll * groups ? 2.0 : 1.4;
+        const long long units = std::max<long long>(groups, (S + seqs - 1) / seqs) * Hkv;
+        const double token = 4.0 * Hkv * D, prefix_bytes = token * groups * max_prefix, own_bytes = token * S * max_suffix / 2;
+        double least = 1e300;
+        int last = 0;
+        for (int p = 1; p <= tiles && p <= 64; p++) {
+            const int tp = (tiles + p - 1) / p;
+            if (tp == last) continue;
+            last = tp;
+            const int parts = (tiles + tp - 1) / tp;
+            const long long items = units * parts;
+            for (long long k = (items + sms - 1) / sms, end = k + 3; k <= end; k++) {
+                const int n = (int)((items + k - 1) / k);
+                const double t_prefix = (double)((items + n - 1) / n) * (tp * t + 6.0);
+                const double beside = std::max(0.0, std::min(6.6e6 - prefix_bytes / t_prefix, (sms - n) * 85e3));
+                const double cost = t_prefix + std::max(0.0, own_bytes - beside * t_prefix) / 6.6e6 +
+                                    (double)parts * S * H * D * 8.0 / 8e6;
+                if (cost < least) {
+                    least = cost;
+                    per = tp;
+                    w.prefix_ctas = n;
+                }
+            }
+        }
+        if (w.prefix_ctas < 1) w.prefix_ctas = 1;
+        // own tokens in partitions of about 512, at most 16 (128 requests of up to 1,024 own tokens after
+        // 8,190 shared ones: 61 us; partitions of 256 64, of 128 70)
+        w.own_parts = std::min(16, std::max(1, (max_suffix + 511) / 512));
+        w.own = std::max(kTok, ((max_suffix + w.own_parts - 1) / w.own_parts + kTok - 1) / kTok * kTok);
+    }
+    w.part = per * 128;
+    w.max_parts = tiles > per ? (tiles + per - 1) / per : 1;      // (one where no prefix is: its launch is always made)
+    const size_t n = (size_t)S * H * (w.max_parts + w.own_parts);
     w.l_off = align256(n * sizeof(float));
     w.o_off = w.l_off + align256(n * sizeof(float));
     w.bytes = w.o_off + align256(n * D * sizeof(float));
     return w;
+}
+
+template <int D, typename T> cudaError_t launch_join(const SpanArgs &a, cudaStream_t st) {
+    const int rows = a.num_seqs * a.num_heads;
+    return launch(span_join_kernel<D, T>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, st,
+                  static_cast<T *>(a.out), a.ctx_lens, a.prefix_lens, rows, a.num_heads, a.max_ctx, a.max_prefix, a.parts);
 }
 
 }  // namespace
@@ -771,20 +891,25 @@ pkv_status paged_attention_decode_window(void *out, const void *query, const voi
     const int NT = a.tile_heads > 8 ? 2 : 1;
     const long long items = (long long)num_seqs * num_kv_heads * a.head_tiles;
     const long long tokens = std::min<long long>(a.max_ctx, (long long)window + num_sinks);
-    const int cluster = choose_cluster(items, tokens, resident_ctas(NT));
-    const cudaError_t e = launch_span<kSpanWindow>(head_dim, NT, dtype == PKV_BF16, a, maps, items, 1, cluster, stream);
+    const cudaError_t e = launch_span<kSpanWindow>(head_dim, NT, dtype == PKV_BF16, a, maps, items, 1,
+                                                   choose_spread(items, tokens, NT), stream);
     if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));
     return PKV_OK;
 }
 
 size_t paged_attention_decode_shared_workspace_size(int num_seqs, int num_groups, int num_heads, int num_kv_heads,
-                                                    int head_dim, int max_prefix_len, int max_group_size) {
+                                                    int head_dim, int max_context_len, int max_prefix_len,
+                                                    int max_group_size, int max_suffix_len) {
     using namespace pkv;
     if (num_seqs <= 0 || num_groups <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
-        head_dim <= 0 || max_prefix_len < 0 || max_group_size < 0)
+        num_heads / num_kv_heads > 128 || head_dim <= 0 || max_context_len < 0 || max_prefix_len < 0 || max_group_size < 0 ||
+        max_suffix_len < 0)
         return 0;
     if (max_group_size == 0 || max_group_size > num_seqs) max_group_size = num_seqs;
-    return shared_layout(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_prefix_len, max_group_size).bytes;
+    if (max_prefix_len == 0 || max_prefix_len > max_context_len) max_prefix_len = max_context_len;
+    if (max_suffix_len == 0 || max_suffix_len > max_context_len) max_suffix_len = max_context_len;
+    return plan_shared(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_prefix_len, max_group_size,
+                       max_suffix_len).bytes;
 }
 
 pkv_status paged_attention_decode_shared(void *out, const void *query, const void *key_cache, const void *value_cache,
@@ -821,35 +946,40 @@ pkv_status paged_attention_decode_shared(void *out, const void *query, const voi
     a.max_prefix = max_prefix;
     a.max_group = max_group;
     const bool bf16 = dtype == PKV_BF16;
-    a.parts.part = 128;
+    const int max_suffix = max_suffix_len > 0 && max_suffix_len < a.max_ctx ? max_suffix_len : a.max_ctx;
     cudaError_t e = cudaSuccess;
-    const SharedLayout w = shared_layout(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_prefix, max_group);
+    const SharedPlan w = plan_shared(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_prefix, max_group,
+                                     max_suffix);
     if (!workspace || workspace_bytes < w.bytes || !aligned16(workspace))
         return fail(PKV_EINVAL, "%s: workspace of %zu bytes needed, %zu given", what, w.bytes,
                     workspace ? workspace_bytes : (size_t)0);
     if (w.max_parts > 65535) return fail(PKV_EINVAL, "%s: %d partitions of a prefix", what, w.max_parts);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     a.parts = {reinterpret_cast<float *>(ws + w.m_off), reinterpret_cast<float *>(ws + w.l_off),
-               reinterpret_cast<float *>(ws + w.o_off), w.part, w.max_parts};
-    // the prefix half
-    const long long rows = (long long)max_group * a.group;
-    if (rows <= kFewRows) {
+               reinterpret_cast<float *>(ws + w.o_off), w.part, w.max_parts, w.own, w.max_parts + w.own_parts};
+    const int NT = a.tile_heads > 8 ? 2 : 1;
+    const long long items = (long long)num_seqs * num_kv_heads * a.head_tiles;
+    if (w.few) {
+        // the prefixes, then the sequences' own tokens and the join
+        const long long rows = (long long)max_group * a.group;
         SpanArgs p = a;
         p.head_tiles = 1;
         e = launch_span<kSpanPrefix>(head_dim, rows > 8 ? 2 : 1, bf16, p, maps, (long long)num_groups * num_kv_heads,
-                                     w.max_parts, 1, stream);
+                                     w.max_parts, {4, 1}, stream);
+        if (e == cudaSuccess) e = launch_span<kSpanSuffix>(head_dim, NT, bf16, a, maps, items, 1,
+                                                          choose_spread(items, max_suffix, NT), stream);
     } else {
+        // the prefixes on some of the SMs, own tokens beside them on the others, then the join
         e = launch_shared_prefix(query, key_cache, value_cache, block_tables, group_start, prefix_lens, num_groups, num_seqs,
                                  max_group, max_prefix, max_blocks_per_seq, block_size, num_blocks, num_heads,
-                                 num_kv_heads, head_dim, a.scale_log2, a.parts, bf16, stream);
+                                 num_kv_heads, head_dim, a.scale_log2, a.parts, bf16, w.prefix_ctas, stream);
+        if (e == cudaSuccess)
+            e = launch_span<kSpanOwn>(head_dim, NT, bf16, a, maps, items, w.own_parts, {2, 1}, stream);
+        if (e == cudaSuccess)
+            e = head_dim == 128 ? bf16 ? launch_join<128, __nv_bfloat16>(a, stream) : launch_join<128, __half>(a, stream)
+                : bf16          ? launch_join<64, __nv_bfloat16>(a, stream)
+                                : launch_join<64, __half>(a, stream);
     }
-    if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: prefix launch: %s", what, cudaGetErrorString(e));
-    // the sequences' own tokens, and the join
-    const int NT = a.tile_heads > 8 ? 2 : 1;
-    const long long items = (long long)num_seqs * num_kv_heads * a.head_tiles;
-    const long long tokens = max_suffix_len > 0 ? std::min(max_suffix_len, a.max_ctx) : a.max_ctx;
-    const int cluster = choose_cluster(items, tokens, resident_ctas(NT));
-    e = launch_span<kSpanSuffix>(head_dim, NT, bf16, a, maps, items, 1, cluster, stream);
     if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));
     return PKV_OK;
 }

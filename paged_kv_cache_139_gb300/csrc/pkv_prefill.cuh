@@ -111,6 +111,7 @@ struct PrefillArgs {
     int num_groups, max_group, max_prefix, num_kv_heads;
     int tile_seqs;                       // sequences per row tile
     int part_tiles, num_parts;           // key tiles per partition of a prefix, partitions
+    int max_ctas;                        // SMs to take at most
     PrefixParts parts;
 };
 
@@ -367,6 +368,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             t = __shfl_sync(0xffffffffu, t, 0);
             return t > (unsigned)a.num_items ? a.num_items : (int)t;
         };
+        // kWindow: no ticket without work.  Tickets run over levels of row tiles from the top; a level
+        // has the sequences with new tokens there, each with its heads.  (A window's items all cost
+        // about the same, so that an equal number each, without a counter, is nearly balanced.)
+        int level = a.num_pairs, level_t = 0, level_seqs = 0;      // tickets before the level, its sequences
+        const int level_rows = a.head_pairs ? kRows : kTiles * kRows, level_heads = a.head_pairs ? a.num_heads / 2 : a.num_heads;
+        auto rows_above = [&](int s, bool report) -> unsigned {    // lanes whose sequence s + lane is in the level
+            bool in = false;
+            if (s + lane < a.num_seqs) {
+                const int qb = a.query_start[s + lane], qe = a.query_start[s + lane + 1], ctx = a.context_lens[s + lane];
+                const int n = qe - qb;
+                if (n < 0 || qb < 0 || qe > a.num_tokens || n > ctx || ctx > a.max_blocks * B) {
+                    if (report) latch(st, kFlagBadContext, s + lane);
+                } else {
+                    in = n > level * level_rows;
+                }
+            }
+            return __ballot_sync(0xffffffffu, in);
+        };
         // the first item with work at or after ticket t (following the claims); stop when none
         auto resolve = [&](int t, Item &o) -> int {
             if constexpr (MODE == kShared) {
@@ -409,7 +428,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
             while (t < a.num_items) {
                 int s, h, pair;
-                ticket_item(a, t, s, h, pair);
+                if constexpr (MODE == kWindow) {
+                    while (t >= level_t + level_seqs * level_heads) {
+                        level_t += level_seqs * level_heads;
+                        level_seqs = 0;
+                        if (--level < 0) break;
+                        for (int i = 0; i < a.num_seqs; i += 32)
+                            level_seqs += __popc(rows_above(i, blockIdx.x == 0 && level == a.num_pairs - 1));
+                    }
+                    if (level < 0) break;
+                    int k = (t - level_t) / level_heads;           // the level's k-th sequence
+                    h = (t - level_t) % level_heads * (a.head_pairs ? 2 : 1);
+                    pair = level;
+                    s = 0;
+                    for (;; s += 32) {
+                        unsigned m = rows_above(s, false);
+                        const int c = __popc(m);
+                        if (k < c) {
+                            for (; k > 0; k--) m &= m - 1;
+                            s += __ffs(m) - 1;
+                            break;
+                        }
+                        k -= c;
+                    }
+                } else {
+                    ticket_item(a, t, s, h, pair);
+                }
                 const int qb = a.query_start[s], qe = a.query_start[s + 1], ctx = a.context_lens[s];
                 const int n = qe - qb, t0 = pair * (a.head_pairs ? kRows : kTiles * kRows);
                 if (n < 0 || qb < 0 || qe > a.num_tokens || n > ctx || ctx > a.max_blocks * B) {
@@ -968,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // 128-byte segments.
                 const int n = rr < rows_x ? rr : 0;
                 const size_t at = ((size_t)(it.q_begin + it.t0 + x * it.rstep + n / a.group) * a.num_heads + it.h +
-                                   n % a.group) * a.parts.max_parts + it.part;
+                                   n % a.group) * a.parts.slots + it.part;
                 if (rr < rows_x) {
                     a.parts.m[at] = split ? fmaxf(m_run, xch[2 * lane]) : m_run;
                     a.parts.l[at] = l_run;
@@ -1100,7 +1144,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, const void *query, const void *
         !encode_tiled16(&tmv, vc, 4, cdims, cstr, cbox, kBf16))
         return cudaErrorInvalidValue;
     // persistent CTAs, one per SM (each holds all of its SM's TMEM), at most one per item
-    const int sms = sm_count();
+    const int sms = MODE == kShared && a.max_ctas < sm_count() ? a.max_ctas : sm_count();
     const int ctas = a.num_items < sms ? a.num_items : sms;
     return launch(kern, dim3((unsigned)(ctas > 0 ? ctas : 1)), dim3(kThreads), L::alloc, stream, a, tmq, tmk, tmv);
 }

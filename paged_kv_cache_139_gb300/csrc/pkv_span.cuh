@@ -12,18 +12,22 @@ namespace pkv {
 // query row (sequence, head) the partition's scores' reference (log2 domain),
 // the sum of 2^(score - reference) and the values' sum under those weights.
 struct PrefixParts {
-    float *m, *l;              // [S][H][max_parts]
-    float *o;                  // [S][H][max_parts][D]
+    float *m, *l;              // [S][H][slots]
+    float *o;                  // [S][H][slots][D]
     int part;                  // tokens, a multiple of 128
-    int max_parts;
+    int max_parts;             // partitions of the longest prefix
+    int own;                   // tokens of a partition of a sequence's own ones, where those go to memory too
+    int slots;                 // of both
 };
 
 // The prefix half over groups of many rows, on the fifth-generation tensor
-// cores (shared_prefix.cu).  Arguments as checked by the caller.
+// cores (shared_prefix.cu), on at most max_ctas SMs.  Arguments as checked by the
+// caller.
 cudaError_t launch_shared_prefix(const void *query, const void *key_cache, const void *value_cache,
                                  const int32_t *block_tables, const int32_t *group_start, const int32_t *prefix_lens,
                                  int num_groups, int num_seqs, int max_group_size, int max_prefix, int max_blocks,
                                  int block_size, int num_blocks, int num_heads, int num_kv_heads, int head_dim,
-                                 float scale_log2, const PrefixParts &parts, bool bf16, cudaStream_t stream);
+                                 float scale_log2, const PrefixParts &parts, bool bf16, int max_ctas,
+                                 cudaStream_t stream);
 
 }  // namespace pkv

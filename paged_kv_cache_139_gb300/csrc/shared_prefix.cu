@@ -9,7 +9,8 @@ cudaError_t launch_shared_prefix(const void *query, const void *key_cache, const
                                  const int32_t *block_tables, const int32_t *group_start, const int32_t *prefix_lens,
                                  int num_groups, int num_seqs, int max_group_size, int max_prefix, int max_blocks,
                                  int block_size, int num_blocks, int num_heads, int num_kv_heads, int head_dim,
-                                 float scale_log2, const PrefixParts &parts, bool bf16, cudaStream_t stream) {
+                                 float scale_log2, const PrefixParts &parts, bool bf16, int max_ctas,
+                                 cudaStream_t stream) {
     PrefillArgs a = {};
     a.block_tables = block_tables;
     a.status = status_ptr();
@@ -35,6 +36,7 @@ cudaError_t launch_shared_prefix(const void *query, const void *key_cache, const
     const long long items = (long long)num_groups * a.num_pairs * a.num_parts * num_kv_heads;
     if (!a.status || items > (1ll << 30)) return cudaErrorInvalidValue;
     a.num_items = (int)items;
+    a.max_ctas = max_ctas;
     return launch_prefill<kShared>(head_dim, bf16, a, query, key_cache, value_cache, num_kv_heads, stream);
 }
 

@@ -177,14 +177,21 @@ def test_captured_steps_and_streams(cuda_device, n):
         shared(c, out=outs[2], stream=streams[2], **kw)
         torch.cuda.synchronize()
         assert all(torch.equal(o, want) for o in outs)
-    size = pkv.paged_attention_decode_shared_workspace_size(len(c.ctx), 2, 8, 2, 128, kw["max_prefix_len"],
-                                                            kw["max_group_size"])
+    size = pkv.paged_attention_decode_shared_workspace_size(len(c.ctx), 2, 8, 2, 128, **kw)
     ws = torch.full((size,), 255, dtype=torch.uint8, device=cuda_device)           # NaN, whatever is read before it is written
     for _ in range(3):
         assert torch.equal(shared(c, workspace=ws, **kw), want)
     with pytest.raises(pkv.PkvError, match="workspace"):
         shared(c, workspace=ws[:-16], **kw)
     pkv.check()
+
+
+def test_a_wrong_guess_of_the_own_tokens_changes_nothing(cuda_device):
+    for groups in ([3, 2], [40, 2]):
+        c = make(cuda_device, groups, [130, 60], (1, 3000), 4, 2, 64, 16, "bf16", seed=12).upload()
+        kw = bounds(c)
+        for guess in (1, 17, 300, 0):
+            verify(c, shared(c, **{**kw, "max_suffix_len": guess}))
 
 
 def test_a_cache_past_32_bit_offsets(cuda_device):
