@@ -532,12 +532,12 @@ pkv_status paged_attention_prefill_window(void *out_dev, const void *query_dev,
  * Groups that leave sequences out, that exceed max_group_size or whose
  * prefix_lens differ latch PKV_EINDEX, as do prefixes beyond max_prefix_len or
  * the context.
- * Probabilities over a prefix enter the product with 11 bits for fp16 where the
- * group has more than 16 query rows per kv head (sequences x heads), with 22
- * otherwise; with 16 for bf16.  A NaN among a group's first tokens reaches all of
- * its sequences.  Two launches, three for groups of more than 16 query rows.  num_seqs <= 65535; up to 128 query heads per kv
- * head; scale > 0; contexts up to 2^30 tokens.  Other arguments as for
- * paged_attention_decode.
+ * Probabilities over a prefix enter the product with 16 bits for bf16 and 22 for
+ * fp16, but 11 where groups of more than 16 query rows per kv head (sequences x
+ * heads) have long prefixes, which then go through the prompt phase's kernel (three
+ * launches instead of two).  A NaN among a group's first tokens reaches all of its
+ * sequences.  num_seqs <= 65535; up to 128 query heads per kv head; scale > 0;
+ * contexts up to 2^30 tokens.  Other arguments as for paged_attention_decode.
  * ------------------------------------------------------------------------- */
 pkv_status paged_attention_decode_shared(void *out_dev, const void *query_dev,
                                          const void *key_cache_dev, const void *value_cache_dev,

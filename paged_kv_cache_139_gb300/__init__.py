@@ -348,7 +348,7 @@ def _raw_stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
 
 def _call(fn, what: str, index: int, *args) -> None:
     """A C call on the tensors' own device: the library launches on the current one."""
-    was = torch.cuda.current_device()
+    was = torch._C._cuda_getDevice()
     if was == index:
         rc = fn(*args)
     else:
@@ -672,9 +672,17 @@ def _check16(what, out, query, key_cache, value_cache, block_tables, context_len
         raise ValueError(f"{what}: shape mismatch")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
         raise ValueError(f"{what}: block_tables must be [S][max_blocks], context_lens [S]")
-    return (_at(out, "out", dt, index), _at(query, "query", dt, index), _at(key_cache, "key_cache", dt, index),
-            _at(value_cache, "value_cache", dt, index), _at(block_tables, "block_tables", i32, index),
-            _at(context_lens, "context_lens", i32, index))
+    if (out.get_device() == index and out.dtype is dt and out.is_contiguous() and query.is_contiguous()
+            and key_cache.get_device() == index and key_cache.dtype is dt and key_cache.is_contiguous()
+            and value_cache.get_device() == index and value_cache.dtype is dt and value_cache.is_contiguous()
+            and block_tables.get_device() == index and block_tables.dtype is i32 and block_tables.is_contiguous()
+            and context_lens.get_device() == index and context_lens.dtype is i32 and context_lens.is_contiguous()):
+        return (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+                context_lens.data_ptr())
+    for t, name, dtype in ((out, "out", dt), (query, "query", dt), (key_cache, "key_cache", dt),         # says what is wrong
+                           (value_cache, "value_cache", dt), (block_tables, "block_tables", i32),
+                           (context_lens, "context_lens", i32)):
+        _at(t, name, dtype, index)
 
 
 _scratches = threading.local()
@@ -687,7 +695,8 @@ def _scratch(index: int, nbytes: int, stream: Optional[torch.cuda.Stream]) -> to
     key = (index, _raw_stream(stream, index))
     held = _scratches.__dict__
     buf = held.get(key)
-    if buf is not None and buf.numel() >= nbytes and not _capturing(stream):
+    if buf is not None and buf.numel() >= nbytes and not (
+            torch._C._cuda_isCurrentStreamCapturing() if stream is None else _capturing(stream)):
         return buf
     with _on(stream):
         buf = torch.empty(max(nbytes, 1 << 16), dtype=torch.uint8, device=torch.device("cuda", index))

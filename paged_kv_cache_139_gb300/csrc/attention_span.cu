@@ -31,10 +31,10 @@
 //   * Few sequences are spread over the GPU by clusters of 2 to 16 CTAs per
 //     (sequence, kv head), which join through distributed shared memory: no
 //     workspace, no second launch, no counters.
-//   * The shared form: groups of up to 16 query rows per kv head take their
-//     prefix through this kernel too, and the launch for own tokens overlaps
-//     that one's end, joining the two halves itself.  Larger groups go to the
-//     tcgen05 kernel, which takes some of the SMs while own tokens, bound by
+//   * The shared form: groups of few query rows per kv head (up to 16, or more
+//     over short prefixes) take their prefix through this kernel too, and the
+//     launch for own tokens overlaps that one's end, joining the two halves
+//     itself.  Larger groups go to the tcgen05 kernel, which takes some of the SMs while own tokens, bound by
 //     memory, take the others; a third launch joins.
 #include <cuda.h>
 
@@ -215,20 +215,22 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
         const int b = __ldcg(a.group_start + unit), e = __ldcg(a.group_start + unit + 1);
         const bool edge = (unit == 0 && b != 0) || (unit == a.num_groups - 1 && e != a.num_seqs);
         if (b < 0 || e < b || e > a.num_seqs || e - b > a.max_group || edge) {
-            if (tid == 0 && g == 0 && blockIdx.y == 0) latch(a.st, kFlagBadGroup, unit);
+            if (tid == 0 && g == 0 && tile == 0 && blockIdx.y == 0) latch(a.st, kFlagBadGroup, unit);
             if (b < 0 || e < b || e > a.num_seqs || e - b > a.max_group) return;
         }
         if (e == b) return;
         prefix = __ldcg(a.prefix_lens + b);
-        if (g == 0 && blockIdx.y == 0)
+        if (g == 0 && tile == 0 && blockIdx.y == 0)
             for (int i = b + tid; i < e; i += C::THREADS)
                 if (__ldcg(a.prefix_lens + i) != prefix) latch(a.st, kFlagBadGroup, unit);
-        if (prefix < 0 || prefix > a.max_prefix) return;           // the suffix half reports it
+        // (one out of bounds is reported by the own tokens' half)
+        if (prefix < 0 || prefix > a.max_prefix || prefix > __ldcg(a.ctx_lens + b)) return;
         low = blockIdx.y * a.parts.part;
         if (low >= prefix) return;
         ctx = min(prefix, low + a.parts.part);
         s = b;
-        cols = (e - b) * a.group;
+        cols = min((e - b) * a.group - tile * COLS, COLS);
+        if (cols <= 0) return;                                     // fewer rows than the largest group
         row0 = b * a.num_heads + g * a.group;
     } else {
         ctx = __ldcg(a.ctx_lens + s);
@@ -254,8 +256,12 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
     }
     // row of column c (a group's columns run over its sequences, each with its heads of kv head g)
     auto row_of = [&](int c) -> size_t {
-        if constexpr (MODE == kSpanPrefix) return (size_t)row0 + (size_t)(c / a.group) * a.num_heads + c % a.group;
-        else return (size_t)row0 + c;
+        if constexpr (MODE == kSpanPrefix) {
+            const int r = tile * COLS + c;
+            return (size_t)row0 + (size_t)(r / a.group) * a.num_heads + r % a.group;
+        } else {
+            return (size_t)row0 + c;
+        }
     };
     // stages: those of the sinks, then those of [low, ctx); a stage that holds both counts once
     const int from = low / kTok;
@@ -791,13 +797,18 @@ pkv_status check_span(const SpanCall &c, SpanArgs &a, SpanMaps &maps) {
 
 // ---- sequences that share a prefix -------------------------------------------
 
-// Groups of up to this many query rows per kv head (sequences x heads) fit the
-// columns of the kernel above; larger ones go to the tcgen05 kernel.
+// A column tile of the kernel above holds this many query rows per kv head
+// (sequences x heads).  Larger groups take several, each with its own pass over the
+// prefix, while the passes of the call come to no more than this many tokens and kv
+// heads; the rest goes to the tcgen05 kernel, whose start costs some 5 us more.  (8
+// sequences of 32/8 heads after 1,024 tokens 8.3 against 11.5 us, after 8,192 18.4
+// against 18.3; 64 after 512 14.5 against 15.0, after 2,048 31 against 18.)
 constexpr int kFewRows = 16;
+constexpr long long kFewPasses = 1 << 16;
 
 // How a call is split.
 struct SharedPlan {
-    bool few;                    // every group fits the columns of the kernel above
+    bool few;                    // the prefixes go through the kernel above
     int part, max_parts;         // tokens of a prefix's partition (a multiple of 128), partitions
     int own, own_parts;          // of a sequence's own tokens, where the join is a launch of its own
     int prefix_ctas;             // SMs for the prefixes, where own tokens run beside them
@@ -808,11 +819,12 @@ SharedPlan plan_shared(int S, int groups, int H, int Hkv, int D, int max_prefix,
     SharedPlan w{};
     const int group = H / Hkv, tiles = (max_prefix + 127) / 128;
     const int sms = sm_count() > 0 ? sm_count() : 152;   // (a size asked for where there is no GPU)
-    w.few = (long long)max_group * group <= kFewRows;
+    const long long col_tiles = ((long long)max_group * group + kFewRows - 1) / kFewRows;
+    w.few = col_tiles == 1 || col_tiles * groups * Hkv * max_prefix <= kFewPasses;
     int per = tiles > 0 ? tiles : 1;                     // key tiles of a partition
     if (w.few) {
         // enough partitions to fill the GPU
-        const long long units = (long long)groups * Hkv;
+        const long long units = (long long)groups * Hkv * col_tiles;
         const long long parts = std::min<long long>(per, (2ll * sms + units - 1) / units);
         per = (int)((per + parts - 1) / parts);
     } else {
@@ -963,14 +975,14 @@ pkv_status paged_attention_decode_shared(void *out, const void *query, const voi
         // the prefixes, then the sequences' own tokens and the join
         const long long rows = (long long)max_group * a.group;
         SpanArgs p = a;
-        p.head_tiles = 1;
-        e = launch_span<kSpanPrefix>(head_dim, rows > 8 ? 2 : 1, bf16, p, maps, (long long)num_groups * num_kv_heads,
-                                     w.max_parts, {4, 1}, stream);
+        p.head_tiles = (int)((rows + kFewRows - 1) / kFewRows);
+        e = launch_span<kSpanPrefix>(head_dim, rows > 8 ? 2 : 1, bf16, p, maps,
+                                     (long long)num_groups * num_kv_heads * p.head_tiles, w.max_parts, {4, 1}, stream);
         if (e == cudaSuccess) e = launch_span<kSpanSuffix>(head_dim, NT, bf16, a, maps, items, 1,
                                                           choose_spread(items, max_suffix, NT), stream);
     } else {
         // the prefixes on some of the SMs, own tokens beside them on the others, then the join
-        e = launch_shared_prefix(query, key_cache, value_cache, block_tables, group_start, prefix_lens, num_groups, num_seqs,
+        e = launch_shared_prefix(query, key_cache, value_cache, block_tables, context_lens, group_start, prefix_lens, num_groups, num_seqs,
                                  max_group, max_prefix, max_blocks_per_seq, block_size, num_blocks, num_heads,
                                  num_kv_heads, head_dim, a.scale_log2, a.parts, bf16, w.prefix_ctas, stream);
         if (e == cudaSuccess)

@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (bad || b + t0 >= e) continue;
                     const int prefix = a.prefix_lens[b], k0 = part * a.part_tiles * kKeys;
-                    // (a prefix out of bounds is reported by the suffix half)
-                    if (prefix < 0 || prefix > a.max_prefix || k0 >= prefix) continue;
+                    // (a prefix out of bounds is reported by the own tokens' half)
+                    if (prefix < 0 || prefix > a.max_prefix || prefix > a.context_lens[b] || k0 >= prefix) continue;
                     o.s = b;
                     o.h = o.h1 = g * a.group;
                     o.t0 = t0;

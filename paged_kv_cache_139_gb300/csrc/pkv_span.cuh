@@ -24,7 +24,8 @@ struct PrefixParts {
 // cores (shared_prefix.cu), on at most max_ctas SMs.  Arguments as checked by the
 // caller.
 cudaError_t launch_shared_prefix(const void *query, const void *key_cache, const void *value_cache,
-                                 const int32_t *block_tables, const int32_t *group_start, const int32_t *prefix_lens,
+                                 const int32_t *block_tables, const int32_t *context_lens,
+                                 const int32_t *group_start, const int32_t *prefix_lens,
                                  int num_groups, int num_seqs, int max_group_size, int max_prefix, int max_blocks,
                                  int block_size, int num_blocks, int num_heads, int num_kv_heads, int head_dim,
                                  float scale_log2, const PrefixParts &parts, bool bf16, int max_ctas,

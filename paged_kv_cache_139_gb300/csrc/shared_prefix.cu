@@ -1,18 +1,20 @@
 // Decode over shared prefixes, its prefix half for groups of many rows: the shared
-// form of the kernel in pkv_prefill.cuh.  Groups of up to 16 rows per kv head and
-// the sequences' own tokens are in attention_span.cu, with the entry point.
+// form of the kernel in pkv_prefill.cuh.  Groups of few rows and the sequences' own
+// tokens are in attention_span.cu, with the entry point.
 #include "pkv_prefill.cuh"
 
 namespace pkv {
 
 cudaError_t launch_shared_prefix(const void *query, const void *key_cache, const void *value_cache,
-                                 const int32_t *block_tables, const int32_t *group_start, const int32_t *prefix_lens,
+                                 const int32_t *block_tables, const int32_t *context_lens,
+                                 const int32_t *group_start, const int32_t *prefix_lens,
                                  int num_groups, int num_seqs, int max_group_size, int max_prefix, int max_blocks,
                                  int block_size, int num_blocks, int num_heads, int num_kv_heads, int head_dim,
                                  float scale_log2, const PrefixParts &parts, bool bf16, int max_ctas,
                                  cudaStream_t stream) {
     PrefillArgs a = {};
     a.block_tables = block_tables;
+    a.context_lens = context_lens;
     a.status = status_ptr();
     a.num_seqs = num_seqs;
     a.num_tokens = num_seqs;                       // of the query's tensor map: one row each

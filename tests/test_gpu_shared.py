@@ -57,6 +57,39 @@ def test_groups(cuda_device, groups, prefix, suffix, H, Hkv, d, B, dtype):
     verify(c, shared(c, **bounds(c)))
 
 
+def wide(c, tokens=1 << 17):
+    """The same tables with room for many more tokens, so that a call without bounds takes the prefixes for long
+    ones: larger groups then go through the prompt phase's kernel."""
+    c.t = torch.nn.functional.pad(c.t, (0, tokens // c.B - c.t.shape[1]), value=-1).contiguous()
+    return c
+
+
+@pytest.mark.parametrize("groups,prefix,suffix", [
+    ([17], [16], (1, 1)),
+    ([30], [100], (0, 9)),
+    ([40, 1, 2], [300, 33, 128], (1, 40)),
+    ([70, 5], [257, 1], (0, 65)),
+    ([64, 20], [0, 512], (1, 300)),
+    ([130, 1, 33], [1000, 128, 127], (1, 17)),
+])
+@pytest.mark.parametrize("H,Hkv,d,B,dtype", [(2, 2, 128, 16, "f16"), (4, 1, 64, 8, "bf16"), (4, 2, 128, 32, "bf16"),
+                                             (14, 2, 64, 16, "f16"), (1, 1, 128, 128, "f16")])
+def test_large_groups(cuda_device, groups, prefix, suffix, H, Hkv, d, B, dtype):
+    if 0 in prefix and suffix[0] == 0:
+        suffix = (1, suffix[1])
+    c = wide(make(cuda_device, groups, prefix, suffix, H, Hkv, d, B, dtype, seed=len(groups) + H).upload())
+    verify(c, shared(c))
+    verify(c, shared(c, max_group_size=max(groups), max_suffix_len=int((c.ctx - c.prefix).max())))
+
+
+@pytest.mark.parametrize("groups,prefix,H,Hkv", [([64], [4000], 8, 4), ([40, 9], [3000, 100], 12, 4), ([300], [700], 8, 2)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_groups_in_partitions(cuda_device, groups, prefix, H, Hkv, dtype, d):
+    c = make(cuda_device, groups, prefix, (1, 1300), H, Hkv, d, 16, dtype, seed=len(groups) + 1).upload()
+    verify(c, shared(c, **bounds(c)))
+
+
 @pytest.mark.parametrize("B", [4, 8, 16, 32, 64, 128])
 @pytest.mark.parametrize("n", [2, 20])
 def test_blocks(cuda_device, B, n):
@@ -70,6 +103,7 @@ def test_blocks(cuda_device, B, n):
 def test_head_groups(cuda_device, H, Hkv, n):
     c = make(cuda_device, [n, 2], [260, 64], (1, 20), H, Hkv, 64 if H % 2 else 128, 16, "bf16", seed=H).upload()
     verify(c, shared(c, **bounds(c)))
+    verify(c, shared(wide(c)))
 
 
 @pytest.mark.parametrize("groups,prefix,suffix,H,Hkv", [
@@ -113,12 +147,16 @@ def test_only_the_first_sequences_table_is_read_for_the_prefix(cuda_device, n):
     c = make(cuda_device, [n], [160], (1, 50), 4, 2, 64, 16, "f16", seed=5).upload()
     c.t[1:, :10] = 1 << 30
     verify(c, shared(c, **bounds(c)))
+    verify(c, shared(wide(c)))
 
 
-@pytest.mark.parametrize("n", [2, 30])
-def test_bad_groups_are_latched(cuda_device, n):
+@pytest.mark.parametrize("n,far", [(2, False), (30, False), (30, True)])
+def test_bad_groups_are_latched(cuda_device, n, far):
     c = make(cuda_device, [n, 2], [100, 40], (1, 30), 4, 2, 64, 16, "f16", seed=6).upload()
     kw = bounds(c)
+    if far:                                              # through the prompt phase's kernel
+        wide(c)
+        kw = dict(max_group_size=n)
     good = shared(c, **kw).clone()
     pkv.check()
 
@@ -139,7 +177,7 @@ def test_bad_groups_are_latched(cuda_device, n):
     refused("context length", pl=at(at(c.pl, n, 1000), n + 1, 1000))
     refused("context length", pl=c.pl.index_fill(0, torch.arange(n, n + 2, device=c.pl.device), -3))
     refused("context length", ctx=at(c.c, 0, 99))
-    refused("context length", max_prefix_len=64)
+    refused("context length", max_prefix_len=64, max_context_len=0 if far else kw["max_context_len"])
     bad = c.t.clone()
     bad[0, 3] = -1
     refused("block-table entry", t=bad)
@@ -150,10 +188,10 @@ def test_bad_groups_are_latched(cuda_device, n):
     pkv.check()
 
 
-@pytest.mark.parametrize("n", [3, 50])
-def test_captured_steps_and_streams(cuda_device, n):
+@pytest.mark.parametrize("n,prefix", [(3, 300), (50, 300), (50, 2700)])
+def test_captured_steps_and_streams(cuda_device, n, prefix):
     """Two captured graphs and an eager stream, each with memory of its own, and one workspace for calls in turn."""
-    c = make(cuda_device, [n, 2], [300, 64], (1, 40), 8, 2, 128, 16, "f16", seed=7).upload()
+    c = make(cuda_device, [n, 2], [prefix, 64], (1, 40), 8, 2, 128, 16, "f16", seed=7).upload()
     kw = bounds(c)
     want = shared(c, **kw).clone()
     outs = [torch.zeros_like(want) for _ in range(3)]
@@ -187,14 +225,16 @@ def test_captured_steps_and_streams(cuda_device, n):
 
 
 def test_a_wrong_guess_of_the_own_tokens_changes_nothing(cuda_device):
-    for groups in ([3, 2], [40, 2]):
+    for groups, far in (([3, 2], False), ([40, 2], False), ([40, 2], True)):
         c = make(cuda_device, groups, [130, 60], (1, 3000), 4, 2, 64, 16, "bf16", seed=12).upload()
-        kw = bounds(c)
+        kw = dict(max_group_size=40) if far else bounds(c)
+        if far:
+            wide(c)
         for guess in (1, 17, 300, 0):
             verify(c, shared(c, **{**kw, "max_suffix_len": guess}))
 
 
 def test_a_cache_past_32_bit_offsets(cuda_device):
-    for n in (2, 20):
-        c = make(cuda_device, [n], [100], (1, 30), 4, 2, 128, 16, "f16", offset=(1 << 32) // (2 * 16 * 128) + 3).upload()
-        verify(c, shared(c, **bounds(c)))
+    c = make(cuda_device, [20], [100], (1, 30), 4, 2, 128, 16, "f16", offset=(1 << 32) // (2 * 16 * 128) + 3).upload()
+    verify(c, shared(c, **bounds(c)))
+    verify(c, shared(wide(c)))
