@@ -745,8 +745,8 @@ struct SpanCall {
     pkv_dtype dtype;
 };
 
-// The checks that both calls share; fills what the kernels need of them.
-pkv_status check_span(const SpanCall &c, SpanArgs &a, SpanMaps &maps) {
+// The checks that both calls share; fills what the kernels need of the arguments.
+pkv_status check_span(const SpanCall &c, SpanArgs &a) {
     if (c.dtype != PKV_F16 && c.dtype != PKV_BF16) return fail(PKV_EINVAL, "%s: bad dtype %d", c.what, (int)c.dtype);
     if (c.num_seqs < 0 || c.num_seqs > 65535 || c.max_blocks < 0 || c.num_blocks < 0)
         return fail(PKV_EINVAL, "%s: bad sizes (seqs %d, table width %d, blocks %d)", c.what, c.num_seqs, c.max_blocks,
@@ -770,8 +770,6 @@ pkv_status check_span(const SpanCall &c, SpanArgs &a, SpanMaps &maps) {
         return fail(PKV_EINVAL, "%s: NULL pointer", c.what);
     if (!aligned16(c.out) || !aligned16(c.query) || !aligned16(c.key_cache) || !aligned16(c.value_cache))
         return fail(PKV_EINVAL, "%s: pointers must be 16-byte aligned", c.what);
-    a.st = status_ptr();
-    if (!a.st) return fail(PKV_ECUDA, "%s: no device status word", c.what);
     a.out = const_cast<void *>(c.out);
     a.q = c.query;
     a.tables = c.block_tables;
@@ -787,6 +785,13 @@ pkv_status check_span(const SpanCall &c, SpanArgs &a, SpanMaps &maps) {
     a.head_tiles = (a.group + 15) / 16;
     a.tile_heads = (a.group + a.head_tiles - 1) / a.head_tiles;
     a.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
+    return PKV_OK;
+}
+
+// What a checked call needs of the device.
+pkv_status open_span(const SpanCall &c, SpanArgs &a, SpanMaps &maps) {
+    a.st = status_ptr();
+    if (!a.st) return fail(PKV_ECUDA, "%s: no device status word", c.what);
     const bool bf16 = c.dtype == PKV_BF16;
     std::memset(&maps, 0, sizeof maps);
     if (!encode_span_map(&maps.k, c.key_cache, c.num_blocks, c.num_kv_heads, c.block_size, c.head_dim, bf16) ||
@@ -892,12 +897,15 @@ pkv_status paged_attention_decode_window(void *out, const void *query, const voi
     const char *what = "paged_attention_decode_window";
     if (window < 1 || num_sinks < 0)
         return fail(PKV_EINVAL, "%s: window %d (at least 1), %d sinks (at least 0)", what, window, num_sinks);
+    const SpanCall call = {what, out, query, key_cache, value_cache, block_tables, context_lens, num_seqs,
+                           max_blocks_per_seq, max_context_len, block_size, num_blocks, num_heads, num_kv_heads, head_dim,
+                           scale, dtype};
     SpanArgs a = {};
     SpanMaps maps;
-    const pkv_status rc = check_span({what, out, query, key_cache, value_cache, block_tables, context_lens, num_seqs,
-                                      max_blocks_per_seq, max_context_len, block_size, num_blocks, num_heads,
-                                      num_kv_heads, head_dim, scale, dtype}, a, maps);
+    pkv_status rc = check_span(call, a);
     if (rc != PKV_OK || num_seqs == 0) return rc;
+    rc = open_span(call, a, maps);
+    if (rc != PKV_OK) return rc;
     a.window = window;
     a.sinks = num_sinks;
     const int NT = a.tile_heads > 8 ? 2 : 1;
@@ -939,11 +947,12 @@ pkv_status paged_attention_decode_shared(void *out, const void *query, const voi
     if (num_groups > num_seqs && num_seqs >= 0)
         return fail(PKV_EINVAL, "%s: %d groups of %d sequences", what, num_groups, num_seqs);
     if (!(scale > 0.f)) return fail(PKV_EINVAL, "%s: scale must be positive", what);
+    const SpanCall call = {what, out, query, key_cache, value_cache, block_tables, context_lens, num_seqs,
+                           max_blocks_per_seq, max_context_len, block_size, num_blocks, num_heads, num_kv_heads, head_dim,
+                           scale, dtype};
     SpanArgs a = {};
     SpanMaps maps;
-    const pkv_status rc = check_span({what, out, query, key_cache, value_cache, block_tables, context_lens, num_seqs,
-                                      max_blocks_per_seq, max_context_len, block_size, num_blocks, num_heads,
-                                      num_kv_heads, head_dim, scale, dtype}, a, maps);
+    pkv_status rc = check_span(call, a);
     if (rc != PKV_OK || num_seqs == 0) return rc;
     if (num_groups == 0) return fail(PKV_EINVAL, "%s: no groups", what);
     if (!group_start || !prefix_lens) return fail(PKV_EINVAL, "%s: NULL pointer", what);
@@ -966,6 +975,8 @@ pkv_status paged_attention_decode_shared(void *out, const void *query, const voi
         return fail(PKV_EINVAL, "%s: workspace of %zu bytes needed, %zu given", what, w.bytes,
                     workspace ? workspace_bytes : (size_t)0);
     if (w.max_parts > 65535) return fail(PKV_EINVAL, "%s: %d partitions of a prefix", what, w.max_parts);
+    rc = open_span(call, a, maps);
+    if (rc != PKV_OK) return rc;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     a.parts = {reinterpret_cast<float *>(ws + w.m_off), reinterpret_cast<float *>(ws + w.l_off),
                reinterpret_cast<float *>(ws + w.o_off), w.part, w.max_parts, w.own, w.max_parts + w.own_parts};

@@ -22,8 +22,10 @@ import math
 
 from . import (BlockAllocator, GrowingWorkspace, PkvError, _on, copy_blocks, kv_reshape_and_cache, kv_rotary_and_cache,
                kv_rotary_and_cache_fp8, kv_scales, make_fp8_workspace, make_workspace, paged_attention_decode,
-               paged_attention_decode_fp8, paged_attention_decode_fp8_workspace_size, paged_attention_prefill,
-               paged_attention_prefill_fp8, paged_attention_prefill_fp8_workspace_size, paged_attention_workspace_size,
+               paged_attention_decode_fp8, paged_attention_decode_fp8_workspace_size, paged_attention_decode_shared,
+               paged_attention_decode_shared_workspace_size, paged_attention_decode_window, paged_attention_prefill,
+               paged_attention_prefill_fp8, paged_attention_prefill_fp8_workspace_size, paged_attention_prefill_window,
+               paged_attention_workspace_size,
                rotary_table, swap_blocks)
 from ._lib import load
 
@@ -59,6 +61,56 @@ class StepPlan:
 
 
 @dataclasses.dataclass
+class SharedGroups:
+    """Consecutive sequences of a step that begin with the same blocks, as
+    paged_attention_decode_shared takes them."""
+
+    start: np.ndarray         # int32 [groups + 1]
+    prefix: np.ndarray        # int32 [n]: shared tokens of each sequence
+
+    @classmethod
+    def find(cls, tables: np.ndarray, context_lens: np.ndarray, block_size: int) -> "SharedGroups":
+        """Groups of the sequences as they stand in a step: one joins the group
+        before it while that saves no less reading (a group's sequences after the
+        first, times the full blocks that all of them begin with) than leaving
+        it out would.  A sequence on its own shares nothing."""
+        n = len(context_lens)
+        full = np.asarray(context_lens, np.int64) // block_size
+        start, common, prefix = [0], int(full[0]) if n else 0, np.zeros(n, np.int32)
+
+        def close(end):
+            if end - start[-1] > 1:
+                prefix[start[-1]:end] = common * block_size
+
+        for s in range(1, n):
+            m = int(min(common, full[s]))
+            differ = np.flatnonzero(tables[start[-1], :m] != tables[s, :m])
+            joined = int(differ[0]) if differ.size else m
+            size = s - start[-1]
+            if joined > 0 and joined * size >= common * (size - 1):
+                common = joined
+            else:
+                close(s)
+                start.append(s)
+                common = int(full[s])
+        if n:
+            close(n)
+            start.append(n)
+        return cls(np.asarray(start, np.int32), prefix)
+
+
+@dataclasses.dataclass
+class DeviceGroups:
+    """The same groups on the device, and their bounds."""
+
+    start: torch.Tensor
+    prefix: torch.Tensor
+    max_prefix_len: int
+    max_group_size: int
+    max_suffix_len: int
+
+
+@dataclasses.dataclass
 class DeviceStep:
     """The same plan on the device."""
 
@@ -68,6 +120,7 @@ class DeviceStep:
     context_lens: torch.Tensor
     max_context_len: int
     positions: Optional[torch.Tensor] = None     # int32, of a cache with rotary positions
+    groups: Optional[DeviceGroups] = None        # sequences that share prefixes, where asked for
 
 
 @dataclasses.dataclass
@@ -185,6 +238,11 @@ class PagedKVCache:
     same).  With `rotary`, write, decode and prefill rotate queries and keys by
     their tokens' positions on the way.
 
+    With `window`, decode and prefill attend to a token's last `window` tokens
+    (itself among them) and the first `sinks` ones of its sequence.  Steps
+    uploaded with shared=True read the prefixes that sequences share (forks, by
+    their block tables) once.  Both are for 16-bit caches.
+
     The 8-bit prompt phase's workspace holds the step's contexts in 16 bits.
     Caches whose calls follow one another on the GPU, as those of a model's
     layers do, need one between them: give the first layer's cache as
@@ -195,7 +253,7 @@ class PagedKVCache:
                  free_order: Optional[Sequence[int]] = None,
                  key_cache: Optional[torch.Tensor] = None, value_cache: Optional[torch.Tensor] = None,
                  scales: Optional[torch.Tensor] = None, rotary: Optional[RotaryPositions] = None,
-                 workspace_of: Optional["PagedKVCache"] = None):
+                 workspace_of: Optional["PagedKVCache"] = None, window: Optional[int] = None, sinks: int = 0):
         shape = (num_blocks, num_kv_heads, block_size, head_dim)
         self.device = torch.device(device)
         self.key_cache = key_cache if key_cache is not None else torch.empty(shape, dtype=dtype, device=self.device)
@@ -210,6 +268,11 @@ class PagedKVCache:
             assert self.scales.dtype == torch.float32 and self.key_cache.dtype == self.value_cache.dtype == dtype
             assert all(t.is_contiguous() for t in (self.scales, self.key_cache, self.value_cache))
         self.rotary = rotary
+        if window is None and sinks:
+            raise ValueError("sinks: first tokens that stay visible need a window that hides others")
+        if window is not None and (self.fp8 or window < 1 or sinks < 0):
+            raise ValueError("window: a 16-bit cache, at least one token, no negative number of sinks")
+        self.window, self.sinks = window, sinks
         self.alloc = BlockAllocator(num_blocks, block_size, free_order)
         self.num_blocks, self.num_kv_heads, self.head_dim, self.block_size = shape[0], shape[1], shape[3], shape[2]
         self.max_blocks_per_seq = max_blocks_per_seq
@@ -280,7 +343,9 @@ class PagedKVCache:
             max_context_len=int(plan.context_lens.max()) if plan.context_lens.size else 0,
             positions=self._upload_positions(plan, non_blocking))
 
-    def upload(self, plan: StepPlan, non_blocking: bool = False) -> DeviceStep:
+    def upload(self, plan: StepPlan, non_blocking: bool = False, shared: bool = False) -> DeviceStep:
+        """shared: find the prefixes that neighbouring sequences share, which
+        attend and decode then read once."""
         d = self.device
         return DeviceStep(
             slots=torch.from_numpy(plan.slots).to(d, non_blocking=non_blocking),
@@ -288,7 +353,19 @@ class PagedKVCache:
             tables=torch.from_numpy(plan.tables).to(d, non_blocking=non_blocking),
             context_lens=torch.from_numpy(plan.context_lens).to(d, non_blocking=non_blocking),
             max_context_len=int(plan.context_lens.max()) if plan.context_lens.size else 0,
-            positions=self._upload_positions(plan, non_blocking) if plan.slots.size else None)
+            positions=self._upload_positions(plan, non_blocking) if plan.slots.size else None,
+            groups=self._upload_groups(plan, non_blocking) if shared else None)
+
+    def _upload_groups(self, plan: StepPlan, non_blocking: bool) -> Optional[DeviceGroups]:
+        if self.fp8 or self.window is not None:
+            raise ValueError("shared: a 16-bit cache without a window")
+        g = SharedGroups.find(plan.tables, plan.context_lens, self.block_size)
+        if not g.prefix.any():
+            return None
+        d = self.device
+        return DeviceGroups(torch.from_numpy(g.start).to(d, non_blocking=non_blocking),
+                            torch.from_numpy(g.prefix).to(d, non_blocking=non_blocking), int(g.prefix.max()),
+                            int(np.diff(g.start).max()), int((plan.context_lens - g.prefix).max()))
 
     def _upload_positions(self, plan, non_blocking: bool) -> Optional[torch.Tensor]:
         if self.rotary is None:
@@ -347,6 +424,18 @@ class PagedKVCache:
             out = torch.empty_like(query)
         mcl = step.max_context_len if max_context_len is None else max_context_len
         mcl = mcl or _table_tokens(self, step)
+        if self.window is not None or step.groups is not None:
+            if partition_size:
+                raise ValueError("partition_size: neither windows nor shared prefixes take one")
+            if self.window is not None:
+                return paged_attention_decode_window(out, query, self.key_cache, self.value_cache, step.tables,
+                                                     step.context_lens, self.window, self.sinks, scale=scale,
+                                                     max_context_len=mcl)
+            g = step.groups
+            return paged_attention_decode_shared(out, query, self.key_cache, self.value_cache, step.tables,
+                                                 step.context_lens, g.start, g.prefix, scale=scale,
+                                                 max_context_len=mcl, max_prefix_len=g.max_prefix_len,
+                                                 max_group_size=g.max_group_size, max_suffix_len=g.max_suffix_len)
         ws = self.workspace(query.shape[0], query.shape[1], mcl, partition_size)
         if self.fp8:
             return paged_attention_decode_fp8(out, query, self.key_cache, self.value_cache, self.scales, step.tables,
@@ -389,6 +478,10 @@ class PagedKVCache:
                                                step.context_lens, step.query_start, scale=scale,
                                                max_query_len=step.max_query_len, max_context_len=step.max_context_len,
                                                workspace=ws)
+        if self.window is not None:
+            return paged_attention_prefill_window(out, query, self.key_cache, self.value_cache, step.tables,
+                                                  step.context_lens, step.query_start, self.window, self.sinks,
+                                                  scale=scale, max_query_len=step.max_query_len)
         return paged_attention_prefill(out, query, self.key_cache, self.value_cache, step.tables,
                                        step.context_lens, step.query_start, scale=scale,
                                        max_query_len=step.max_query_len, workspace=self.prefill_workspace())
@@ -496,6 +589,16 @@ def _scratch_queries(eng: PagedKVCache, query, stream):
         return torch.empty_like(query)
 
 
+def _scratch_shared(eng: PagedKVCache, groups, S, H, d, mcl, stream):
+    """What a prepared step with shared prefixes keeps its partial results in:
+    memory of its own, made on its stream (with a window there is none)."""
+    n = 0 if groups is None else paged_attention_decode_shared_workspace_size(
+        S, groups.start.shape[0] - 1, H, eng.num_kv_heads, d, mcl, groups.max_prefix_len, groups.max_group_size,
+        groups.max_suffix_len)
+    with _on(stream):
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=eng.device)
+
+
 def _copy_calls(eng: PagedKVCache, step, st):
     n = step.pairs.shape[0] if step.pairs.dim() == 2 else 0
     return [(c.data_ptr(), step.pairs.data_ptr(), n, c.numel() // c.shape[0] * c.element_size(), eng.num_blocks, st)
@@ -533,10 +636,16 @@ class PreparedStep:
         stream = stream if stream is not None else torch.cuda.current_stream(eng.device)
         st = ctypes.c_void_p(stream.cuda_stream)
         mcl = step.max_context_len or _table_tokens(eng, step)
-        ws = eng.workspace(S, H, mcl, partition_size)
+        NB, B, groups = eng.num_blocks, eng.block_size, step.groups
+        plain = eng.window is None and groups is None
+        if plain:
+            ws = eng.workspace(S, H, mcl, partition_size)
+        else:
+            if partition_size:
+                raise ValueError("partition_size: neither windows nor shared prefixes take one")
+            ws = _scratch_shared(eng, groups, S, H, d, mcl, stream)
         q = _scratch_queries(eng, query, stream)
         self._keep = (query, q, key, value, step, out, _held(eng, ws, stream))
-        NB, B = eng.num_blocks, eng.block_size
         self._copy = _copy_calls(eng, step, st)
         T = self._tokens = step.slots.shape[0]
         self._write_name, self._write = _write_call(eng, query, q, key, value, step, code, st)
@@ -547,10 +656,26 @@ class PreparedStep:
                         mcl, B, NB, H, eng.num_kv_heads, d,
                         float(1.0 / math.sqrt(d) if scale is None else scale), partition_size, ws.data_ptr(),
                         ws.numel(), code, st)
+        if not plain:
+            ptrs = (out.data_ptr(), q.data_ptr(), eng.key_cache.data_ptr(), eng.value_cache.data_ptr(),
+                    step.tables.data_ptr(), step.context_lens.data_ptr())
+            sizes = (step.tables.shape[1], mcl, B, NB, H, eng.num_kv_heads, d,
+                     float(1.0 / math.sqrt(d) if scale is None else scale))
+            if eng.window is not None:
+                self._attend_name = "paged_attention_decode_window"
+                self._attend = (*ptrs, S, *sizes, eng.window, eng.sinks, code, st)
+            else:
+                for t in (groups.start, groups.prefix):
+                    assert t.dtype == torch.int32 and t.device == query.device and t.is_contiguous()
+                assert groups.prefix.shape == (S,)
+                self._attend_name = "paged_attention_decode_shared"
+                self._attend = (*ptrs, groups.start.data_ptr(), groups.prefix.data_ptr(), S, groups.start.shape[0] - 1,
+                                groups.max_group_size, groups.max_prefix_len, groups.max_suffix_len, *sizes,
+                                ws.data_ptr(), ws.numel(), code, st)
         # one new token per sequence, in sequence order, written as it is in 16 bits: the write can ride in the
         # attention launch
         self._write_attend = None
-        if T == S and not eng.fp8 and eng.rotary is None:
+        if T == S and not eng.fp8 and eng.rotary is None and plain:
             self._write_attend = (out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(),
                                   eng.key_cache.data_ptr(), eng.value_cache.data_ptr(), step.slots.data_ptr(),
                                   step.tables.data_ptr(), step.context_lens.data_ptr(), S, step.tables.shape[1],
@@ -578,10 +703,10 @@ class PreparedStep:
 
     def write_attend(self) -> None:
         """The cache write and the attention in one launch (paged_attention_decode_write): of a 16-bit cache without
-        rotary positions, for a step of one token per sequence."""
+        rotary positions or a window, for a step of one token per sequence and no groups."""
         if self._write_attend is None:
-            raise ValueError("write_attend: only a 16-bit cache without rotary positions, one new token per sequence, is "
-                             "written in the attention launch")
+            raise ValueError("write_attend: only a 16-bit cache without rotary positions or window, one new token per "
+                             "sequence and no groups, is written in the attention launch")
         rc = self._L.paged_attention_decode_write(*self._write_attend)
         if rc:
             raise PkvError(rc, "paged_attention_decode_write")
@@ -626,13 +751,14 @@ class PreparedPrefill:
         self._copy = _copy_calls(eng, step, st)
         self._tokens = step.slots.shape[0]
         self._write_name, self._write = _write_call(eng, query, q, key, value, step, code, st)
-        self._attend_name = "paged_attention_prefill_fp8" if eng.fp8 else "paged_attention_prefill"
+        self._attend_name = ("paged_attention_prefill_fp8" if eng.fp8 else "paged_attention_prefill" if eng.window is None
+                             else "paged_attention_prefill_window")
         self._attend = (out.data_ptr(), q.data_ptr(), eng.key_cache.data_ptr(), eng.value_cache.data_ptr(),
                         *((eng.scales.data_ptr(),) if eng.fp8 else ()),
                         step.tables.data_ptr(), step.context_lens.data_ptr(), step.query_start.data_ptr(), S, T,
                         step.max_query_len, *((step.max_context_len,) if eng.fp8 else ()), mb, B, NB, H,
-                        eng.num_kv_heads, d, float(1.0 / math.sqrt(d) if scale is None else scale), ws.data_ptr(),
-                        ws.numel(), code, st)
+                        eng.num_kv_heads, d, float(1.0 / math.sqrt(d) if scale is None else scale),
+                        *((eng.window, eng.sinks) if eng.window is not None else ()), ws.data_ptr(), ws.numel(), code, st)
 
     copy, write, attend = PreparedStep.copy, PreparedStep.write, PreparedStep.attend
 
