@@ -666,23 +666,26 @@ def paged_attention_prefill_fp8(out: torch.Tensor, query: torch.Tensor, key_cach
 
 # -- sliding windows and shared prefixes ------------------------------------------------
 
-def _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S, index):
-    qs, ks, dt, i32 = query.shape, key_cache.shape, query.dtype, torch.int32
-    if out.shape != qs or value_cache.shape != ks or len(ks) != 4 or qs[2] != ks[3]:
+def _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S):
+    """The device, the six pointers, the table's width and the sizes [NB, Hkv, B] of a
+    call over a 16-bit cache of S sequences."""
+    qs, ks, bs = query.shape, key_cache.shape, block_tables.shape
+    if len(qs) != 3 or len(ks) != 4 or qs[2] != ks[3] or out.shape != qs or value_cache.shape != ks:
         raise ValueError(f"{what}: shape mismatch")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+    if len(bs) != 2 or bs[0] != S or context_lens.shape != (S,):
         raise ValueError(f"{what}: block_tables must be [S][max_blocks], context_lens [S]")
-    if (out.get_device() == index and out.dtype is dt and out.is_contiguous() and query.is_contiguous()
+    index, dt, i32 = _cuda_index(query, "query"), query.dtype, torch.int32
+    if not (out.get_device() == index and out.dtype is dt and out.is_contiguous() and query.is_contiguous()
             and key_cache.get_device() == index and key_cache.dtype is dt and key_cache.is_contiguous()
             and value_cache.get_device() == index and value_cache.dtype is dt and value_cache.is_contiguous()
             and block_tables.get_device() == index and block_tables.dtype is i32 and block_tables.is_contiguous()
             and context_lens.get_device() == index and context_lens.dtype is i32 and context_lens.is_contiguous()):
-        return (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
-                context_lens.data_ptr())
-    for t, name, dtype in ((out, "out", dt), (query, "query", dt), (key_cache, "key_cache", dt),         # says what is wrong
-                           (value_cache, "value_cache", dt), (block_tables, "block_tables", i32),
-                           (context_lens, "context_lens", i32)):
-        _at(t, name, dtype, index)
+        for t, name, dtype in ((out, "out", dt), (query, "query", dt), (key_cache, "key_cache", dt),     # says what is wrong
+                               (value_cache, "value_cache", dt), (block_tables, "block_tables", i32),
+                               (context_lens, "context_lens", i32)):
+            _at(t, name, dtype, index)
+    return (index, (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                    block_tables.data_ptr(), context_lens.data_ptr()), bs[1], ks)
 
 
 _scratches = threading.local()
@@ -715,13 +718,10 @@ def paged_attention_decode_window(out: torch.Tensor, query: torch.Tensor, key_ca
     without a visible token are not read.  No workspace; calls may overlap.
     Returns out."""
     what = "paged_attention_decode_window"
-    index = _cuda_index(query, "query")
     S, H, d = query.shape
-    ptrs = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S, index)
-    NB, Hkv, B, _ = key_cache.shape
-    _call(load().paged_attention_decode_window, what, index, *ptrs, S, block_tables.shape[1], max_context_len, B, NB, H,
-          Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale, window, num_sinks, _dtype_code(query),
-          _raw_stream(stream, index))
+    index, ptrs, mb, (NB, Hkv, B, _) = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S)
+    _call(load().paged_attention_decode_window, what, index, *ptrs, S, mb, max_context_len, B, NB, H, Hkv, d,
+          1.0 / math.sqrt(d) if scale is None else scale, window, num_sinks, _dtype_code(query), _raw_stream(stream, index))
     return out
 
 
@@ -736,17 +736,15 @@ def paged_attention_prefill_window(out: torch.Tensor, query: torch.Tensor, key_c
     from make_workspace (its counter balances the work over the SMs), one call at
     a time; None: each SM takes a fixed share, and calls may overlap.  Returns out."""
     what = "paged_attention_prefill_window"
-    index = _cuda_index(query, "query")
     T, H, d = query.shape
     S = context_lens.shape[0]
-    ptrs = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S, index)
+    index, ptrs, mb, (NB, Hkv, B, _) = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S)
     if query_start.shape != (S + 1,):
         raise ValueError(f"{what}: query_start must be [S+1]")
-    NB, Hkv, B, _ = key_cache.shape
     ws = (None, 0) if workspace is None else (_at(workspace, "workspace", torch.uint8, index), workspace.numel())
     _call(load().paged_attention_prefill_window, what, index, *ptrs,
-          _at(query_start, "query_start", torch.int32, index), S, T, max_query_len, block_tables.shape[1], B, NB, H, Hkv,
-          d, 1.0 / math.sqrt(d) if scale is None else scale, window, num_sinks, *ws, _dtype_code(query),
+          _at(query_start, "query_start", torch.int32, index), S, T, max_query_len, mb, B, NB, H, Hkv, d,
+          1.0 / math.sqrt(d) if scale is None else scale, window, num_sinks, *ws, _dtype_code(query),
           _raw_stream(stream, index))
     return out
 
@@ -777,13 +775,11 @@ def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_ca
     particular state, for one call at a time; None takes the binding's own, kept
     for the calling thread and stream.  Returns out."""
     what = "paged_attention_decode_shared"
-    index = _cuda_index(query, "query")
     S, H, d = query.shape
-    ptrs = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S, index)
+    index, ptrs, mb, (NB, Hkv, B, _) = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S)
     if group_start.dim() != 1 or not group_start.shape[0] or prefix_lens.shape != (S,):
         raise ValueError(f"{what}: group_start must be [G+1], prefix_lens [S]")
-    NB, Hkv, B, _ = key_cache.shape
-    G, mb = group_start.shape[0] - 1, block_tables.shape[1]
+    G = group_start.shape[0] - 1
     if workspace is None:
         need = paged_attention_decode_shared_workspace_size(S, G, H, Hkv, d, max_context_len or mb * B, max_prefix_len,
                                                             max_group_size, max_suffix_len)

@@ -197,11 +197,8 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
     // (Loads here go past L1.)
     if constexpr (MODE == kSpanWindow || MODE == kSpanPrefix) pdl_wait();
     pdl_trigger();
-    bool dead = __any_sync(kFull, timed_out(a.st));     // an earlier wait gave up: no copies, nothing waited for
-    if (smem_u32(sm) & 1023u) {
-        if (tid == 0) latch(a.st, kFlagTimeout, -2);
-        dead = true;
-    }
+    // (used once the lengths are here too: one round trip for all)
+    const unsigned gave_up = *reinterpret_cast<const volatile unsigned int *>(&a.st->flags) & kFlagTimeout;
 
     // ---- this CTA's rows and tokens ----
     const int B = 1 << a.log2_block;
@@ -220,11 +217,12 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
         }
         if (e == b) return;
         prefix = __ldcg(a.prefix_lens + b);
+        const int most = min(a.max_prefix, __ldcg(a.ctx_lens + b));
         if (g == 0 && tile == 0 && blockIdx.y == 0)
             for (int i = b + tid; i < e; i += C::THREADS)
                 if (__ldcg(a.prefix_lens + i) != prefix) latch(a.st, kFlagBadGroup, unit);
         // (one out of bounds is reported by the own tokens' half)
-        if (prefix < 0 || prefix > a.max_prefix || prefix > __ldcg(a.ctx_lens + b)) return;
+        if (prefix < 0 || prefix > most) return;
         low = blockIdx.y * a.parts.part;
         if (low >= prefix) return;
         ctx = min(prefix, low + a.parts.part);
@@ -234,6 +232,7 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
         row0 = b * a.num_heads + g * a.group;
     } else {
         ctx = __ldcg(a.ctx_lens + s);
+        if constexpr (MODE != kSpanWindow) prefix = __ldcg(a.prefix_lens + s);
         if (ctx < 0 || ctx > a.max_ctx) {
             if (tid == 0 && g == 0 && tile == 0 && rank == 0 && blockIdx.y == 0) latch(a.st, kFlagBadContext, ctx);
             ctx = ctx < 0 ? 0 : a.max_ctx;
@@ -242,7 +241,6 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
             low = max(0, ctx - a.window);
             first = min(a.sinks, low);
         } else {
-            prefix = __ldcg(a.prefix_lens + s);
             if (prefix < 0 || prefix > ctx || prefix > a.max_prefix) {
                 if (tid == 0 && g == 0 && tile == 0 && rank == 0 && blockIdx.y == 0) latch(a.st, kFlagBadContext, prefix);
                 prefix = prefix < 0 ? 0 : min(ctx, a.max_prefix);
@@ -269,6 +267,11 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
     if (nsink > from) nsink = from;
     const int nst = low < ctx ? nsink + (ctx + kTok - 1) / kTok - from : 0;
     const int st0 = (int)((long long)nst * rank / nrank), st1 = (int)((long long)nst * (rank + 1) / nrank);
+    bool dead = __any_sync(kFull, gave_up != 0);         // an earlier wait gave up: no copies, nothing waited for
+    if (smem_u32(sm) & 1023u) {
+        if (tid == 0) latch(a.st, kFlagTimeout, -2);
+        dead = true;
+    }
     const int mine = dead ? 0 : max(0, (st1 - st0 - warp + W - 1) / W);
     auto token0 = [&](int i) {                          // first token of this warp's stage i
         const int v = st0 + warp + W * i;
@@ -828,10 +831,25 @@ SharedPlan plan_shared(int S, int groups, int H, int Hkv, int D, int max_prefix,
     w.few = col_tiles == 1 || col_tiles * groups * Hkv * max_prefix <= kFewPasses;
     int per = tiles > 0 ? tiles : 1;                     // key tiles of a partition
     if (w.few) {
-        // enough partitions to fill the GPU
-        const long long units = (long long)groups * Hkv * col_tiles;
-        const long long parts = std::min<long long>(per, (2ll * sms + units - 1) / units);
-        per = (int)((per + parts - 1) / parts);
+        // CTAs in waves; a key tile's time in us at full occupancy, or when the GPU is not full, a CTA's
+        // start and end, the parts' way through L2 (16 groups of 8 after 1,024 tokens, 32 heads: one
+        // partition leaves a second wave of 56 CTAs: 72 us in all, 68 with four)
+        const long long units = (long long)groups * Hkv * col_tiles, slots = sms * ((long long)max_group * group > 8 ? 2 : 3);
+        const double full = 128 * 4.0 * D / (6.6e6 / slots);
+        double least = 1e300;
+        for (int p = 1, last = 0; p <= tiles && p <= 64; p++) {
+            const int tp = (tiles + p - 1) / p;
+            if (tp == last) continue;
+            last = tp;
+            const int parts = (tiles + tp - 1) / tp;
+            const long long ctas = units * parts, waves = (ctas + slots - 1) / slots;
+            const double tile = full * std::max(0.7, std::min(1.0, (double)ctas / slots));
+            const double cost = waves * (tp * tile + 3.0) + (double)parts * S * H * D * 8.0 / 8e6;
+            if (cost < least) {
+                least = cost;
+                per = tp;
+            }
+        }
     } else {
         // The prefixes are bound by the tensor cores and run on n SMs; own tokens are bound by memory
         // and run on the others, then on all.  Times in us, measured on the kernels: a key tile of 256
