@@ -348,7 +348,7 @@ def _raw_stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
 
 def _call(fn, what: str, index: int, *args) -> None:
     """A C call on the tensors' own device: the library launches on the current one."""
-    was = torch._C._cuda_getDevice()
+    was = torch.cuda.current_device()
     if was == index:
         rc = fn(*args)
     else:
@@ -695,6 +695,9 @@ def _scratch(index: int, nbytes: int, stream: Optional[torch.cuda.Stream]) -> to
     """Uninitialised scratch of one call.  Kept per thread and stream, where calls
     follow one another (two threads may interleave their launches on one stream);
     a captured call takes memory of its own, which its graph keeps."""
+    if torch.cuda.current_device() != index:               # streams and captures are asked for on the current device
+        with torch.cuda.device(index):
+            return _scratch(index, nbytes, stream)
     key = (index, _raw_stream(stream, index))
     held = _scratches.__dict__
     buf = held.get(key)

@@ -101,7 +101,7 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return y;
 }
 
-// A 2^x that is never slower than its one instruction; 2^-inf = 0.
+// 2^x by the hardware approximation; 2^-inf = 0.
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -761,6 +761,8 @@ pkv_status check_span(const SpanCall &c, SpanArgs &a) {
     if (c.num_heads <= 0 || c.num_kv_heads <= 0 || c.num_heads % c.num_kv_heads || c.num_heads > 65535)
         return fail(PKV_EINVAL, "%s: %d query heads do not group over %d kv heads (at most 65535)", c.what, c.num_heads,
                     c.num_kv_heads);
+    if ((long long)c.num_seqs * c.num_heads > 1 << 30)
+        return fail(PKV_EINVAL, "%s: %d sequences of %d query heads (at most 2^30 rows)", c.what, c.num_seqs, c.num_heads);
     if (!std::isfinite(c.scale)) return fail(PKV_EINVAL, "%s: scale must be finite", c.what);
     const int64_t cap = (int64_t)c.max_blocks * c.block_size;
     if (c.max_context_len < 0 || c.max_context_len > cap)
@@ -828,7 +830,7 @@ SharedPlan plan_shared(int S, int groups, int H, int Hkv, int D, int max_prefix,
     const int group = H / Hkv, tiles = (max_prefix + 127) / 128;
     const int sms = sm_count() > 0 ? sm_count() : 152;   // (a size asked for where there is no GPU)
     const long long col_tiles = ((long long)max_group * group + kFewRows - 1) / kFewRows;
-    w.few = col_tiles == 1 || col_tiles * groups * Hkv * max_prefix <= kFewPasses;
+    w.few = col_tiles == 1 || col_tiles * groups * Hkv * std::max(1, max_prefix) <= kFewPasses;
     int per = tiles > 0 ? tiles : 1;                     // key tiles of a partition
     if (w.few) {
         // CTAs in waves; a key tile's time in us at full occupancy, or when the GPU is not full, a CTA's
@@ -992,7 +994,11 @@ pkv_status paged_attention_decode_shared(void *out, const void *query, const voi
     if (!workspace || workspace_bytes < w.bytes || !aligned16(workspace))
         return fail(PKV_EINVAL, "%s: workspace of %zu bytes needed, %zu given", what, w.bytes,
                     workspace ? workspace_bytes : (size_t)0);
-    if (w.max_parts > 65535) return fail(PKV_EINVAL, "%s: %d partitions of a prefix", what, w.max_parts);
+    const long long seqs = 2 * (128 / a.group);           // of an item of the tcgen05 kernel
+    const long long prefix_items = (long long)num_groups * ((max_group + seqs - 1) / seqs) * w.max_parts * num_kv_heads;
+    if (!w.few && prefix_items > kMaxPrefillItems)
+        return fail(PKV_EINVAL, "%s: %lld work items (groups x pairs of row tiles x partitions x kv heads) above 2^30", what,
+                    prefix_items);
     rc = open_span(call, a, maps);
     if (rc != PKV_OK) return rc;
     unsigned char *ws = static_cast<unsigned char *>(workspace);

@@ -19,7 +19,11 @@
 //            row's window on; of two row tiles the second skips the first of those
 //            when none of its rows sees it.  Blocks that no row of the item sees
 //            are not read: the tile's first visible block stands in their place
-//            (their scores are masked, and its values are as finite as the others).
+//            (their scores are masked, and its values are as finite as the others);
+//            in a sink tile that is not full, the sinks' values alone are.
+//            (Skipping such a tile's other products and chunks, or zeroing its values
+//            in the softmax warps, made every tile's code slower: 290 to 304 us against
+//            270 for 8 prompts of 512 to 4,096 tokens with a window of 1,024.)
 //   kShared  rows are (sequence, head) pairs of one group and kv head, 128 /
 //            (heads per kv head) sequences to a tile; all see the same keys, a
 //            partition of the group's prefix.  Their maximum, sum and unscaled
@@ -106,6 +110,7 @@ struct PrefillArgs {
     int num_items;                       // num_pairs x (query heads, or head pairs) x num_seqs tickets
     float scale_log2;                    // scale * log2(e)
     int window, sinks;                   // kWindow
+    int sink_unit;                       // the largest power of two that divides sinks, at most a block
     // kShared; tickets are num_groups x num_pairs x num_parts x kv heads
     const int32_t *group_start, *prefix_lens;
     int num_groups, max_group, max_prefix, num_kv_heads;
@@ -292,7 +297,8 @@ __device__ __forceinline__ int tile_entry(const PrefillArgs &a, const PfItemOf<M
 template <int D, typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tmq,
-                         const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+                         const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                         const __grid_constant__ CUtensorMap tms) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     using Item = PfItemOf<MODE>;
     using L = PfLayout<D, Item>;
@@ -371,7 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // kWindow: no ticket without work.  Tickets run over levels of row tiles from the top; a level
         // has the sequences with new tokens there, each with its heads.  (A window's items all cost
         // about the same, so that an equal number each, without a counter, is nearly balanced.)
+        // (Tickets only grow, so the search for a level's k-th sequence goes on from the last one found.)
         int level = a.num_pairs, level_t = 0, level_seqs = 0;      // tickets before the level, its sequences
+        int seen_s = 0, seen_k = 0;                                // the level's sequences below seen_s: seen_k
         const int level_rows = a.head_pairs ? kRows : kTiles * kRows, level_heads = a.head_pairs ? a.num_heads / 2 : a.num_heads;
         auto rows_above = [&](int s, bool report) -> unsigned {    // lanes whose sequence s + lane is in the level
             bool in = false;
@@ -431,26 +439,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (MODE == kWindow) {
                     while (t >= level_t + level_seqs * level_heads) {
                         level_t += level_seqs * level_heads;
-                        level_seqs = 0;
+                        level_seqs = seen_s = seen_k = 0;
                         if (--level < 0) break;
                         for (int i = 0; i < a.num_seqs; i += 32)
                             level_seqs += __popc(rows_above(i, blockIdx.x == 0 && level == a.num_pairs - 1));
                     }
                     if (level < 0) break;
-                    int k = (t - level_t) / level_heads;           // the level's k-th sequence
+                    const int k = (t - level_t) / level_heads;     // the level's k-th sequence
                     h = (t - level_t) % level_heads * (a.head_pairs ? 2 : 1);
                     pair = level;
-                    s = 0;
-                    for (;; s += 32) {
-                        unsigned m = rows_above(s, false);
-                        const int c = __popc(m);
-                        if (k < c) {
-                            for (; k > 0; k--) m &= m - 1;
-                            s += __ffs(m) - 1;
-                            break;
-                        }
-                        k -= c;
+                    unsigned m = rows_above(seen_s, false);
+                    for (int c = __popc(m); seen_k + c <= k; c = __popc(m)) {
+                        seen_k += c;
+                        seen_s += 32;
+                        m = rows_above(seen_s, false);
                     }
+                    for (int i = seen_k; i < k; i++) m &= m - 1;
+                    s = seen_s + __ffs(m) - 1;
                 } else {
                     ticket_item(a, t, s, h, pair);
                 }
@@ -625,6 +630,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                 }
                 uint64_t *full = &bars[bVFull + stg];
+                if constexpr (MODE == kWindow) {
+                    const int t0 = j * kKeys;                       // (a sink tile's first token)
+                    if (j < it.nsink && t0 + kKeys > a.sinks) {
+                        // A last sink tile that is not full: the tokens behind the sinks, which no row sees, may hold
+                        // anything (P is 0 there, but 0 x NaN is not).  The sinks' values come in boxes that hold
+                        // nothing else, and the first of them once more in the place of every other.
+                        if (lane == 0) mbar_arrive_expect_tx(full, kKeys * 128u * NP);
+                        __syncwarp();
+                        uint8_t *vs = sm + L::v + (uint32_t)stg * NP * kPanelBytes;
+#pragma unroll 1
+                        for (int u = lane; u < kKeys / a.sink_unit; u += 32) {
+                            const int tok = t0 + u * a.sink_unit < a.sinks ? t0 + u * a.sink_unit : 0;
+                            int phys = row[tok >> a.log2_block];
+                            if (phys < 0 || phys >= a.num_blocks) {
+                                latch(st, kFlagBadBlock, phys);
+                                phys = 0;
+                            }
+                            for (int p = 0; p < NP; p++)
+                                tma_load_4d(vs + p * kPanelBytes + (uint32_t)(u * a.sink_unit) * 128u, &tms, 64 * p,
+                                            tok & (B - 1), g, phys, full, pol_kv);
+                        }
+                        cb = nxt;
+                        continue;
+                    }
+                }
                 if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)nb * (uint32_t)B * 128u * NP);
                 __syncwarp();
                 uint8_t *dst = sm + L::v + (uint32_t)stg * NP * kPanelBytes;
@@ -1127,10 +1157,11 @@ cudaError_t launch_prefill(const PrefillArgs &a, const void *query, const void *
     const cudaError_t sized_rc = allow_smem(kern, L::alloc, sized);
     if (sized_rc != cudaSuccess) return sized_rc;
     const int B = 1 << a.log2_block;
-    CUtensorMap tmq, tmk, tmv;
+    CUtensorMap tmq, tmk, tmv, tms;
     std::memset(&tmq, 0, sizeof tmq);
     std::memset(&tmk, 0, sizeof tmk);
     std::memset(&tmv, 0, sizeof tmv);
+    std::memset(&tms, 0, sizeof tms);
     // query [T][H][D]: box of 64 elements x 1 head x 128 tokens, or (kShared) x a kv head's heads x tile_seqs
     const cuuint64_t qdims[3] = {(cuuint64_t)D, (cuuint64_t)a.num_heads, (cuuint64_t)a.num_tokens};
     const cuuint64_t qstr[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.num_heads * D * 2};
@@ -1143,10 +1174,14 @@ cudaError_t launch_prefill(const PrefillArgs &a, const void *query, const void *
     if (!encode_tiled16(&tmq, query, 3, qdims, qstr, qbox, kBf16) || !encode_tiled16(&tmk, kc, 4, cdims, cstr, cbox, kBf16) ||
         !encode_tiled16(&tmv, vc, 4, cdims, cstr, cbox, kBf16))
         return cudaErrorInvalidValue;
+    if constexpr (MODE == kWindow) {                     // the values of sinks alone
+        const cuuint32_t sbox[4] = {64u, (cuuint32_t)a.sink_unit, 1u, 1u};
+        if (!encode_tiled16(&tms, vc, 4, cdims, cstr, sbox, kBf16)) return cudaErrorInvalidValue;
+    }
     // persistent CTAs, one per SM (each holds all of its SM's TMEM), at most one per item
     const int sms = MODE == kShared && a.max_ctas < sm_count() ? a.max_ctas : sm_count();
     const int ctas = a.num_items < sms ? a.num_items : sms;
-    return launch(kern, dim3((unsigned)(ctas > 0 ? ctas : 1)), dim3(kThreads), L::alloc, stream, a, tmq, tmk, tmv);
+    return launch(kern, dim3((unsigned)(ctas > 0 ? ctas : 1)), dim3(kThreads), L::alloc, stream, a, tmq, tmk, tmv, tms);
 }
 
 

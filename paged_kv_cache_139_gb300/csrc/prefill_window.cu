@@ -23,6 +23,7 @@ extern "C" pkv_status paged_attention_prefill_window(void *out, const void *quer
     if (rc != PKV_OK || a.num_items == 0) return rc;
     a.window = window;
     a.sinks = num_sinks;
+    a.sink_unit = num_sinks > 0 && (num_sinks & -num_sinks) < block_size ? num_sinks & -num_sinks : block_size;
     const cudaError_t e = launch_prefill<kWindow>(head_dim, dtype == PKV_BF16, a, query, key_cache, value_cache,
                                                   num_kv_heads, stream);
     if (e != cudaSuccess) return fail(PKV_ECUDA, "%s: launch: %s", what, cudaGetErrorString(e));

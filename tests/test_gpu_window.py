@@ -237,6 +237,35 @@ def test_prompt_shapes(cuda_device, H, Hkv, B, dtype, d):
         check(prompt(c, 150, 20, workspace=ws), *want, d, 700, dtype, prompt_bits(dtype))
 
 
+@pytest.mark.parametrize("sinks", [1, 4, 15, 16, 17, 33, 64, 100, 127, 129, 150])
+@pytest.mark.parametrize("H,Hkv,B,dtype,d", [(2, 2, 16, "f16", 128), (4, 2, 4, "bf16", 64), (1, 1, 128, "f16", 64), (2, 1, 64, "bf16", 128)])
+def test_what_lies_behind_the_sinks_has_no_effect(cuda_device, sinks, H, Hkv, B, dtype, d):
+    """NaN from the last sink up to well before the first row's window, in the sinks' own blocks too."""
+    c = SpanCase(cuda_device, [1000, 1130], H, Hkv, d, B, dtype, new=[300, 90], seed=sinks)
+    window = 200
+    for s in range(2):
+        low = int(c.ctx[s]) - int(c.new[s]) - window + 1
+        for t in range(sinks, low - 127):
+            for x in c.pools:
+                x[c.tables[s, t // B], :, t % B] = math.nan
+    c = blocks_unseen(c, window, sinks).upload()
+    check(prompt(c, window, sinks), *c.expect(window, sinks), d, 1130, dtype, prompt_bits(dtype))
+
+
+@pytest.mark.parametrize("S", [1, 33, 70])
+def test_prompts_of_many_lengths(cuda_device, S):
+    """More sequences than a warp looks at in one go, some without new tokens."""
+    rng = np.random.default_rng(S)
+    new = rng.integers(0, 300, S) * (rng.random(S) < 0.8)
+    new[0] = max(1, new[0])
+    ctx = new + rng.integers(0, 200, S)
+    for H, Hkv in ((1, 1), (2, 1)):
+        c = SpanCase(cuda_device, np.maximum(ctx, 1), H, Hkv, 64, 16, "f16", new=new, seed=S).upload()
+        want = c.expect(90, 20)
+        check(prompt(c, 90, 20), *want, 64, 500, "f16", 11)
+        check(prompt(c, 90, 20, max_query_len=299, workspace=pkv.make_workspace(cuda_device, 256)), *want, 64, 500, "f16", 11)
+
+
 def test_prompt_rows_are_single_tokens(cuda_device):
     """Every row of a prompt is the decode of its own context."""
     c = SpanCase(cuda_device, [300], 4, 2, 128, 16, "bf16", new=[300], seed=8).upload()

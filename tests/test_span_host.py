@@ -37,7 +37,7 @@ COMMON = [dict(d=96), dict(d=256), dict(d=0), dict(B=12), dict(B=2), dict(B=256)
 
 
 @pytest.mark.parametrize("over", COMMON + [dict(window=0), dict(window=-1), dict(sinks=-1), dict(mcl=65), dict(mcl=-1),
-                                           dict(mb=(1 << 26) + 1), dict(H=65536, Hkv=1)])
+                                           dict(mb=(1 << 26) + 1), dict(H=65536, Hkv=1), dict(S=40000, H=32768, Hkv=1)])
 def test_window_refusals(over):
     assert call("paged_attention_decode_window", WINDOW, over) == 1
     assert message().startswith("paged_attention_decode_window")
