@@ -85,14 +85,15 @@ template <int D, int NT, int W> struct SpanConf {
     static constexpr int CTAS = (NT == 1 ? 12 : 8) / W;
     static constexpr int COLS = 8 * NT;
     static constexpr int LD = D + 4;                                   // fp32 row of an output: 8 columns apart on 8 banks
-    static constexpr uint32_t ring = 0;
-    static constexpr uint32_t wml = W * R * STAGE_BYTES;               // the warps' m, l [W][2][COLS]
+    static constexpr uint32_t ring_bytes = R * STAGE_BYTES;            // a warp's, from offset 0 on
+    static constexpr uint32_t wml = W * ring_bytes;                    // the warps' m, l [W][2][COLS]
     static constexpr uint32_t bars = wml + W * 2 * COLS * 4;
-    static constexpr uint32_t ml = bars + W * R * 8;                   // the CTA's m, l [COLS] and o [COLS][LD], for its
-    static constexpr uint32_t comb = ml + 2 * COLS * 4;                // cluster (CTAs of four warps)
-    static constexpr uint32_t bytes = W == 4 ? comb + COLS * LD * 4 : ml;
-    static_assert(COLS * LD * 4 <= R * STAGE_BYTES, "a warp's outputs fit its ring");
-    static_assert(comb % 16 == 0 && bars % 8 == 0, "alignment");
+    static constexpr uint32_t got = bars + W * R * 8;                  // parts from the cluster's CTAs (CTAs of four warps):
+    static constexpr int GOT = COLS * D / 4 + kMaxCluster;             // units of four elements, o [GOT][4] and m, l [GOT][2]
+    static constexpr uint32_t got_ml = got + GOT * 16;
+    static constexpr uint32_t bytes = W == 4 ? got_ml + GOT * 8 : got;
+    static_assert(COLS * LD * 4 <= ring_bytes, "a warp's outputs fit its ring");
+    static_assert(bars % 8 == 0 && got % 16 == 0 && got_ml % 8 == 0, "alignment");
 };
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
@@ -139,16 +140,12 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster4(uint32_t addr, const float4 &v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
 }
-__device__ __forceinline__ float ld_cluster1(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster2(uint32_t addr, float x, float y) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 
 // A running (m, l, o) of four output elements, and another part joined to it.
@@ -181,7 +178,7 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t nrank = kClusters ? cluster_size() : 1u, rank = kClusters ? cluster_rank() : 0u;
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::bars) + warp * R;      // this warp's own
-    unsigned char *ring = sm + C::ring + warp * R * C::STAGE_BYTES;
+    unsigned char *ring = sm + warp * C::ring_bytes;
     if (lane == 0) {
         for (int i = 0; i < R; i++) mbar_init(&full[i], 1);
         fence_mbar_init();
@@ -191,6 +188,7 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
         }
     }
     __syncwarp();
+    if (kClusters && nrank > 1) cluster_arrive();        // awaited before another CTA's memory is written: it has started
     // The suffix half starts while the prefix half runs.  That one began after every grid before it
     // had finished (it waits for them before it lets this one start), so queries, lengths, tables and
     // caches are in place; only its partial results are not, and the wait for those comes below.
@@ -495,7 +493,7 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
 #pragma unroll
         for (int w = 0; w < W; w++)
             r.add(all_ml[w * 2 * COLS + c], all_ml[w * 2 * COLS + COLS + c],
-                  *reinterpret_cast<const float4 *>(sm + C::ring + w * R * C::STAGE_BYTES + (c * LD + e) * 4));
+                  *reinterpret_cast<const float4 *>(sm + w * C::ring_bytes + (c * LD + e) * 4));
         return r;
     };
     constexpr int UPR = D / 4;                          // units of four elements per row
@@ -524,7 +522,6 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
         if constexpr (MODE == kSpanOwn)
             if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) pdl_wait();
     } else {
-        if constexpr (MODE == kSpanSuffix) pdl_wait();              // the prefix half's results
         const int np = MODE == kSpanSuffix ? (prefix + a.parts.part - 1) / a.parts.part : 0;
         auto join_prefix = [&](int c, int e, Joined &r) {
             const size_t at = row_of(c) * a.parts.slots;
@@ -544,6 +541,7 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
             }
         };
         if (!kClusters || nrank == 1) {
+            if constexpr (MODE == kSpanSuffix) pdl_wait();          // the prefix half's results
             for (int u = tid; u < cols * UPR; u += C::THREADS) {
                 const int c = u / UPR, e = u % UPR * 4;
                 Joined r = join_warps(c, e);
@@ -551,46 +549,44 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
                 store_out(c, e, r);
             }
         } else if constexpr (kClusters) {
-            // the CTA's part into its own shared memory, then every CTA joins its share of the
-            // elements over all CTAs of the cluster
-            float *comb = reinterpret_cast<float *>(sm + C::comb), *cml = reinterpret_cast<float *>(sm + C::ml);
+            // CTA k of the cluster joins the units k, k + nrank, ...: every CTA writes its part of them into
+            // that CTA's shared memory, so that after one barrier each reads its own
+            const int share = (cols * UPR + (int)nrank - 1) / (int)nrank;
+            __syncwarp();
+            cluster_wait();
+            const uint32_t got = smem_u32(sm + C::got), got_ml = smem_u32(sm + C::got_ml);
             for (int u = tid; u < cols * UPR; u += C::THREADS) {
-                const int c = u / UPR, e = u % UPR * 4;
-                const Joined r = join_warps(c, e);
-                *reinterpret_cast<float4 *>(comb + c * LD + e) = r.o;
-                if (e == 0) {
-                    cml[c] = r.m;
-                    cml[COLS + c] = r.l;
-                }
+                const Joined r = join_warps(u / UPR, u % UPR * 4);
+                const uint32_t to = (uint32_t)u % nrank, at = rank * (uint32_t)share + (uint32_t)u / nrank;
+                st_cluster4(map_rank(got + at * 16, to), r.o);
+                st_cluster2(map_rank(got_ml + at * 8, to), r.m, r.l);
             }
             __syncwarp();
             cluster_arrive();
+            if constexpr (MODE == kSpanSuffix) pdl_wait();
             cluster_wait();
-            const uint32_t comb_s = smem_u32(comb), cml_s = smem_u32(cml);
-            for (int u = tid * nrank + rank; u < cols * UPR; u += C::THREADS * nrank) {
+            const float4 *go = reinterpret_cast<const float4 *>(sm + C::got);
+            const float2 *gm = reinterpret_cast<const float2 *>(sm + C::got_ml);
+            for (int i = tid, u; (u = i * (int)nrank + (int)rank) < cols * UPR; i += C::THREADS) {
                 const int c = u / UPR, e = u % UPR * 4;
-                Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-                for (uint32_t k0 = 0; k0 < nrank; k0 += 4) {
-                    float pm[4], pl2[4];
-                    float4 po[4];
-#pragma unroll
-                    for (uint32_t k = 0; k < 4; k++) {
-                        const bool there = k0 + k < nrank;
-                        const uint32_t from_rank = there ? k0 + k : rank;
-                        pm[k] = there ? ld_cluster1(map_rank(cml_s + c * 4, from_rank)) : -INFINITY;
-                        pl2[k] = ld_cluster1(map_rank(cml_s + (COLS + c) * 4, from_rank));
-                        po[k] = ld_cluster4(map_rank(comb_s + (c * LD + e) * 4, from_rank));
-                    }
-#pragma unroll
-                    for (uint32_t k = 0; k < 4; k++)
-                        if (k0 + k < nrank) r.add(pm[k], pl2[k], po[k]);
+                float M = -INFINITY;
+                for (uint32_t k = 0; k < nrank; k++) M = fmaxf(M, gm[k * share + i].x);
+                const float z = M == -INFINITY ? 0.f : M;
+                Joined r{M, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+                for (uint32_t k = 0; k < nrank; k++) {
+                    const float2 ml = gm[k * share + i];
+                    const float4 v = go[k * share + i];
+                    const float w = ex2(ml.x - z);
+                    r.l = fmaf(ml.y, w, r.l);
+                    r.o.x = fmaf(v.x, w, r.o.x);
+                    r.o.y = fmaf(v.y, w, r.o.y);
+                    r.o.z = fmaf(v.z, w, r.o.z);
+                    r.o.w = fmaf(v.w, w, r.o.w);
                 }
                 if constexpr (MODE == kSpanSuffix) join_prefix(c, e, r);
                 store_out(c, e, r);
             }
-            __syncwarp();
-            cluster_arrive();                            // no CTA leaves while others read its memory
-            cluster_wait();
         }
     }
 }
@@ -669,8 +665,7 @@ struct SpanMaps {
 };
 
 template <int D, int NT, int W, typename T, int MODE>
-cudaError_t launch_span_kernel(const SpanArgs &a, const SpanMaps &maps, long long items, int parts, int cluster,
-                               cudaStream_t st) {
+cudaError_t launch_span_kernel(const SpanArgs &a, const SpanMaps &maps, long long items, int parts, int cluster, cudaStream_t st) {
     auto kern = span_attention_kernel<D, NT, W, T, MODE>;
     using C = SpanConf<D, NT, W>;
     static std::atomic<unsigned long long> sized{0}, wide{0};
