@@ -22,12 +22,18 @@
 //            (their scores are masked, and its values are as finite as the others);
 //            in a sink tile that is not full, the sinks' values alone are.
 //            (Skipping such a tile's other products and chunks, or zeroing its values
-//            in the softmax warps, made every tile's code slower: 290 to 304 us against
-//            270 for 8 prompts of 512 to 4,096 tokens with a window of 1,024.)
+//            in the softmax warps, made every tile's code slower: 8 prompts of 512 to
+//            4,096 tokens, 32 heads of fp16, window 1,024, took 290 to 314 us against 278.)
+//            Bound by the tensor core as the causal form: those prompts run at 870
+//            TFLOP/s, chunks of 4,096 tokens with a window of 4,096 (32/8 heads, bf16)
+//            at 990.  In steady state a key tile of 256 rows takes 1.63 us in fp16 (1.57
+//            at the issue rate of its 32 products) and 2.4 us in bf16 (48 products); an
+//            item's start and end take 4 us, which weighs in short windows.
 //   kShared  rows are (sequence, head) pairs of one group and kv head, 128 /
 //            (heads per kv head) sequences to a tile; all see the same keys, a
 //            partition of the group's prefix.  Their maximum, sum and unscaled
-//            output go to memory in fp32 (PrefixParts).
+//            output go to memory in fp32 (PrefixParts).  Groups of up to 128 rows
+//            run at about the rate of memory (1.2 us a key tile of 64 KB and SM).
 //
 // How (sm_103a):
 //   * Work items: (sequence, query head, 256 new tokens) = two query tiles of
@@ -643,10 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int u = lane; u < kKeys / a.sink_unit; u += 32) {
                             const int tok = t0 + u * a.sink_unit < a.sinks ? t0 + u * a.sink_unit : 0;
                             int phys = row[tok >> a.log2_block];
-                            if (phys < 0 || phys >= a.num_blocks) {
-                                latch(st, kFlagBadBlock, phys);
-                                phys = 0;
-                            }
+                            if ((unsigned)phys >= (unsigned)a.num_blocks) phys = 0;      // (latched with the keys)
                             for (int p = 0; p < NP; p++)
                                 tma_load_4d(vs + p * kPanelBytes + (uint32_t)(u * a.sink_unit) * 128u, &tms, 64 * p,
                                             tok & (B - 1), g, phys, full, pol_kv);

@@ -281,3 +281,43 @@ def test_a_prepared_step_with_groups(world, monkeypatch):  # noqa: F811
     assert ((4096,), STREAM) in world.made               # the step's own memory, made on its stream
     with pytest.raises(ValueError):
         step.write_attend()
+
+
+@pytest.fixture
+def scratch(monkeypatch):
+    """The binding's scratch with streams, captures and devices stood in for: state["capturing"], state["stream"]."""
+    state = dict(capturing=False, stream=5)
+    make = torch.empty
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(pkv, "_raw_stream", lambda s, index: s.cuda_stream if s else state["stream"])
+    monkeypatch.setattr(pkv, "_capturing", lambda s: state["capturing"])
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: state["capturing"], raising=False)
+    monkeypatch.setattr(pkv, "_on", lambda s: __import__("contextlib").nullcontext())
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: make(*a, **kw))
+    monkeypatch.setattr(pkv, "_scratches", __import__("threading").local())
+    return state
+
+
+def test_scratch_is_kept_per_stream_and_thread(scratch):
+    a = pkv._scratch(0, 100, None)
+    assert pkv._scratch(0, 50, None) is a and pkv._scratch(0, a.numel(), None) is a
+    scratch["stream"] = 6
+    b = pkv._scratch(0, 100, None)
+    assert b is not a and pkv._scratch(0, 100, STREAM) is not b
+    big = pkv._scratch(0, b.numel() + 1, None)
+    assert big.numel() > b.numel() and pkv._scratch(0, 100, None) is big
+    import threading
+    got = []
+    t = threading.Thread(target=lambda: got.append(pkv._scratch(0, 100, None)))
+    t.start()
+    t.join()
+    assert got[0] is not big
+
+
+def test_captured_calls_take_scratch_of_their_own(scratch):
+    a = pkv._scratch(0, 100, None)
+    scratch["capturing"] = True
+    b, c = pkv._scratch(0, 100, None), pkv._scratch(0, 100, None)
+    assert a is not b and b is not c
+    scratch["capturing"] = False
+    assert pkv._scratch(0, 100, None) is a
