@@ -23,8 +23,8 @@
 //            in a sink tile that is not full, the sinks' values alone are.
 //            (Skipping such a tile's other products and chunks, or zeroing its values
 //            in the softmax warps, made every tile's code slower: 8 prompts of 512 to
-//            4,096 tokens, 32 heads of fp16, window 1,024, took 290 to 314 us against 278.)
-//            Bound by the tensor core as the causal form: those prompts run at 870
+//            4,096 tokens, 32 heads of fp16, window 1,024, took 290 to 314 us against 272.)
+//            Bound by the tensor core as the causal form: those prompts run at 890
 //            TFLOP/s, chunks of 4,096 tokens with a window of 4,096 (32/8 heads, bf16)
 //            at 990.  In steady state a key tile of 256 rows takes 1.63 us in fp16 (1.57
 //            at the issue rate of its 32 products) and 2.4 us in bf16 (48 products); an
@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (MODE == kWindow) {
                             const uint32_t vis = bits_below(t + 1) &
                                                  (~bits_below(win_lo - 32 * c) | bits_below(snk - 32 * c));
-                            if (!full && __any_sync(0xffffffffu, vis != ~0u)) {
+                            if (!full) {                       // (asking each chunk whether it needs it: 283 against 272 us)
 #pragma unroll
                                 for (int i = 0; i < 32; i++) sr[c][i] = (vis >> i) & 1u ? sr[c][i] : 0xff800000u;
                                 tc::tmem_st32(tS + 32 * c, sr[c]);
@@ -932,24 +932,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int g = gbase + j;
                     ok = wait_warp(&bars[bVFull + (g & 1)], (g >> 1) & 1, kWaitLimitCycles);
                     if (!ok) break;
-                    const int first = it.ctx - kbase;
                     uint8_t *vs = sm + L::v + (uint32_t)(g & 1) * NP * kPanelBytes;
-                    const int nvec = (kKeys - first) * 8;    // 16-byte vectors per panel
-                    for (int i = r; i < nvec * NP; i += kSoftmaxWarps * 32) {
-                        const int p = i / nvec, rem = i % nvec;
-                        *reinterpret_cast<uint4 *>(vs + p * kPanelBytes + (first + rem / 8) * 128 + (rem % 8) * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                    }
                     if constexpr (MODE == kWindow) {
-                        // and so may a block that stands in the place of one that no row sees, when it is
-                        // the context's last: those places
+                        // and so may a block that stands in the place of one that no row sees, when it is the
+                        // context's last: every place without a visible token
                         const int low = max(0, it.pos00 - a.window + 1);
-                        for (int i = r; i < kKeys * 8 * NP; i += kSoftmaxWarps * 32) {
-                            const int p = i / (kKeys * 8), rem = i % (kKeys * 8), row = rem / 8;
-                            const int tok = kbase + (row & ~(B - 1));
-                            if (tok >= a.sinks && tok + B <= low)
-                                *reinterpret_cast<uint4 *>(vs + p * kPanelBytes + row * 128 + (rem % 8) * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+                        for (int i = r; i < kKeys * 8; i += kSoftmaxWarps * 32) {
+                            const int row = i / 8, tok = kbase + row;
+                            if (tok >= it.ctx || (tok >= a.sinks && tok < low))
+                                for (int p = 0; p < NP; p++)
+                                    *reinterpret_cast<uint4 *>(vs + p * kPanelBytes + row * 128 + (i % 8) * 16) =
+                                        make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    } else {
+                        const int first = it.ctx - kbase;
+                        const int nvec = (kKeys - first) * 8;    // 16-byte vectors per panel
+                        for (int i = r; i < nvec * NP; i += kSoftmaxWarps * 32) {
+                            const int p = i / nvec, rem = i % nvec;
+                            *reinterpret_cast<uint4 *>(vs + p * kPanelBytes + (first + rem / 8) * 128 + (rem % 8) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                     fence_proxy_async_smem();                // generic writes -> tensor-core reads
