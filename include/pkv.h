@@ -465,7 +465,7 @@ pkv_status paged_attention_prefill(void *out_dev, const void *query_dev,
  * Table entries of blocks that hold no visible token are not read: such blocks
  * may be freed and their entries hold anything.  What invisible tokens of other
  * blocks hold has no effect (NaN included).  Probabilities enter the product
- * with 22 bits for fp16 and 16 for bf16.
+ * with 22 bits for fp16 and 16 for bf16; an infinite value may give NaN.
  *   window     at least 1;  num_sinks  at least 0
  * Needs no workspace, keeps nothing between calls and does not depend on what
  * else runs: calls may overlap on the GPU.  The result of a sequence does not

@@ -733,7 +733,8 @@ cudaError_t launch_span(int D, int NT, bool bf16, const SpanArgs &a, const SpanM
 // its stream): 512 items of 512 tokens 25.1 against 30.6 us, of 2,048 tokens 83 against
 // 97, 8,192 of 64 tokens 59 against 74; but 2,048 of 1,024 tokens 163 against 157.
 // Clusters split items while they leave SMs without one, or with one and long
-// streams: 8 items of 4,096 tokens 27, 15.8, 10.8, 9.7 us for 2, 4, 8, 16 CTAs each;
+// streams: 8 items of 4,096 tokens 27, 15.8, 10.8, 9.7 us for 2, 4, 8, 16 CTAs each
+// (8.6 for 16 since their parts are written and not read across the cluster);
 // 128 of 512 tokens 10.1 us unsplit, 10.9 in two.  (head_dim 128, bf16.)
 Spread choose_spread(long long items, long long max_tokens, int NT) {
     const long long sms = sm_count(), four = sms * (NT == 1 ? 3 : 2);      // CTAs of four warps that fit at once

@@ -455,12 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     h = (t - level_t) % level_heads * (a.head_pairs ? 2 : 1);
                     pair = level;
                     unsigned m = rows_above(seen_s, false);
-                    for (int c = __popc(m); seen_k + c <= k; c = __popc(m)) {
+                    for (int c = __popc(m); seen_k + c <= k && seen_s + 32 < a.num_seqs; c = __popc(m)) {
                         seen_k += c;
                         seen_s += 32;
                         m = rows_above(seen_s, false);
                     }
                     for (int i = seen_k; i < k; i++) m &= m - 1;
+                    if (!m) break;                                 // (lengths that changed while the kernel ran)
                     s = seen_s + __ffs(m) - 1;
                 } else {
                     ticket_item(a, t, s, h, pair);
@@ -1179,7 +1180,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, const void *query, const void *
     if (!encode_tiled16(&tmq, query, 3, qdims, qstr, qbox, kBf16) || !encode_tiled16(&tmk, kc, 4, cdims, cstr, cbox, kBf16) ||
         !encode_tiled16(&tmv, vc, 4, cdims, cstr, cbox, kBf16))
         return cudaErrorInvalidValue;
-    if constexpr (MODE == kWindow) {                     // the values of sinks alone
+    if (MODE == kWindow && a.sinks > 0) {                // the values of sinks alone
         const cuuint32_t sbox[4] = {64u, (cuuint32_t)a.sink_unit, 1u, 1u};
         if (!encode_tiled16(&tms, vc, 4, cdims, cstr, sbox, kBf16)) return cudaErrorInvalidValue;
     }
