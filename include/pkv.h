@@ -535,8 +535,8 @@ pkv_status paged_attention_prefill_window(void *out_dev, const void *query_dev,
  * Probabilities over a prefix enter the product with 16 bits for bf16 and 22 for
  * fp16, but 11 where groups of more than 16 query rows per kv head (sequences x
  * heads) have long prefixes, which then go through the prompt phase's kernel (three
- * launches instead of two).  A NaN among a group's first tokens reaches all of its
- * sequences.  num_seqs <= 65535; up to 128 query heads per kv head; scale > 0;
+ * launches instead of two); an infinite value may give NaN.  A NaN among a group's
+ * first tokens reaches all of its sequences.  num_seqs <= 65535; up to 128 query heads per kv head; scale > 0;
  * contexts up to 2^30 tokens.  Other arguments as for paged_attention_decode.
  * ------------------------------------------------------------------------- */
 pkv_status paged_attention_decode_shared(void *out_dev, const void *query_dev,
