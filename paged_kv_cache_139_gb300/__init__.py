@@ -688,6 +688,9 @@ def _check16(what, out, query, key_cache, value_cache, block_tables, context_len
                     block_tables.data_ptr(), context_lens.data_ptr()), bs[1], ks)
 
 
+_MOST = 2 ** 31 - 1        # a window or number of sinks beyond every context, as the C calls take it
+
+
 _scratches = threading.local()
 
 
@@ -711,6 +714,12 @@ def _scratch(index: int, nbytes: int, stream: Optional[torch.cuda.Stream]) -> to
     return buf
 
 
+def _limits(what: str, window: int, num_sinks: int):
+    if window < 1 or num_sinks < 0:
+        raise ValueError(f"{what}: window {window} (at least 1), {num_sinks} sinks (at least 0)")
+    return min(window, _MOST), min(num_sinks, _MOST)
+
+
 def paged_attention_decode_window(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
                                   value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
                                   window: int, num_sinks: int = 0, scale: Optional[float] = None,
@@ -721,6 +730,8 @@ def paged_attention_decode_window(out: torch.Tensor, query: torch.Tensor, key_ca
     without a visible token are not read.  No workspace; calls may overlap.
     Returns out."""
     what = "paged_attention_decode_window"
+    if window > _MOST or num_sinks > _MOST or window < 1 or num_sinks < 0:
+        window, num_sinks = _limits(what, window, num_sinks)
     S, H, d = query.shape
     index, ptrs, mb, (NB, Hkv, B, _) = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S)
     _call(load().paged_attention_decode_window, what, index, *ptrs, S, mb, max_context_len, B, NB, H, Hkv, d,
@@ -739,6 +750,8 @@ def paged_attention_prefill_window(out: torch.Tensor, query: torch.Tensor, key_c
     from make_workspace (its counter balances the work over the SMs), one call at
     a time; None: each SM takes a fixed share, and calls may overlap.  Returns out."""
     what = "paged_attention_prefill_window"
+    if window > _MOST or num_sinks > _MOST or window < 1 or num_sinks < 0:
+        window, num_sinks = _limits(what, window, num_sinks)
     T, H, d = query.shape
     S = context_lens.shape[0]
     index, ptrs, mb, (NB, Hkv, B, _) = _check16(what, out, query, key_cache, value_cache, block_tables, context_lens, S)

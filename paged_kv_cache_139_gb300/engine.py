@@ -272,7 +272,8 @@ class PagedKVCache:
             raise ValueError("sinks: first tokens that stay visible need a window that hides others")
         if window is not None and (self.fp8 or window < 1 or sinks < 0):
             raise ValueError("window: a 16-bit cache, at least one token, no negative number of sinks")
-        self.window, self.sinks = window, sinks
+        # (more than every context: as much as the calls take)
+        self.window, self.sinks = None if window is None else min(window, 2 ** 31 - 1), min(sinks, 2 ** 31 - 1)
         self.alloc = BlockAllocator(num_blocks, block_size, free_order)
         self.num_blocks, self.num_kv_heads, self.head_dim, self.block_size = shape[0], shape[1], shape[3], shape[2]
         self.max_blocks_per_seq = max_blocks_per_seq

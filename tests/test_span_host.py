@@ -157,6 +157,23 @@ def test_bindings_pass_their_arguments_on(passes):
                                            ws.data_ptr(), 99, 0, 0))]
 
 
+def test_windows_beyond_32_bits_see_everything(passes):
+    """ctypes would take the lower 32 bits."""
+    a, qs = window_args(), torch.zeros(4, dtype=torch.int32)
+    pkv.paged_attention_decode_window(**a, window=(1 << 32) + 5, num_sinks=(1 << 40) + 1)
+    pkv.paged_attention_prefill_window(**a, query_start=qs, window=1 << 31, num_sinks=1 << 32)
+    assert passes.lib.calls[0][1][15:17] == (2 ** 31 - 1,) * 2 and passes.lib.calls[1][1][17:19] == (2 ** 31 - 1,) * 2
+    eng = engine.PagedKVCache(4, 2, 64, 16, torch.float16, "cpu", 4, window=1 << 40, sinks=1 << 33)
+    assert (eng.window, eng.sinks) == (2 ** 31 - 1,) * 2
+    passes.lib.calls.clear()
+    for window, sinks in ((0, 0), (-(1 << 32) + 5, 0), (4, -1), (4, -(1 << 32) + 1)):
+        with pytest.raises(ValueError):
+            pkv.paged_attention_decode_window(**a, window=window, num_sinks=sinks)
+        with pytest.raises(ValueError):
+            pkv.paged_attention_prefill_window(**a, query_start=qs, window=window, num_sinks=sinks)
+    assert passes.lib.calls == []
+
+
 # -- the groups of a step ------------------------------------------------------------------
 
 def groups(rows, ctx, B=4):
