@@ -38,10 +38,10 @@
 //     memory, take the others; a third launch joins.
 //
 // Measured on one GB300: 256 sequences of up to 4,096 tokens, window 1,024, 32 heads:
-// 7.29 TB/s (492 us; the copy rate is 6.79); 48 of up to 32,768, window 4,096, 32/8
-// heads: 6.8 TB/s; 64 of the OPT-13B layer, window 255: 6.0 TB/s (44 us, of which
+// 7.42 TB/s (483 us; the copy rate is 6.79); 48 of up to 32,768, window 4,096, 32/8
+// heads: 6.8 TB/s; 64 of the OPT-13B layer, window 255: 6.2 TB/s (43 us, of which
 // start and tail some 5); one sequence, window 4,096, 32/8 heads: 8.6 us; four small
-// ones 3.4 us.  Shared: 64 x 4 samples 163 us (6.7 TB/s over what is read once).
+// ones 3.4 us.  Shared: 64 x 4 samples 161 us (6.8 TB/s over what is read once).
 // Under ncu the tensor pipe is 13 % and issue slots 23 % busy on the OPT-13B batch.
 // Tried and not kept: CTAs of one warp (8,192 items of 64 tokens 56 against 59 us, but
 // 64 x 2,048 96 against 83); rings twice as deep where each CTA has an SM to itself
@@ -62,6 +62,7 @@ namespace pkv {
 namespace {
 
 constexpr int kTok = 16;                       // tokens of a stage: the rows of one product
+constexpr int kFine = 4;                       // tokens of the small boxes
 constexpr int kMaxCluster = 16;
 
 // What a launch computes: a window; a prefix (to memory); own tokens, joined with the prefix's parts at
@@ -81,6 +82,7 @@ struct SpanArgs {
     int group;                   // query heads per kv head
     int head_tiles, tile_heads;  // a kv head's query heads in tiles of at most 8 NT
     int window, sinks;
+    int fine;                    // stages with invisible tokens come in boxes of four tokens, as far as they are seen
     float scale_log2;
     PrefixParts parts;
 };
@@ -179,9 +181,11 @@ struct Joined {
 template <int D, int NT, int W, typename T, int MODE>
 __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W>::CTAS)
     span_attention_kernel(const SpanArgs a, const __grid_constant__ CUtensorMap tmk,
-                          const __grid_constant__ CUtensorMap tmv) {
+                          const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmk4,
+                          const __grid_constant__ CUtensorMap tmv4) {
     using C = SpanConf<D, NT, W>;
     constexpr bool kClusters = W == 4 && (MODE == kSpanWindow || MODE == kSpanSuffix);
+    constexpr bool kFineBoxes = D == 128 && MODE != kSpanPrefix;
     constexpr int R = C::R, HALVES = C::HALVES, COLS = C::COLS, LD = C::LD;
     // the 128-byte swizzle repeats every 1024 bytes: the ring starts on such a boundary
     extern __shared__ __align__(1024) unsigned char smem_span[];
@@ -196,6 +200,10 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
         if (warp == 0) {
             prefetch_tensor_map(&tmk);
             prefetch_tensor_map(&tmv);
+            if (kFineBoxes && a.fine) {
+                prefetch_tensor_map(&tmk4);
+                prefetch_tensor_map(&tmv4);
+            }
         }
     }
     __syncwarp();
@@ -292,12 +300,13 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
     const int rows_per_copy = B < kTok ? B : kTok;
     const int per_load = 32 >> lcps;                                 // stages whose table entries one load brings
     const int32_t *table = a.tables + (size_t)s * a.max_blocks;
-    auto seen_block = [&](int t) { return t < ctx && (t < first || t + rows_per_copy > low); };
+    auto seen_any = [&](int t, int n) { return t < ctx && (t < first || t + n > low); };       // of tokens t .. t + n - 1
+    auto seen_all = [&](int t, int n) { return t + n <= ctx && (t >= low || t + n <= first); };
     auto load_entries = [&](int base) -> int {
         const int i = base + (lane >> lcps);
         if (i >= mine) return -1;
         const int t = token0(i) + (lane & ((1 << lcps) - 1)) * rows_per_copy;
-        return seen_block(t) ? __ldcg(table + (t >> a.log2_block)) : -1;
+        return seen_any(t, rows_per_copy) ? __ldcg(table + (t >> a.log2_block)) : -1;
     };
     const uint64_t policy = policy_evict_first();
     int ent = load_entries(0), base = 0;
@@ -310,9 +319,11 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
             ent = ent_next;
             ent_next = load_entries(base + per_load);
         }
-        const int p = __shfl_sync(kFull, ent, (((i - base) << lcps) + cj) & 31);
-        const int t0 = token0(i), t = t0 + cj * rows_per_copy;
-        bool go = cj < (1 << lcps) && seen_block(t);
+        const int t0 = token0(i);
+        const bool part = kFineBoxes && a.fine && !seen_all(t0, kTok);        // uniform over the warp
+        const int rows = part ? kFine : rows_per_copy, off = cj * rows, t = t0 + off;
+        const int p = __shfl_sync(kFull, ent, (((i - base) << lcps) + (lcps ? off >> a.log2_block : 0)) & 31);
+        bool go = off < kTok && seen_any(t, rows);
         const bool bad = go && (p < 0 || p >= a.num_blocks);
         const unsigned badm = __ballot_sync(kFull, bad);
         if (badm) {
@@ -321,12 +332,12 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
         }
         const unsigned n = __popc(__ballot_sync(kFull, go));
         const int slot = i % R;
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], n * (uint32_t)rows_per_copy * 128u);
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], n * (uint32_t)rows * 128u);
         __syncwarp();
         if (go) {
-            unsigned char *dst = ring + slot * C::STAGE_BYTES + ct * C::TENSOR_BYTES + ch * C::HALF_BYTES +
-                                 cj * rows_per_copy * 128;
-            tma_load_4d(dst, ct ? (const void *)&tmv : (const void *)&tmk, ch * 64, t & (B - 1), g, p, &full[slot], policy);
+            unsigned char *dst = ring + slot * C::STAGE_BYTES + ct * C::TENSOR_BYTES + ch * C::HALF_BYTES + off * 128;
+            const void *map = part ? (ct ? &tmv4 : &tmk4) : (ct ? &tmv : &tmk);
+            tma_load_4d(dst, map, ch * 64, t & (B - 1), g, p, &full[slot], policy);
         }
     };
     for (int i = 0; i < R && i < mine; i++) issue(i);
@@ -395,7 +406,7 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
 #pragma unroll
             for (int e = 0; e < 4; e++) x[n][e] = (x[n][e] + y[n][e]) * a.scale_log2;
         // tokens of the stage that the rows see (the same for every row)
-        const bool whole = t0 + kTok <= ctx && (t0 >= low || t0 + kTok <= first);
+        const bool whole = seen_all(t0, kTok);
         uint32_t vm0 = ~0u, vm1 = ~0u;                  // value fragments: tokens 2 cq, 2 cq + 1, and those + 8
         if (!whole) {
             auto seen = [&](int t) { return t0 + t < ctx && (t0 + t >= low || t0 + t < first); };
@@ -663,16 +674,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 }
 
 // The cache [NB][Hkv][B][D] as a 4-D tensor (innermost first); a box is 64
-// elements of d by min(B, 16) tokens of one (block, kv head).
-bool encode_span_map(CUtensorMap *map, const void *base, int num_blocks, int Hkv, int B, int D, bool bf16) {
+// elements of d by min(B, tokens) tokens of one (block, kv head).
+bool encode_span_map(CUtensorMap *map, const void *base, int num_blocks, int Hkv, int B, int D, bool bf16, int tokens) {
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)B, (cuuint64_t)Hkv, (cuuint64_t)(num_blocks > 0 ? num_blocks : 1)};
     const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)B * D * 2, (cuuint64_t)Hkv * B * D * 2};
-    const cuuint32_t box[4] = {64u, (cuuint32_t)(B < kTok ? B : kTok), 1u, 1u};
+    const cuuint32_t box[4] = {64u, (cuuint32_t)(B < tokens ? B : tokens), 1u, 1u};
     return encode_tiled16(map, base, 4, dims, strides, box, bf16);
 }
 
 struct SpanMaps {
-    CUtensorMap k, v;
+    CUtensorMap k, v, k4, v4;
 };
 
 template <int D, int NT, int W, typename T, int MODE>
@@ -693,7 +704,7 @@ cudaError_t launch_span_kernel(const SpanArgs &a, const SpanMaps &maps, long lon
         }
     }
     return launch_clusters(kern, dim3((unsigned)(items * cluster), (unsigned)parts), dim3(C::THREADS), (unsigned)cluster,
-                           C::bytes, st, a, maps.k, maps.v);
+                           C::bytes, st, a, maps.k, maps.v, maps.k4, maps.v4);
 }
 
 // How a launch is spread: warps per CTA, CTAs per cluster.
@@ -806,8 +817,18 @@ pkv_status open_span(const SpanCall &c, SpanArgs &a, SpanMaps &maps) {
     if (!a.st) return fail(PKV_ECUDA, "%s: no device status word", c.what);
     const bool bf16 = c.dtype == PKV_BF16;
     std::memset(&maps, 0, sizeof maps);
-    if (!encode_span_map(&maps.k, c.key_cache, c.num_blocks, c.num_kv_heads, c.block_size, c.head_dim, bf16) ||
-        !encode_span_map(&maps.v, c.value_cache, c.num_blocks, c.num_kv_heads, c.block_size, c.head_dim, bf16))
+    auto encode = [&](CUtensorMap *map, const void *cache, int tokens) {
+        return encode_span_map(map, cache, c.num_blocks, c.num_kv_heads, c.block_size, c.head_dim, bf16, tokens);
+    };
+    // Items beyond one wave are bound by memory: at head_dim 128 they read the edges of what is seen in
+    // boxes of four tokens (a window of 64 and 4 sinks are 6 stages, 96 tokens, as a rule; so 72).  8,192
+    // items with windows of 64, 128, 256, 1,024: 58.4, 94.7, 165.4, 492 us without, 53.6, 85.8, 154.7, 483
+    // with.  At head_dim 64 it is slower (window 128: 55.6 against 58.5 us: the small copies count for more);
+    // fewer items wait for round trips, and the two maps more would only cost their callers.
+    const long long items = (long long)c.num_seqs * c.num_kv_heads * a.head_tiles;
+    a.fine = c.head_dim == 128 && c.block_size > kFine && items > 3ll * sm_count();
+    if (!encode(&maps.k, c.key_cache, kTok) || !encode(&maps.v, c.value_cache, kTok) ||
+        (a.fine && (!encode(&maps.k4, c.key_cache, kFine) || !encode(&maps.v4, c.value_cache, kFine))))
         return fail(PKV_ECUDA, "%s: no tensor map of the cache", c.what);
     return PKV_OK;
 }
@@ -1018,6 +1039,7 @@ pkv_status paged_attention_decode_shared(void *out, const void *query, const voi
         const long long rows = (long long)max_group * a.group;
         SpanArgs p = a;
         p.head_tiles = (int)((rows + kFewRows - 1) / kFewRows);
+        p.fine = 0;
         e = launch_span<kSpanPrefix>(head_dim, rows > 8 ? 2 : 1, bf16, p, maps,
                                      (long long)num_groups * num_kv_heads * p.head_tiles, w.max_parts, {4, 1}, stream);
         if (e == cudaSuccess) e = launch_span<kSpanSuffix>(head_dim, NT, bf16, a, maps, items, 1,
