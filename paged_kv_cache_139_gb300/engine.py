@@ -70,33 +70,91 @@ class SharedGroups:
 
     @classmethod
     def find(cls, tables: np.ndarray, context_lens: np.ndarray, block_size: int) -> "SharedGroups":
-        """Groups of the sequences as they stand in a step: one joins the group
-        before it while that saves no less reading (a group's sequences after the
-        first, times the full blocks that all of them begin with) than leaving
-        it out would.  A sequence on its own shares nothing."""
+        """Groups of the sequences as they stand in a step, cut where that
+        saves the most reading: a group's sequences after the first, times the
+        full blocks that all of them begin with, summed over the groups (of equal
+        savings, the fewest groups).  A sequence on its own shares nothing."""
         n = len(context_lens)
+        if n == 0:
+            return cls(np.zeros(1, np.int32), np.zeros(0, np.int32))
+        # what neighbours share; a group shares the least of what its neighbours do
         full = np.asarray(context_lens, np.int64) // block_size
-        start, common, prefix = [0], int(full[0]) if n else 0, np.zeros(n, np.int32)
+        common = np.minimum(full[:-1], full[1:])
+        rows = np.flatnonzero(common > 0)
+        rows = rows[tables[rows, 0] == tables[rows + 1, 0]] if rows.size else rows
+        joined = np.zeros(n - 1, np.int64)
+        if rows.size:
+            most = common[rows]
+            differ = tables[rows, :most.max()] != tables[rows + 1, :most.max()]
+            first = differ.argmax(1)
+            joined[rows] = np.where(differ[np.arange(rows.size), first], np.minimum(first, most), most)
+        cut = joined == 0
+        _cut_runs(joined, cut)
+        start = np.concatenate([[0], np.flatnonzero(cut) + 1, [n]])
+        least = np.full(n, np.iinfo(np.int64).max)
+        least[1:][~cut] = joined[~cut]
+        blocks = np.minimum.reduceat(least, start[:-1])
+        size = np.diff(start)
+        prefix = np.repeat(np.where(size > 1, blocks, 0) * block_size, size)
+        return cls(start.astype(np.int32), prefix.astype(np.int32))
 
-        def close(end):
-            if end - start[-1] > 1:
-                prefix[start[-1]:end] = common * block_size
 
-        for s in range(1, n):
-            m = int(min(common, full[s]))
-            differ = np.flatnonzero(tables[start[-1], :m] != tables[s, :m])
-            joined = int(differ[0]) if differ.size else m
-            size = s - start[-1]
-            if joined > 0 and joined * size >= common * (size - 1):
-                common = joined
-            else:
-                close(s)
-                start.append(s)
-                common = int(full[s])
-        if n:
-            close(n)
-            start.append(n)
-        return cls(np.asarray(start, np.int32), prefix)
+def _cut_runs(joined: np.ndarray, cut: np.ndarray) -> None:
+    """Marks the neighbours (joined[e] blocks shared by sequences e and e + 1) that
+    are to be parted, besides those that share nothing.  Stretches of one value
+    stay whole, as samples of one prompt are."""
+    # runs of equal values, and the stretches of runs between zeros
+    if not joined.size:
+        return
+    begin = np.concatenate([[0], np.flatnonzero(np.diff(joined)) + 1])
+    end = np.concatenate([begin[1:], [joined.size]])
+    live = joined[begin] > 0
+    several = np.flatnonzero(live[1:] & live[:-1]) + 1                      # runs that follow another one directly
+    i = 0
+    while i < several.size:
+        a = b = int(several[i])
+        while i < several.size and several[i] == b:
+            i, b = i + 1, b + 1
+        _cut_stretch(begin[a - 1:b].tolist(), end[a - 1:b].tolist(), joined[begin[a - 1:b]].tolist(), cut)
+
+
+def _cut_stretch(begin, end, value, cut) -> None:
+    """The best cuts of one stretch of runs of neighbours: a part of k neighbours
+    between cuts saves k times its least value.  Moving a cut within a run changes the
+    saving linearly, so that only a run's first and last neighbours are candidates."""
+    unit = end[-1] - begin[0] + 1                # savings in this unit, less one for each cut
+    # A part that may still grow: (its first neighbour, the best of all before it, the cut before it, the part
+    # before that).  `open` holds them by the least value so far, which rises along it; among those of one value an
+    # earlier one stays only while it is better, since a falling value favours the later.
+    open_, fresh = [], [(begin[0], 0, None, None)]
+
+    def best(e):                                 # the best of the neighbours before e, and its last part
+        top, part = max(((p[1], p) for p in fresh), key=lambda x: x[0], default=(-1, None))
+        for v, parts in open_:
+            saved = parts[0][1] + (e - parts[0][0]) * v
+            if saved > top:
+                top, part = saved, parts[0]
+        return top, part
+
+    for s, e, v in zip(begin, end, value):
+        v *= unit
+        top, part = best(s)
+        after = (s + 1, top - 1, s, part)
+        parts, fresh = (fresh, [after]) if e - s == 1 else (fresh + [after], [])
+        while open_ and open_[-1][0] >= v:
+            parts = open_.pop()[1] + parts
+        kept = []
+        for p in reversed(parts):                # at value v, the earlier ones that beat every later one
+            if not kept or p[1] - p[0] * v > kept[-1][1] - kept[-1][0] * v:
+                kept.append(p)
+        open_.append((v, kept[::-1]))
+        if e - s > 1:
+            top, part = best(e - 1)
+            fresh = [(e, top - 1, e - 1, part)]
+    _, part = best(end[-1])
+    while part[2] is not None:
+        cut[part[2]] = True
+        part = part[3]
 
 
 @dataclasses.dataclass
