@@ -765,13 +765,30 @@ def paged_attention_prefill_window(out: torch.Tensor, query: torch.Tensor, key_c
     return out
 
 
-@functools.lru_cache(maxsize=4096)
 def paged_attention_decode_shared_workspace_size(num_seqs: int, num_groups: int, num_heads: int, num_kv_heads: int,
                                                  head_dim: int, max_context_len: int, max_prefix_len: int = 0,
-                                                 max_group_size: int = 0, max_suffix_len: int = 0) -> int:
-    return int(load().paged_attention_decode_shared_workspace_size(num_seqs, num_groups, num_heads, num_kv_heads,
-                                                                   head_dim, max_context_len, max_prefix_len,
-                                                                   max_group_size, max_suffix_len))
+                                                 max_group_size: int = 0, max_suffix_len: int = 0,
+                                                 device: Optional[int] = None) -> int:
+    """Bytes of scratch of a call on GPU number `device` (None: the current one),
+    whose SMs decide how the work is split."""
+    sizes = (num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_context_len, max_prefix_len, max_group_size,
+             max_suffix_len)
+    if device is None and torch.cuda.is_initialized():
+        device = torch.cuda.current_device()
+    return _shared_size(*sizes) if device is None else _shared_size_on(device, *sizes)
+
+
+def _shared_size(*sizes) -> int:
+    return int(load().paged_attention_decode_shared_workspace_size(*sizes))
+
+
+@functools.lru_cache(maxsize=4096)
+def _shared_size_on(index: int, *sizes) -> int:
+    """Kept per device: asked of the device the first time."""
+    if torch.cuda.current_device() == index:
+        return _shared_size(*sizes)
+    with torch.cuda.device(index):
+        return _shared_size(*sizes)
 
 
 def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -798,7 +815,7 @@ def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_ca
     G = group_start.shape[0] - 1
     if workspace is None:
         need = paged_attention_decode_shared_workspace_size(S, G, H, Hkv, d, max_context_len or mb * B, max_prefix_len,
-                                                            max_group_size, max_suffix_len)
+                                                            max_group_size, max_suffix_len, index)
         workspace = _scratch(index, need, stream)
     _call(load().paged_attention_decode_shared, what, index, *ptrs, _at(group_start, "group_start", torch.int32, index),
           _at(prefix_lens, "prefix_lens", torch.int32, index), S, G, max_group_size, max_prefix_len, max_suffix_len, mb,

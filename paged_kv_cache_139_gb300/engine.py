@@ -653,7 +653,7 @@ def _scratch_shared(eng: PagedKVCache, groups, S, H, d, mcl, stream):
     memory of its own, made on its stream (with a window there is none)."""
     n = 0 if groups is None else paged_attention_decode_shared_workspace_size(
         S, groups.start.shape[0] - 1, H, eng.num_kv_heads, d, mcl, groups.max_prefix_len, groups.max_group_size,
-        groups.max_suffix_len)
+        groups.max_suffix_len, eng.key_cache.get_device())
     with _on(stream):
         return torch.empty(max(n, 16), dtype=torch.uint8, device=eng.device)
 
