@@ -383,23 +383,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         // kWindow: no ticket without work.  Tickets run over levels of row tiles from the top; a level
         // has the sequences with new tokens there, each with its heads.  (A window's items all cost
         // about the same, so that an equal number each, without a counter, is nearly balanced.)
+        // The sequences are gone through only for a level where another one joins: as often as the
+        // longest of them differ, not once for each level: 511 tokens beside a prompt of 16,384, window 512, take
+        // 475 us (730 with a pass for each level), and 60,000 would outlast the other warps' waits.  Loops here
+        // stay rolled (unrolled, 8 prompts of 512 to 4,096 tokens take 1.5 % longer).
         // (Tickets only grow, so the search for a level's k-th sequence goes on from the last one found.)
-        int level = a.num_pairs, level_t = 0, level_seqs = 0;      // tickets before the level, its sequences
+        int level = a.num_pairs - 1, level_t = 0, level_seqs = 0;  // tickets before the level, its sequences
+        int joins = -1, first_s = 0;                               // the next level that has more of them; where they begin
         int seen_s = 0, seen_k = 0;                                // the level's sequences below seen_s: seen_k
-        const int level_rows = a.head_pairs ? kRows : kTiles * kRows, level_heads = a.head_pairs ? a.num_heads / 2 : a.num_heads;
-        auto rows_above = [&](int s, bool report) -> unsigned {    // lanes whose sequence s + lane is in the level
-            bool in = false;
-            if (s + lane < a.num_seqs) {
-                const int qb = a.query_start[s + lane], qe = a.query_start[s + lane + 1], ctx = a.context_lens[s + lane];
-                const int n = qe - qb;
-                if (n < 0 || qb < 0 || qe > a.num_tokens || n > ctx || ctx > a.max_blocks * B) {
-                    if (report) latch(st, kFlagBadContext, s + lane);
+        const int level_rows = a.head_pairs ? 7 : 8, level_heads = a.head_pairs ? a.num_heads / 2 : a.num_heads;      // (log2)
+        static_assert(kRows == 1 << 7 && kTiles * kRows == 1 << 8, "rows of a level");
+        auto top_level = [&](int s) -> int {                       // of sequence s; -1: without rows, -2: out of bounds
+            if (s >= a.num_seqs) return -1;
+            const int qb = a.query_start[s], qe = a.query_start[s + 1], ctx = a.context_lens[s], n = qe - qb;
+            if (n < 0 || qb < 0 || qe > a.num_tokens || n > ctx || ctx > a.max_blocks * B) return -2;
+            return min((n - 1) >> level_rows, a.num_pairs - 1);
+        };
+        auto rows_above = [&](int s) { return __ballot_sync(0xffffffffu, top_level(s + lane) >= level); };   // of s + lane
+        auto scan_level = [&](bool report) {
+            int count = 0, below = -1, head = INT_MAX;
+#pragma unroll 1
+            for (int i = 0; i < a.num_seqs; i += 32) {
+                const int top = top_level(i + lane);
+                if (report && top == -2) latch(st, kFlagBadContext, i + lane);
+                if (top >= level) {
+                    count++;
+                    head = min(head, i);
                 } else {
-                    in = n > level * level_rows;
+                    below = max(below, top);
                 }
             }
-            return __ballot_sync(0xffffffffu, in);
+            level_seqs = __reduce_add_sync(0xffffffffu, count);
+            joins = __reduce_max_sync(0xffffffffu, below);
+            seen_s = first_s = __reduce_min_sync(0xffffffffu, head);
+            seen_k = 0;
         };
+        if constexpr (MODE == kWindow) scan_level(blockIdx.x == 0);
         // the first item with work at or after ticket t (following the claims); stop when none
         auto resolve = [&](int t, Item &o) -> int {
             if constexpr (MODE == kShared) {
@@ -443,23 +462,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (t < a.num_items) {
                 int s, h, pair;
                 if constexpr (MODE == kWindow) {
-                    while (t >= level_t + level_seqs * level_heads) {
-                        level_t += level_seqs * level_heads;
-                        level_seqs = seen_s = seen_k = 0;
-                        if (--level < 0) break;
-                        for (int i = 0; i < a.num_seqs; i += 32)
-                            level_seqs += __popc(rows_above(i, blockIdx.x == 0 && level == a.num_pairs - 1));
+                    for (int per; t >= level_t + (per = level_seqs * level_heads);) {
+                        // the levels above `joins` have this one's sequences
+                        const int down = per ? min((t - level_t) / per, level - 1 - joins) : 0;
+                        if (down > 0) {
+                            level -= down;
+                            level_t += down * per;
+                            seen_s = first_s;
+                            seen_k = 0;
+                        } else {
+                            level_t += per;
+                            level = joins;
+                            if (level < 0) break;
+                            scan_level(false);
+                        }
                     }
                     if (level < 0) break;
                     const int k = (t - level_t) / level_heads;     // the level's k-th sequence
                     h = (t - level_t) % level_heads * (a.head_pairs ? 2 : 1);
                     pair = level;
-                    unsigned m = rows_above(seen_s, false);
+                    unsigned m = rows_above(seen_s);
+#pragma unroll 1
                     for (int c = __popc(m); seen_k + c <= k && seen_s + 32 < a.num_seqs; c = __popc(m)) {
                         seen_k += c;
                         seen_s += 32;
-                        m = rows_above(seen_s, false);
+                        m = rows_above(seen_s);
                     }
+#pragma unroll 1
                     for (int i = seen_k; i < k; i++) m &= m - 1;
                     if (!m) break;                                 // (lengths that changed while the kernel ran)
                     s = seen_s + __ffs(m) - 1;
