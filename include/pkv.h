@@ -536,8 +536,11 @@ pkv_status paged_attention_prefill_window(void *out_dev, const void *query_dev,
  * fp16, but 11 where groups of more than 16 query rows per kv head (sequences x
  * heads) have long prefixes, which then go through the prompt phase's kernel (three
  * launches instead of two); an infinite value may give NaN.  A NaN among a group's
- * first tokens reaches all of its sequences.  num_seqs <= 65535; up to 128 query heads per kv head; scale > 0;
- * contexts up to 2^30 tokens.  Other arguments as for paged_attention_decode.
+ * first tokens reaches all of its sequences.  num_seqs <= 65535; up to 128 query
+ * heads per kv head; scale > 0; contexts up to 2^30 tokens.  Prefixes that go
+ * through the prompt phase's kernel: (groups + num_seqs / sequences of 256 query
+ * rows) x partitions of a prefix (64 at most) x kv heads <= 2^28.  Other arguments
+ * as for paged_attention_decode.
  * ------------------------------------------------------------------------- */
 pkv_status paged_attention_decode_shared(void *out_dev, const void *query_dev,
                                          const void *key_cache_dev, const void *value_cache_dev,

@@ -1022,11 +1022,10 @@ pkv_status paged_attention_decode_shared(void *out, const void *query, const voi
     if (!workspace || workspace_bytes < w.bytes || !aligned16(workspace))
         return fail(PKV_EINVAL, "%s: workspace of %zu bytes needed, %zu given", what, w.bytes,
                     workspace ? workspace_bytes : (size_t)0);
-    const long long seqs = 2 * (128 / a.group);           // of an item of the tcgen05 kernel
-    const long long prefix_items = (long long)num_groups * ((max_group + seqs - 1) / seqs) * w.max_parts * num_kv_heads;
-    if (!w.few && prefix_items > kMaxPrefillItems)
-        return fail(PKV_EINVAL, "%s: %lld work items (groups x pairs of row tiles x partitions x kv heads) above 2^30", what,
-                    prefix_items);
+    const long long prefix_items = ((long long)num_groups + more_pairs(num_seqs, max_group, a.group)) * w.max_parts * num_kv_heads;
+    if (!w.few && prefix_items > kMaxSharedItems)
+        return fail(PKV_EINVAL, "%s: %lld work items ((groups + further pairs of row tiles) x partitions x kv heads) above 2^28",
+                    what, prefix_items);
     rc = open_span(call, a, maps);
     if (rc != PKV_OK) return rc;
     unsigned char *ws = static_cast<unsigned char *>(workspace);

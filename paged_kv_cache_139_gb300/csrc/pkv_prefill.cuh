@@ -117,7 +117,7 @@ struct PrefillArgs {
     float scale_log2;                    // scale * log2(e)
     int window, sinks;                   // kWindow
     int sink_unit;                       // the largest power of two that divides sinks, at most a block
-    // kShared; tickets are num_groups x num_pairs x num_parts x kv heads
+    // kShared; tickets are (num_groups + num_pairs, those after the groups' first ones) x num_parts x kv heads
     const int32_t *group_start, *prefix_lens;
     int num_groups, max_group, max_prefix, num_kv_heads;
     int tile_seqs;                       // sequences per row tile
@@ -422,38 +422,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the first item with work at or after ticket t (following the claims); stop when none
         auto resolve = [&](int t, Item &o) -> int {
             if constexpr (MODE == kShared) {
-                for (; t < a.num_items; t = next_ticket(t)) {
-                    const int g = t % a.num_kv_heads, part = t / a.num_kv_heads % a.num_parts;
-                    const int rest = t / a.num_kv_heads / a.num_parts, pair = rest % a.num_pairs, gr = rest / a.num_pairs;
-                    const int b = a.group_start[gr], e = a.group_start[gr + 1], t0 = pair * kTiles * a.tile_seqs;
+                // Units, each with its partitions and kv heads: the first pair of row tiles of every group, then, where
+                // groups may have more, those that begin q = (u + 1) pairs' sequences or less into the batch: of
+                // the group that q lies in, as many pairs after its first as such q lie between.  (All pairs of
+                // the largest group for each of thousands of lone sequences would outlast the other warps'
+                // waits, and so would asking for one ticket at a time.)
+                const int seqs = kTiles * a.tile_seqs;
+                for (; t < a.num_items; t += 32 * G) {
+                    // one ticket to a lane
+                    const int mine = t + lane * G, rest = min(mine, a.num_items - 1) / a.num_kv_heads, unit = rest / a.num_parts;
+                    const int g = mine - rest * a.num_kv_heads, part = rest - unit * a.num_parts;
+                    int gr = unit, pair = 0;
+                    if (unit >= a.num_groups) {
+                        pair = unit - a.num_groups + 1;                    // q in pairs' sequences
+                        gr = 0;
+                        for (int last = a.num_groups - 1; gr < last;) {
+                            const int mid = (gr + last + 1) / 2;
+                            if (a.group_start[mid] <= pair * seqs) gr = mid;
+                            else last = mid - 1;
+                        }
+                    }
+                    const int b = a.group_start[gr], e = a.group_start[gr + 1];
                     const bool bad = b < 0 || e < b || e > a.num_seqs || e - b > a.max_group;
                     const bool edge = (gr == 0 && b != 0) || (gr == a.num_groups - 1 && e != a.num_seqs);
-                    if (g == 0 && part == 0 && pair == 0) {       // once for each group
-                        if ((bad || edge) && lane == 0) latch(st, kFlagBadGroup, gr);
-                        if (!bad)
-                            for (int i = b + lane; i < e; i += 32)
-                                if (a.prefix_lens[i] != a.prefix_lens[b]) latch(st, kFlagBadGroup, gr);
+                    const bool more = pair > 0;
+                    if (more) pair -= b / seqs;
+                    int prefix = 0;
+                    bool work = mine < a.num_items && !bad && (!more || pair > 0) && pair * seqs < e - b;
+                    if (work) {
+                        prefix = a.prefix_lens[b];
+                        // (a prefix out of bounds is reported by the own tokens' half)
+                        work = prefix >= 0 && prefix <= a.max_prefix && prefix <= a.context_lens[b] &&
+                               part * a.part_tiles * kKeys < prefix;
                     }
-                    if (bad || b + t0 >= e) continue;
-                    const int prefix = a.prefix_lens[b], k0 = part * a.part_tiles * kKeys;
-                    // (a prefix out of bounds is reported by the own tokens' half)
-                    if (prefix < 0 || prefix > a.max_prefix || prefix > a.context_lens[b] || k0 >= prefix) continue;
-                    o.s = b;
-                    o.h = o.h1 = g * a.group;
-                    o.t0 = t0;
-                    o.q_begin = b;
-                    o.ctx = min(prefix, k0 + a.part_tiles * kKeys);
+                    const unsigned m = __ballot_sync(0xffffffffu, work);
+                    const int f = m ? __ffs(m) - 1 : 31;
+                    // what groups are looked at for the first time
+                    const bool head = mine < a.num_items && !more && part == 0 && g == 0;
+                    if (head && lane <= f && (bad || edge)) latch(st, kFlagBadGroup, gr);
+                    unsigned look = __ballot_sync(0xffffffffu, head && lane <= f && !bad && e - b > 1);
+#pragma unroll 1
+                    for (; look; look &= look - 1) {
+                        const int from = __ffs(look) - 1, i0 = __shfl_sync(0xffffffffu, b, from), i1 = __shfl_sync(0xffffffffu, e, from);
+                        const int group0 = __shfl_sync(0xffffffffu, gr, from);
+#pragma unroll 1
+                        for (int i = i0 + lane; i < i1; i += 32)
+                            if (a.prefix_lens[i] != a.prefix_lens[i0]) latch(st, kFlagBadGroup, group0);
+                    }
+                    if (!m) continue;
+                    o.part = __shfl_sync(0xffffffffu, part, f);
+                    o.koff = o.part * a.part_tiles;
+                    const int k0 = o.koff * kKeys;
+                    const int rows = __shfl_sync(0xffffffffu, e - b, f) - __shfl_sync(0xffffffffu, pair, f) * seqs;
+                    t = __shfl_sync(0xffffffffu, mine, f);
+                    o.s = o.q_begin = __shfl_sync(0xffffffffu, b, f);
+                    o.h = o.h1 = __shfl_sync(0xffffffffu, g, f) * a.group;
+                    o.t0 = __shfl_sync(0xffffffffu, pair, f) * seqs;
+                    o.ctx = min(__shfl_sync(0xffffffffu, prefix, f), k0 + a.part_tiles * kKeys);
                     o.pos00 = 0;
-                    o.rows0 = min(a.tile_seqs, e - b - t0) * a.group;
-                    o.rows1 = max(0, min(a.tile_seqs, e - b - t0 - a.tile_seqs)) * a.group;
+                    o.rows0 = min(a.tile_seqs, rows) * a.group;
+                    o.rows1 = max(0, min(a.tile_seqs, rows - a.tile_seqs)) * a.group;
                     o.nkv0 = (o.ctx - k0 + kKeys - 1) / kKeys;
                     o.nkv1 = o.rows1 ? o.nkv0 : 0;
                     o.rstep = a.tile_seqs;
                     o.stop = 0;
                     o.split = (o.rows1 == 0 && o.nkv0 >= 2) ? 1 : 0;
                     o.nsink = o.skip1 = 0;
-                    o.koff = part * a.part_tiles;
-                    o.part = part;
                     return t;
                 }
                 o.stop = 1;

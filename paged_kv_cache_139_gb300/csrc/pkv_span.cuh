@@ -20,6 +20,16 @@ struct PrefixParts {
     int slots;                 // of both
 };
 
+// Pairs of row tiles that groups may have after their first ones: `group` query
+// heads per kv head, 128 rows to a tile.
+inline int more_pairs(int num_seqs, int max_group_size, int group) {
+    const int seqs = 2 * (128 / group);
+    return max_group_size > seqs ? (num_seqs - 1) / seqs : 0;
+}
+
+// Its work items at most: beyond, looking for those with work could outlast the kernel's waits.
+constexpr long long kMaxSharedItems = 1ll << 28;
+
 // The prefix half over groups of many rows, on the fifth-generation tensor
 // cores (shared_prefix.cu), on at most max_ctas SMs.  Arguments as checked by the
 // caller.

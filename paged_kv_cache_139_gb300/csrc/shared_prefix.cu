@@ -34,8 +34,8 @@ cudaError_t launch_shared_prefix(const void *query, const void *key_cache, const
     a.part_tiles = parts.part / kKeys;
     a.num_parts = parts.max_parts;
     a.parts = parts;
-    a.num_pairs = (max_group_size + kTiles * a.tile_seqs - 1) / (kTiles * a.tile_seqs);
-    a.num_items = num_groups * a.num_pairs * a.num_parts * num_kv_heads;     // (the caller has checked that it is one)
+    a.num_pairs = more_pairs(num_seqs, max_group_size, a.group);
+    a.num_items = (num_groups + a.num_pairs) * a.num_parts * num_kv_heads;   // (the caller has checked that it is one)
     if (!a.status) return cudaErrorInvalidValue;
     a.max_ctas = max_ctas;
     return launch_prefill<kShared>(head_dim, bf16, a, query, key_cache, value_cache, num_kv_heads, stream);
