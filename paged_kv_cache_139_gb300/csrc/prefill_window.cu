@@ -21,7 +21,10 @@ extern "C" pkv_status paged_attention_prefill_window(void *out, const void *quer
                                        num_seqs, num_tokens, max_query_len, max_blocks_per_seq, block_size, num_blocks,
                                        num_heads, num_kv_heads, head_dim, scale, workspace, workspace_bytes, dtype);
     if (rc != PKV_OK || a.num_items == 0) return rc;
-    a.window = window;
+    // The kernel takes up to 96 + window from a row's place against a key tile, which goes down to -255: that stays
+    // within 32 bits.  (Contexts of 2^31 - 1024 tokens and more, which would see less, fit no memory.  The same done
+    // in the kernel, against its own limits, makes fp16 prompts 2.5 % slower.)
+    a.window = window < INT_MAX - 1024 ? window : INT_MAX - 1024;
     a.sinks = num_sinks;
     a.sink_unit = num_sinks > 0 && (num_sinks & -num_sinks) < block_size ? num_sinks & -num_sinks : block_size;
     const cudaError_t e = launch_prefill<kWindow>(head_dim, dtype == PKV_BF16, a, query, key_cache, value_cache,
