@@ -489,9 +489,9 @@ pkv_status paged_attention_decode_window(void *out_dev, const void *query_dev,
  * sequence sees the tokens t <= p with
  *   t > p - window  or  t < num_sinks.
  * Table entries of blocks that no new token of the sequence sees are not read.
- * As in paged_attention_prefill, a value that is NaN may also reach rows that do
- * not see it: here up to 255 tokens before it, and up to 383 tokens after the
- * last one whose window holds it (its probability there is 0, and 0 x NaN is NaN).
+ * As in paged_attention_prefill, a value that is NaN or infinite may also reach rows
+ * that do not see it, as NaN: here up to 255 tokens before it, and up to 383 tokens after
+ * the last one whose window holds it (its probability there is 0, and 0 x NaN is NaN).
  *   window     at least 1;  num_sinks  at least 0
  * Other arguments, and the workspace, as for paged_attention_prefill.
  * ------------------------------------------------------------------------- */

@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(SpanConf<D, NT, W>::THREADS, SpanConf<D, NT, W
     // The suffix half starts while the prefix half runs.  That one began after every grid before it
     // had finished (it waits for them before it lets this one start), so queries, lengths, tables and
     // caches are in place; only its partial results are not, and the wait for those comes below.
-    // (Loads here go past L1.)
+    // (Loads here go past L1.  So every CTA of a prefix half, here and in pkv_prefill.cuh, waits before it triggers.)
     if constexpr (MODE == kSpanWindow || MODE == kSpanPrefix) pdl_wait();
     pdl_trigger();
     // (used once the lengths are here too: one round trip for all)

@@ -18,7 +18,11 @@ int sm_count();
 
 // Launch with programmatic stream serialisation: the kernel may begin while
 // the previous grid in the stream finishes, and every kernel of this library
-// calls pdl_wait() before it touches global memory.
+// calls pdl_wait() before it touches global memory.  One exception: own tokens in
+// decode over shared prefixes (attention_span.cu, kSpanSuffix and kSpanOwn) read
+// the caller's tensors, and write partial results that nothing else touches,
+// before they wait.  That holds only right after the prefix half of the same call,
+// whose every CTA calls pdl_wait() before pdl_trigger(): what ran before it is done.
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                    Args &&...args) {

@@ -1,5 +1,5 @@
 """The engine's shared steps over groups large and long enough for the prompt
-phase's kernel: direct, prepared and captured, against 64 bits on the CPU."""
+phase's kernel: direct and prepared, against 64 bits on the CPU."""
 import pytest
 import torch
 
