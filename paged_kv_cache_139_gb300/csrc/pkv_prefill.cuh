@@ -426,11 +426,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the first item with work at or after ticket t (following the claims); stop when none
         auto resolve = [&](int t, Item &o) -> int {
             if constexpr (MODE == kShared) {
-                // Units, each with its partitions and kv heads: the first pair of row tiles of every group, then, where
-                // groups may have more, those that begin q = (u + 1) pairs' sequences or less into the batch: of
-                // the group that q lies in, as many pairs after its first as such q lie between.  (All pairs of
-                // the largest group for each of thousands of lone sequences would outlast the other warps'
-                // waits, and so would asking for one ticket at a time.)
+                // Units of work, each with its partitions and kv heads.  A pair of row tiles holds `seqs` sequences.
+                // The first num_groups units are the groups' first pairs.  Unit num_groups + u (where a group may
+                // have more than one pair) stands for sequence q = (u + 1) seqs of the batch: with the i-th such q
+                // inside it, a group has its i-th pair after the first.  So there are no more units than groups and
+                // whole pairs in the batch.  (All pairs of the largest group for each of thousands of lone sequences
+                // would outlast the other warps' waits, and so would asking for one ticket at a time.)
                 const int seqs = kTiles * a.tile_seqs;
                 for (; t < a.num_items; t += 32 * G) {
                     // one ticket to a lane
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int g = mine - rest * a.num_kv_heads, part = rest - unit * a.num_parts;
                     int gr = unit, pair = 0;
                     if (unit >= a.num_groups) {
-                        pair = unit - a.num_groups + 1;                    // q in pairs' sequences
+                        pair = unit - a.num_groups + 1;                    // q / seqs
                         gr = 0;
                         for (int last = a.num_groups - 1; gr < last;) {
                             const int mid = (gr + last + 1) / 2;
@@ -497,84 +498,84 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o.stop = 1;
                 return t;
             } else {
-            while (t < a.num_items) {
-                int s, h, pair;
-                if constexpr (MODE == kWindow) {
-                    for (int per; t >= level_t + (per = level_seqs * level_heads);) {
-                        // the levels above `joins` have this one's sequences
-                        const int down = per ? min((t - level_t) / per, level - 1 - joins) : 0;
-                        if (down > 0) {
-                            level -= down;
-                            level_t += down * per;
-                            seen_s = first_s;
-                            seen_k = 0;
-                        } else {
-                            level_t += per;
-                            level = joins;
-                            if (level < 0) break;
-                            scan_level(false);
-                        }
-                    }
-                    if (level < 0) break;
-                    const int k = (t - level_t) / level_heads;     // the level's k-th sequence
-                    h = (t - level_t) % level_heads * (a.head_pairs ? 2 : 1);
-                    pair = level;
-                    unsigned m = rows_above(seen_s);
-#pragma unroll 1
-                    for (int c = __popc(m); seen_k + c <= k && seen_s + 32 < a.num_seqs; c = __popc(m)) {
-                        seen_k += c;
-                        seen_s += 32;
-                        m = rows_above(seen_s);
-                    }
-#pragma unroll 1
-                    for (int i = seen_k; i < k; i++) m &= m - 1;
-                    if (!m) break;                                 // (lengths that changed while the kernel ran)
-                    s = seen_s + __ffs(m) - 1;
-                } else {
-                    ticket_item(a, t, s, h, pair);
-                }
-                const int qb = a.query_start[s], qe = a.query_start[s + 1], ctx = a.context_lens[s];
-                const int n = qe - qb, t0 = pair * (a.head_pairs ? kRows : kTiles * kRows);
-                if (n < 0 || qb < 0 || qe > a.num_tokens || n > ctx || ctx > a.max_blocks * B) {
-                    if (lane == 0 && pair == 0 && h == 0) latch(st, kFlagBadContext, s);
-                } else if (t0 < n) {
-                    o.s = s;
-                    o.h = h;
-                    o.t0 = t0;
-                    o.q_begin = qb;
-                    o.ctx = ctx;
-                    o.pos00 = ctx - n + t0;
-                    o.rows0 = min(kRows, n - t0);
-                    o.nkv0 = (o.pos00 + o.rows0 - 1) / kKeys + 1;
-                    if (a.head_pairs) {                        // the same rows of the next head
-                        o.rows1 = o.rows0;
-                        o.nkv1 = o.nkv0;
-                        o.h1 = h + 1;
-                        o.rstep = 0;
-                    } else {
-                        o.rows1 = max(0, min(kRows, n - t0 - kRows));
-                        o.nkv1 = o.rows1 ? (o.pos00 + kRows + o.rows1 - 1) / kKeys + 1 : 0;
-                        o.h1 = h;
-                        o.rstep = kRows;
-                    }
+                while (t < a.num_items) {
+                    int s, h, pair;
                     if constexpr (MODE == kWindow) {
-                        const int low0 = max(0, o.pos00 - a.window + 1) / kKeys;      // its first row's window
-                        const int low1 = max(0, o.pos00 - a.window + 1 + o.rstep) / kKeys;
-                        o.nsink = a.sinks > 0 ? min((a.sinks - 1) / kKeys + 1, low0) : 0;
-                        o.koff = low0 - o.nsink;
-                        o.nkv0 -= o.koff;
-                        if (o.rows1) o.nkv1 -= o.koff;
-                        o.skip1 = o.rows1 && low1 > low0 && low0 * kKeys >= a.sinks ? 1 : 0;
-                        o.part = 0;
+                        for (int per; t >= level_t + (per = level_seqs * level_heads);) {
+                            // the levels above `joins` have this one's sequences
+                            const int down = per ? min((t - level_t) / per, level - 1 - joins) : 0;
+                            if (down > 0) {
+                                level -= down;
+                                level_t += down * per;
+                                seen_s = first_s;
+                                seen_k = 0;
+                            } else {
+                                level_t += per;
+                                level = joins;
+                                if (level < 0) break;
+                                scan_level(false);
+                            }
+                        }
+                        if (level < 0) break;
+                        const int k = (t - level_t) / level_heads;     // the level's k-th sequence
+                        h = (t - level_t) % level_heads * (a.head_pairs ? 2 : 1);
+                        pair = level;
+                        unsigned m = rows_above(seen_s);
+#pragma unroll 1
+                        for (int c = __popc(m); seen_k + c <= k && seen_s + 32 < a.num_seqs; c = __popc(m)) {
+                            seen_k += c;
+                            seen_s += 32;
+                            m = rows_above(seen_s);
+                        }
+#pragma unroll 1
+                        for (int i = seen_k; i < k; i++) m &= m - 1;
+                        if (!m) break;                                 // (lengths that changed while the kernel ran)
+                        s = seen_s + __ffs(m) - 1;
+                    } else {
+                        ticket_item(a, t, s, h, pair);
                     }
-                    o.stop = 0;
-                    o.split = (o.rows1 == 0 && o.nkv0 >= 2) ? 1 : 0;
-                    return t;
+                    const int qb = a.query_start[s], qe = a.query_start[s + 1], ctx = a.context_lens[s];
+                    const int n = qe - qb, t0 = pair * (a.head_pairs ? kRows : kTiles * kRows);
+                    if (n < 0 || qb < 0 || qe > a.num_tokens || n > ctx || ctx > a.max_blocks * B) {
+                        if (lane == 0 && pair == 0 && h == 0) latch(st, kFlagBadContext, s);
+                    } else if (t0 < n) {
+                        o.s = s;
+                        o.h = h;
+                        o.t0 = t0;
+                        o.q_begin = qb;
+                        o.ctx = ctx;
+                        o.pos00 = ctx - n + t0;
+                        o.rows0 = min(kRows, n - t0);
+                        o.nkv0 = (o.pos00 + o.rows0 - 1) / kKeys + 1;
+                        if (a.head_pairs) {                        // the same rows of the next head
+                            o.rows1 = o.rows0;
+                            o.nkv1 = o.nkv0;
+                            o.h1 = h + 1;
+                            o.rstep = 0;
+                        } else {
+                            o.rows1 = max(0, min(kRows, n - t0 - kRows));
+                            o.nkv1 = o.rows1 ? (o.pos00 + kRows + o.rows1 - 1) / kKeys + 1 : 0;
+                            o.h1 = h;
+                            o.rstep = kRows;
+                        }
+                        if constexpr (MODE == kWindow) {
+                            const int low0 = max(0, o.pos00 - a.window + 1) / kKeys;      // its first row's window
+                            const int low1 = max(0, o.pos00 - a.window + 1 + o.rstep) / kKeys;
+                            o.nsink = a.sinks > 0 ? min((a.sinks - 1) / kKeys + 1, low0) : 0;
+                            o.koff = low0 - o.nsink;
+                            o.nkv0 -= o.koff;
+                            if (o.rows1) o.nkv1 -= o.koff;
+                            o.skip1 = o.rows1 && low1 > low0 && low0 * kKeys >= a.sinks ? 1 : 0;
+                            o.part = 0;
+                        }
+                        o.stop = 0;
+                        o.split = (o.rows1 == 0 && o.nkv0 >= 2) ? 1 : 0;
+                        return t;
+                    }
+                    t = next_ticket(t);
                 }
-                t = next_ticket(t);
-            }
-            o.stop = 1;
-            return t;
+                o.stop = 1;
+                return t;
             }
         };
         bool ok = true;
@@ -627,22 +628,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     phys = 0;                                   // keep the byte count; the output is flagged
                 }
                 const uint32_t bytes = (uint32_t)nb * (uint32_t)B * 128u * NP;
-                for (int which = 0; which < 1; which++) {       // K (the value warp loads V)
-                    if (gj >= kStages) {
-                        ok = wait_warp(&bars[(which ? bVEmpty : bKEmpty) + stg], ((gj >> 1) - 1) & 1,
-                                       kWaitLimitCycles);
-                        if (!ok) break;
-                    }
-                    uint64_t *full = &bars[(which ? bVFull : bKFull) + stg];
-                    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-                    __syncwarp();
-                    uint8_t *dst = sm + (which ? L::v : L::k) + (uint32_t)stg * NP * kPanelBytes;
-                    if (lane < nb)
-                        for (int p = 0; p < NP; p++)
-                            tma_load_4d(dst + p * kPanelBytes + (uint32_t)lane * B * 128u, which ? &tmv : &tmk,
-                                        64 * p, 0, g, phys, full, pol_kv);
+                if (gj >= kStages) {
+                    ok = wait_warp(&bars[bKEmpty + stg], ((gj >> 1) - 1) & 1, kWaitLimitCycles);
+                    if (!ok) break;
                 }
-                if (!ok) break;
+                uint64_t *full = &bars[bKFull + stg];
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                __syncwarp();
+                uint8_t *dst = sm + L::k + (uint32_t)stg * NP * kPanelBytes;
+                if (lane < nb)
+                    for (int p = 0; p < NP; p++)
+                        tma_load_4d(dst + p * kPanelBytes + (uint32_t)lane * B * 128u, &tmk, 64 * p, 0, g, phys, full, pol_kv);
                 cb = nxt;
                 // claim and look up the next item while this one's tiles stream in
                 if (j == 0) nxt_t = resolve(next_ticket(cur_t), nxt_item);
