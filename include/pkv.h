@@ -539,7 +539,7 @@ pkv_status paged_attention_prefill_window(void *out_dev, const void *query_dev,
  * first tokens reaches all of its sequences.  num_seqs <= 65535; up to 128 query
  * heads per kv head; scale > 0; contexts up to 2^30 tokens.  Prefixes that go
  * through the prompt phase's kernel: (groups + num_seqs / sequences of 256 query
- * rows) x partitions of a prefix (64 at most) x kv heads <= 2^28.  Other arguments
+ * rows) x partitions of a prefix (64 at most) x kv heads <= 2^27.  Other arguments
  * as for paged_attention_decode.
  * ------------------------------------------------------------------------- */
 pkv_status paged_attention_decode_shared(void *out_dev, const void *query_dev,

@@ -1024,7 +1024,7 @@ pkv_status paged_attention_decode_shared(void *out, const void *query, const voi
                     workspace ? workspace_bytes : (size_t)0);
     const long long prefix_items = ((long long)num_groups + more_pairs(num_seqs, max_group, a.group)) * w.max_parts * num_kv_heads;
     if (!w.few && prefix_items > kMaxSharedItems)
-        return fail(PKV_EINVAL, "%s: %lld work items ((groups + further pairs of row tiles) x partitions x kv heads) above 2^28",
+        return fail(PKV_EINVAL, "%s: %lld work items ((groups + further pairs of row tiles) x partitions x kv heads) above 2^27",
                     what, prefix_items);
     rc = open_span(call, a, maps);
     if (rc != PKV_OK) return rc;

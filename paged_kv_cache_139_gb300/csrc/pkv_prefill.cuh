@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             seen_k = 0;
         };
         if constexpr (MODE == kWindow) scan_level(blockIdx.x == 0);
+        int near = 0;                                              // kShared: where this lane's search for a group goes on
         // the first item with work at or after ticket t (following the claims); stop when none
         auto resolve = [&](int t, Item &o) -> int {
             if constexpr (MODE == kShared) {
@@ -440,12 +441,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     int gr = unit, pair = 0;
                     if (unit >= a.num_groups) {
                         pair = unit - a.num_groups + 1;                    // q / seqs
-                        gr = 0;
-                        for (int last = a.num_groups - 1; gr < last;) {
-                            const int mid = (gr + last + 1) / 2;
-                            if (a.group_start[mid] <= pair * seqs) gr = mid;
-                            else last = mid - 1;
-                        }
+                        auto begun = [&](int i) { return i < a.num_groups && a.group_start[i] <= pair * seqs; };
+                        int step = 1;                                      // on from the last one found: tickets only grow
+                        for (; begun(near + step); step *= 2) near += step;
+                        for (; step > 0; step /= 2)
+                            if (begun(near + step)) near += step;
+                        gr = near;
                     }
                     const int b = a.group_start[gr], e = a.group_start[gr + 1];
                     const bool bad = b < 0 || e < b || e > a.num_seqs || e - b > a.max_group;

@@ -28,7 +28,7 @@ inline int more_pairs(int num_seqs, int max_group_size, int group) {
 }
 
 // Its work items at most: beyond, looking for those with work could outlast the kernel's waits.
-constexpr long long kMaxSharedItems = 1ll << 28;
+constexpr long long kMaxSharedItems = 1ll << 27;
 
 // The prefix half over groups of many rows, on the fifth-generation tensor
 // cores (shared_prefix.cu), on at most max_ctas SMs.  Arguments as checked by the

@@ -10,7 +10,7 @@ MANY = dict(S=20000, G=20000, H=16384, Hkv=16384, mgs=17, mpl=128, msl=16, mb=25
 def test_more_prefix_items_than_the_kernel_can_go_through():
     """20,000 groups x 16,384 kv heads."""
     assert call("paged_attention_decode_shared", SHARED, MANY) == 1
-    assert "above 2^28" in message()
+    assert "above 2^27" in message()
 
 
 @pytest.mark.parametrize("over", [dict(S=-1), dict(G=0), dict(mgs=-1), MANY])
