@@ -814,8 +814,7 @@ def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_ca
         raise ValueError(f"{what}: group_start must be [G+1], prefix_lens [S]")
     G = group_start.shape[0] - 1
     if workspace is None:
-        need = paged_attention_decode_shared_workspace_size(S, G, H, Hkv, d, max_context_len or mb * B, max_prefix_len,
-                                                            max_group_size, max_suffix_len, index)
+        need = _shared_size_on(index, S, G, H, Hkv, d, max_context_len or mb * B, max_prefix_len, max_group_size, max_suffix_len)
         workspace = _scratch(index, need, stream)
     _call(load().paged_attention_decode_shared, what, index, *ptrs, _at(group_start, "group_start", torch.int32, index),
           _at(prefix_lens, "prefix_lens", torch.int32, index), S, G, max_group_size, max_prefix_len, max_suffix_len, mb,
