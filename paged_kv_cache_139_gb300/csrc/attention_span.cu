@@ -40,7 +40,7 @@
 // Measured on one GB300: 256 sequences of up to 4,096 tokens, window 1,024, 32 heads:
 // 7.42 TB/s (483 us; the copy rate is 6.79); 48 of up to 32,768, window 4,096, 32/8
 // heads: 6.8 TB/s; 64 of the OPT-13B layer, window 255: 6.2 TB/s (43 us, of which
-// start and tail some 5); one sequence, window 4,096, 32/8 heads: 8.6 us; four small
+// start and tail some 5); one sequence, window 4,096, 32/8 heads: 8.8 us; four small
 // ones 3.4 us.  Shared: 64 x 4 samples 161 us (6.8 TB/s over what is read once).
 // Under ncu the tensor pipe is 13 % and issue slots 23 % busy on the OPT-13B batch.
 // Tried and not kept: CTAs of one warp (8,192 items of 64 tokens 56 against 59 us, but
