@@ -80,14 +80,19 @@ class SharedGroups:
         # what neighbours share; a group shares the least of what its neighbours do
         full = np.asarray(context_lens, np.int64) // block_size
         common = np.minimum(full[:-1], full[1:])
-        rows = np.flatnonzero(common > 0)
-        rows = rows[tables[rows, 0] == tables[rows + 1, 0]] if rows.size else rows
         joined = np.zeros(n - 1, np.int64)
-        if rows.size:
-            most = common[rows]
-            differ = tables[rows, :most.max()] != tables[rows + 1, :most.max()]
+        rows, at, width = np.flatnonzero(common > 0), 0, 1
+        while rows.size:                         # some blocks of those that have been equal so far
+            a, b = int(rows[0]), int(rows[-1]) + 1
+            if rows.size == b - a:
+                differ = tables[a:b, at:at + width] != tables[a + 1:b + 1, at:at + width]
+            else:
+                differ = tables[rows, at:at + width] != tables[rows + 1, at:at + width]
             first = differ.argmax(1)
-            joined[rows] = np.where(differ[np.arange(rows.size), first], np.minimum(first, most), most)
+            parted = differ[np.arange(rows.size), first]
+            at += width
+            joined[rows] = np.minimum(common[rows], np.where(parted, at - width + first, at))
+            rows, width = rows[~parted & (common[rows] > at)], min(8 * width, 512)
         cut = joined == 0
         _cut_runs(joined, cut)
         start = np.concatenate([[0], np.flatnonzero(cut) + 1, [n]])

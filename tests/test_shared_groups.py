@@ -90,3 +90,17 @@ def test_full_blocks_bound_what_neighbours_share():
     assert g.start.tolist() == [0, 3] and g.prefix.tolist() == [12] * 3
     g = engine.SharedGroups.find(t, np.array([24, 3, 24]), B)
     assert g.start.tolist() == [0, 1, 2, 3] and not g.prefix.any()
+
+
+def test_prefixes_of_many_lengths():
+    """Neighbours part before, at and behind every stretch of blocks that is compared at once."""
+    common = [0, 1, 2, 8, 9, 10, 72, 73, 74, 512, 583, 584, 585, 586, 1096, 1097, 1098, 1300, 0, 1300, 585, 1]
+    t = tables_of(common, 1301)
+    for full in (1300, 1301):
+        ctx = np.full(len(t), full * B)
+        g = engine.SharedGroups.find(t, ctx, B)
+        assert saved(g) == saved(find(common, 1301))
+        for a, b in zip(g.start[:-1], g.start[1:]):
+            assert (g.prefix[a:b] == min(common[a:b - 1], default=0) * B).all()
+    pair = engine.SharedGroups.find(t[[0, 0]], np.array([1301 * B, 1301 * B]), B)
+    assert pair.prefix.tolist() == [1301 * B] * 2
